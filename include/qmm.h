@@ -80,7 +80,9 @@ enum {
   QMM_ERR_CUDA = 5,        /* a CUDA call failed; see qmm_last_cuda_error()     */
   QMM_ERR_TIMEOUT = 6,     /* a bounded device wait expired (qmm_sync_status)   */
   QMM_ERR_STATE = 7,       /* NULL, destroyed or otherwise unusable handle      */
-  QMM_ERR_DEVICE = 8       /* no sm_103 device, or the handle's device is not current */
+  QMM_ERR_DEVICE = 8,      /* no sm_103 device, or the handle's device is not current */
+  QMM_ERR_INDEX = 9        /* a length, page id or path entry in device memory was out of
+                              range (qmm_cache_sync_status)                       */
 };
 
 /* ---- formats and flags ---------------------------------------------------- */
@@ -298,6 +300,184 @@ int qmm_prefill(qmm_t h, const uint16_t* act, int64_t lda, float* out, int64_t l
  * 256, plus M * 4).  Errors: INVALID_ARG (NULL bytes, not an FP8 handle),
  * STATE, M_RANGE. */
 int qmm_prefill_workspace(qmm_t h, int64_t M, int64_t* bytes);
+
+/* ---- the paged cache and tree attention ---------------------------------------- */
+
+/* Besides the weight matmuls, a speculative step attends, verifies and keeps
+ * the cache: qmm_tree_attention gives the drafted tree's nodes their attention
+ * over the cached prefix, qmm_verify_sample picks the branch that is kept, and
+ * qmm_cache_commit moves that branch's cache rows behind the prefix.
+ *
+ * Keys and values live in two pools of pages, each
+ *     [n_layers][n_pages][n_kv_heads][page_size][head_dim]
+ * of 16-bit values, so that one head's rows of a page are contiguous.  Row j
+ * of sequence b (its j-th token) is row j % page_size of page
+ * page_table[b][j / page_size].  The caller owns the pools and the page
+ * tables, and decides which page belongs to whom; pages may be shared by
+ * sequences as long as no call writes to them. */
+typedef enum { QMM_DT_BF16 = 0, QMM_DT_F16 = 1, QMM_DT_F32 = 2 } qmm_dtype;
+
+#define QMM_TREE_MAX_T 64      /* nodes of a drafted tree: one bit each of a mask word */
+#define QMM_CACHE_MAX_BATCH 4096
+
+typedef struct {
+  uint32_t struct_size; /* = sizeof(qmm_cache_desc)                             */
+  uint32_t dtype;       /* QMM_DT_BF16 or QMM_DT_F16: pools, queries, outputs   */
+  int32_t n_layers;
+  int32_t page_size;    /* rows of a page: a power of two, 16 to 1024           */
+  int32_t n_q_heads;    /* a multiple of n_kv_heads, at most 64 times it        */
+  int32_t n_kv_heads;
+  int32_t head_dim;     /* 64 or 128                                            */
+  int32_t max_batch;    /* sequences of one call, 1 to QMM_CACHE_MAX_BATCH      */
+  int64_t n_pages;      /* pages of one layer, 1 to 2^31 - 1                    */
+  void* k_pool;         /* device, 16-byte aligned; must outlive the handle     */
+  void* v_pool;         /* device, 16-byte aligned; must outlive the handle     */
+} qmm_cache_desc;
+
+/* Opaque handle: the pools' description, a workspace for partial results and a
+ * status word.  Used from one stream at a time. */
+typedef struct qmm_cache* qmm_cache_t;
+
+/* Create a handle for the two pools; their contents are not touched.
+ * Errors: INVALID_ARG (NULL out/desc/pool, bad struct_size or dtype), SHAPE
+ * (a size outside the ranges above), ALIGN (pools), DEVICE, CUDA (allocation;
+ * nothing is leaked and *out is NULL). */
+int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* desc, void* stream);
+
+/* Free what the handle owns (waits for the device); the pools stay.  NULL is
+ * accepted; a destroyed handle gives QMM_ERR_STATE. */
+int qmm_cache_destroy(qmm_cache_t h);
+
+/* Wait for `stream`, then read and clear the handle's device error word:
+ * QMM_OK, QMM_ERR_INDEX (a length, page id or path entry read from device
+ * memory was out of range; what it named was neither read nor written),
+ * QMM_ERR_TIMEOUT (a bounded device wait expired), QMM_ERR_CUDA. */
+int qmm_cache_sync_status(qmm_cache_t h, void* stream);
+
+typedef struct {
+  uint32_t struct_size;     /* = sizeof(qmm_attn_args)                          */
+  int32_t layer;            /* 0 .. n_layers - 1                                */
+  int32_t B;                /* sequences, 1 .. max_batch                        */
+  int32_t T;                /* nodes per sequence, 1 .. QMM_TREE_MAX_T          */
+  const void* q;            /* [B][T][n_q_heads][head_dim], strides below       */
+  const void* k_new;        /* [B][T][n_kv_heads][head_dim]                     */
+  const void* v_new;        /* [B][T][n_kv_heads][head_dim]                     */
+  void* out;                /* [B][T][n_q_heads][head_dim]                      */
+  int64_t q_stride[3];      /* in elements: sequence, node, head; multiples of 8 */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t out_stride[3];
+  float* lse;               /* [B][T][n_q_heads], contiguous, or NULL           */
+  const int32_t* page_table; /* [B][table_width], row stride ld_table           */
+  int64_t ld_table;
+  int32_t table_width;
+  float scale;              /* of the scores; finite and > 0                    */
+  const int32_t* lens;      /* [B]: cached rows of every sequence               */
+  const int32_t* n_tokens;  /* [B]: nodes of every sequence, <= T; NULL: all T  */
+  const uint64_t* mask;     /* [B][T], row stride ld_mask; NULL: a chain        */
+  int64_t ld_mask;
+} qmm_attn_args;
+
+/* Attention of T drafted nodes per sequence over the cached prefix and each
+ * other.  For sequence b with L = lens[b] cached rows and n = n_tokens[b]
+ * nodes, the nodes' keys and values are written to rows L .. L + n - 1 of
+ * `layer`, and for node t < n and query head h (key/value head h / (n_q_heads /
+ * n_kv_heads))
+ *     s_j = scale * dot(q[b][t][h], K_j)
+ *     out[b][t][h] = sum_j exp(s_j) V_j / sum_j exp(s_j),  lse = log sum_j exp(s_j)
+ * over the rows j < L and the nodes j = L + i, i < n, with bit i of mask[b][t]
+ * set (mask NULL: i <= t).  A plain decoding step is T = 1; a prompt is fed as
+ * chains of up to QMM_TREE_MAX_T.  A row that may see nothing, and rows t >= n,
+ * give out = 0 and lse = -inf.  Rows that a node may not see do not influence
+ * it, whatever they hold, NaN and infinities included; nothing past row
+ * L + n - 1 is read.
+ * Scores, softmax statistics and sums are fp32; the exponentials are rounded
+ * to the 16-bit type for the product with V, as the outputs are at the end.
+ * All pointers to 16-bit data are 16-byte aligned.  Asynchronous on `stream`,
+ * one kernel, results independent of what runs beside it (no atomics on
+ * values).
+ * Errors: STATE, INVALID_ARG (NULL pointers, bad struct_size or scale), SHAPE
+ * (layer, B, T or table_width out of range), ALIGN (pointers, strides,
+ * ld_table < table_width, ld_mask < T), DEVICE, CUDA.  Lengths and page ids
+ * are checked on the device (qmm_cache_sync_status). */
+int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* args, void* stream);
+
+/* Keep one branch of every sequence's drafted nodes: in every layer and both
+ * pools, row L + path[b][j] moves to row L + 1 + j for j < k, with L = lens[b]
+ * and k = accept[2 b] (the layout qmm_verify_sample writes: nodes of the branch
+ * after the root, then anything), and lens_out[b] = L + 1 + k.  path[b][0 .. k - 1]
+ * increases and path[b][j] >= j + 1, as in any tree whose parents come first;
+ * a sequence with other entries is refused on the device: its rows stay and
+ * lens_out[b] = lens[b].
+ * Rows that are in place already cost nothing.
+ *   path: device, int32 [B][T], row stride ld_path.  accept: device, int32 [B][2].
+ *   lens_out: device, int32 [B]; not lens, which every CTA of the call reads.
+ * Asynchronous.  Errors: STATE, INVALID_ARG (NULL, lens_out is lens), SHAPE (B, T, table_width),
+ * ALIGN (ld_path < T, ld_table < table_width), DEVICE, CUDA. */
+int qmm_cache_commit(qmm_cache_t h, int B, int T, const int32_t* page_table, int64_t ld_table,
+                     int table_width, const int32_t* lens, const int32_t* path, int64_t ld_path,
+                     const int32_t* accept, int32_t* lens_out, void* stream);
+
+/* Copy pages in every layer and both pools: the first rows[i] rows (NULL: all)
+ * of page src[i] to page dst[i], i < n.  A sequence is forked by sharing its
+ * full pages and copying the last, partly filled one.  No page may be both
+ * copied to and named again in the same call.  src, dst, rows: device, int32
+ * [n]; entries out of range are skipped and reported.  Asynchronous.
+ * Errors: STATE, INVALID_ARG (NULL src/dst with n > 0), SHAPE (n < 0 or above
+ * 2^20), DEVICE, CUDA. */
+int qmm_cache_copy(qmm_cache_t h, int n, const int32_t* src, const int32_t* dst,
+                   const int32_t* rows, void* stream);
+
+/* ---- verification of drafted tokens by rejection sampling ------------------------ */
+
+typedef struct {
+  uint32_t struct_size;     /* = sizeof(qmm_sample_args)                        */
+  uint32_t dtype;           /* QMM_DT_*: type of target and draft               */
+  int32_t B;                /* sequences, 1 .. 65535                            */
+  int32_t T;                /* nodes per sequence, node 0 the last committed token;
+                               1 .. QMM_TREE_MAX_T                              */
+  int64_t V;                /* vocabulary, 1 .. 2^24                            */
+  const void* target;       /* [B][T][V] scores, entries of a row contiguous    */
+  int64_t target_stride[2]; /* in elements: sequence, node                      */
+  const void* draft;        /* [B][T or T - 1][V]; NULL: tokens drafted without
+                               probabilities (Q is 1 at the drafted token)      */
+  int64_t draft_stride[2];
+  const int32_t* tokens;    /* [B][T], contiguous                               */
+  const int32_t* parents;   /* [B][T], contiguous; NULL: a chain (t - 1)        */
+  const int32_t* n_tokens;  /* [B]; NULL: all T                                 */
+  const float* u;           /* [B][T], contiguous: uniform in [0, 1)            */
+  const float* noise;       /* [B][V], contiguous: exponential variates, > 0    */
+  const float* temperature; /* [B], > 0; NULL: 1                                */
+  int32_t* accept;          /* [B][2]: accepted nodes k, next token             */
+  int32_t* path;            /* [B][T], contiguous: the k accepted nodes, then -1 */
+  void* workspace;          /* device, 256-byte aligned                         */
+  int64_t workspace_bytes;  /* at least qmm_verify_sample_workspace(B, T, V)    */
+} qmm_sample_args;
+
+/* Lossless acceptance of a drafted tree for sampled decoding (qmm_verify_greedy
+ * is the greedy one).  Row i of target holds the target's scores after node i,
+ * row i of draft the drafter's scores from which node i's children were drawn
+ * without replacement in index order; parents[i] < i.  From node c = 0, with
+ * P = softmax(target[c] / temperature), Q = softmax(draft[c] / temperature):
+ *   the children i of c (i < n_tokens) are tried in index order, x = tokens[i]:
+ *     u[i] Q(x) < P(x): node i is accepted, c = i, and so on from there;
+ *     else P <- max(P - Q, 0) / sum (P as it is where that sum is 0),
+ *          Q <- Q with Q(x) = 0 / sum;
+ *   where no child is accepted the walk ends, and the next token is the v with
+ *   the largest P(v) / noise[v], the lowest on ties: a draw from P.
+ * The emitted tokens are distributed as the target's own sampling
+ * would have them.  Scores of -inf have probability 0.  Nodes whose token is
+ * outside [0, V) are never accepted and change nothing.  The next token is in
+ * [0, V) whatever the inputs.  Arithmetic in fp32; sums in an order fixed by the
+ * sizes, so equal inputs give equal results.  Asynchronous.
+ * Errors: INVALID_ARG (NULL, bad struct_size or dtype, workspace too small),
+ * SHAPE (B, T, V), ALIGN (pointers not aligned to their element, workspace),
+ * DEVICE, CUDA. */
+int qmm_verify_sample(const qmm_sample_args* args, void* stream);
+
+/* Bytes of workspace for those sizes; contents need no preparation.
+ * Errors: INVALID_ARG (NULL bytes), SHAPE. */
+int qmm_verify_sample_workspace(int B, int T, int64_t V, int64_t* bytes);
 
 /* ---- status ------------------------------------------------------------------ */
 

@@ -14,10 +14,13 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (QMM_ERR_ALIGN, QMM_ERR_CUDA, QMM_ERR_DEVICE, QMM_ERR_INVALID_ARG,
+from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_ERR_INDEX, QMM_TREE_MAX_T, QMM_ERR_ALIGN, QMM_ERR_CUDA, QMM_ERR_DEVICE, QMM_ERR_INVALID_ARG,
                    QMM_ERR_M_RANGE, QMM_ERR_SHAPE, QMM_ERR_STATE, QMM_ERR_TIMEOUT,
                    QMM_FLAG_HADAMARD32, QMM_FLAG_HADAMARD64, QMM_FLAG_HADAMARD128, QMM_FLAG_TCGEN05, QMM_FLAG_SIMT, QMM_FMT_FP8_E4M3_B128, QMM_FMT_Q4_0, QMM_FMT_Q8_0,
                    QMM_OK, QmmError, load, qmm_desc, qmm_info)
+from .paged import (PagedCache, Sequence, qmm_cache_commit, qmm_cache_copy, qmm_cache_create,
+                    qmm_cache_destroy, qmm_cache_sync_status, qmm_tree_attention, qmm_verify_sample,
+                    qmm_verify_sample_workspace, tree_mask, verify_sample)
 
 __all__ = [
     "Matrix", "qmm_create", "qmm_create_rows", "shard_rows", "qmm_destroy", "qmm_verify", "qmm_verify_greedy", "qmm_verify_host",
@@ -31,6 +34,10 @@ __all__ = [
     "QMM_FMT_Q4_0", "QMM_FMT_FP8_E4M3_B128", "QMM_FMT_Q8_0", "qmm_quantize_q8_0", "quantize_q8_0", "QMM_FLAG_HADAMARD32", "QMM_FLAG_SIMT",
     "QMM_FLAG_TCGEN05", "QMM_FLAG_HADAMARD64", "QMM_FLAG_HADAMARD128", "qmm_hadamard",
     "rotation_flag", "hadamard",
+    "PagedCache", "Sequence", "verify_sample", "tree_mask", "qmm_cache_create", "qmm_cache_destroy",
+    "qmm_cache_sync_status", "qmm_tree_attention", "qmm_cache_commit", "qmm_cache_copy",
+    "qmm_verify_sample", "qmm_verify_sample_workspace", "QMM_ERR_INDEX", "QMM_DT_BF16", "QMM_DT_F16",
+    "QMM_DT_F32", "QMM_TREE_MAX_T",
 ]
 
 

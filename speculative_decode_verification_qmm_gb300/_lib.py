@@ -19,6 +19,7 @@ QMM_ERR_CUDA = 5
 QMM_ERR_TIMEOUT = 6
 QMM_ERR_STATE = 7
 QMM_ERR_DEVICE = 8
+QMM_ERR_INDEX = 9
 
 QMM_FMT_Q4_0 = 0
 QMM_FMT_FP8_E4M3_B128 = 1
@@ -28,6 +29,10 @@ QMM_FLAG_SIMT = 2
 QMM_FLAG_TCGEN05 = 4
 QMM_FLAG_HADAMARD64 = 8
 QMM_FLAG_HADAMARD128 = 16
+QMM_DT_BF16 = 0
+QMM_DT_F16 = 1
+QMM_DT_F32 = 2
+QMM_TREE_MAX_T = 64
 
 
 class qmm_desc(ctypes.Structure):
@@ -65,6 +70,72 @@ class qmm_info(ctypes.Structure):
     ]
 
 
+class qmm_cache_desc(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+        ("n_layers", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("k_pool", ctypes.c_void_p),
+        ("v_pool", ctypes.c_void_p),
+    ]
+
+
+class qmm_attn_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("layer", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("k_new", ctypes.c_void_p),
+        ("v_new", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("out_stride", ctypes.c_int64 * 3),
+        ("lse", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("table_width", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("lens", ctypes.c_void_p),
+        ("n_tokens", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("ld_mask", ctypes.c_int64),
+    ]
+
+
+class qmm_sample_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+        ("B", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("V", ctypes.c_int64),
+        ("target", ctypes.c_void_p),
+        ("target_stride", ctypes.c_int64 * 2),
+        ("draft", ctypes.c_void_p),
+        ("draft_stride", ctypes.c_int64 * 2),
+        ("tokens", ctypes.c_void_p),
+        ("parents", ctypes.c_void_p),
+        ("n_tokens", ctypes.c_void_p),
+        ("u", ctypes.c_void_p),
+        ("noise", ctypes.c_void_p),
+        ("temperature", ctypes.c_void_p),
+        ("accept", ctypes.c_void_p),
+        ("path", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
@@ -81,6 +152,14 @@ SIGNATURES = {
     "qmm_verify_noalloc": (_INT, [_P, _P, _I64, _P, _I64, _INT, _P]),
     "qmm_prefill": (_INT, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _P]),
     "qmm_prefill_workspace": (_INT, [_P, _I64, ctypes.POINTER(_I64)]),
+    "qmm_cache_create": (_INT, [ctypes.POINTER(_P), ctypes.POINTER(qmm_cache_desc), _P]),
+    "qmm_cache_destroy": (_INT, [_P]),
+    "qmm_cache_sync_status": (_INT, [_P, _P]),
+    "qmm_tree_attention": (_INT, [_P, ctypes.POINTER(qmm_attn_args), _P]),
+    "qmm_cache_commit": (_INT, [_P, _INT, _INT, _P, _I64, _INT, _P, _P, _I64, _P, _P, _P]),
+    "qmm_cache_copy": (_INT, [_P, _INT, _P, _P, _P, _P]),
+    "qmm_verify_sample": (_INT, [ctypes.POINTER(qmm_sample_args), _P]),
+    "qmm_verify_sample_workspace": (_INT, [_INT, _INT, _I64, ctypes.POINTER(_I64)]),
     "qmm_sync_status": (_INT, [_P, _P]),
     "qmm_last_cuda_error": (_INT, [_P]),
     "qmm_get_info": (_INT, [_P, ctypes.POINTER(qmm_info)]),

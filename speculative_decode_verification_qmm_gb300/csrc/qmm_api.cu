@@ -11,6 +11,7 @@
 #include <unordered_set>
 
 #include "qmm.h"
+#include "qmm_attn.h"
 #include "qmm_kernels.h"
 
 using namespace qmm;
@@ -358,6 +359,14 @@ cudaError_t launch_verify_kernel(qmm_handle* h, const VerifyParams& vp, const Ve
 
 }  // namespace
 
+namespace qmm {
+
+cudaError_t host_dev_alloc(void** p, size_t bytes) { return dev_alloc(p, bytes); }
+int host_check_device(int* dev, int* sms) { return check_device(dev, sms); }
+int host_cuda_fail(cudaError_t e) { return cuda_fail(nullptr, e); }
+
+}  // namespace qmm
+
 extern "C" {
 
 const char* qmm_strerror(int code) {
@@ -371,6 +380,7 @@ const char* qmm_strerror(int code) {
     case QMM_ERR_TIMEOUT: return "QMM_ERR_TIMEOUT";
     case QMM_ERR_STATE: return "QMM_ERR_STATE";
     case QMM_ERR_DEVICE: return "QMM_ERR_DEVICE";
+    case QMM_ERR_INDEX: return "QMM_ERR_INDEX";
     default: return "QMM_ERR_UNKNOWN";
   }
 }

@@ -1,0 +1,389 @@
+"""The paged key/value cache of a speculative decoder and the operators on it.
+
+    cache = PagedCache(n_layers, n_pages, page_size, n_q_heads, n_kv_heads, head_dim)
+    seq = cache.new_sequence()
+    cache.reserve([seq], T)                  # pages for T more rows
+    table, lens = cache.tables([seq])
+    out, lse = cache.attend(layer, q, k, v, table, lens, mask=mask)
+    accept, path = verify_sample(target, draft, tokens, u, noise, parents=parents)
+    lens = cache.commit(table, lens, path, accept)
+    cache.advance([seq], accepted)           # once the host knows the counts
+    other = cache.fork(seq)
+
+The arithmetic runs in libqmm.so's kernels (qmm_tree_attention,
+qmm_cache_commit, qmm_cache_copy, qmm_verify_sample of include/qmm.h).  What
+stays on the host is bookkeeping: which pages are free, which sequence holds
+which page, and how many sequences share one.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_attn_args,
+                   qmm_cache_desc, qmm_sample_args)
+
+
+def _stream_ptr(stream=None) -> int:
+    import torch
+    s = torch.cuda.current_stream() if stream is None else stream
+    return int(s.cuda_stream)
+
+
+def _check(func: str, rc: int):
+    if rc != QMM_OK:
+        raise QmmError(func, rc)
+
+
+def _dtype(dtype):
+    import torch
+    codes = {torch.bfloat16: QMM_DT_BF16, torch.float16: QMM_DT_F16, torch.float32: QMM_DT_F32}
+    if dtype not in codes:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, not {dtype}")
+    return codes[dtype]
+
+
+def _cuda(name, t, dtype, shape):
+    """The tensor's address after a check of its device, type and shape (None: any size)."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}, not {t.dtype} on {t.device}")
+    if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
+                         f"not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(name, t):
+    """Tensors whose last dimension has to be contiguous."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _flat(name, t):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+# ------------------------------------------------------------------ raw C names
+def qmm_cache_create(dtype, n_layers, n_pages, page_size, n_q_heads, n_kv_heads, head_dim, max_batch,
+                     k_pool, v_pool, stream=None) -> int:
+    """A handle over the two pools (CUDA tensors, which must outlive it)."""
+    d = qmm_cache_desc(ctypes.sizeof(qmm_cache_desc), dtype, n_layers, page_size, n_q_heads, n_kv_heads, head_dim,
+                       max_batch, n_pages, k_pool.data_ptr(), v_pool.data_ptr())
+    h = ctypes.c_void_p()
+    _check("qmm_cache_create", load().qmm_cache_create(ctypes.byref(h), ctypes.byref(d), _stream_ptr(stream)))
+    return h.value
+
+
+def qmm_cache_destroy(h) -> None:
+    _check("qmm_cache_destroy", load().qmm_cache_destroy(h))
+
+
+def qmm_cache_sync_status(h, stream=None) -> int:
+    return load().qmm_cache_sync_status(h, _stream_ptr(stream))
+
+
+def qmm_tree_attention(h, layer, q, k_new, v_new, page_table, lens, out, lse=None, mask=None, n_tokens=None,
+                       scale=None, stream=None) -> None:
+    """q, out CUDA [B, T, Hq, D]; k_new, v_new [B, T, Hkv, D]; page_table int32
+    [B, pages]; lens, n_tokens int32 [B]; mask int64 [B, T]; lse fp32 [B, T, Hq]
+    or None; asynchronous."""
+    B, T, Hq, D = q.shape
+    a = qmm_attn_args()
+    a.struct_size = ctypes.sizeof(qmm_attn_args)
+    a.layer, a.B, a.T = layer, B, T
+    a.q, a.k_new, a.v_new, a.out = q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr()
+    a.q_stride[:], a.k_stride[:] = q.stride()[:3], k_new.stride()[:3]
+    a.v_stride[:], a.out_stride[:] = v_new.stride()[:3], out.stride()[:3]
+    a.lse = lse.data_ptr() if lse is not None else None
+    a.page_table, a.ld_table, a.table_width = page_table.data_ptr(), page_table.stride(0), page_table.shape[1]
+    a.scale = D ** -0.5 if scale is None else scale
+    a.lens = lens.data_ptr()
+    a.n_tokens = n_tokens.data_ptr() if n_tokens is not None else None
+    a.mask, a.ld_mask = (mask.data_ptr(), mask.stride(0)) if mask is not None else (None, 0)
+    _check("qmm_tree_attention", load().qmm_tree_attention(h, ctypes.byref(a), _stream_ptr(stream)))
+
+
+def qmm_cache_commit(h, page_table, lens, path, accept, lens_out, stream=None) -> None:
+    """Compacts the accepted branches (path int32 [B, T], accept int32 [B, 2]); asynchronous."""
+    B, T = path.shape
+    _check("qmm_cache_commit", load().qmm_cache_commit(
+        h, B, T, page_table.data_ptr(), page_table.stride(0), page_table.shape[1], lens.data_ptr(), path.data_ptr(),
+        path.stride(0), accept.data_ptr(), lens_out.data_ptr(), _stream_ptr(stream)))
+
+
+def qmm_cache_copy(h, src, dst, rows=None, stream=None) -> None:
+    """Copies pages src[i] to dst[i] (int32), their first rows[i] rows; asynchronous."""
+    _check("qmm_cache_copy", load().qmm_cache_copy(
+        h, src.numel(), src.data_ptr(), dst.data_ptr(), rows.data_ptr() if rows is not None else None,
+        _stream_ptr(stream)))
+
+
+def qmm_verify_sample_workspace(B: int, T: int, V: int) -> int:
+    """Bytes of device workspace qmm_verify_sample needs for those sizes."""
+    n = ctypes.c_int64(0)
+    _check("qmm_verify_sample_workspace", load().qmm_verify_sample_workspace(B, T, V, ctypes.byref(n)))
+    return n.value
+
+
+def qmm_verify_sample(target, draft, tokens, u, noise, accept, path, workspace, parents=None, temperature=None,
+                      n_tokens=None, stream=None) -> None:
+    """target [B, T, V] and draft [B, T or T - 1, V] (or None) fp32, bf16 or f16;
+    the other arguments as in qmm_sample_args; asynchronous."""
+    B, T, V = target.shape
+    a = qmm_sample_args()
+    a.struct_size = ctypes.sizeof(qmm_sample_args)
+    a.dtype, a.B, a.T, a.V = _dtype(target.dtype), B, T, V
+    a.target, a.target_stride[:] = target.data_ptr(), target.stride()[:2]
+    if draft is not None:
+        a.draft, a.draft_stride[:] = draft.data_ptr(), draft.stride()[:2]
+    opt = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    a.tokens, a.parents, a.n_tokens, a.temperature = tokens.data_ptr(), opt(parents), opt(n_tokens), opt(temperature)
+    a.u, a.noise, a.accept, a.path = u.data_ptr(), noise.data_ptr(), accept.data_ptr(), path.data_ptr()
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check("qmm_verify_sample", load().qmm_verify_sample(ctypes.byref(a), _stream_ptr(stream)))
+
+
+# ------------------------------------------------------------------ convenience
+def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=None, n_tokens=None, stream=None):
+    """(accept, path) of a drafted tree under rejection sampling; see
+    qmm_verify_sample.  accept[:, 0] nodes are accepted, path[b, :accept[b, 0]]
+    names them, accept[:, 1] is the token that follows them."""
+    import torch
+    if target.dim() != 3 or not target.is_cuda:
+        raise ValueError("target must be a CUDA tensor [B, T, V]")
+    B, T, V = target.shape
+    _dtype(target.dtype)
+    _rows("target", target)
+    if draft is not None:
+        _cuda("draft", draft, target.dtype, (B, None, V))
+        if draft.shape[1] not in (T, T - 1):
+            raise ValueError(f"draft must hold {T} or {T - 1} rows a sequence, not {draft.shape[1]}")
+        _rows("draft", draft)
+        if draft.shape[1] == 0:
+            draft = None
+    for name, t, dt, shape in (("tokens", tokens, torch.int32, (B, T)), ("u", u, torch.float32, (B, T)),
+                               ("noise", noise, torch.float32, (B, V)), ("parents", parents, torch.int32, (B, T)),
+                               ("temperature", temperature, torch.float32, (B,)),
+                               ("n_tokens", n_tokens, torch.int32, (B,))):
+        if t is not None:
+            _cuda(name, t, dt, shape)
+            _flat(name, t)
+    accept = torch.empty((B, 2), dtype=torch.int32, device=target.device)
+    path = torch.empty((B, T), dtype=torch.int32, device=target.device)
+    ws = torch.empty(qmm_verify_sample_workspace(B, T, V), dtype=torch.uint8, device=target.device)
+    qmm_verify_sample(target, draft, tokens, u, noise, accept, path, ws, parents, temperature, n_tokens, stream)
+    if stream is not None:
+        ws.record_stream(stream)
+    return accept, path
+
+
+def tree_mask(parents):
+    """int64 [B, T] visibility words of drafted trees from parents [B, T] (CPU
+    values; a node sees itself and its ancestors; roots have parent -1)."""
+    import torch
+    words = []
+    for row in parents.tolist():
+        seen = []
+        for i, par in enumerate(row):
+            if par >= i:
+                raise ValueError(f"parent {par} of node {i} does not come before it")
+            seen.append((seen[par] if par >= 0 else 0) | 1 << i)
+        words.append([w - (1 << 64) if w >> 63 else w for w in seen])
+    return torch.tensor(words, dtype=torch.int64)
+
+
+class Sequence:
+    """One sequence's pages, in order, and its number of cached rows."""
+
+    def __init__(self):
+        self.pages: list[int] = []
+        self.length = 0
+
+
+class PagedCache:
+    """Key and value pools [n_layers, n_pages, n_kv_heads, page_size, head_dim], a
+    handle for the kernels, and the host's page bookkeeping."""
+
+    def __init__(self, n_layers: int, n_pages: int, page_size: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                 dtype=None, max_batch: int = 64, k_pool=None, v_pool=None, device="cuda", stream=None):
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        shape = (n_layers, n_pages, n_kv_heads, page_size, head_dim)
+        pools = []
+        for name, pool in (("k_pool", k_pool), ("v_pool", v_pool)):
+            if pool is None:
+                pool = torch.zeros(shape, dtype=dtype, device=device)
+            _cuda(name, pool, dtype, shape)
+            _flat(name, pool)
+            pools.append(pool)
+        self.k_pool, self.v_pool = pools
+        self.n_layers, self.n_pages, self.page_size = n_layers, n_pages, page_size
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
+        self.handle = None
+        self.handle = qmm_cache_create(_dtype(dtype), n_layers, n_pages, page_size, n_q_heads, n_kv_heads, head_dim,
+                                       max_batch, self.k_pool, self.v_pool, stream)
+        self._users = [0] * n_pages
+        self._free = list(range(n_pages - 1, -1, -1))
+
+    # -------------------------------------------------------------- operators
+    def attend(self, layer: int, q, k, v, page_table, lens, mask=None, n_tokens=None, scale=None, out=None,
+               lse=None, stream=None):
+        """(out, lse): the nodes' attention over cache and tree; their keys and
+        values are written behind the cached rows.  See qmm_tree_attention."""
+        import torch
+        if q.dim() != 4:
+            raise ValueError("q must be [B, T, n_q_heads, head_dim]")
+        B, T = q.shape[:2]
+        new = (B, T, self.n_kv_heads, self.head_dim)
+        if out is None:
+            out = torch.empty((B, T, self.n_q_heads, self.head_dim), dtype=self.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, T, self.n_q_heads), dtype=torch.float32, device=q.device)
+        for name, t, shape in (("q", q, (B, T, self.n_q_heads, self.head_dim)), ("k", k, new), ("v", v, new),
+                               ("out", out, (B, T, self.n_q_heads, self.head_dim))):
+            _cuda(name, t, self.dtype, shape)
+            _rows(name, t)
+        _cuda("lse", lse, torch.float32, (B, T, self.n_q_heads))
+        _flat("lse", lse)
+        self._table(page_table, lens, B)
+        if mask is not None:
+            _cuda("mask", mask, torch.int64, (B, T))
+            _rows("mask", mask)
+        if n_tokens is not None:
+            _cuda("n_tokens", n_tokens, torch.int32, (B,))
+            _flat("n_tokens", n_tokens)
+        qmm_tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale, stream)
+        return out, lse
+
+    def commit(self, page_table, lens, path, accept, lens_out=None, stream=None):
+        """The new lengths: the accepted branches' rows move behind the cached ones
+        in every layer.  See qmm_cache_commit."""
+        import torch
+        B = lens.shape[0]
+        if lens_out is None:
+            lens_out = torch.empty_like(lens)
+        self._table(page_table, lens, B)
+        _cuda("path", path, torch.int32, (B, None))
+        _rows("path", path)
+        _cuda("accept", accept, torch.int32, (B, 2))
+        _flat("accept", accept)
+        _cuda("lens_out", lens_out, torch.int32, (B,))
+        _flat("lens_out", lens_out)
+        qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out, stream)
+        return lens_out
+
+    def copy_pages(self, src, dst, rows=None, stream=None):
+        """Copies the first rows[i] rows (None: all) of page src[i] to page dst[i]
+        in every layer.  See qmm_cache_copy."""
+        import torch
+        n = src.shape[0]
+        for name, t in (("src", src), ("dst", dst), ("rows", rows)):
+            if t is not None:
+                _cuda(name, t, torch.int32, (n,))
+                _flat(name, t)
+        qmm_cache_copy(self.handle, src, dst, rows, stream)
+
+    def sync_status(self, stream=None) -> int:
+        return qmm_cache_sync_status(self.handle, stream)
+
+    def _table(self, page_table, lens, B):
+        import torch
+        _cuda("page_table", page_table, torch.int32, (B, None))
+        _rows("page_table", page_table)
+        _cuda("lens", lens, torch.int32, (B,))
+        _flat("lens", lens)
+
+    # -------------------------------------------------------------- bookkeeping
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def new_sequence(self) -> Sequence:
+        return Sequence()
+
+    def _take(self, n):
+        if n > len(self._free):
+            raise MemoryError(f"{n} pages wanted, {len(self._free)} free")
+        pages = [self._free.pop() for _ in range(n)]
+        for p in pages:
+            self._users[p] = 1
+        return pages
+
+    def reserve(self, seqs, rows: int) -> None:
+        """Pages of their own for `rows` more rows of every sequence: fresh ones
+        where more are needed, and a copy of a partly filled last page that
+        others share.  Nothing is taken when there are too few."""
+        need, shared, left = [], [], list(self._users)
+        for s in seqs:
+            tail = s.length // self.page_size
+            shared.append([])
+            for i in range(tail, len(s.pages)):
+                if left[s.pages[i]] > 1:
+                    left[s.pages[i]] -= 1
+                    shared[-1].append(i)
+            need.append(max(0, -(-(s.length + rows) // self.page_size) - len(s.pages)))
+        total = sum(need) + sum(map(len, shared))
+        if total > len(self._free):
+            raise MemoryError(f"{total} pages wanted, {len(self._free)} free")
+        copies = []
+        for s, n, at in zip(seqs, need, shared):
+            for i in at:
+                (fresh,) = self._take(1)
+                used = min(max(s.length - i * self.page_size, 0), self.page_size)
+                if used:
+                    copies.append((s.pages[i], fresh, used))
+                self._users[s.pages[i]] -= 1
+                s.pages[i] = fresh
+            s.pages += self._take(n)
+        self._copy(copies)
+
+    def _copy(self, copies, stream=None):
+        import torch
+        if copies:
+            t = torch.tensor(copies, dtype=torch.int32).t().contiguous().to(self.k_pool.device)
+            self.copy_pages(t[0], t[1], t[2], stream)
+
+    def advance(self, seqs, counts) -> None:
+        """The host's record of `counts` committed rows a sequence."""
+        for s, n in zip(seqs, counts):
+            if s.length + int(n) > len(s.pages) * self.page_size:
+                raise ValueError("more rows than the sequence has pages for")
+            s.length += int(n)
+
+    def fork(self, seq: Sequence) -> Sequence:
+        """A second sequence with the same cached rows: pages are shared until
+        reserve() gives one of them rows of its own."""
+        other = Sequence()
+        other.length = seq.length
+        other.pages = seq.pages[:-(-seq.length // self.page_size)]
+        for p in other.pages:
+            self._users[p] += 1
+        return other
+
+    def free(self, seq: Sequence) -> None:
+        """Return the sequence's pages; those that others share stay."""
+        for p in seq.pages:
+            self._users[p] -= 1
+            if self._users[p] == 0:
+                self._free.append(p)
+        seq.pages, seq.length = [], 0
+
+    def tables(self, seqs):
+        """(page_table, lens) CUDA tensors for a call over `seqs`."""
+        import torch
+        width = max(1, max(len(s.pages) for s in seqs))
+        rows = [s.pages + [0] * (width - len(s.pages)) for s in seqs]
+        dev = self.k_pool.device
+        return (torch.tensor(rows, dtype=torch.int32).to(dev),
+                torch.tensor([s.length for s in seqs], dtype=torch.int32).to(dev))
+
+    def close(self):
+        if self.handle:
+            qmm_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
