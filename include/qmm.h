@@ -553,6 +553,9 @@ int qmm_quantize_fp8(const float* w, int64_t N, int64_t K, uint32_t flags, uint8
  * still drain their own copies in flight before returning. */
 int qmm_debug_set_wait_limit(qmm_t h, int64_t ns);
 
+/* The same for the attention kernels of a cache handle. */
+int qmm_debug_set_cache_wait_limit(qmm_cache_t h, int64_t ns);
+
 /* Test hook: make the n-th device allocation made by qmm_create from now on
  * fail as if cudaMalloc had failed (n = 0 disables; the hook fires once). */
 int qmm_debug_fail_allocs(int n);

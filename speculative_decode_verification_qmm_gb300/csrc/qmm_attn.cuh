@@ -238,4 +238,91 @@ __device__ __forceinline__ uint64_t attn_bits(const AttnParams& p, int b, int n,
   return m & live;
 }
 
+// Two packed fp32 operations at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+// One thread's four columns of row r (of ROWS) of an item's output.
+template <bool BF16>
+__device__ __forceinline__ void attn_store4(const AttnParams& p, const AttnCursor& cur, int ro, int c4, float4 a,
+                                            float m, float l) {
+  const int t = ro / p.g, i = ro - t * p.g;
+  const bool live = t < cur.n;
+  uint2 v = make_uint2(0u, 0u);
+  if (live && l != 0.f) {
+    const float iv = 1.f / l;
+    v = make_uint2(pack16<BF16>(a.x * iv, a.y * iv), pack16<BF16>(a.z * iv, a.w * iv));
+  }
+  *reinterpret_cast<uint2*>(p.out + cur.b * p.o_sb + t * p.o_st + (int64_t)(cur.h * p.g + i) * p.o_sh + c4) = v;
+  if (p.lse && c4 == 0)
+    p.lse[((int64_t)cur.b * p.T + t) * p.Hq + cur.h * p.g + i] =
+        live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Join the partials that CTAs c0 .. c1 left of an item, in their order, and
+// write its outputs; called by the WARPS warps of the item's last CTA.  D / 4
+// lanes share a row, and first take one part's statistics each; RU rows are in
+// flight at a time, because the loads' latency is all that there is to it.
+template <bool BF16, int D, int ROWS, int WARPS>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnCursor& cur, int c0, int c1, int warp,
+                                          int lane) {
+  constexpr int PART = ROWS * (D + 2);
+  constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+  constexpr int RU = 4;
+  const int sub = lane % LPR, c4 = sub * 4;
+  int rows = p.R - cur.rt * ROWS;
+  rows = rows < ROWS ? rows : ROWS;
+  for (int r0 = warp * RPW * RU; r0 < rows; r0 += WARPS * RPW * RU) {
+    float4 acc[RU];
+    float mn[RU], lt[RU];
+#pragma unroll
+    for (int k = 0; k < RU; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), mn[k] = -INFINITY, lt[k] = 0.f;
+    for (int cb = c0; cb <= c1; cb += LPR) {
+      const int mine = cb + sub;
+      float m[RU], l[RU], w[RU];
+#pragma unroll
+      for (int k = 0; k < RU; ++k) {
+        const int r = r0 + k * RPW + lane / LPR;
+        m[k] = -INFINITY, l[k] = 0.f;
+        if (mine <= c1) {
+          const float* pp = p.ws + ((int64_t)mine * 2 + (mine == c0)) * PART + ROWS * D + r;
+          m[k] = __ldcg(pp);
+          l[k] = __ldcg(pp + ROWS);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < RU; ++k) {
+        float x = m[k];
+#pragma unroll
+        for (int d = LPR / 2; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+        x = fmaxf(x, mn[k]);
+        const float old = attn_weight(mn[k], lt[k], x);
+        w[k] = attn_weight(m[k], l[k], x);
+        float sum = w[k] * l[k];
+#pragma unroll
+        for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        lt[k] = lt[k] * old + sum;
+        acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
+        mn[k] = x;
+      }
+      const int n = c1 - cb + 1 < LPR ? c1 - cb + 1 : LPR;
+#pragma unroll 2
+      for (int i = 0; i < n; ++i) {
+        const int c = cb + i;
+        const float* pp = p.ws + ((int64_t)c * 2 + (c == c0)) * PART + c4;
+#pragma unroll
+        for (int k = 0; k < RU; ++k) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + (r0 + k * RPW + lane / LPR) * D));
+          const float x = __shfl_sync(0xFFFFFFFFu, w[k], i, LPR);
+          acc[k].x += x * v.x, acc[k].y += x * v.y, acc[k].z += x * v.z, acc[k].w += x * v.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < RU; ++k) {
+      const int r = r0 + k * RPW + lane / LPR;
+      if (r < rows) attn_store4<BF16>(p, cur, cur.rt * ROWS + r, c4, acc[k], mn[k], lt[k]);
+    }
+  }
+}
+
 }  // namespace qmm

@@ -23,4 +23,10 @@ int attn_mma_tile_rows(int R);
 cudaError_t prepare_attn_mma(bool bf16, int D);
 cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, int ctas, cudaStream_t st);
 
+
+// tcgen05 kernel (more rows than the mma.sync kernel's tile holds), one CTA per SM.
+int attn_tc_tile_rows(int R);
+cudaError_t prepare_attn_tc(bool bf16, int D);
+cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, int ctas, cudaStream_t st);
+
 }  // namespace qmm

@@ -432,39 +432,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) attn_mma_kernel(const __grid_co
         __syncthreads();
         if (s_flag[0]) {
           __threadfence();
-          for (int id = tid; id < ROWS * D / 4; id += WARPS * 32) {
-            const int r = id / (D / 4), c4 = (id % (D / 4)) * 4;
-            float mn = -INFINITY, lt = 0.f;
-            for (int c = c0; c <= c1; ++c)
-              mn = fmaxf(mn, __ldcg(p.ws + ((int64_t)c * 2 + (c == c0)) * PART + ROWS * D + r));
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = c0; c <= c1; ++c) {
-              const float* pp = p.ws + ((int64_t)c * 2 + (c == c0)) * PART;
-              const float lc = __ldcg(pp + ROWS * D + ROWS + r);
-              const float wgt = attn_weight(__ldcg(pp + ROWS * D + r), lc, mn);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + r * D + c4));
-              lt += wgt * lc;
-              a.x += wgt * v.x;
-              a.y += wgt * v.y;
-              a.z += wgt * v.z;
-              a.w += wgt * v.w;
-            }
-            const int ro = cur.rt * ROWS + r;
-            if (ro < p.R) {
-              const int t = ro / p.g, i = ro - t * p.g;
-              const bool live = t < cur.n;
-              uint2 v = make_uint2(0u, 0u);
-              if (live && lt != 0.f) {
-                const float iv = 1.f / lt;
-                v = make_uint2(pack16<BF16>(a.x * iv, a.y * iv), pack16<BF16>(a.z * iv, a.w * iv));
-              }
-              *reinterpret_cast<uint2*>(p.out + cur.b * p.o_sb + t * p.o_st + (int64_t)(cur.h * p.g + i) * p.o_sh +
-                                        c4) = v;
-              if (p.lse && c4 == 0)
-                p.lse[((int64_t)cur.b * p.T + t) * p.Hq + cur.h * p.g + i] =
-                    live ? (mn + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-            }
-          }
+          attn_join<BF16, D, ROWS, WARPS>(p, cur, c0, c1, warp, lane);
         }
       }
       __syncthreads();

@@ -223,10 +223,14 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   while ((1 << h->page_shift) < d->page_size) ++h->page_shift;
   cudaStream_t st = (cudaStream_t)stream;
   const int ctas = sms * ATTN_MMA_CTAS_PER_SM;
-  const size_t part = (size_t)attn_mma_tile_rows(1 << 30) * (d->head_dim + 2) * sizeof(float);
+  // two partials of a CTA's largest row tile each
+  const size_t rows_mma = (size_t)ctas * attn_mma_tile_rows(INT32_MAX);
+  const size_t rows_tc = (size_t)sms * attn_tc_tile_rows(INT32_MAX);
+  const size_t ws_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
+  if (e == cudaSuccess) e = prepare_attn_tc(d->dtype == QMM_DT_BF16, d->head_dim);
   void* ptr = nullptr;
-  if (e == cudaSuccess && (e = host_dev_alloc(&ptr, (size_t)ctas * 2 * part)) == cudaSuccess)
+  if (e == cudaSuccess && (e = host_dev_alloc(&ptr, ws_bytes)) == cudaSuccess)
     h->ws = static_cast<float*>(ptr);
   if (e == cudaSuccess && (e = host_dev_alloc(&ptr, (size_t)ctas * sizeof(int))) == cudaSuccess)
     h->counters = static_cast<int*>(ptr);
@@ -269,7 +273,10 @@ int qmm_cache_sync_status(qmm_cache_t h, void* stream) {
   if (e == cudaSuccess) e = cudaMemcpyAsync(&word, h->status, sizeof(int), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && word != 0) {
+    // a kernel that gave up may have left tickets behind
     e = cudaMemsetAsync(h->status, 0, sizeof(int), st);
+    if (e == cudaSuccess && (word & ~DEV_ERR_INDEX))
+      e = cudaMemsetAsync(h->counters, 0, (size_t)h->sm_count * ATTN_MMA_CTAS_PER_SM * sizeof(int), st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   }
   if (e != cudaSuccess) return host_cuda_fail(e);
@@ -332,10 +339,12 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
   const bool bf16 = d.dtype == QMM_DT_BF16;
-  const int rows = attn_mma_tile_rows(p.R);
+  const bool tc = p.R > attn_mma_tile_rows(p.R);
+  const int rows = tc ? attn_tc_tile_rows(p.R) : attn_mma_tile_rows(p.R);
   p.RT = (p.R + rows - 1) / rows;
   const cudaError_t e =
-      launch_attn_mma(p, bf16, d.head_dim, h->sm_count * ATTN_MMA_CTAS_PER_SM, (cudaStream_t)stream);
+      tc ? launch_attn_tc(p, bf16, d.head_dim, h->sm_count, (cudaStream_t)stream)
+         : launch_attn_mma(p, bf16, d.head_dim, h->sm_count * ATTN_MMA_CTAS_PER_SM, (cudaStream_t)stream);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }
 
@@ -405,6 +414,13 @@ int qmm_cache_copy(qmm_cache_t h, int n, const int32_t* src, const int32_t* dst,
   copy_kernel<<<dim3((unsigned)n, (unsigned)(2 * h->d.n_layers)), COPY_THREADS, 0, (cudaStream_t)stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
+}
+
+int qmm_debug_set_cache_wait_limit(qmm_cache_t h, int64_t ns) {
+  if (!is_live(h)) return QMM_ERR_STATE;
+  if (ns < 0) return QMM_ERR_INVALID_ARG;
+  h->wait_limit_ns = (uint64_t)ns;
+  return QMM_OK;
 }
 
 }  // extern "C"

@@ -118,6 +118,10 @@ def qmm_cache_copy(h, src, dst, rows=None, stream=None) -> None:
         _stream_ptr(stream)))
 
 
+def qmm_debug_set_cache_wait_limit(h, ns: int) -> None:
+    _check("qmm_debug_set_cache_wait_limit", load().qmm_debug_set_cache_wait_limit(h, ns))
+
+
 def qmm_verify_sample_workspace(B: int, T: int, V: int) -> int:
     """Bytes of device workspace qmm_verify_sample needs for those sizes."""
     n = ctypes.c_int64(0)
