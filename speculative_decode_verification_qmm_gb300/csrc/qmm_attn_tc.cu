@@ -59,22 +59,33 @@ struct Smem {
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
-// D[tmem] (+)= A[smem] * B[smem], kind::f16, fp32 accumulate.
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_t, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// Shared-memory operands, 128-byte swizzle, as the two words of a matrix
+// descriptor: the upper word is the same for all (8-row groups 1024 bytes apart,
+// version 1, layout type 2), the lower one holds the start address / 16 and, for
+// an operand whose rows along K are 128 bytes of 64 consecutive M or N values,
+// the distance of the next 64 values / 16.  A step along K adds a constant to
+// it, which keeps the issuing thread short: with descriptors built anew for each
+// MMA it took 180 cycles to issue one that the tensor cores run in 64.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mn(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
+
+// D[tmem] (+)= A * B, kind::f16, fp32 accumulate; A in shared or tensor memory, B in shared.
+__device__ __forceinline__ void mma_ss(uint32_t d_t, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_t),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_t),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
       : "memory");
 }
-
-// Matrix descriptor of an operand whose rows along K are 128 bytes of 64
-// consecutive M or N values (128-byte swizzle): 8-row groups along K 1024 bytes
-// apart, blocks of 64 values along M or N `lead` bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ void mma_ts(uint32_t d_t, uint32_t a_t, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_t),
+      "r"(a_t), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(DESC_HI)
+      : "memory");
 }
 
 template <int N>
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
       if (!got && lane == 0) fail(DEV_ERR_TIMEOUT_EMPTY);
       return got;
     };
-    int64_t load = 0;  // tiles of K and V requested
+    int slot = 0, round = 0;  // of the next tile of K or V
     // The page ids of the warp's blocks of a cache tile.
     auto pages = [&](const AttnCursor& c, int j, int (&ids)[MINE]) {
 #pragma unroll
@@ -245,10 +256,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
       }
     };
     auto tile = [&](const AttnCursor& c, int j, int kind, int seg, const int (&ids)[MINE]) {
-      const int slot = (int)(load % SLOTS);
-      if (ok && load >= SLOTS) ok = wait(b_empty + 8 * slot, (uint32_t)((load / SLOTS - 1) & 1));
+      if (ok && round > 0) ok = wait(b_empty + 8 * slot, (uint32_t)((round - 1) & 1));
       if (!ok) return;
-      ++load;
       const uint32_t dst = base + S::RING + slot * S::TILE;
       const int j0 = j * TK;
       const uint16_t* pool = (kind == 1 ? p.k_pool : p.v_pool) + c.h * head;
@@ -292,6 +301,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
       } else {
         push(b_full + 8 * slot);
       }
+      if (++slot == SLOTS) slot = 0, ++round;
     };
 
     int seg = 0;
@@ -334,35 +344,39 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
       bool ok = s_flag[0] == 0;
-      auto need = [&](uint32_t bar, int64_t phase) {
+      auto need = [&](uint32_t bar, int phase) {
         if (ok && !wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag)) {
           fail(DEV_ERR_TIMEOUT_FULL);
           ok = false;
         }
         return ok;
       };
-      int64_t load = 0;  // tiles consumed
-      int64_t done = 0;  // cache tiles whose Q K^T was issued before this segment
-      auto qk = [&](int q, int buf, uint32_t kt) {
-        const uint32_t qt = base + S::Q + q * S::TILE;
+      int slot = 0, round = 0;  // of the next tile of K or V
+      auto next = [&]() {
+        if (++slot == SLOTS) slot = 0, ++round;
+      };
+      int done = 0;  // cache tiles whose Q K^T was issued before this segment (parities only)
+      auto qk = [&](int q, int buf, int sl) {
+        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::RING + sl * S::TILE);
         const uint32_t d = tmem + q * COL_Q + buf * TK;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (uint32_t)(kk >> 2) * S::HALF + (uint32_t)(kk & 3) * 32u;
-          tc_mma_ss(d, smem_desc_sw128(qt + o), smem_desc_sw128(kt + o), IDESC_S, kk > 0);
+          constexpr uint32_t STEP = 32 >> 4, HALF = S::HALF >> 4;
+          const uint32_t o = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * STEP;
+          mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
         }
         tc_commit(b_sfull + 8 * (NQ == 1 ? buf : q));
       };
-      auto pv = [&](int q, int buf, uint32_t vt, bool first) {
+      auto pv = [&](int q, int buf, int sl, bool first) {
         const uint32_t a = tmem + q * COL_Q + buf * TK, d = tmem + q * COL_Q + COL_O;
+        const uint32_t b = desc_lo_mn(base + S::RING + sl * S::TILE, S::HALF);
         tc_fence_after();
+        mma_ts(d, a, b, IDESC_O, !first);
 #pragma unroll
-        for (int kk = 0; kk < TK / 16; ++kk)
-          tc_mma(d, a + kk * 8, smem_desc_mn_sw128(vt + kk * 2048u, S::HALF), IDESC_O, kk > 0 || !first);
+        for (int kk = 1; kk < TK / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
         tc_commit(b_odone + 8 * q);
       };
-      auto slot_of = [&](int64_t i) { return base + S::RING + (uint32_t)(i % SLOTS) * S::TILE; };
       int seg = 0;
       for (int64_t u = u0; u < u1 && ok; ++seg) {
         int64_t left = cur.ntiles - cur.tile;
@@ -372,60 +386,59 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
         if constexpr (NQ == 1) {
           for (int j = 0; j <= count && ok; ++j) {
             if (j < count) {
-              const int64_t n = done + j;
-              if (!need(b_full + 8 * (load % SLOTS), load / SLOTS)) break;
+              const int n = done + j;
+              if (!need(b_full + 8 * slot, round)) break;
               // its S holds P of two tiles ago until that product is done (at a
               // segment's start the product of the last tile is the newest one)
               if (j == 0 ? n >= 1 && !need(b_odone, n - 1) : n >= 2 && !need(b_odone, n - 2)) break;
-              qk(0, (int)(n & 1), slot_of(load));
-              tc_commit(b_empty + 8 * (load % SLOTS));
+              qk(0, n & 1, slot);
+              tc_commit(b_empty + 8 * slot);
               if (j == count - 1) tc_commit(b_qempty);
-              ++load;
+              next();
             }
             if (j > 0) {
-              const int64_t n = done + j - 1;
-              if (!need(b_full + 8 * (load % SLOTS), load / SLOTS)) break;
+              const int n = done + j - 1;
+              if (!need(b_full + 8 * slot, round)) break;
               if (!need(b_pfull + 8 * (n & 1), n >> 1)) break;
               if (j == 1 && seg > 0 && !need(b_oempty, seg - 1)) break;
-              pv(0, (int)(n & 1), slot_of(load), j == 1);
-              tc_commit(b_empty + 8 * (load % SLOTS));
-              ++load;
+              pv(0, n & 1, slot, j == 1);
+              tc_commit(b_empty + 8 * slot);
+              next();
             }
           }
         } else {
+          if (!need(b_full + 8 * slot, round)) break;
+          for (int q = 0; q < 2 && ok; ++q)
+            if (done == 0 || need(b_odone + 8 * q, done - 1)) qk(q, 0, slot);
+          if (!ok) break;
+          tc_commit(b_empty + 8 * slot);
+          if (count == 1) tc_commit(b_qempty);
+          next();
           for (int j = 0; j < count && ok; ++j) {
-            const int64_t n = done + j;
-            if (j == 0) {
-              if (!need(b_full + 8 * (load % SLOTS), load / SLOTS)) break;
-              for (int q = 0; q < 2 && ok; ++q) {
-                if (n > 0 && !need(b_odone + 8 * q, n - 1)) break;
-                qk(q, 0, slot_of(load));
-              }
-              if (!ok) break;
-              tc_commit(b_empty + 8 * (load % SLOTS));
-              if (count == 1) tc_commit(b_qempty);
-            }
-            const int64_t lv = load + 1, lk = load + 2;
-            if (!need(b_full + 8 * (lv % SLOTS), lv / SLOTS)) break;
+            const int n = done + j;
             const bool more = j + 1 < count;
-            for (int q = 0; q < 2 && ok; ++q) {
+            if (!need(b_full + 8 * slot, round)) break;
+            const int vslot = slot;
+            next();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
               if (!need(b_pfull + 8 * q, n)) break;
               if (j == 0 && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) break;
-              pv(q, 0, slot_of(lv), j == 0);
-              if (q == 1) tc_commit(b_empty + 8 * (lv % SLOTS));
+              pv(q, 0, vslot, j == 0);
+              if (q == 1) tc_commit(b_empty + 8 * vslot);
               if (more) {
-                if (q == 0 && !need(b_full + 8 * (lk % SLOTS), lk / SLOTS)) break;
+                if (q == 0 && !need(b_full + 8 * slot, round)) break;
                 // P lies in S: the next S may follow when its product is done
                 if (!need(b_odone + 8 * q, n)) break;
-                qk(q, 0, slot_of(lk));
+                qk(q, 0, slot);
               }
             }
             if (!ok) break;
             if (more) {
-              tc_commit(b_empty + 8 * (lk % SLOTS));
+              tc_commit(b_empty + 8 * slot);
               if (j + 2 == count) tc_commit(b_qempty);
+              next();
             }
-            load += 2;
           }
         }
         done += count;
@@ -545,6 +558,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
+        // Every product is waited for in turn, before the one that follows it can
+        // start: a parity tells one phase of a barrier from the next, no more.
+        if (n > 0 && !need(b_odone + 8 * q, n - 1)) continue;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull + 8 * (NQ == 1 ? buf : q));
