@@ -329,7 +329,8 @@ typedef struct {
   int32_t n_kv_heads;
   int32_t head_dim;     /* 64 or 128                                            */
   int32_t max_batch;    /* sequences of one call, 1 to QMM_CACHE_MAX_BATCH      */
-  int64_t n_pages;      /* pages of one layer, 1 to 2^31 - 1                    */
+  int64_t n_pages;      /* pages of one layer; a pool has at most 2^31 - 1 rows
+                           (n_layers * n_pages * n_kv_heads * page_size)        */
   void* k_pool;         /* device, 16-byte aligned; must outlive the handle     */
   void* v_pool;         /* device, 16-byte aligned; must outlive the handle     */
 } qmm_cache_desc;
@@ -393,9 +394,9 @@ typedef struct {
  * L + n - 1 is read.
  * Scores, softmax statistics and sums are fp32; the exponentials are rounded
  * to the 16-bit type for the product with V, as the outputs are at the end.
- * All pointers to 16-bit data are 16-byte aligned.  Asynchronous on `stream`,
- * one kernel, results independent of what runs beside it (no atomics on
- * values).
+ * All pointers to 16-bit data are 16-byte aligned.  Asynchronous on `stream`
+ * (the attention kernel, and one that adds up the parts of rows that it cut
+ * between CTAs, in a fixed order: equal calls give equal bits).
  * Errors: STATE, INVALID_ARG (NULL pointers, bad struct_size or scale), SHAPE
  * (layer, B, T or table_width out of range), ALIGN (pointers, strides,
  * ld_table < table_width, ld_mask < T), DEVICE, CUDA.  Lengths and page ids

@@ -364,6 +364,9 @@ namespace qmm {
 cudaError_t host_dev_alloc(void** p, size_t bytes) { return dev_alloc(p, bytes); }
 int host_check_device(int* dev, int* sms) { return check_device(dev, sms); }
 int host_cuda_fail(cudaError_t e) { return cuda_fail(nullptr, e); }
+cudaError_t host_pool_map(void* map, const void* base, int64_t rows, int D, int box_rows, bool f16) {
+  return encode_act_map_2d(static_cast<CUtensorMap*>(map), base, D, (int)rows, D, f16, box_rows, 64);
+}
 
 }  // namespace qmm
 

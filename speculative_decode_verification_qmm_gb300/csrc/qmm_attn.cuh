@@ -9,9 +9,8 @@
 // ragged batches and single long sequences load the SMs alike and no plan is
 // needed from the host, which does not know the lengths.  A CTA's part of an
 // item is a segment.  An item that is one segment is written out directly; the
-// others leave (O, m, l) partials in the workspace, and the last CTA to finish
-// one (a ticket per item) joins them in CTA order, so the result does not
-// depend on which that was.
+// others leave (O, m, l) partials in the workspace, at most two of a CTA, which
+// a second kernel (qmm_attn_join.cu) adds up in CTA order.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -50,7 +49,8 @@ struct AttnParams {
   int RT;   // row tiles
   float scale_log2;  // scale * log2(e): the softmax runs in powers of two
   float* ws;         // partials: [CTA][2][rows of a tile * (D + 2)]
-  int* counters;     // [CTA] tickets, zero between calls
+  int grid;          // CTAs of the launch
+  int64_t row0;      // first row of the layer in the pools' tensor maps
   int* status;
   uint64_t wait_limit_ns;
 };
@@ -140,11 +140,26 @@ __device__ __forceinline__ int attn_tiles(int L, int n) {
   return t < 1 ? 1 : t;  // an item without rows still writes its outputs
 }
 
-// The cursor at the first unit of CTA c's range, for every lane of a warp
-// (all lanes call it), and the range [u0, u1) of `W` units over `G` CTAs.
+// Cache tiles of the sequences before b, and of all, in every lane of a warp.
+__device__ __forceinline__ void attn_count(const AttnParams& p, int tk, int lane, int b, int64_t& before, int64_t& all) {
+  before = all = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int nt = 0;
+    if (b0 + lane < p.B) {
+      int L, n;
+      attn_sizes(p, b0 + lane, L, n);
+      nt = (L + n + tk - 1) / tk;
+      nt = nt < 1 ? 1 : nt;
+    }
+    all += __reduce_add_sync(0xFFFFFFFFu, nt);
+    before += __reduce_add_sync(0xFFFFFFFFu, b0 + lane < b ? nt : 0);
+  }
+}
+
+// The cursor at the first unit of CTA c's range [u0, u1), for every lane of a
+// warp (all lanes call it).
 template <int TK>
-__device__ __forceinline__ AttnCursor attn_begin(const AttnParams& p, int lane, int c, int grid,
-                                                 int64_t& W, int& G, int64_t& u0, int64_t& u1) {
+__device__ __forceinline__ AttnCursor attn_begin(const AttnParams& p, int lane, int c, int64_t& u0, int64_t& u1) {
   const int64_t hr = (int64_t)p.Hkv * p.RT;
   int64_t sum = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -154,13 +169,10 @@ __device__ __forceinline__ AttnCursor attn_begin(const AttnParams& p, int lane, 
       if (!attn_sizes(p, b0 + lane, L, n) && c == 0) atomicOr(p.status, DEV_ERR_INDEX);
       nt = attn_tiles<TK>(L, n);
     }
-    int s = nt;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    sum += s;
+    sum += __reduce_add_sync(0xFFFFFFFFu, nt);
   }
-  W = sum * hr;
-  G = W < grid ? (int)W : grid;
+  const int64_t W = sum * hr;
+  const int G = W < p.grid ? (int)W : p.grid;
   AttnCursor cur{};
   if (c >= G) {
     u0 = u1 = 0;
@@ -256,73 +268,6 @@ __device__ __forceinline__ void attn_store4(const AttnParams& p, const AttnCurso
   if (p.lse && c4 == 0)
     p.lse[((int64_t)cur.b * p.T + t) * p.Hq + cur.h * p.g + i] =
         live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
-// Join the partials that CTAs c0 .. c1 left of an item, in their order, and
-// write its outputs; called by the WARPS warps of the item's last CTA.  D / 4
-// lanes share a row, and first take one part's statistics each; RU rows are in
-// flight at a time, because the loads' latency is all that there is to it.
-template <bool BF16, int D, int ROWS, int WARPS>
-__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnCursor& cur, int c0, int c1, int warp,
-                                          int lane) {
-  constexpr int PART = ROWS * (D + 2);
-  constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp
-  constexpr int RU = 4;
-  const int sub = lane % LPR, c4 = sub * 4;
-  int rows = p.R - cur.rt * ROWS;
-  rows = rows < ROWS ? rows : ROWS;
-  for (int r0 = warp * RPW * RU; r0 < rows; r0 += WARPS * RPW * RU) {
-    float4 acc[RU];
-    float mn[RU], lt[RU];
-#pragma unroll
-    for (int k = 0; k < RU; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), mn[k] = -INFINITY, lt[k] = 0.f;
-    for (int cb = c0; cb <= c1; cb += LPR) {
-      const int mine = cb + sub;
-      float m[RU], l[RU], w[RU];
-#pragma unroll
-      for (int k = 0; k < RU; ++k) {
-        const int r = r0 + k * RPW + lane / LPR;
-        m[k] = -INFINITY, l[k] = 0.f;
-        if (mine <= c1) {
-          const float* pp = p.ws + ((int64_t)mine * 2 + (mine == c0)) * PART + ROWS * D + r;
-          m[k] = __ldcg(pp);
-          l[k] = __ldcg(pp + ROWS);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < RU; ++k) {
-        float x = m[k];
-#pragma unroll
-        for (int d = LPR / 2; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-        x = fmaxf(x, mn[k]);
-        const float old = attn_weight(mn[k], lt[k], x);
-        w[k] = attn_weight(m[k], l[k], x);
-        float sum = w[k] * l[k];
-#pragma unroll
-        for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        lt[k] = lt[k] * old + sum;
-        acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
-        mn[k] = x;
-      }
-      const int n = c1 - cb + 1 < LPR ? c1 - cb + 1 : LPR;
-#pragma unroll 2
-      for (int i = 0; i < n; ++i) {
-        const int c = cb + i;
-        const float* pp = p.ws + ((int64_t)c * 2 + (c == c0)) * PART + c4;
-#pragma unroll
-        for (int k = 0; k < RU; ++k) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + (r0 + k * RPW + lane / LPR) * D));
-          const float x = __shfl_sync(0xFFFFFFFFu, w[k], i, LPR);
-          acc[k].x += x * v.x, acc[k].y += x * v.y, acc[k].z += x * v.z, acc[k].w += x * v.w;
-        }
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < RU; ++k) {
-      const int r = r0 + k * RPW + lane / LPR;
-      if (r < rows) attn_store4<BF16>(p, cur, cur.rt * ROWS + r, c4, acc[k], mn[k], lt[k]);
-    }
-  }
 }
 
 }  // namespace qmm

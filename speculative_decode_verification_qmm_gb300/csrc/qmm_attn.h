@@ -17,16 +17,27 @@ cudaError_t host_dev_alloc(void** p, size_t bytes);
 int host_check_device(int* dev, int* sms);
 int host_cuda_fail(cudaError_t e);
 
-// mma.sync kernel: rows of an item's tile for R rows, and two CTAs per SM.
+// A tensor map over the rows of a pool ([rows][D] 16-bit values): boxes of 64
+// columns x box_rows rows, 128-byte swizzle.  map: a CUtensorMap.
+cudaError_t host_pool_map(void* map, const void* base, int64_t rows, int D, int box_rows, bool f16);
+
+// Rows of an item's tile for R rows, and cache rows of a unit.  mma.sync kernel:
+// two CTAs per SM.
 constexpr int ATTN_MMA_CTAS_PER_SM = 2;
 int attn_mma_tile_rows(int R);
+int attn_mma_tile_cache_rows();
 cudaError_t prepare_attn_mma(bool bf16, int D);
-cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, int ctas, cudaStream_t st);
+cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st);
 
-
-// tcgen05 kernel (more rows than the mma.sync kernel's tile holds), one CTA per SM.
+// tcgen05 kernel (more rows than the mma.sync kernel's tile holds), one CTA per
+// SM; kmap, vmap: host_pool_map with boxes of min(page_size, 128) rows.
 int attn_tc_tile_rows(int R);
+int attn_tc_tile_cache_rows();
 cudaError_t prepare_attn_tc(bool bf16, int D);
-cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, int ctas, cudaStream_t st);
+cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, const void* kmap, const void* vmap,
+                           cudaStream_t st);
+
+// Sums of the partials that a launch with those tiles left (qmm_attn_join.cu).
+cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, cudaStream_t st);
 
 }  // namespace qmm

@@ -37,8 +37,7 @@ struct Smem {
   static constexpr int RING = 0;
   static constexpr int SUM = RING + WARPS * STAGES * STAGE_BYTES;
   static constexpr int ML = SUM + WARPS * ROWS * PITCH * 4;  // m, then l: [warp][row]
-  static constexpr int FLAG = ML + 2 * WARPS * ROWS * 4;
-  static constexpr int BYTES = FLAG + 16;
+  static constexpr int BYTES = ML + 2 * WARPS * ROWS * 4;
 };
 
 template <bool BF16, int D, int MT>
@@ -53,9 +52,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2) attn_mma_kernel(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, gt = lane & 3;
 
-  int64_t W, u0, u1;
-  int G;
-  AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, gridDim.x, W, G, u0, u1);
+  pdl_trigger();  // the joining kernel may take its place and wait
+  int64_t u0, u1;
+  AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, u0, u1);
   if (u0 >= u1) return;
   AttnCursor ld = cur;
 
@@ -333,7 +332,6 @@ __global__ void __launch_bounds__(WARPS * 32, 2) attn_mma_kernel(const __grid_co
       // ------------------------------------------------ end of the segment
       float* s_ml = reinterpret_cast<float*>(smem + S::ML);
       float* s_sum = reinterpret_cast<float*>(smem + S::SUM);
-      int* s_flag = reinterpret_cast<int*>(smem + S::FLAG);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -421,19 +419,6 @@ __global__ void __launch_bounds__(WARPS * 32, 2) attn_mma_kernel(const __grid_co
           part[ROWS * D + cr] = cm;
           part[ROWS * D + ROWS + cr] = cl;
         }
-        __threadfence();
-        __syncthreads();
-        const int c0 = attn_owner(item_u, W, G), c1 = attn_owner(item_u + cur.ntiles - 1, W, G);
-        if (tid == 0) {
-          const int prev = atomicAdd(p.counters + c0, 1);
-          s_flag[0] = prev == c1 - c0;
-          if (s_flag[0]) p.counters[c0] = 0;
-        }
-        __syncthreads();
-        if (s_flag[0]) {
-          __threadfence();
-          attn_join<BF16, D, ROWS, WARPS>(p, cur, c0, c1, warp, lane);
-        }
       }
       __syncthreads();
       fresh_item = true;
@@ -450,13 +435,14 @@ cudaError_t prepare() {
 }
 
 template <bool BF16, int D, int MT>
-cudaError_t launch(const AttnParams& p, int ctas, cudaStream_t st) {
-  attn_mma_kernel<BF16, D, MT><<<(unsigned)ctas, WARPS * 32, Smem<D, MT>::BYTES, st>>>(p);
+cudaError_t launch(const AttnParams& p, cudaStream_t st) {
+  attn_mma_kernel<BF16, D, MT><<<(unsigned)p.grid, WARPS * 32, Smem<D, MT>::BYTES, st>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
+int attn_mma_tile_cache_rows() { return TK; }
 int attn_mma_tile_rows(int R) { return R <= 16 ? 16 : 32; }
 
 cudaError_t prepare_attn_mma(bool bf16, int D) {
@@ -471,14 +457,14 @@ cudaError_t prepare_attn_mma(bool bf16, int D) {
   return e;
 }
 
-cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, int ctas, cudaStream_t st) {
+cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st) {
   const bool one = attn_mma_tile_rows(p.R) == 16;
   if (D == 128) {
-    if (bf16) return one ? launch<true, 128, 1>(p, ctas, st) : launch<true, 128, 2>(p, ctas, st);
-    return one ? launch<false, 128, 1>(p, ctas, st) : launch<false, 128, 2>(p, ctas, st);
+    if (bf16) return one ? launch<true, 128, 1>(p, st) : launch<true, 128, 2>(p, st);
+    return one ? launch<false, 128, 1>(p, st) : launch<false, 128, 2>(p, st);
   }
-  if (bf16) return one ? launch<true, 64, 1>(p, ctas, st) : launch<true, 64, 2>(p, ctas, st);
-  return one ? launch<false, 64, 1>(p, ctas, st) : launch<false, 64, 2>(p, ctas, st);
+  if (bf16) return one ? launch<true, 64, 1>(p, st) : launch<true, 64, 2>(p, st);
+  return one ? launch<false, 64, 1>(p, st) : launch<false, 64, 2>(p, st);
 }
 
 }  // namespace qmm

@@ -12,18 +12,22 @@
 // behind the true maximum by up to 8 (P <= 256): O is rescaled, by the softmax
 // warps and through their registers, only when a row of the warp grows more.
 //   warps 0 .. 4 NQ - 1   softmax, rescaling, output (four warps a row tile)
-//   warp 4 NQ             one thread issues the MMAs
-//   the last three warps  load: cp.async of 32 KB tiles (D = 128) of K and V in
-//                         turn into a ring, Q once a segment, the tree's nodes
-//                         from the caller's rows (and on to the cache)
+//   two warps             one thread each issues MMAs: NQ = 1, the Q K^T and the
+//                         P V products; NQ = 2, those of one row tile each
+//   two warps             load K and V tiles, one ring each: tensor copies of whole
+//                         page parts; cp.async for an item's last tile, with the
+//                         tree's nodes from the caller's rows (and on to the
+//                         cache); Q, once a segment, by both
 // Why this split.  At 128 rows a tile of K and V (64 KB) takes 1.5 us of an
 // SM's share of the HBM stream, and its two products 0.55 us of the tensor cores
 // and its 16,384 exponentials about as long: with one row tile the stream is the
 // bound, and S is double-buffered so that Q K^T of the next tile runs under the
 // softmax.  With two, each tile of K and V serves 256 rows, and the products of
-// one row tile run under the softmax of the other.  Tensor memory: NQ = 1 holds
-// S twice (256 columns) and O; NQ = 2 S and O for both (512).  P overwrites the
-// first half of its S.
+// one row tile run under the softmax of the other.  The issue of an MMA blocks
+// until the one before it is nearly done, so that a barrier test between two
+// products leaves the tensor cores idle for its 130 cycles: hence two issuers.
+// Tensor memory: NQ = 1 holds S twice (256 columns) and O; NQ = 2 S and O for
+// both (512).  P overwrites the first half of its S.
 // Every wait is bounded; on a timeout the CTA records it, its roles run out of
 // their loops without waiting, its copies and MMAs in flight are drained and
 // tensor memory is freed.
@@ -39,22 +43,23 @@ namespace qmm {
 namespace {
 
 constexpr int TK = 128;   // cache rows of a tile
-constexpr int LOAD_WARPS = 3;  // and the MMA warp: one warpgroup
-constexpr int LAG = 3;    // groups of cp.async in flight behind the newest
-constexpr int BAD_BUFS = 8;
+constexpr int BAD_BUFS = 16;  // more than twice the segments that the rings hold
 
 template <int D, int NQ>
 struct Smem {
   static constexpr int TILE = TK * D * 2;           // one of K, V; also 128 rows of Q
   static constexpr int HALF = TK * 128;             // 64 columns of a tile
-  static constexpr int SLOTS = (D == 128 ? 7 - NQ : 10);
+  static constexpr int KS = D == 128 ? 3 : 4;       // ring of K tiles
+  static constexpr int VS = D == 128 ? 4 - NQ : 4;  // ring of V tiles
   static constexpr int Q = 0;
-  static constexpr int RING = Q + NQ * TILE;
-  static constexpr int BAR = RING + SLOTS * TILE;
-  // full[SLOTS], empty[SLOTS], qfull, qempty, sfull[2], pfull[2], odone[2], oempty[2], drain
-  static constexpr int NBAR = 2 * SLOTS + 11;
+  static constexpr int K = Q + NQ * TILE;
+  static constexpr int V = K + KS * TILE;
+  static constexpr int BAR = V + VS * TILE;
+  // kfull[KS], kempty[KS], vfull[VS], vempty[VS], qfull, qempty, sfull[2],
+  // sfree[2], pfull[2], odone[2], oempty[2], drain
+  static constexpr int NBAR = 2 * (KS + VS) + 13;
   static constexpr int BAD = BAR + NBAR * 8;        // nodes with non-finite V, by segment
-  static constexpr int FLAG = BAD + BAD_BUFS * 8;   // [0] abort, [1] tensor memory, [2] last
+  static constexpr int FLAG = BAD + BAD_BUFS * 8;   // [0] abort, [1] tensor memory
   static constexpr int BYTES = FLAG + 16;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
@@ -88,11 +93,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_t, uint32_t a_t, uint32_t b_lo
       : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void bar_named(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
-}
-
 // Bounded wait that also gives up when another role did.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint64_t lim, volatile int* abort) {
   if (lim == 0) return false;
@@ -106,39 +106,47 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
 }
 
 template <bool BF16, int D, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(NQ * 128 + 128, 1)
+    attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D, NQ>;
   constexpr int ROWS = NQ * 128;
-  constexpr int SOFT = NQ * 128;  // softmax threads
-  constexpr int SLOTS = S::SLOTS;
   constexpr uint32_t IDESC_S = tc_idesc_n(BF16 ? 1u : 0u, TK);
   constexpr uint32_t IDESC_O = tc_idesc_n(BF16 ? 1u : 0u, D) | (1u << 16);  // B along N
   // tensor memory columns: NQ = 1: S twice, O; NQ = 2: S, O of each row tile
   constexpr uint32_t COL_O = NQ == 1 ? 2 * TK : TK;
   constexpr uint32_t COL_Q = 256;  // of the second row tile
+  constexpr int MMA_WARP = NQ * 4, LOAD_WARP = MMA_WARP + 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = smem_u32(smem);
-  const uint32_t b_full = base + S::BAR, b_empty = b_full + SLOTS * 8, b_qfull = b_empty + SLOTS * 8,
-                 b_qempty = b_qfull + 8, b_sfull = b_qempty + 8, b_pfull = b_sfull + 16, b_odone = b_pfull + 16,
+  const uint32_t b_kfull = base + S::BAR, b_kempty = b_kfull + S::KS * 8, b_vfull = b_kempty + S::KS * 8,
+                 b_vempty = b_vfull + S::VS * 8, b_qfull = b_vempty + S::VS * 8, b_qempty = b_qfull + 8,
+                 b_sfull = b_qempty + 8, b_sfree = b_sfull + 16, b_pfull = b_sfree + 16, b_odone = b_pfull + 16,
                  b_oempty = b_odone + 16, b_drain = b_oempty + 16;
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::FLAG);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + S::BAD);
 
+  pdl_trigger();  // the joining kernel may take its place and wait
   if (tid == 0) {
-    for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(b_full + 8 * i, LOAD_WARPS);
-      mbar_init(b_empty + 8 * i, 1);
+    for (int i = 0; i < S::KS; ++i) {
+      mbar_init(b_kfull + 8 * i, 1);
+      mbar_init(b_kempty + 8 * i, NQ);
     }
-    mbar_init(b_qfull, LOAD_WARPS);
-    mbar_init(b_qempty, 1);
+    for (int i = 0; i < S::VS; ++i) {
+      mbar_init(b_vfull + 8 * i, 1);
+      mbar_init(b_vempty + 8 * i, NQ);
+    }
+    mbar_init(b_qfull, 2);
+    mbar_init(b_qempty, NQ);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
+      mbar_init(b_sfree + 8 * i, 1);
       mbar_init(b_pfull + 8 * i, 4);
       mbar_init(b_odone + 8 * i, 1);
       mbar_init(b_oempty + 8 * i, 4);
     }
-    mbar_init(b_drain, 1);
+    mbar_init(b_drain, 2);
     for (int i = 0; i < BAD_BUFS; ++i) s_bad[i] = 0;
     s_flag[0] = 0;
     if (base & 1023u) {
@@ -147,8 +155,9 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
     }
     fence_mbar_init();
   }
-  constexpr int MMA_WARP = NQ * 4;
   if (warp == MMA_WARP) tmem_alloc(base + S::FLAG + 4, 512);
+  int64_t u0, u1;
+  AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, u0, u1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -159,159 +168,50 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
     if (!s_flag[0]) atomicOr(p.status, code);
     s_flag[0] = 1;
   };
-  int64_t W, u0, u1;
-  int G;
-  AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, gridDim.x, W, G, u0, u1);
-  const int64_t head = (int64_t)D << p.page_shift;
-  if (warp > MMA_WARP) {
-    // ------------------------------------------------------------ load
-    const int lw = warp - (MMA_WARP + 1);
-    constexpr int CH = D / 8;                     // 16-byte chunks of a row
-    constexpr int PER = 16 * CH / 32;             // chunks of a block per lane
-    // A tile is eight blocks of 16 rows, each in one page; warp lw takes blocks
-    // lw, lw + LOAD_WARPS, ...
-    constexpr int BLOCKS = TK / 16, MINE = (BLOCKS + LOAD_WARPS - 1) / LOAD_WARPS;
-    bool ok = s_flag[0] == 0;
-    uint32_t pend[LAG];  // barriers of the groups in flight, oldest first
-    int pend_n = 0;
-#pragma unroll
-    for (int i = 0; i < LAG; ++i) pend[i] = 0;
+  // The cache tiles of the segment that starts at unit u.
+  auto segment = [&](int64_t u) {
+    const int64_t left = cur.ntiles - cur.tile;
+    return (int)(left < u1 - u ? left : u1 - u);
+  };
 
-    // The warp's blocks of a tile with nodes, once they have landed: on to the
-    // cache, and non-finite V out of the product.
-    auto finish = [&](const AttnCursor& c, uint32_t dst, int j0, int kind, int seg) {
-      uint16_t* pool = kind == 1 ? p.k_pool : p.v_pool;
-#pragma unroll 1
-      for (int i = 0; i < MINE * PER; ++i) {
-        const int blk = lw + i / PER * LOAD_WARPS, id = i % PER * 32 + lane;  // the chunks that it requested
-        const int row = blk * 16 + id / CH, ch = id % CH;
-        if (blk >= BLOCKS) break;
-        const int j = j0 + row, t = j - c.L;
-        if (t < 0 || t >= c.n) continue;
-        const uint32_t so = dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-        uint4 v = lds128(so);
-        if (c.rt == 0) {
-          const int pid = __ldg(p.table + c.b * p.ld_table + (j >> p.page_shift));
-          if (pid >= 0 && pid < p.n_pages)
-            *reinterpret_cast<uint4*>(pool + pid * p.page_stride + c.h * head +
-                                      (int64_t)(j & ((1 << p.page_shift) - 1)) * D + ch * 8) = v;
-          else
-            atomicOr(p.status, DEV_ERR_INDEX);
-        }
-        if (kind == 2 && any_nonfinite<BF16>(v)) {
-          v.x = zero_nonfinite<BF16>(v.x);
-          v.y = zero_nonfinite<BF16>(v.y);
-          v.z = zero_nonfinite<BF16>(v.z);
-          v.w = zero_nonfinite<BF16>(v.w);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(so), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
-          atomicOr(s_bad + (seg & (BAD_BUFS - 1)), 1ull << t);
-        }
-      }
+  if (warp >= LOAD_WARP) {
+    // ------------------------------------------------------------ load
+    const bool is_v = warp > LOAD_WARP;
+    constexpr int CH = D / 8;  // 16-byte chunks of a row
+    const uint32_t full = is_v ? b_vfull : b_kfull, empty = is_v ? b_vempty : b_kempty;
+    const uint32_t ring = base + (is_v ? S::V : S::K);
+    const int slots = is_v ? S::VS : S::KS;
+    const CUtensorMap* map = is_v ? &vmap : &kmap;
+    uint16_t* pool = is_v ? p.v_pool : p.k_pool;
+    const int64_t head = (int64_t)D << p.page_shift;
+    const int box = p.page_shift < 7 ? 1 << p.page_shift : TK;  // rows of one tensor copy
+    bool ok = s_flag[0] == 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      ok = __all_sync(0xFFFFFFFFu, ok && wait_or_abort(bar, parity, lim, s_flag));
+      if (!ok && lane == 0) fail(DEV_ERR_TIMEOUT_EMPTY);
     };
     auto hand_on = [&](uint32_t bar) {
+      cp_async_commit();
+      cp_async_wait<0>();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // One more group is under way: hand on the oldest once LAG are behind it.
-    auto push = [&](uint32_t bar) {
-      cp_async_commit();
-      if (pend_n == LAG) {
-        cp_async_wait<LAG>();
-        hand_on(pend[0]);
-#pragma unroll
-        for (int i = 0; i + 1 < LAG; ++i) pend[i] = pend[i + 1];
-        pend[LAG - 1] = bar;
-      } else {
-#pragma unroll
-        for (int i = 0; i < LAG; ++i)
-          if (i == pend_n) pend[i] = bar;
-        ++pend_n;
+    auto page_of = [&](int j) {  // a valid page for row j, whatever the table says
+      int pid = __ldg(p.table + cur.b * p.ld_table + (j >> p.page_shift));
+      if (pid < 0 || pid >= p.n_pages) {
+        atomicOr(p.status, DEV_ERR_INDEX);
+        pid = -1;
       }
+      return pid;
     };
-    auto flush = [&]() {
-      cp_async_wait<0>();
-#pragma unroll
-      for (int i = 0; i < LAG; ++i)
-        if (i < pend_n) hand_on(pend[i]);
-      pend_n = 0;
-    };
-    // Before a wait everything under way is handed on: what is waited for may
-    // depend on it.
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (lim != 0 && __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-      flush();
-      const bool got = __all_sync(0xFFFFFFFFu, wait_or_abort(bar, parity, lim, s_flag));
-      if (!got && lane == 0) fail(DEV_ERR_TIMEOUT_EMPTY);
-      return got;
-    };
-    int slot = 0, round = 0;  // of the next tile of K or V
-    // The page ids of the warp's blocks of a cache tile.
-    auto pages = [&](const AttnCursor& c, int j, int (&ids)[MINE]) {
-#pragma unroll
-      for (int x = 0; x < MINE; ++x) {
-        const int blk = lw + x * LOAD_WARPS, jb = j * TK + blk * 16;
-        ids[x] = blk < BLOCKS && jb < c.L ? __ldg(p.table + c.b * p.ld_table + (jb >> p.page_shift)) : 0;
-      }
-    };
-    auto tile = [&](const AttnCursor& c, int j, int kind, int seg, const int (&ids)[MINE]) {
-      if (ok && round > 0) ok = wait(b_empty + 8 * slot, (uint32_t)((round - 1) & 1));
-      if (!ok) return;
-      const uint32_t dst = base + S::RING + slot * S::TILE;
-      const int j0 = j * TK;
-      const uint16_t* pool = (kind == 1 ? p.k_pool : p.v_pool) + c.h * head;
-      const uint16_t* fresh = kind == 1 ? p.kn + c.b * p.k_sb + c.h * p.k_sh : p.vn + c.b * p.v_sb + c.h * p.v_sh;
-      const int64_t fresh_st = kind == 1 ? p.k_st : p.v_st;
-      bool bad_page = false;
-#pragma unroll
-      for (int x = 0; x < MINE; ++x) {
-        const int blk = lw + x * LOAD_WARPS;
-        if (blk >= BLOCKS) break;
-        const int jb = j0 + blk * 16;
-        const bool valid = ids[x] >= 0 && ids[x] < p.n_pages;
-        bad_page |= !valid;
-        const uint32_t have = valid ? 16 : 0;
-        const uint16_t* from = pool + (valid ? ids[x] : 0) * p.page_stride +
-                               (int64_t)(jb & ((1 << p.page_shift) - 1)) * D;
-        if (jb + 16 <= c.L) {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
-            cp_async16(dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4), from + id * 8, have);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
-            const int t = j0 + row - c.L;
-            const bool node = t >= 0 && t < c.n;
-            const uint32_t bytes = node ? 16 : (t < 0 ? have : 0);
-            const uint16_t* src = node ? fresh + t * fresh_st + ch * 8 : (bytes ? from + id * 8 : p.k_pool);
-            cp_async16(dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, bytes);
-          }
-        }
-      }
-      if (bad_page) atomicOr(p.status, DEV_ERR_INDEX);
-      if (j0 + TK > c.L && j0 < c.L + c.n) {
-        cp_async_commit();
-        flush();
-        finish(c, dst, j0, kind, seg);
-        hand_on(b_full + 8 * slot);
-      } else {
-        push(b_full + 8 * slot);
-      }
-      if (++slot == SLOTS) slot = 0, ++round;
-    };
-
-    int seg = 0;
+    int slot = 0, round = 0, seg = 0;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
-      int64_t left = cur.ntiles - cur.tile;
-      if (left > u1 - u) left = u1 - u;
-      const int first = cur.tile, count = (int)left;
-      if (seg > 0) ok = wait(b_qempty, (uint32_t)((seg - 1) & 1));
+      const int count = segment(u);
+      // Q: both warps, in turn rows of 32
+      if (seg > 0) wait(b_qempty, (uint32_t)((seg - 1) & 1));
       if (!ok) break;
-      for (int id = lw * 32 + lane; id < ROWS * CH; id += LOAD_WARPS * 32) {
+      for (int id = (warp - LOAD_WARP) * 32 + lane; id < ROWS * CH; id += 64) {
         const int row = id / CH, ch = id % CH;  // row of all NQ tiles
         const int r = cur.rt * ROWS + row, t = r / p.g, h = r - t * p.g;
         const uint16_t* src = p.q + cur.b * p.q_sb + t * p.q_st + (int64_t)(cur.h * p.g + h) * p.q_sh + ch * 8;
@@ -319,30 +219,100 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
                        (((ch & 7) ^ (row & 7)) << 4),
                    r < p.R ? src : p.q, r < p.R ? 16 : 0);
       }
-      push(b_qfull);
-      // in the order in which the MMAs read them; page ids are fetched a tile ahead
-      int ids[MINE] = {}, ahead[MINE], old[MINE];
-      pages(cur, first, ahead);
+      int ahead = -1;  // this lane's page of the next tile
+      auto lookup = [&](int j) {
+        const int row = j * TK + lane * box;
+        ahead = lane * box < TK && j * TK + TK <= cur.L ? page_of(row) : -1;
+      };
+      lookup(cur.tile);
+      hand_on(b_qfull);
       for (int j = 0; j < count; ++j) {
+        const int j0 = (cur.tile + j) * TK;
+        const int pid = ahead;
+        if (j + 1 < count) lookup(cur.tile + j + 1);
+        if (round > 0) wait(empty + 8 * slot, (uint32_t)((round - 1) & 1));
+        if (!ok) break;
+        const uint32_t bar = full + 8 * slot, dst = ring + slot * S::TILE;
+        if (j0 + TK <= cur.L) {
+          // a page id out of range is reported; rows of page 0 take its place
+          if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE);
+          __syncwarp();
+          if (lane * box < TK) {
+            const int64_t row = p.row0 + (((int64_t)(pid < 0 ? 0 : pid) * p.Hkv + cur.h) << p.page_shift) +
+                                ((j0 + lane * box) & ((1 << p.page_shift) - 1));
 #pragma unroll
-        for (int x = 0; x < MINE; ++x) old[x] = ids[x], ids[x] = ahead[x];
-        if (j + 1 < count) pages(cur, first + j + 1, ahead);
-        tile(cur, first + j, 1, seg, ids);
-        if constexpr (NQ == 1) {
-          if (j > 0) tile(cur, first + j - 1, 2, seg, old);
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_2d(dst + half * S::HALF + lane * box * 128, map, half * 64, (int)row, bar);
+          }
         } else {
-          tile(cur, first + j, 2, seg, ids);
+          const uint16_t* fresh = is_v ? p.vn + cur.b * p.v_sb + cur.h * p.v_sh : p.kn + cur.b * p.k_sb + cur.h * p.k_sh;
+          const int64_t fresh_st = is_v ? p.v_st : p.k_st;
+#pragma unroll 1
+          for (int blk = 0; blk < TK / 16; ++blk) {
+            const int jb = j0 + blk * 16;
+            const int id0 = jb < cur.L ? page_of(jb) : -1;
+            const uint16_t* from = pool + (id0 < 0 ? 0 : id0) * p.page_stride + cur.h * head +
+                                   (int64_t)(jb & ((1 << p.page_shift) - 1)) * D;
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
+              const int t = j0 + row - cur.L;
+              const bool node = t >= 0 && t < cur.n;
+              const uint32_t bytes = node || (t < 0 && id0 >= 0) ? 16 : 0;
+              const uint16_t* src = node ? fresh + t * fresh_st + ch * 8 : (bytes ? from + id * 8 : pool);
+              cp_async16(dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, bytes);
+            }
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          // Nodes: on to the cache, and non-finite V out of the product.  A
+          // lane reads back the chunks that it requested.
+          const int first_blk = cur.L > j0 ? (cur.L - j0) / 16 : 0;
+          const int end = cur.L + cur.n - j0;
+          for (int blk = first_blk; blk < TK / 16 && blk * 16 < end; ++blk) {
+            const int jb = j0 + blk * 16;
+            const int id0 = cur.rt == 0 ? page_of(jb) : -1;
+            uint16_t* to = pool + (id0 < 0 ? 0 : id0) * p.page_stride + cur.h * head +
+                           (int64_t)(jb & ((1 << p.page_shift) - 1)) * D;
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
+              const int t = j0 + row - cur.L;
+              if (t < 0 || t >= cur.n) continue;
+              const uint32_t so = dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+              uint4 v = lds128(so);
+              if (id0 >= 0) *reinterpret_cast<uint4*>(to + id * 8) = v;
+              if (is_v && any_nonfinite<BF16>(v)) {
+                v.x = zero_nonfinite<BF16>(v.x);
+                v.y = zero_nonfinite<BF16>(v.y);
+                v.z = zero_nonfinite<BF16>(v.z);
+                v.w = zero_nonfinite<BF16>(v.w);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(so), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+                atomicOr(s_bad + (seg & (BAD_BUFS - 1)), 1ull << t);
+              }
+            }
+          }
+          hand_on(bar);
         }
+        if (++slot == slots) slot = 0, ++round;
       }
-      if constexpr (NQ == 1) tile(cur, first + count - 1, 2, seg, ids);
-      cur.tile = first + count - 1;
+      cur.tile += count - 1;
       attn_next<TK>(p, cur);
       u += count;
     }
-    flush();
-  } else if (warp == MMA_WARP) {
+    cp_async_wait<0>();
+    // tensor copies in flight land before the CTA leaves: the last tile of every slot
+    for (int i = 0; i < slots; ++i) {
+      const int rounds = i < slot ? round + 1 : round;
+      if (rounds > 0 && s_flag[0] && lane == 0 && !mbar_wait_bounded(full + 8 * i, (rounds - 1) & 1, 1000000000ull))
+        atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
+    }
+  } else if (warp >= MMA_WARP) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
+      const int who = warp - MMA_WARP;
+      const int q = NQ == 1 ? 0 : who;  // row tile
       bool ok = s_flag[0] == 0;
       auto need = [&](uint32_t bar, int phase) {
         if (ok && !wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag)) {
@@ -351,97 +321,60 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
         }
         return ok;
       };
-      int slot = 0, round = 0;  // of the next tile of K or V
-      auto next = [&]() {
-        if (++slot == SLOTS) slot = 0, ++round;
-      };
-      int done = 0;  // cache tiles whose Q K^T was issued before this segment (parities only)
-      auto qk = [&](int q, int buf, int sl) {
-        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::RING + sl * S::TILE);
-        const uint32_t d = tmem + q * COL_Q + buf * TK;
+      const uint32_t t_q = tmem + q * COL_Q;
+      int ks = 0, kr = 0, vs = 0, vr = 0;  // slot and round of the next tile of K, of V
+      // Q K^T of the n-th tile of the CTA, the last of its segment or not.
+      auto qk = [&](int n, bool last) {
+        const int buf = NQ == 1 ? n & 1 : 0;
+        if (!need(b_kfull + 8 * ks, kr)) return;
+        // its S held P of an earlier tile until that product was done
+        if (NQ == 1 ? n >= 2 && !need(b_sfree + 8 * buf, (n >> 1) - 1) : n >= 1 && !need(b_sfree + 8 * q, n - 1)) return;
+        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + ks * S::TILE);
+        const uint32_t d = t_q + buf * TK;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          constexpr uint32_t STEP = 32 >> 4, HALF = S::HALF >> 4;
-          const uint32_t o = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * STEP;
+          const uint32_t o = (uint32_t)(kk >> 2) * (S::HALF >> 4) + (uint32_t)(kk & 3) * (32 >> 4);
           mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
         }
         tc_commit(b_sfull + 8 * (NQ == 1 ? buf : q));
+        tc_commit(b_kempty + 8 * ks);
+        if (last) tc_commit(b_qempty);
+        if (++ks == S::KS) ks = 0, ++kr;
       };
-      auto pv = [&](int q, int buf, int sl, bool first) {
-        const uint32_t a = tmem + q * COL_Q + buf * TK, d = tmem + q * COL_Q + COL_O;
-        const uint32_t b = desc_lo_mn(base + S::RING + sl * S::TILE, S::HALF);
+      // P V of the n-th tile, the first of segment `seg` or not.
+      auto pv = [&](int n, bool first, int seg) {
+        const int buf = NQ == 1 ? n & 1 : 0;
+        if (!need(b_vfull + 8 * vs, vr)) return;
+        if (!(NQ == 1 ? need(b_pfull + 8 * buf, n >> 1) : need(b_pfull + 8 * q, n))) return;
+        if (first && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) return;
+        const uint32_t a = t_q + buf * TK, d = t_q + COL_O;
+        const uint32_t b = desc_lo_mn(base + S::V + vs * S::TILE, S::HALF);
         tc_fence_after();
         mma_ts(d, a, b, IDESC_O, !first);
 #pragma unroll
         for (int kk = 1; kk < TK / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
         tc_commit(b_odone + 8 * q);
+        tc_commit(b_sfree + 8 * (NQ == 1 ? buf : q));
+        tc_commit(b_vempty + 8 * vs);
+        if (++vs == S::VS) vs = 0, ++vr;
       };
-      int seg = 0;
+      int n = 0, seg = 0;  // n: parities only
       for (int64_t u = u0; u < u1 && ok; ++seg) {
-        int64_t left = cur.ntiles - cur.tile;
-        if (left > u1 - u) left = u1 - u;
-        const int count = (int)left;
-        if (!need(b_qfull, seg)) break;
-        if constexpr (NQ == 1) {
-          for (int j = 0; j <= count && ok; ++j) {
-            if (j < count) {
-              const int n = done + j;
-              if (!need(b_full + 8 * slot, round)) break;
-              // its S holds P of two tiles ago until that product is done (at a
-              // segment's start the product of the last tile is the newest one)
-              if (j == 0 ? n >= 1 && !need(b_odone, n - 1) : n >= 2 && !need(b_odone, n - 2)) break;
-              qk(0, n & 1, slot);
-              tc_commit(b_empty + 8 * slot);
-              if (j == count - 1) tc_commit(b_qempty);
-              next();
-            }
-            if (j > 0) {
-              const int n = done + j - 1;
-              if (!need(b_full + 8 * slot, round)) break;
-              if (!need(b_pfull + 8 * (n & 1), n >> 1)) break;
-              if (j == 1 && seg > 0 && !need(b_oempty, seg - 1)) break;
-              pv(0, n & 1, slot, j == 1);
-              tc_commit(b_empty + 8 * slot);
-              next();
-            }
-          }
-        } else {
-          if (!need(b_full + 8 * slot, round)) break;
-          for (int q = 0; q < 2 && ok; ++q)
-            if (done == 0 || need(b_odone + 8 * q, done - 1)) qk(q, 0, slot);
-          if (!ok) break;
-          tc_commit(b_empty + 8 * slot);
-          if (count == 1) tc_commit(b_qempty);
-          next();
-          for (int j = 0; j < count && ok; ++j) {
-            const int n = done + j;
-            const bool more = j + 1 < count;
-            if (!need(b_full + 8 * slot, round)) break;
-            const int vslot = slot;
-            next();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              if (!need(b_pfull + 8 * q, n)) break;
-              if (j == 0 && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) break;
-              pv(q, 0, vslot, j == 0);
-              if (q == 1) tc_commit(b_empty + 8 * vslot);
-              if (more) {
-                if (q == 0 && !need(b_full + 8 * slot, round)) break;
-                // P lies in S: the next S may follow when its product is done
-                if (!need(b_odone + 8 * q, n)) break;
-                qk(q, 0, slot);
-              }
-            }
-            if (!ok) break;
-            if (more) {
-              tc_commit(b_empty + 8 * slot);
-              if (j + 2 == count) tc_commit(b_qempty);
-              next();
-            }
+        const int count = segment(u);
+        if ((NQ == 2 || who == 0) && !need(b_qfull, seg)) break;
+        for (int j = 0; j < count && ok; ++j, ++n) {
+          if constexpr (NQ == 1) {
+            if (who == 0)
+              qk(n, j + 1 == count);
+            else
+              pv(n, j == 0, seg);
+          } else {
+            if (j == 0) qk(n, count == 1);
+            if (ok) pv(n, j == 0, seg);
+            if (ok && j + 1 < count) qk(n + 1, j + 2 == count);
           }
         }
-        done += count;
         cur.tile += count - 1;
         attn_next<TK>(p, cur);
         u += count;
@@ -457,7 +390,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + q * COL_Q;
     const uint32_t t_o = tl + COL_O;
     bool ok = s_flag[0] == 0;
-    auto need = [&](uint32_t bar, int64_t phase) {
+    auto need = [&](uint32_t bar, int phase) {
       if (ok) {
         const bool got = __all_sync(0xFFFFFFFFu, wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag));
         if (!got) {
@@ -467,19 +400,16 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
       }
       return ok;
     };
-    int64_t done = 0;
-    int seg = 0;
+    int done = 0, seg = 0;  // done: parities only
     for (int64_t u = u0; u < u1; ++seg) {
-      int64_t left = cur.ntiles - cur.tile;
-      if (left > u1 - u) left = u1 - u;
-      const int count = (int)left;
+      const int count = segment(u);
       const int r = cur.rt * ROWS + q * 128 + row;
       const bool in = r < p.R;
       const uint64_t bits = in ? attn_bits(p, cur.b, cur.n, r) : 0;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < count; ++j) {
-        const int64_t n = done + j;
-        const int buf = NQ == 1 ? (int)(n & 1) : 0;
+        const int n = done + j;
+        const int buf = NQ == 1 ? n & 1 : 0;
         const uint32_t t_s = tl + buf * TK;
         if (!need(b_sfull + 8 * (NQ == 1 ? buf : q), NQ == 1 ? n >> 1 : n)) continue;
         tc_fence_after();
@@ -577,6 +507,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
       const int t_row = r / p.g, i_row = r - t_row * p.g;
       const bool live = in && t_row < cur.n;
       const unsigned long long bad = s_bad[seg & (BAD_BUFS - 1)];
+      if (tid == 0) s_bad[(seg + BAD_BUFS / 2) & (BAD_BUFS - 1)] = 0;  // read by all, not yet written again
       auto write16 = [&](int t, int i, int c, const float (&a)[32], float inv) {
         uint16_t* to = p.out + cur.b * p.o_sb + t * p.o_st + (int64_t)(cur.h * p.g + i) * p.o_sh + c;
 #pragma unroll
@@ -630,31 +561,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1) attn_tc_kernel(const __grid
         if (ok && in && p.lse)
           p.lse[((int64_t)cur.b * p.T + t_row) * p.Hq + cur.h * p.g + i_row] =
               live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        bar_named<SOFT>(1);
-      } else {
-        if (ok) {
-          part[ROWS * D + q * 128 + row] = m;
-          part[ROWS * D + ROWS + q * 128 + row] = l;
-        }
-        __threadfence();
-        bar_named<SOFT>(1);
-        const int c0 = attn_owner(item_u, W, G), c1 = attn_owner(item_u + cur.ntiles - 1, W, G);
-        if (tid == 0) {
-          int is_last = 0;
-          if (s_flag[0] == 0) {
-            is_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
-            if (is_last) p.counters[c0] = 0;
-          }
-          s_flag[2] = is_last;
-        }
-        bar_named<SOFT>(1);
-        if (s_flag[2]) {
-          __threadfence();
-          attn_join<BF16, D, ROWS, SOFT / 32>(p, cur, c0, c1, warp, lane);
-        }
-        bar_named<SOFT>(1);
+      } else if (ok) {
+        part[ROWS * D + q * 128 + row] = m;
+        part[ROWS * D + ROWS + q * 128 + row] = l;
       }
-      if (tid == 0) s_bad[seg & (BAD_BUFS - 1)] = 0;
       done += count;
       cur.tile += count - 1;
       attn_next<TK>(p, cur);
@@ -676,13 +586,15 @@ cudaError_t prepare() {
 }
 
 template <bool BF16, int D, int NQ>
-cudaError_t launch(const AttnParams& p, int ctas, cudaStream_t st) {
-  attn_tc_kernel<BF16, D, NQ><<<(unsigned)ctas, NQ * 128 + 128, Smem<D, NQ>::BYTES, st>>>(p);
+cudaError_t launch(const AttnParams& p, const void* kmap, const void* vmap, cudaStream_t st) {
+  attn_tc_kernel<BF16, D, NQ><<<(unsigned)p.grid, NQ * 128 + 128, Smem<D, NQ>::BYTES, st>>>(
+      p, *static_cast<const CUtensorMap*>(kmap), *static_cast<const CUtensorMap*>(vmap));
   return cudaGetLastError();
 }
 
 }  // namespace
 
+int attn_tc_tile_cache_rows() { return TK; }
 int attn_tc_tile_rows(int R) { return R <= 128 ? 128 : 256; }
 
 cudaError_t prepare_attn_tc(bool bf16, int D) {
@@ -697,14 +609,15 @@ cudaError_t prepare_attn_tc(bool bf16, int D) {
   return e;
 }
 
-cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, int ctas, cudaStream_t st) {
+cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, const void* kmap, const void* vmap,
+                           cudaStream_t st) {
   const bool one = attn_tc_tile_rows(p.R) == 128;
   if (D == 128) {
-    if (bf16) return one ? launch<true, 128, 1>(p, ctas, st) : launch<true, 128, 2>(p, ctas, st);
-    return one ? launch<false, 128, 1>(p, ctas, st) : launch<false, 128, 2>(p, ctas, st);
+    if (bf16) return one ? launch<true, 128, 1>(p, kmap, vmap, st) : launch<true, 128, 2>(p, kmap, vmap, st);
+    return one ? launch<false, 128, 1>(p, kmap, vmap, st) : launch<false, 128, 2>(p, kmap, vmap, st);
   }
-  if (bf16) return one ? launch<true, 64, 1>(p, ctas, st) : launch<true, 64, 2>(p, ctas, st);
-  return one ? launch<false, 64, 1>(p, ctas, st) : launch<false, 64, 2>(p, ctas, st);
+  if (bf16) return one ? launch<true, 64, 1>(p, kmap, vmap, st) : launch<true, 64, 2>(p, kmap, vmap, st);
+  return one ? launch<false, 64, 1>(p, kmap, vmap, st) : launch<false, 64, 2>(p, kmap, vmap, st);
 }
 
 }  // namespace qmm

@@ -1,6 +1,7 @@
 // qmm_cache.cu -- the paged cache's handle and entry points (include/qmm.h), and
 // the two kernels that move its rows: compaction of an accepted branch and
 // copies of pages.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -20,8 +21,8 @@ struct qmm_cache {
   int device = 0;
   int sm_count = 0;
   int page_shift = 0;
+  CUtensorMap kmap, vmap;   // the pools' rows
   float* ws = nullptr;      // partials of split attention items
-  int* counters = nullptr;  // their tickets, zero between calls
   int* status = nullptr;    // device error word
   uint64_t wait_limit_ns = 2000000000ull;  // 2 s
 };
@@ -45,7 +46,6 @@ void free_cache(qmm_cache* h) {
   cudaGetDevice(&old);
   if (old != h->device) cudaSetDevice(h->device);
   cudaFree(h->ws);
-  cudaFree(h->counters);
   cudaFree(h->status);
   if (old >= 0 && old != h->device) cudaSetDevice(old);
   delete h;
@@ -211,6 +211,10 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
       (d->head_dim != 64 && d->head_dim != 128) || d->max_batch < 1 || d->max_batch > QMM_CACHE_MAX_BATCH ||
       d->n_pages < 1 || d->n_pages > INT32_MAX)
     return QMM_ERR_SHAPE;
+  // tensor copies count the pools' rows in 32 bits
+  const int64_t layer_rows = (int64_t)d->n_kv_heads * d->page_size;
+  if (d->n_pages > INT32_MAX / layer_rows || d->n_layers > INT32_MAX / (d->n_pages * layer_rows)) return QMM_ERR_SHAPE;
+  const int64_t pool_rows = d->n_layers * d->n_pages * layer_rows;
   if (((uintptr_t)d->k_pool | (uintptr_t)d->v_pool) & 15) return QMM_ERR_ALIGN;
   int dev = 0, sms = 0;
   const int rc = host_check_device(&dev, &sms);
@@ -229,14 +233,15 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   const size_t ws_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
   if (e == cudaSuccess) e = prepare_attn_tc(d->dtype == QMM_DT_BF16, d->head_dim);
+  const int box = d->page_size < attn_tc_tile_cache_rows() ? d->page_size : attn_tc_tile_cache_rows();
+  const bool f16 = d->dtype == QMM_DT_F16;
+  if (e == cudaSuccess) e = host_pool_map(&h->kmap, d->k_pool, pool_rows, d->head_dim, box, f16);
+  if (e == cudaSuccess) e = host_pool_map(&h->vmap, d->v_pool, pool_rows, d->head_dim, box, f16);
   void* ptr = nullptr;
   if (e == cudaSuccess && (e = host_dev_alloc(&ptr, ws_bytes)) == cudaSuccess)
     h->ws = static_cast<float*>(ptr);
-  if (e == cudaSuccess && (e = host_dev_alloc(&ptr, (size_t)ctas * sizeof(int))) == cudaSuccess)
-    h->counters = static_cast<int*>(ptr);
   if (e == cudaSuccess && (e = host_dev_alloc(&ptr, sizeof(int))) == cudaSuccess)
     h->status = static_cast<int*>(ptr);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->counters, 0, (size_t)ctas * sizeof(int), st);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, sizeof(int), st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) {
@@ -273,10 +278,7 @@ int qmm_cache_sync_status(qmm_cache_t h, void* stream) {
   if (e == cudaSuccess) e = cudaMemcpyAsync(&word, h->status, sizeof(int), cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && word != 0) {
-    // a kernel that gave up may have left tickets behind
     e = cudaMemsetAsync(h->status, 0, sizeof(int), st);
-    if (e == cudaSuccess && (word & ~DEV_ERR_INDEX))
-      e = cudaMemsetAsync(h->counters, 0, (size_t)h->sm_count * ATTN_MMA_CTAS_PER_SM * sizeof(int), st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   }
   if (e != cudaSuccess) return host_cuda_fail(e);
@@ -335,16 +337,19 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   p.R = p.T * p.g;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.ws = h->ws;
-  p.counters = h->counters;
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
   const bool bf16 = d.dtype == QMM_DT_BF16;
   const bool tc = p.R > attn_mma_tile_rows(p.R);
   const int rows = tc ? attn_tc_tile_rows(p.R) : attn_mma_tile_rows(p.R);
+  const int tk = tc ? attn_tc_tile_cache_rows() : attn_mma_tile_cache_rows();
   p.RT = (p.R + rows - 1) / rows;
-  const cudaError_t e =
-      tc ? launch_attn_tc(p, bf16, d.head_dim, h->sm_count, (cudaStream_t)stream)
-         : launch_attn_mma(p, bf16, d.head_dim, h->sm_count * ATTN_MMA_CTAS_PER_SM, (cudaStream_t)stream);
+  p.grid = tc ? h->sm_count : h->sm_count * ATTN_MMA_CTAS_PER_SM;
+  p.row0 = (int64_t)a->layer * d.n_pages * d.n_kv_heads * d.page_size;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = tc ? launch_attn_tc(p, bf16, d.head_dim, &h->kmap, &h->vmap, st)
+                     : launch_attn_mma(p, bf16, d.head_dim, st);
+  if (e == cudaSuccess) e = launch_attn_join(p, bf16, d.head_dim, tk, rows, st);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }
 
