@@ -26,8 +26,12 @@
 // one row tile run under the softmax of the other.  The issue of an MMA blocks
 // until the one before it is nearly done, so that a barrier test between two
 // products leaves the tensor cores idle for its 130 cycles: hence two issuers.
-// Tensor memory: NQ = 1 holds S twice (256 columns) and O; NQ = 2 S and O for
-// both (512).  P overwrites the first half of its S.
+// S is computed SW cache rows at a time into two buffers, so that the next
+// Q K^T runs under the softmax of the last; SW is the whole tile for NQ = 1, and
+// half of it for NQ = 2, whose tensor memory (512 columns) would not hold two
+// whole S and O of both row tiles.  With one whole S each, a step took 5,700
+// cycles of which the tensor cores worked 2,048.  P overwrites the first half of
+// its S.
 // Every wait is bounded; on a timeout the CTA records it, its roles run out of
 // their loops without waiting, its copies and MMAs in flight are drained and
 // tensor memory is freed.
@@ -55,9 +59,9 @@ struct Smem {
   static constexpr int K = Q + NQ * TILE;
   static constexpr int V = K + KS * TILE;
   static constexpr int BAR = V + VS * TILE;
-  // kfull[KS], kempty[KS], vfull[VS], vempty[VS], qfull, qempty, sfull[2],
-  // sfree[2], pfull[2], odone[2], oempty[2], drain
-  static constexpr int NBAR = 2 * (KS + VS) + 13;
+  // kfull[KS], kempty[KS], vfull[VS], vempty[VS], qfull, qempty, sfull[4],
+  // sfree[4], pfull[4], odone[2], oempty[2], drain
+  static constexpr int NBAR = 2 * (KS + VS) + 19;
   static constexpr int BAD = BAR + NBAR * 8;        // nodes with non-finite V, by segment
   static constexpr int FLAG = BAD + BAD_BUFS * 8;   // [0] abort, [1] tensor memory
   static constexpr int BYTES = FLAG + 16;
@@ -111,10 +115,11 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
                    const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D, NQ>;
   constexpr int ROWS = NQ * 128;
-  constexpr uint32_t IDESC_S = tc_idesc_n(BF16 ? 1u : 0u, TK);
+  constexpr int SW = TK / NQ, SUB = TK / SW;  // columns of S, steps of a tile
+  constexpr uint32_t IDESC_S = tc_idesc_n(BF16 ? 1u : 0u, SW);
   constexpr uint32_t IDESC_O = tc_idesc_n(BF16 ? 1u : 0u, D) | (1u << 16);  // B along N
-  // tensor memory columns: NQ = 1: S twice, O; NQ = 2: S, O of each row tile
-  constexpr uint32_t COL_O = NQ == 1 ? 2 * TK : TK;
+  // tensor memory columns: S twice, then O, of each row tile
+  constexpr uint32_t COL_O = 2 * SW;
   constexpr uint32_t COL_Q = 256;  // of the second row tile
   constexpr int MMA_WARP = NQ * 4, LOAD_WARP = MMA_WARP + 2;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -122,8 +127,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
   const uint32_t base = smem_u32(smem);
   const uint32_t b_kfull = base + S::BAR, b_kempty = b_kfull + S::KS * 8, b_vfull = b_kempty + S::KS * 8,
                  b_vempty = b_vfull + S::VS * 8, b_qfull = b_vempty + S::VS * 8, b_qempty = b_qfull + 8,
-                 b_sfull = b_qempty + 8, b_sfree = b_sfull + 16, b_pfull = b_sfree + 16, b_odone = b_pfull + 16,
-                 b_oempty = b_odone + 16, b_drain = b_oempty + 16;
+                 b_sfull = b_qempty + 8, b_sfree = b_sfull + 32, b_pfull = b_sfree + 32, b_odone = b_pfull + 32,
+                 b_oempty = b_odone + 16, b_drain = b_oempty + 16;  // sfull, sfree, pfull: [row tile][buffer]
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::FLAG);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + S::BAD);
 
@@ -139,10 +144,12 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
     }
     mbar_init(b_qfull, 2);
     mbar_init(b_qempty, NQ);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
       mbar_init(b_sfree + 8 * i, 1);
       mbar_init(b_pfull + 8 * i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(b_odone + 8 * i, 1);
       mbar_init(b_oempty + 8 * i, 4);
     }
@@ -323,56 +330,60 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
       };
       const uint32_t t_q = tmem + q * COL_Q;
       int ks = 0, kr = 0, vs = 0, vr = 0;  // slot and round of the next tile of K, of V
-      // Q K^T of the n-th tile of the CTA, the last of its segment or not.
-      auto qk = [&](int n, bool last) {
-        const int buf = NQ == 1 ? n & 1 : 0;
-        if (!need(b_kfull + 8 * ks, kr)) return;
-        // its S held P of an earlier tile until that product was done
-        if (NQ == 1 ? n >= 2 && !need(b_sfree + 8 * buf, (n >> 1) - 1) : n >= 1 && !need(b_sfree + 8 * q, n - 1)) return;
-        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + ks * S::TILE);
-        const uint32_t d = t_q + buf * TK;
+      // Q K^T of the CTA's n-th step, step `sub` of its tile; `last` of its segment.
+      auto qk = [&](int n, int sub, bool last) {
+        const int buf = 2 * q + (n & 1);
+        if (sub == 0 && !need(b_kfull + 8 * ks, kr)) return;
+        // its S held P of two steps ago until that product was done
+        if (n >= 2 && !need(b_sfree + 8 * buf, (n >> 1) - 1)) return;
+        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + ks * S::TILE + sub * SW * 128);
+        const uint32_t d = t_q + (n & 1) * SW;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = (uint32_t)(kk >> 2) * (S::HALF >> 4) + (uint32_t)(kk & 3) * (32 >> 4);
           mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
         }
-        tc_commit(b_sfull + 8 * (NQ == 1 ? buf : q));
-        tc_commit(b_kempty + 8 * ks);
+        tc_commit(b_sfull + 8 * buf);
+        if (sub == SUB - 1) {
+          tc_commit(b_kempty + 8 * ks);
+          if (++ks == S::KS) ks = 0, ++kr;
+        }
         if (last) tc_commit(b_qempty);
-        if (++ks == S::KS) ks = 0, ++kr;
       };
-      // P V of the n-th tile, the first of segment `seg` or not.
-      auto pv = [&](int n, bool first, int seg) {
-        const int buf = NQ == 1 ? n & 1 : 0;
-        if (!need(b_vfull + 8 * vs, vr)) return;
-        if (!(NQ == 1 ? need(b_pfull + 8 * buf, n >> 1) : need(b_pfull + 8 * q, n))) return;
+      // P V of the n-th step; the first of segment `seg` or not.
+      auto pv = [&](int n, int sub, bool first, int seg) {
+        const int buf = 2 * q + (n & 1);
+        if (sub == 0 && !need(b_vfull + 8 * vs, vr)) return;
+        if (!need(b_pfull + 8 * buf, n >> 1)) return;
         if (first && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) return;
-        const uint32_t a = t_q + buf * TK, d = t_q + COL_O;
-        const uint32_t b = desc_lo_mn(base + S::V + vs * S::TILE, S::HALF);
+        const uint32_t a = t_q + (n & 1) * SW, d = t_q + COL_O;
+        const uint32_t b = desc_lo_mn(base + S::V + vs * S::TILE + sub * SW * 128, S::HALF);
         tc_fence_after();
         mma_ts(d, a, b, IDESC_O, !first);
 #pragma unroll
-        for (int kk = 1; kk < TK / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
+        for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
         tc_commit(b_odone + 8 * q);
-        tc_commit(b_sfree + 8 * (NQ == 1 ? buf : q));
-        tc_commit(b_vempty + 8 * vs);
-        if (++vs == S::VS) vs = 0, ++vr;
+        tc_commit(b_sfree + 8 * buf);
+        if (sub == SUB - 1) {
+          tc_commit(b_vempty + 8 * vs);
+          if (++vs == S::VS) vs = 0, ++vr;
+        }
       };
       int n = 0, seg = 0;  // n: parities only
       for (int64_t u = u0; u < u1 && ok; ++seg) {
-        const int count = segment(u);
+        const int count = segment(u), steps = count * SUB;
         if ((NQ == 2 || who == 0) && !need(b_qfull, seg)) break;
-        for (int j = 0; j < count && ok; ++j, ++n) {
+        if (NQ == 2) qk(n, 0, steps == 1);
+        for (int j = 0; j < steps && ok; ++j, ++n) {
           if constexpr (NQ == 1) {
             if (who == 0)
-              qk(n, j + 1 == count);
+              qk(n, 0, j + 1 == steps);
             else
-              pv(n, j == 0, seg);
+              pv(n, 0, j == 0, seg);
           } else {
-            if (j == 0) qk(n, count == 1);
-            if (ok) pv(n, j == 0, seg);
-            if (ok && j + 1 < count) qk(n + 1, j + 2 == count);
+            if (j + 1 < steps) qk(n + 1, (j + 1) % SUB, j + 2 == steps);
+            if (ok) pv(n, j % SUB, j == 0, seg);
           }
         }
         cur.tile += count - 1;
@@ -407,40 +418,33 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
       const bool in = r < p.R;
       const uint64_t bits = in ? attn_bits(p, cur.b, cur.n, r) : 0;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < count; ++j) {
+      const int steps = count * SUB;
+      for (int j = 0; j < steps; ++j) {
         const int n = done + j;
-        const int buf = NQ == 1 ? n & 1 : 0;
-        const uint32_t t_s = tl + buf * TK;
-        if (!need(b_sfull + 8 * (NQ == 1 ? buf : q), NQ == 1 ? n >> 1 : n)) continue;
+        const int buf = 2 * q + (n & 1);
+        const uint32_t t_s = tl + (n & 1) * SW;
+        if (!need(b_sfull + 8 * buf, n >> 1)) continue;
         tc_fence_after();
-        const int t0 = (cur.tile + j) * TK - cur.L;  // node of the tile's first row, if it is one
-        const bool edge = t0 + TK > 0;
-        // One row tile: the row's 128 scores stay in registers.  Two: 64 at a time
-        // (168 registers a thread), the second half first, as P of the first
-        // half then takes the place of scores that are in registers.
-        constexpr int PARTS = NQ, CPP = TK / 32 / PARTS;
-        uint32_t v[CPP][32];
-        auto fetch = [&](int part) {
+        const int t0 = cur.tile * TK + j * SW - cur.L;  // node of the step's first row, if it is one
+        const bool edge = t0 + SW > 0;
+        uint32_t v[SW / 32][32];  // the row's scores
 #pragma unroll
-          for (int c = 0; c < CPP; ++c) tmem_ld32(t_s + (part * CPP + c) * 32, v[c]);
-          tmem_wait_ld();
-          if (edge) {
+        for (int c = 0; c < SW / 32; ++c) tmem_ld32(t_s + c * 32, v[c]);
+        tmem_wait_ld();
+        if (edge) {
 #pragma unroll
-            for (int c = 0; c < CPP; ++c)
+          for (int c = 0; c < SW / 32; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int t = t0 + (part * CPP + c) * 32 + i;
-                if (t >= 0 && (t >= 64 || !(bits >> t & 1))) v[c][i] = 0xFF800000u;  // -inf
-              }
-          }
-        };
-        float mx = -INFINITY;
+            for (int i = 0; i < 32; ++i) {
+              const int t = t0 + c * 32 + i;
+              if (t >= 0 && (t >= 64 || !(bits >> t & 1))) v[c][i] = 0xFF800000u;  // -inf
+            }
+        }
+        float mx;
+        {
+          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int part = PARTS - 1; part >= 0; --part) {
-          fetch(part);
-          float x[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < CPP; ++c)
+          for (int c = 0; c < SW / 32; ++c)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
               x[(i >> 1) & 3] = fmaxf(x[(i >> 1) & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
@@ -470,21 +474,17 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         const float2 c2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(-mb, -mb);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
-          if (part > 0) fetch(part);
+        for (int c = 0; c < SW / 32; ++c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < CPP; ++c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float2 e = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), c2, m2);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
-              w[i / 2] = pack16<BF16>(e.x, e.y);
-            }
-            tmem_st16(t_s + (part * CPP + c) * 16, w);
+          for (int i = 0; i < 32; i += 2) {
+            float2 e = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), c2, m2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
+            w[i / 2] = pack16<BF16>(e.x, e.y);
           }
+          tmem_st16(t_s + c * 16, w);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
@@ -493,11 +493,11 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         if (n > 0 && !need(b_odone + 8 * q, n - 1)) continue;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_pfull + 8 * (NQ == 1 ? buf : q));
+        if (lane == 0) mbar_arrive(b_pfull + 8 * buf);
       }
 
       // ------------------------------------------------ end of the segment
-      need(b_odone + 8 * q, done + count - 1);
+      need(b_odone + 8 * q, done + steps - 1);
       tc_fence_after();
       const int64_t item_u = u - cur.tile;  // the item's first unit
       const bool last_tile = cur.tile + count == cur.ntiles;
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         part[ROWS * D + q * 128 + row] = m;
         part[ROWS * D + ROWS + q * 128 + row] = l;
       }
-      done += count;
+      done += steps;
       cur.tile += count - 1;
       attn_next<TK>(p, cur);
       u += count;
