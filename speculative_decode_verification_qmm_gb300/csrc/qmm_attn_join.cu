@@ -2,10 +2,11 @@
 // cut between CTAs (qmm_attn.cuh).
 //
 //   m = max m_c,  l = sum l_c 2^(m_c - m),  O = sum O_c 2^(m_c - m),  out = O / l
-// over the item's CTAs c in order.  The partials are read from L2; what bounds
-// the kernel is latency, so the work is spread over the GPU (RU rows of one
-// item per warp), loads of several parts and rows are in flight at a time, and
-// everything that does not depend on the partials is done before the wait for
+// over the item's CTAs c.  The partials are read from L2; what bounds the kernel
+// is latency, so a CTA takes four rows (eight at head size 64), its four warps
+// every fourth part of them, and all of a warp's loads of two parts are in
+// flight at a time; the warps' sums are added in order through shared memory.
+// Everything that does not depend on the partials is done before the wait for
 // the kernel that writes them (programmatic dependent launch).  As a tail of the
 // attention kernels' last CTA of an item the same sums took up to 30 us (64
 // items of 256 rows, 4 parts each), because one SM had to read them all.
@@ -19,12 +20,16 @@ namespace qmm {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int RU = 2;  // rows of a lane
+constexpr int RU = 4;  // rows of a lane
+constexpr int U = 2;   // parts in flight
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int tk, int rows,
                                                                int chunks) {
-  constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp at a time
+  constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp's load
+  constexpr int RPC = RPW * RU;               // rows of the CTA
+  __shared__ float4 s_acc[WARPS][RPC][LPR];
+  __shared__ float s_m[WARPS][RPC], s_l[WARPS][RPC];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
   AttnCursor cur{};
@@ -41,76 +46,75 @@ __global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const __grid_cons
   const int64_t u = before * p.Hkv * p.RT + (int64_t)(cur.h * p.RT + cur.rt) * nt;
   const int c0 = attn_owner(u, W, G), c1 = attn_owner(u + nt - 1, W, G);
   const int part = rows * (D + 2);
-  const int r0 = (chunk * WARPS + warp) * RPW * RU + lane / LPR;
-  const int left = p.R - cur.rt * rows < rows ? p.R - cur.rt * rows : rows;
-  const int sub = lane % LPR, c4 = sub * 4;
+  const int r0 = chunk * RPC, left = p.R - cur.rt * rows < rows ? p.R - cur.rt * rows : rows;
+  const int sub = lane % LPR, row = lane / LPR;
   pdl_wait();  // every CTA: the call has not ended before the attention kernel has
-  if (c0 == c1 || r0 - lane / LPR >= left) return;
+  if (c0 == c1) return;
 
   float4 acc[RU];
   float mn[RU], lt[RU];
 #pragma unroll
   for (int k = 0; k < RU; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), mn[k] = -INFINITY, lt[k] = 0.f;
-  for (int cb = c0; cb <= c1; cb += LPR) {
-    // each lane of a row takes one part's statistics
-    const int mine = cb + sub;
-    float m[RU], l[RU], w[RU];
+  for (int c = c0 + warp; c <= c1; c += WARPS * U) {
+    float4 v[U][RU];
+    float m[U][RU], l[U][RU];
 #pragma unroll
-    for (int k = 0; k < RU; ++k) {
-      m[k] = -INFINITY, l[k] = 0.f;
-      if (mine <= c1) {
-        const float* pp = p.ws + ((int64_t)mine * 2 + (mine == c0)) * part + rows * D + r0 + k * RPW;
-        m[k] = __ldcg(pp);
-        l[k] = __ldcg(pp + rows);
+    for (int j = 0; j < U; ++j) {
+      const int cc = c + j * WARPS;
+      const float* pp = p.ws + ((int64_t)cc * 2 + (cc == c0)) * part;
+#pragma unroll
+      for (int k = 0; k < RU; ++k) {
+        const int r = r0 + k * RPW + row;
+        const bool have = cc <= c1;
+        m[j][k] = have ? __ldcg(pp + rows * D + r) : -INFINITY;
+        l[j][k] = have ? __ldcg(pp + rows * D + rows + r) : 0.f;
+        v[j][k] = have ? __ldcg(reinterpret_cast<const float4*>(pp + r * D) + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
 #pragma unroll
-    for (int k = 0; k < RU; ++k) {
-      float x = m[k];
+    for (int j = 0; j < U; ++j)
 #pragma unroll
-      for (int d = LPR / 2; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-      x = fmaxf(x, mn[k]);
-      const float old = attn_weight(mn[k], lt[k], x);
-      w[k] = attn_weight(m[k], l[k], x);
-      float sum = w[k] * l[k];
-#pragma unroll
-      for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-      lt[k] = lt[k] * old + sum;
-      acc[k].x *= old, acc[k].y *= old, acc[k].z *= old, acc[k].w *= old;
-      mn[k] = x;
-    }
-    const int n = c1 - cb + 1 < LPR ? c1 - cb + 1 : LPR;
-    constexpr int U = 4;
-    for (int i = 0; i < n; i += U) {
-      float4 v[U][RU];
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int k = 0; k < RU; ++k) {
-          v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int c = cb + i + j;
-          if (c <= c1 && i + j < n)
-            v[j][k] = __ldcg(reinterpret_cast<const float4*>(p.ws + ((int64_t)c * 2 + (c == c0)) * part +
-                                                             (r0 + k * RPW) * D + c4));
-        }
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int k = 0; k < RU; ++k) {
-          const float x = __shfl_sync(0xFFFFFFFFu, w[k], i + j < n ? i + j : 0, LPR);
-          if (i + j < n)
-            acc[k].x += x * v[j][k].x, acc[k].y += x * v[j][k].y, acc[k].z += x * v[j][k].z, acc[k].w += x * v[j][k].w;
-        }
-    }
+      for (int k = 0; k < RU; ++k) {
+        const float x = fmaxf(mn[k], m[j][k]);
+        const float a = attn_weight(mn[k], lt[k], x), w = attn_weight(m[j][k], l[j][k], x);
+        lt[k] = lt[k] * a + l[j][k] * w;
+        acc[k].x = acc[k].x * a + v[j][k].x * w;
+        acc[k].y = acc[k].y * a + v[j][k].y * w;
+        acc[k].z = acc[k].z * a + v[j][k].z * w;
+        acc[k].w = acc[k].w * a + v[j][k].w * w;
+        mn[k] = x;
+      }
   }
 #pragma unroll
-  for (int k = 0; k < RU; ++k)
-    if (r0 + k * RPW < left) attn_store4<BF16>(p, cur, cur.rt * rows + r0 + k * RPW, c4, acc[k], mn[k], lt[k]);
+  for (int k = 0; k < RU; ++k) {
+    s_acc[warp][k * RPW + row][sub] = acc[k];
+    if (sub == 0) {
+      s_m[warp][k * RPW + row] = mn[k];
+      s_l[warp][k * RPW + row] = lt[k];
+    }
+  }
+  __syncthreads();
+  // one thread a float4 of a row
+  const int rr = threadIdx.x / LPR;
+  static_assert(RPC * LPR == WARPS * 32, "a thread for each float4");
+  if (r0 + rr >= left) return;
+  float mx = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, s_m[w][rr]);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float x = attn_weight(s_m[w][rr], s_l[w][rr], mx);
+    const float4 v = s_acc[w][rr][sub];
+    l += s_l[w][rr] * x;
+    a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
+  }
+  attn_store4<BF16>(p, cur, cur.rt * rows + r0 + rr, sub * 4, a, mx, l);
 }
 
 template <bool BF16, int D>
 cudaError_t launch(const AttnParams& p, int tk, int rows, cudaStream_t st) {
-  constexpr int PER = WARPS * (128 / D) * RU;
+  constexpr int PER = 128 / D * RU;
   const int chunks = ((p.R < rows ? p.R : rows) + PER - 1) / PER;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hkv * p.RT * chunks));

@@ -41,7 +41,7 @@ struct Smem {
 };
 
 template <bool BF16, int D, int MT>
-__global__ void __launch_bounds__(WARPS * 32, 2) attn_mma_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255) attn_mma_kernel(const __grid_constant__ AttnParams p) {
   using Op = typename std::conditional<BF16, Bf16Op, F16Op>::type;
   using S = Smem<D, MT>;
   constexpr int ROWS = S::ROWS;
