@@ -12,8 +12,7 @@
 // behind the true maximum by up to 8 (P <= 256): O is rescaled, by the softmax
 // warps and through their registers, only when a row of the warp grows more.
 //   warps 0 .. 4 NQ - 1   softmax, rescaling, output (four warps a row tile)
-//   two warps             one thread each issues MMAs: NQ = 1, the Q K^T and the
-//                         P V products; NQ = 2, those of one row tile each
+//   two warps             issue the MMAs: one all Q K^T, the other all P V
 //   two warps             load K and V tiles, one ring each: tensor copies of whole
 //                         page parts; cp.async for an item's last tile, with the
 //                         tree's nodes from the caller's rows (and on to the
@@ -25,7 +24,8 @@
 // softmax.  With two, each tile of K and V serves 256 rows, and the products of
 // one row tile run under the softmax of the other.  The issue of an MMA blocks
 // until the one before it is nearly done, so that a barrier test between two
-// products leaves the tensor cores idle for its 130 cycles: hence two issuers.
+// products leaves the tensor cores idle for its 130 cycles, and a product whose
+// operands are ready waits behind one whose are not: hence two issuers.
 // S is computed SW cache rows at a time into two buffers, so that the next
 // Q K^T runs under the softmax of the last; SW is the whole tile for NQ = 1, and
 // half of it for NQ = 2, whose tensor memory (512 columns) would not hold two
@@ -60,8 +60,8 @@ struct Smem {
   static constexpr int V = K + KS * TILE;
   static constexpr int BAR = V + VS * TILE;
   // kfull[KS], kempty[KS], vfull[VS], vempty[VS], qfull, qempty, sfull[4],
-  // sfree[4], pfull[4], odone[2], oempty[2], drain
-  static constexpr int NBAR = 2 * (KS + VS) + 19;
+  // sfree[4], pfull[4], odone[2], olast[2], oempty[2], drain
+  static constexpr int NBAR = 2 * (KS + VS) + 21;
   static constexpr int BAD = BAR + NBAR * 8;        // nodes with non-finite V, by segment
   static constexpr int FLAG = BAD + BAD_BUFS * 8;   // [0] abort, [1] tensor memory
   static constexpr int BYTES = FLAG + 16;
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
   constexpr uint32_t COL_Q = 256;  // of the second row tile
   constexpr int MMA_WARP = NQ * 4, LOAD_WARP = MMA_WARP + 2;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = smem_u32(smem);
   const uint32_t b_kfull = base + S::BAR, b_kempty = b_kfull + S::KS * 8, b_vfull = b_kempty + S::KS * 8,
                  b_vempty = b_vfull + S::VS * 8, b_qfull = b_vempty + S::VS * 8, b_qempty = b_qfull + 8,
                  b_sfull = b_qempty + 8, b_sfree = b_sfull + 32, b_pfull = b_sfree + 32, b_odone = b_pfull + 32,
-                 b_oempty = b_odone + 16, b_drain = b_oempty + 16;  // sfull, sfree, pfull: [row tile][buffer]
+                 b_olast = b_odone + 16, b_oempty = b_olast + 16, b_drain = b_oempty + 16;  // sfull, sfree, pfull: [row tile][buffer]
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::FLAG);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + S::BAD);
 
@@ -136,14 +136,14 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
   if (tid == 0) {
     for (int i = 0; i < S::KS; ++i) {
       mbar_init(b_kfull + 8 * i, 1);
-      mbar_init(b_kempty + 8 * i, NQ);
+      mbar_init(b_kempty + 8 * i, 1);
     }
     for (int i = 0; i < S::VS; ++i) {
       mbar_init(b_vfull + 8 * i, 1);
-      mbar_init(b_vempty + 8 * i, NQ);
+      mbar_init(b_vempty + 8 * i, 1);
     }
     mbar_init(b_qfull, 2);
-    mbar_init(b_qempty, NQ);
+    mbar_init(b_qempty, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
       mbar_init(b_sfree + 8 * i, 1);
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_odone + 8 * i, 1);
+      mbar_init(b_olast + 8 * i, 1);
       mbar_init(b_oempty + 8 * i, 4);
     }
     mbar_init(b_drain, 2);
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = (uint32_t)s_flag[1];
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
 
   const uint64_t lim = p.wait_limit_ns;
   auto fail = [&](int code) {
@@ -317,73 +318,77 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
     }
   } else if (warp >= MMA_WARP) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      const int who = warp - MMA_WARP;
-      const int q = NQ == 1 ? 0 : who;  // row tile
+    // The warp stays together and one elected lane issues: operands then live in
+    // uniform registers, and an MMA costs 48 to 64 cycles to issue, what it
+    // takes to run; from a branch on the lane it was 63 alone and above 130
+    // beside two softmax warps.
+    {
+      uint32_t leader;
+      asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+      const int who = warp - MMA_WARP;  // 0: Q K^T, 1: P V
       bool ok = s_flag[0] == 0;
       auto need = [&](uint32_t bar, int phase) {
-        if (ok && !wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag)) {
-          fail(DEV_ERR_TIMEOUT_FULL);
+        if (ok && !__all_sync(0xFFFFFFFFu, wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag))) {
+          if (leader) fail(DEV_ERR_TIMEOUT_FULL);
           ok = false;
         }
         return ok;
       };
-      const uint32_t t_q = tmem + q * COL_Q;
-      int ks = 0, kr = 0, vs = 0, vr = 0;  // slot and round of the next tile of K, of V
-      // Q K^T of the CTA's n-th step, step `sub` of its tile; `last` of its segment.
-      auto qk = [&](int n, int sub, bool last) {
-        const int buf = 2 * q + (n & 1);
-        if (sub == 0 && !need(b_kfull + 8 * ks, kr)) return;
-        // its S held P of two steps ago until that product was done
-        if (n >= 2 && !need(b_sfree + 8 * buf, (n >> 1) - 1)) return;
-        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + ks * S::TILE + sub * SW * 128);
-        const uint32_t d = t_q + (n & 1) * SW;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (uint32_t)(kk >> 2) * (S::HALF >> 4) + (uint32_t)(kk & 3) * (32 >> 4);
-          mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
-        }
-        tc_commit(b_sfull + 8 * buf);
-        if (sub == SUB - 1) {
-          tc_commit(b_kempty + 8 * ks);
-          if (++ks == S::KS) ks = 0, ++kr;
-        }
-        if (last) tc_commit(b_qempty);
-      };
-      // P V of the n-th step; the first of segment `seg` or not.
-      auto pv = [&](int n, int sub, bool first, int seg) {
-        const int buf = 2 * q + (n & 1);
-        if (sub == 0 && !need(b_vfull + 8 * vs, vr)) return;
-        if (!need(b_pfull + 8 * buf, n >> 1)) return;
-        if (first && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) return;
-        const uint32_t a = t_q + (n & 1) * SW, d = t_q + COL_O;
-        const uint32_t b = desc_lo_mn(base + S::V + vs * S::TILE + sub * SW * 128, S::HALF);
-        tc_fence_after();
-        mma_ts(d, a, b, IDESC_O, !first);
-#pragma unroll
-        for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
-        tc_commit(b_odone + 8 * q);
-        tc_commit(b_sfree + 8 * buf);
-        if (sub == SUB - 1) {
-          tc_commit(b_vempty + 8 * vs);
-          if (++vs == S::VS) vs = 0, ++vr;
-        }
-      };
-      int n = 0, seg = 0;  // n: parities only
+      int n = 0, seg = 0;          // steps and segments so far (n: parities only)
+      int slot = 0, round = 0;     // of the tile of K or V
       for (int64_t u = u0; u < u1 && ok; ++seg) {
         const int count = segment(u), steps = count * SUB;
-        if ((NQ == 2 || who == 0) && !need(b_qfull, seg)) break;
-        if (NQ == 2) qk(n, 0, steps == 1);
-        for (int j = 0; j < steps && ok; ++j, ++n) {
-          if constexpr (NQ == 1) {
-            if (who == 0)
-              qk(n, 0, j + 1 == steps);
-            else
-              pv(n, 0, j == 0, seg);
-          } else {
-            if (j + 1 < steps) qk(n + 1, (j + 1) % SUB, j + 2 == steps);
-            if (ok) pv(n, j % SUB, j == 0, seg);
+        if (who == 0) {
+          if (!need(b_qfull, seg)) break;
+          for (int j = 0; j < steps && ok; ++j, ++n) {
+            const int sub = j % SUB;
+            if (sub == 0 && !need(b_kfull + 8 * slot, round)) break;
+            const uint32_t b = desc_lo(base + S::K + slot * S::TILE + sub * SW * 128);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const int buf = 2 * q + (n & 1);
+              // its S held P of two steps ago until that product was done
+              if (n >= 2 && !need(b_sfree + 8 * buf, (n >> 1) - 1)) break;
+              const uint32_t a = desc_lo(base + S::Q + q * S::TILE), d = tmem + q * COL_Q + (n & 1) * SW;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t o = (uint32_t)(kk >> 2) * (S::HALF >> 4) + (uint32_t)(kk & 3) * (32 >> 4);
+                  mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
+                }
+                tc_commit(b_sfull + 8 * buf);
+              }
+            }
+            if (!ok) break;
+            if (leader && sub == SUB - 1) tc_commit(b_kempty + 8 * slot);
+            if (leader && j + 1 == steps) tc_commit(b_qempty);
+            if (sub == SUB - 1 && ++slot == S::KS) slot = 0, ++round;
+          }
+        } else {
+          for (int j = 0; j < steps && ok; ++j, ++n) {
+            const int sub = j % SUB;
+            if (sub == 0 && !need(b_vfull + 8 * slot, round)) break;
+            const uint32_t b = desc_lo_mn(base + S::V + slot * S::TILE + sub * SW * 128, S::HALF);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const int buf = 2 * q + (n & 1);
+              if (!need(b_pfull + 8 * buf, n >> 1)) break;
+              if (j == 0 && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) break;
+              const uint32_t a = tmem + q * COL_Q + (n & 1) * SW, d = tmem + q * COL_Q + COL_O;
+              tc_fence_after();
+              if (leader) {
+                mma_ts(d, a, b, IDESC_O, j > 0);
+#pragma unroll
+                for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
+                tc_commit(b_odone + 8 * q);
+                tc_commit(b_sfree + 8 * buf);
+                if (j + 1 == steps) tc_commit(b_olast + 8 * q);
+              }
+            }
+            if (!ok) break;
+            if (leader && sub == SUB - 1) tc_commit(b_vempty + 8 * slot);
+            if (sub == SUB - 1 && ++slot == S::VS) slot = 0, ++round;
           }
         }
         cur.tile += count - 1;
@@ -391,8 +396,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         u += count;
       }
       // all MMAs of the CTA have ended before tensor memory is given back
-      tc_commit(b_drain);
-      if (!mbar_wait_bounded(b_drain, 0, 1000000000ull)) atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
+      if (leader) {
+        tc_commit(b_drain);
+        if (!mbar_wait_bounded(b_drain, 0, 1000000000ull)) atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -457,6 +464,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
           m = mn;
           l *= a;
           if (j > 0) {
+            // a parity tells a phase from the next one only: the product before
+            // the last was done when this S was computed
             if (!need(b_odone + 8 * q, n - 1)) continue;
             tc_fence_after();
 #pragma unroll
@@ -488,16 +497,13 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
-        // Every product is waited for in turn, before the one that follows it can
-        // start: a parity tells one phase of a barrier from the next, no more.
-        if (n > 0 && !need(b_odone + 8 * q, n - 1)) continue;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_pfull + 8 * buf);
       }
 
       // ------------------------------------------------ end of the segment
-      need(b_odone + 8 * q, done + steps - 1);
+      need(b_olast + 8 * q, seg);
       tc_fence_after();
       const int64_t item_u = u - cur.tile;  // the item's first unit
       const bool last_tile = cur.tile + count == cur.ntiles;
