@@ -30,7 +30,7 @@ cudaError_t prepare_attn_mma(bool bf16, int D);
 cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st);
 
 // tcgen05 kernel (more rows than the mma.sync kernel's tile holds), one CTA per
-// SM; kmap, vmap: host_pool_map with boxes of min(page_size, 128) rows.
+// SM; kmap, vmap: host_pool_map with boxes of 16 rows.
 int attn_tc_tile_rows(int R);
 int attn_tc_tile_cache_rows();
 cudaError_t prepare_attn_tc(bool bf16, int D);

@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const __grid_cons
   constexpr int RPC = RPW * RU;               // rows of the CTA
   __shared__ float4 s_acc[WARPS][RPC][LPR];
   __shared__ float s_m[WARPS][RPC], s_l[WARPS][RPC];
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
   AttnCursor cur{};

@@ -52,7 +52,10 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, gt = lane & 3;
 
-  pdl_trigger();  // the joining kernel may take its place and wait
+  // What the call reads is there, and the last call's partials were read; only
+  // then may the joining kernel, which reads the lengths, take its place.
+  pdl_wait();
+  pdl_trigger();
   int64_t u0, u1;
   AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, u0, u1);
   if (u0 >= u1) return;
@@ -436,8 +439,17 @@ cudaError_t prepare() {
 
 template <bool BF16, int D, int MT>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
-  attn_mma_kernel<BF16, D, MT><<<(unsigned)p.grid, WARPS * 32, Smem<D, MT>::BYTES, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.grid);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = Smem<D, MT>::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_mma_kernel<BF16, D, MT>, p);
 }
 
 }  // namespace

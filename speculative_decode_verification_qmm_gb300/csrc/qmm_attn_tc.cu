@@ -13,10 +13,10 @@
 // warps and through their registers, only when a row of the warp grows more.
 //   warps 0 .. 4 NQ - 1   softmax, rescaling, output (four warps a row tile)
 //   two warps             issue the MMAs: one all Q K^T, the other all P V
-//   two warps             load K and V tiles, one ring each: tensor copies of whole
-//                         page parts; cp.async for an item's last tile, with the
-//                         tree's nodes from the caller's rows (and on to the
-//                         cache); Q, once a segment, by both
+//   two warps             load K and V tiles, one ring each: tensor copies of 16
+//                         rows, which lie in one page; cp.async for the tree's
+//                         nodes, from the caller's rows (and on to the cache), and
+//                         the rows around them; Q, once a segment, by both
 // Why this split.  At 128 rows a tile of K and V (64 KB) takes 1.5 us of an
 // SM's share of the HBM stream, and its two products 0.55 us of the tensor cores
 // and its 16,384 exponentials about as long: with one row tile the stream is the
@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::FLAG);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + S::BAD);
 
-  pdl_trigger();  // the joining kernel may take its place and wait
   if (tid == 0) {
     for (int i = 0; i < S::KS; ++i) {
       mbar_init(b_kfull + 8 * i, 1);
@@ -164,6 +163,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
     fence_mbar_init();
   }
   if (warp == MMA_WARP) tmem_alloc(base + S::FLAG + 4, 512);
+  // What the call reads is there, and the last call's partials were read; only
+  // then may the joining kernel, which reads the lengths, take its place.
+  pdl_wait();
+  pdl_trigger();
   int64_t u0, u1;
   AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, u0, u1);
   tc_fence_before();
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
     const CUtensorMap* map = is_v ? &vmap : &kmap;
     uint16_t* pool = is_v ? p.v_pool : p.k_pool;
     const int64_t head = (int64_t)D << p.page_shift;
-    const int box = p.page_shift < 7 ? 1 << p.page_shift : TK;  // rows of one tensor copy
+    constexpr int BLOCKS = TK / 16;  // 16 rows, one tensor copy a half
     bool ok = s_flag[0] == 0;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       ok = __all_sync(0xFFFFFFFFu, ok && wait_or_abort(bar, parity, lim, s_flag));
@@ -205,32 +208,34 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto page_of = [&](int j) {  // a valid page for row j, whatever the table says
-      int pid = __ldg(p.table + cur.b * p.ld_table + (j >> p.page_shift));
-      if (pid < 0 || pid >= p.n_pages) {
-        atomicOr(p.status, DEV_ERR_INDEX);
-        pid = -1;
-      }
-      return pid;
-    };
     int slot = 0, round = 0, seg = 0;
     for (int64_t u = u0; u < u1 && ok; ++seg) {
       const int count = segment(u);
-      // Q: both warps, in turn rows of 32
+      // Q, by both warps; rows past the item's stay as they are, and so do their results
       if (seg > 0) wait(b_qempty, (uint32_t)((seg - 1) & 1));
       if (!ok) break;
-      for (int id = (warp - LOAD_WARP) * 32 + lane; id < ROWS * CH; id += 64) {
+      const int rows = p.R - cur.rt * ROWS < ROWS ? p.R - cur.rt * ROWS : ROWS;
+      for (int id = (warp - LOAD_WARP) * 32 + lane; id < rows * CH; id += 64) {
         const int row = id / CH, ch = id % CH;  // row of all NQ tiles
         const int r = cur.rt * ROWS + row, t = r / p.g, h = r - t * p.g;
         const uint16_t* src = p.q + cur.b * p.q_sb + t * p.q_st + (int64_t)(cur.h * p.g + h) * p.q_sh + ch * 8;
         cp_async16(base + S::Q + (row >> 7) * S::TILE + (ch >> 3) * S::HALF + (row & 127) * 128 +
                        (((ch & 7) ^ (row & 7)) << 4),
-                   r < p.R ? src : p.q, r < p.R ? 16 : 0);
+                   src, 16);
       }
-      int ahead = -1;  // this lane's page of the next tile
+      // Lane i < BLOCKS looks up the page of the tile's block i, a tile ahead.  An
+      // id out of range is reported; rows of page 0 take its place, unwritten.
+      int ahead = 0;
       auto lookup = [&](int j) {
-        const int row = j * TK + lane * box;
-        ahead = lane * box < TK && j * TK + TK <= cur.L ? page_of(row) : -1;
+        const int jb = j * TK + lane * 16;
+        ahead = 0;
+        if (lane < BLOCKS && jb < cur.L + cur.n) {
+          ahead = __ldg(p.table + cur.b * p.ld_table + (jb >> p.page_shift));
+          if (ahead < 0 || ahead >= p.n_pages) {
+            atomicOr(p.status, DEV_ERR_INDEX);
+            ahead = -1;
+          }
+        }
       };
       lookup(cur.tile);
       hand_on(b_qfull);
@@ -241,26 +246,32 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         if (round > 0) wait(empty + 8 * slot, (uint32_t)((round - 1) & 1));
         if (!ok) break;
         const uint32_t bar = full + 8 * slot, dst = ring + slot * S::TILE;
-        if (j0 + TK <= cur.L) {
-          // a page id out of range is reported; rows of page 0 take its place
-          if (lane == 0) mbar_arrive_expect_tx(bar, S::TILE);
-          __syncwarp();
-          if (lane * box < TK) {
-            const int64_t row = p.row0 + (((int64_t)(pid < 0 ? 0 : pid) * p.Hkv + cur.h) << p.page_shift) +
-                                ((j0 + lane * box) & ((1 << p.page_shift) - 1));
+        // blocks that hold cached rows only
+        int whole = cur.L > j0 ? (cur.L - j0) / 16 : 0;
+        whole = whole < BLOCKS ? whole : BLOCKS;
+        if (lane == 0) {
+          if (whole == BLOCKS)
+            mbar_arrive_expect_tx(bar, S::TILE);
+          else if (whole > 0)
+            mbar_expect_tx(bar, whole * 16 * D * 2);
+        }
+        __syncwarp();
+        if (lane < whole) {
+          const int64_t row = p.row0 + (((int64_t)(pid < 0 ? 0 : pid) * p.Hkv + cur.h) << p.page_shift) +
+                              ((j0 + lane * 16) & ((1 << p.page_shift) - 1));
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half)
-              tma_load_2d(dst + half * S::HALF + lane * box * 128, map, half * 64, (int)row, bar);
-          }
-        } else {
+          for (int half = 0; half < D / 64; ++half)
+            tma_load_2d(dst + half * S::HALF + lane * 2048, map, half * 64, (int)row, bar);
+        }
+        if (whole < BLOCKS) {
           const uint16_t* fresh = is_v ? p.vn + cur.b * p.v_sb + cur.h * p.v_sh : p.kn + cur.b * p.k_sb + cur.h * p.k_sh;
           const int64_t fresh_st = is_v ? p.v_st : p.k_st;
+          const int end = cur.L + cur.n - j0;  // rows of the tile that exist
 #pragma unroll 1
-          for (int blk = 0; blk < TK / 16; ++blk) {
-            const int jb = j0 + blk * 16;
-            const int id0 = jb < cur.L ? page_of(jb) : -1;
+          for (int blk = whole; blk < BLOCKS; ++blk) {
+            const int id0 = __shfl_sync(0xFFFFFFFFu, pid, blk);
             const uint16_t* from = pool + (id0 < 0 ? 0 : id0) * p.page_stride + cur.h * head +
-                                   (int64_t)(jb & ((1 << p.page_shift) - 1)) * D;
+                                   (int64_t)((j0 + blk * 16) & ((1 << p.page_shift) - 1)) * D;
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
               const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
@@ -275,13 +286,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
           cp_async_wait<0>();
           // Nodes: on to the cache, and non-finite V out of the product.  A
           // lane reads back the chunks that it requested.
-          const int first_blk = cur.L > j0 ? (cur.L - j0) / 16 : 0;
-          const int end = cur.L + cur.n - j0;
-          for (int blk = first_blk; blk < TK / 16 && blk * 16 < end; ++blk) {
-            const int jb = j0 + blk * 16;
-            const int id0 = cur.rt == 0 ? page_of(jb) : -1;
+          for (int blk = whole; blk < BLOCKS && blk * 16 < end; ++blk) {
+            const int id0 = __shfl_sync(0xFFFFFFFFu, pid, blk);
             uint16_t* to = pool + (id0 < 0 ? 0 : id0) * p.page_stride + cur.h * head +
-                           (int64_t)(jb & ((1 << p.page_shift) - 1)) * D;
+                           (int64_t)((j0 + blk * 16) & ((1 << p.page_shift) - 1)) * D;
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
               const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
               if (t < 0 || t >= cur.n) continue;
               const uint32_t so = dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
               uint4 v = lds128(so);
-              if (id0 >= 0) *reinterpret_cast<uint4*>(to + id * 8) = v;
+              if (id0 >= 0 && cur.rt == 0) *reinterpret_cast<uint4*>(to + id * 8) = v;
               if (is_v && any_nonfinite<BF16>(v)) {
                 v.x = zero_nonfinite<BF16>(v.x);
                 v.y = zero_nonfinite<BF16>(v.y);
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
     for (int64_t u = u0; u < u1; ++seg) {
       const int count = segment(u);
       const int r = cur.rt * ROWS + q * 128 + row;
-      const bool in = r < p.R;
+      const bool in = r < p.R, idle = r - lane >= p.R;
       const uint64_t bits = in ? attn_bits(p, cur.b, cur.n, r) : 0;
       float m = -INFINITY, l = 0.f;
       const int steps = count * SUB;
@@ -431,6 +439,10 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         const int buf = 2 * q + (n & 1);
         const uint32_t t_s = tl + (n & 1) * SW;
         if (!need(b_sfull + 8 * buf, n >> 1)) continue;
+        if (idle) {  // no row of the warp is the item's: whatever P is, nobody looks
+          if (lane == 0) mbar_arrive(b_pfull + 8 * buf);
+          continue;
+        }
         tc_fence_after();
         const int t0 = cur.tile * TK + j * SW - cur.L;  // node of the step's first row, if it is one
         const bool edge = t0 + SW > 0;
@@ -458,7 +470,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
           mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
         mx *= p.scale_log2;
-        if (__any_sync(0xFFFFFFFFu, mx > m + 8.f)) {
+        // (rows past the item's hold anything and must not decide for the others)
+        if (__any_sync(0xFFFFFFFFu, in && mx > m + 8.f)) {
           const float mn = fmaxf(m, mx);
           const float a = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;
@@ -593,9 +606,18 @@ cudaError_t prepare() {
 
 template <bool BF16, int D, int NQ>
 cudaError_t launch(const AttnParams& p, const void* kmap, const void* vmap, cudaStream_t st) {
-  attn_tc_kernel<BF16, D, NQ><<<(unsigned)p.grid, NQ * 128 + 128, Smem<D, NQ>::BYTES, st>>>(
-      p, *static_cast<const CUtensorMap*>(kmap), *static_cast<const CUtensorMap*>(vmap));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.grid);
+  cfg.blockDim = dim3(NQ * 128 + 128);
+  cfg.dynamicSmemBytes = Smem<D, NQ>::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<BF16, D, NQ>, p, *static_cast<const CUtensorMap*>(kmap),
+                            *static_cast<const CUtensorMap*>(vmap));
 }
 
 }  // namespace

@@ -233,10 +233,9 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   const size_t ws_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
   if (e == cudaSuccess) e = prepare_attn_tc(d->dtype == QMM_DT_BF16, d->head_dim);
-  const int box = d->page_size < attn_tc_tile_cache_rows() ? d->page_size : attn_tc_tile_cache_rows();
   const bool f16 = d->dtype == QMM_DT_F16;
-  if (e == cudaSuccess) e = host_pool_map(&h->kmap, d->k_pool, pool_rows, d->head_dim, box, f16);
-  if (e == cudaSuccess) e = host_pool_map(&h->vmap, d->v_pool, pool_rows, d->head_dim, box, f16);
+  if (e == cudaSuccess) e = host_pool_map(&h->kmap, d->k_pool, pool_rows, d->head_dim, 16, f16);
+  if (e == cudaSuccess) e = host_pool_map(&h->vmap, d->v_pool, pool_rows, d->head_dim, 16, f16);
   void* ptr = nullptr;
   if (e == cudaSuccess && (e = host_dev_alloc(&ptr, ws_bytes)) == cudaSuccess)
     h->ws = static_cast<float*>(ptr);
