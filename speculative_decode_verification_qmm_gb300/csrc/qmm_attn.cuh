@@ -270,4 +270,13 @@ __device__ __forceinline__ void attn_store4(const AttnParams& p, const AttnCurso
         live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
+// Which of the 32 cache rows from node t on (cached rows where t < 0) a row with
+// node bits `bits` sees.
+__device__ __forceinline__ uint32_t attn_seen32(uint64_t bits, int t) {
+  if (t >= 64) return 0u;
+  if (t >= 0) return (uint32_t)(bits >> t);
+  if (t <= -32) return ~0u;
+  return (uint32_t)(bits << -t) | ((1u << -t) - 1);
+}
+
 }  // namespace qmm

@@ -228,13 +228,14 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t see = attn_seen32(bits[mt][half], j0 + gt * 2 - cur.L);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = j0 + nt * 8 + gt * 2 + (e & 1) - cur.L;
-            const bool see = t < 0 || (t < 64 && ((bits[mt][e >> 1] >> t) & 1));
-            if (!see) s[mt][nt][e] = -INFINITY;
-          }
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!(see >> (nt * 8 + e) & 1)) s[mt][nt][2 * half + e] = -INFINITY;
+        }
     }
 
     // running softmax

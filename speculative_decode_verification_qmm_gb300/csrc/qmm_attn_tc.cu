@@ -215,13 +215,20 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
       if (seg > 0) wait(b_qempty, (uint32_t)((seg - 1) & 1));
       if (!ok) break;
       const int rows = p.R - cur.rt * ROWS < ROWS ? p.R - cur.rt * ROWS : ROWS;
-      for (int id = (warp - LOAD_WARP) * 32 + lane; id < rows * CH; id += 64) {
-        const int row = id / CH, ch = id % CH;  // row of all NQ tiles
-        const int r = cur.rt * ROWS + row, t = r / p.g, h = r - t * p.g;
-        const uint16_t* src = p.q + cur.b * p.q_sb + t * p.q_st + (int64_t)(cur.h * p.g + h) * p.q_sh + ch * 8;
-        cp_async16(base + S::Q + (row >> 7) * S::TILE + (ch >> 3) * S::HALF + (row & 127) * 128 +
-                       (((ch & 7) ^ (row & 7)) << 4),
-                   src, 16);
+      {
+        constexpr int STEP = 64 / CH;  // rows of both warps at a time
+        const int id = (warp - LOAD_WARP) * 32 + lane, ch = id % CH;
+        const int dt = STEP / p.g, dh = STEP % p.g;
+        int row = id / CH, t = (cur.rt * ROWS + row) / p.g, h = (cur.rt * ROWS + row) % p.g;
+        const uint16_t* src = p.q + cur.b * p.q_sb + (int64_t)cur.h * p.g * p.q_sh + ch * 8;
+#pragma unroll 4
+        for (; row < rows; row += STEP) {
+          cp_async16(base + S::Q + (row >> 7) * S::TILE + (ch >> 3) * S::HALF + (row & 127) * 128 +
+                         (((ch & 7) ^ (row & 7)) << 4),
+                     src + t * p.q_st + h * p.q_sh, 16);
+          t += dt, h += dh;
+          if (h >= p.g) h -= p.g, ++t;
+        }
       }
       // Lane i < BLOCKS looks up the page of the tile's block i, a tile ahead.  An
       // id out of range is reported; rows of page 0 take its place, unwritten.
@@ -290,20 +297,23 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
             const int id0 = __shfl_sync(0xFFFFFFFFu, pid, blk);
             uint16_t* to = pool + (id0 < 0 ? 0 : id0) * p.page_stride + cur.h * head +
                            (int64_t)((j0 + blk * 16) & ((1 << p.page_shift) - 1)) * D;
+            uint4 v[CH / 2];
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
+              v[i] = lds128(dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            }
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
               const int id = i * 32 + lane, row = blk * 16 + id / CH, ch = id % CH;
               const int t = j0 + row - cur.L;
               if (t < 0 || t >= cur.n) continue;
-              const uint32_t so = dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-              uint4 v = lds128(so);
-              if (id0 >= 0 && cur.rt == 0) *reinterpret_cast<uint4*>(to + id * 8) = v;
-              if (is_v && any_nonfinite<BF16>(v)) {
-                v.x = zero_nonfinite<BF16>(v.x);
-                v.y = zero_nonfinite<BF16>(v.y);
-                v.z = zero_nonfinite<BF16>(v.z);
-                v.w = zero_nonfinite<BF16>(v.w);
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(so), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+              if (id0 >= 0 && cur.rt == 0) *reinterpret_cast<uint4*>(to + id * 8) = v[i];
+              if (is_v && any_nonfinite<BF16>(v[i])) {
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                 dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                             "r"(zero_nonfinite<BF16>(v[i].x)), "r"(zero_nonfinite<BF16>(v[i].y)),
+                             "r"(zero_nonfinite<BF16>(v[i].z)), "r"(zero_nonfinite<BF16>(v[i].w))
                              : "memory");
                 atomicOr(s_bad + (seg & (BAD_BUFS - 1)), 1ull << t);
               }
@@ -452,12 +462,12 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         tmem_wait_ld();
         if (edge) {
 #pragma unroll
-          for (int c = 0; c < SW / 32; ++c)
+          for (int c = 0; c < SW / 32; ++c) {
+            const uint32_t see = attn_seen32(bits, t0 + c * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int t = t0 + c * 32 + i;
-              if (t >= 0 && (t >= 64 || !(bits >> t & 1))) v[c][i] = 0xFF800000u;  // -inf
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!(see >> i & 1)) v[c][i] = 0xFF800000u;  // -inf
+          }
         }
         float mx;
         {
