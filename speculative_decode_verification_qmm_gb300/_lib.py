@@ -155,10 +155,10 @@ SIGNATURES = {
     "qmm_cache_create": (_INT, [ctypes.POINTER(_P), ctypes.POINTER(qmm_cache_desc), _P]),
     "qmm_cache_destroy": (_INT, [_P]),
     "qmm_cache_sync_status": (_INT, [_P, _P]),
-    "qmm_tree_attention": (_INT, [_P, ctypes.POINTER(qmm_attn_args), _P]),
+    "qmm_tree_attention": (_INT, [_P, _P, _P]),
     "qmm_cache_commit": (_INT, [_P, _INT, _INT, _P, _I64, _INT, _P, _P, _I64, _P, _P, _P]),
     "qmm_cache_copy": (_INT, [_P, _INT, _P, _P, _P, _P]),
-    "qmm_verify_sample": (_INT, [ctypes.POINTER(qmm_sample_args), _P]),
+    "qmm_verify_sample": (_INT, [_P, _P]),
     "qmm_verify_sample_workspace": (_INT, [_INT, _INT, _I64, ctypes.POINTER(_I64)]),
     "qmm_sync_status": (_INT, [_P, _P]),
     "qmm_last_cuda_error": (_INT, [_P]),

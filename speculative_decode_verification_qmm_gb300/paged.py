@@ -18,15 +18,30 @@ which page, and how many sequences share one.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_attn_args,
                    qmm_cache_desc, qmm_sample_args)
 
 
-def _stream_ptr(stream=None) -> int:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+# The argument structs of the C calls, packed in one go: filling a ctypes
+# structure field by field costs more than a small kernel.
+_ATTN = struct.Struct("@IiiiPPPP12qPPqifPPPq")
+_SAMPLE = struct.Struct("@IIiiqPqqPqqPPPPPPPPPq")
+assert _ATTN.size == ctypes.sizeof(qmm_attn_args) and _SAMPLE.size == ctypes.sizeof(qmm_sample_args)
+_raw_stream = None
+_CODES = {}
+
+
+def _stream_ptr(stream, device_index) -> int:
+    """The address of `stream`, or of the device's current stream."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(device_index)
 
 
 def _check(func: str, rc: int):
@@ -35,32 +50,37 @@ def _check(func: str, rc: int):
 
 
 def _dtype(dtype):
-    import torch
-    codes = {torch.bfloat16: QMM_DT_BF16, torch.float16: QMM_DT_F16, torch.float32: QMM_DT_F32}
-    if dtype not in codes:
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: QMM_DT_BF16, torch.float16: QMM_DT_F16, torch.float32: QMM_DT_F32})
+    if dtype not in _CODES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, not {dtype}")
-    return codes[dtype]
+    return _CODES[dtype]
 
 
-def _cuda(name, t, dtype, shape):
-    """The tensor's address after a check of its device, type and shape (None: any size)."""
+def _refuse(name, t, dtype, shape):
     if not t.is_cuda or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}, not {t.dtype} on {t.device}")
-    if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
-                         f"not {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
 
 
-def _rows(name, t):
-    """Tensors whose last dimension has to be contiguous."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+def _need(name, t, dtype, shape):
+    """Refuses a tensor that is not on the GPU, or of another type or shape."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _refuse(name, t, dtype, shape)
 
 
 def _flat(name, t):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(name, t):
+    """Tensors whose last dimension has to be contiguous; the strides."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return st
 
 
 # ------------------------------------------------------------------ raw C names
@@ -70,7 +90,8 @@ def qmm_cache_create(dtype, n_layers, n_pages, page_size, n_q_heads, n_kv_heads,
     d = qmm_cache_desc(ctypes.sizeof(qmm_cache_desc), dtype, n_layers, page_size, n_q_heads, n_kv_heads, head_dim,
                        max_batch, n_pages, k_pool.data_ptr(), v_pool.data_ptr())
     h = ctypes.c_void_p()
-    _check("qmm_cache_create", load().qmm_cache_create(ctypes.byref(h), ctypes.byref(d), _stream_ptr(stream)))
+    _check("qmm_cache_create", load().qmm_cache_create(ctypes.byref(h), ctypes.byref(d),
+                                                       _stream_ptr(stream, k_pool.device.index)))
     return h.value
 
 
@@ -79,7 +100,8 @@ def qmm_cache_destroy(h) -> None:
 
 
 def qmm_cache_sync_status(h, stream=None) -> int:
-    return load().qmm_cache_sync_status(h, _stream_ptr(stream))
+    import torch
+    return load().qmm_cache_sync_status(h, _stream_ptr(stream, torch.cuda.current_device()))
 
 
 def qmm_tree_attention(h, layer, q, k_new, v_new, page_table, lens, out, lse=None, mask=None, n_tokens=None,
@@ -87,20 +109,17 @@ def qmm_tree_attention(h, layer, q, k_new, v_new, page_table, lens, out, lse=Non
     """q, out CUDA [B, T, Hq, D]; k_new, v_new [B, T, Hkv, D]; page_table int32
     [B, pages]; lens, n_tokens int32 [B]; mask int64 [B, T]; lse fp32 [B, T, Hq]
     or None; asynchronous."""
-    B, T, Hq, D = q.shape
-    a = qmm_attn_args()
-    a.struct_size = ctypes.sizeof(qmm_attn_args)
-    a.layer, a.B, a.T = layer, B, T
-    a.q, a.k_new, a.v_new, a.out = q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr()
-    a.q_stride[:], a.k_stride[:] = q.stride()[:3], k_new.stride()[:3]
-    a.v_stride[:], a.out_stride[:] = v_new.stride()[:3], out.stride()[:3]
-    a.lse = lse.data_ptr() if lse is not None else None
-    a.page_table, a.ld_table, a.table_width = page_table.data_ptr(), page_table.stride(0), page_table.shape[1]
-    a.scale = D ** -0.5 if scale is None else scale
-    a.lens = lens.data_ptr()
-    a.n_tokens = n_tokens.data_ptr() if n_tokens is not None else None
-    a.mask, a.ld_mask = (mask.data_ptr(), mask.stride(0)) if mask is not None else (None, 0)
-    _check("qmm_tree_attention", load().qmm_tree_attention(h, ctypes.byref(a), _stream_ptr(stream)))
+    B, T, _, D = q.shape
+    qs, ks, vs, os = q.stride(), k_new.stride(), v_new.stride(), out.stride()
+    args = _ATTN.pack(
+        _ATTN.size, layer, B, T, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(),
+        qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0], os[1], os[2],
+        0 if lse is None else lse.data_ptr(), page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+        D ** -0.5 if scale is None else scale, lens.data_ptr(), 0 if n_tokens is None else n_tokens.data_ptr(),
+        0 if mask is None else mask.data_ptr(), 0 if mask is None else mask.stride(0))
+    rc = load().qmm_tree_attention(h, args, _stream_ptr(stream, q.device.index))
+    if rc:
+        _check("qmm_tree_attention", rc)
 
 
 def qmm_cache_commit(h, page_table, lens, path, accept, lens_out, stream=None) -> None:
@@ -108,14 +127,14 @@ def qmm_cache_commit(h, page_table, lens, path, accept, lens_out, stream=None) -
     B, T = path.shape
     _check("qmm_cache_commit", load().qmm_cache_commit(
         h, B, T, page_table.data_ptr(), page_table.stride(0), page_table.shape[1], lens.data_ptr(), path.data_ptr(),
-        path.stride(0), accept.data_ptr(), lens_out.data_ptr(), _stream_ptr(stream)))
+        path.stride(0), accept.data_ptr(), lens_out.data_ptr(), _stream_ptr(stream, lens.device.index)))
 
 
 def qmm_cache_copy(h, src, dst, rows=None, stream=None) -> None:
     """Copies pages src[i] to dst[i] (int32), their first rows[i] rows; asynchronous."""
     _check("qmm_cache_copy", load().qmm_cache_copy(
         h, src.numel(), src.data_ptr(), dst.data_ptr(), rows.data_ptr() if rows is not None else None,
-        _stream_ptr(stream)))
+        _stream_ptr(stream, src.device.index)))
 
 
 def qmm_debug_set_cache_wait_limit(h, ns: int) -> None:
@@ -134,17 +153,16 @@ def qmm_verify_sample(target, draft, tokens, u, noise, accept, path, workspace, 
     """target [B, T, V] and draft [B, T or T - 1, V] (or None) fp32, bf16 or f16;
     the other arguments as in qmm_sample_args; asynchronous."""
     B, T, V = target.shape
-    a = qmm_sample_args()
-    a.struct_size = ctypes.sizeof(qmm_sample_args)
-    a.dtype, a.B, a.T, a.V = _dtype(target.dtype), B, T, V
-    a.target, a.target_stride[:] = target.data_ptr(), target.stride()[:2]
-    if draft is not None:
-        a.draft, a.draft_stride[:] = draft.data_ptr(), draft.stride()[:2]
-    opt = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    a.tokens, a.parents, a.n_tokens, a.temperature = tokens.data_ptr(), opt(parents), opt(n_tokens), opt(temperature)
-    a.u, a.noise, a.accept, a.path = u.data_ptr(), noise.data_ptr(), accept.data_ptr(), path.data_ptr()
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check("qmm_verify_sample", load().qmm_verify_sample(ctypes.byref(a), _stream_ptr(stream)))
+    ts = target.stride()
+    ds = (0, 0) if draft is None else draft.stride()
+    opt = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    args = _SAMPLE.pack(
+        _SAMPLE.size, _dtype(target.dtype), B, T, V, target.data_ptr(), ts[0], ts[1], opt(draft), ds[0], ds[1],
+        tokens.data_ptr(), opt(parents), opt(n_tokens), u.data_ptr(), noise.data_ptr(), opt(temperature),
+        accept.data_ptr(), path.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    rc = load().qmm_verify_sample(args, _stream_ptr(stream, target.device.index))
+    if rc:
+        _check("qmm_verify_sample", rc)
 
 
 # ------------------------------------------------------------------ convenience
@@ -153,28 +171,29 @@ def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=Non
     qmm_verify_sample.  accept[:, 0] nodes are accepted, path[b, :accept[b, 0]]
     names them, accept[:, 1] is the token that follows them."""
     import torch
+    import torch
     if target.dim() != 3 or not target.is_cuda:
         raise ValueError("target must be a CUDA tensor [B, T, V]")
     B, T, V = target.shape
-    _dtype(target.dtype)
     _rows("target", target)
     if draft is not None:
-        _cuda("draft", draft, target.dtype, (B, None, V))
-        if draft.shape[1] not in (T, T - 1):
-            raise ValueError(f"draft must hold {T} or {T - 1} rows a sequence, not {draft.shape[1]}")
+        if draft.dim() != 3 or draft.shape[1] not in (T, T - 1):
+            raise ValueError(f"draft must hold {T} or {T - 1} rows a sequence")
+        _need("draft", draft, target.dtype, (B, draft.shape[1], V))
         _rows("draft", draft)
         if draft.shape[1] == 0:
             draft = None
-    for name, t, dt, shape in (("tokens", tokens, torch.int32, (B, T)), ("u", u, torch.float32, (B, T)),
-                               ("noise", noise, torch.float32, (B, V)), ("parents", parents, torch.int32, (B, T)),
-                               ("temperature", temperature, torch.float32, (B,)),
-                               ("n_tokens", n_tokens, torch.int32, (B,))):
+    i32, f32 = torch.int32, torch.float32
+    for name, t, dt, shape in (("tokens", tokens, i32, (B, T)), ("u", u, f32, (B, T)), ("noise", noise, f32, (B, V)),
+                               ("parents", parents, i32, (B, T)), ("temperature", temperature, f32, (B,)),
+                               ("n_tokens", n_tokens, i32, (B,))):
         if t is not None:
-            _cuda(name, t, dt, shape)
+            _need(name, t, dt, shape)
             _flat(name, t)
-    accept = torch.empty((B, 2), dtype=torch.int32, device=target.device)
-    path = torch.empty((B, T), dtype=torch.int32, device=target.device)
-    ws = torch.empty(qmm_verify_sample_workspace(B, T, V), dtype=torch.uint8, device=target.device)
+    dev = target.device
+    accept = torch.empty((B, 2), dtype=i32, device=dev)
+    path = torch.empty((B, T), dtype=i32, device=dev)
+    ws = torch.empty(qmm_verify_sample_workspace(B, T, V), dtype=torch.uint8, device=dev)
     qmm_verify_sample(target, draft, tokens, u, noise, accept, path, ws, parents, temperature, n_tokens, stream)
     if stream is not None:
         ws.record_stream(stream)
@@ -217,7 +236,7 @@ class PagedCache:
         for name, pool in (("k_pool", k_pool), ("v_pool", v_pool)):
             if pool is None:
                 pool = torch.zeros(shape, dtype=dtype, device=device)
-            _cuda(name, pool, dtype, shape)
+            _need(name, pool, dtype, shape)
             _flat(name, pool)
             pools.append(pool)
         self.k_pool, self.v_pool = pools
@@ -235,26 +254,34 @@ class PagedCache:
         """(out, lse): the nodes' attention over cache and tree; their keys and
         values are written behind the cached rows.  See qmm_tree_attention."""
         import torch
+        import torch
         if q.dim() != 4:
             raise ValueError("q must be [B, T, n_q_heads, head_dim]")
         B, T = q.shape[:2]
-        new = (B, T, self.n_kv_heads, self.head_dim)
+        dt, Hq, D = self.dtype, self.n_q_heads, self.head_dim
+        wide, new = (B, T, Hq, D), (B, T, self.n_kv_heads, D)
+        _need("q", q, dt, wide)
+        _rows("q", q)
+        _need("k", k, dt, new)
+        _rows("k", k)
+        _need("v", v, dt, new)
+        _rows("v", v)
         if out is None:
-            out = torch.empty((B, T, self.n_q_heads, self.head_dim), dtype=self.dtype, device=q.device)
+            out = torch.empty(wide, dtype=dt, device=q.device)
+        else:
+            _need("out", out, dt, wide)
+            _rows("out", out)
         if lse is None:
-            lse = torch.empty((B, T, self.n_q_heads), dtype=torch.float32, device=q.device)
-        for name, t, shape in (("q", q, (B, T, self.n_q_heads, self.head_dim)), ("k", k, new), ("v", v, new),
-                               ("out", out, (B, T, self.n_q_heads, self.head_dim))):
-            _cuda(name, t, self.dtype, shape)
-            _rows(name, t)
-        _cuda("lse", lse, torch.float32, (B, T, self.n_q_heads))
-        _flat("lse", lse)
+            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+        else:
+            _need("lse", lse, torch.float32, (B, T, Hq))
+            _flat("lse", lse)
         self._table(page_table, lens, B)
         if mask is not None:
-            _cuda("mask", mask, torch.int64, (B, T))
+            _need("mask", mask, torch.int64, (B, T))
             _rows("mask", mask)
         if n_tokens is not None:
-            _cuda("n_tokens", n_tokens, torch.int32, (B,))
+            _need("n_tokens", n_tokens, torch.int32, (B,))
             _flat("n_tokens", n_tokens)
         qmm_tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale, stream)
         return out, lse
@@ -263,16 +290,19 @@ class PagedCache:
         """The new lengths: the accepted branches' rows move behind the cached ones
         in every layer.  See qmm_cache_commit."""
         import torch
-        B = lens.shape[0]
+        B, i32 = lens.shape[0], torch.int32
         if lens_out is None:
             lens_out = torch.empty_like(lens)
+        else:
+            _need("lens_out", lens_out, i32, (B,))
+            _flat("lens_out", lens_out)
         self._table(page_table, lens, B)
-        _cuda("path", path, torch.int32, (B, None))
+        if path.dim() != 2:
+            raise ValueError("path must be [B, T]")
+        _need("path", path, i32, (B, path.shape[1]))
         _rows("path", path)
-        _cuda("accept", accept, torch.int32, (B, 2))
+        _need("accept", accept, i32, (B, 2))
         _flat("accept", accept)
-        _cuda("lens_out", lens_out, torch.int32, (B,))
-        _flat("lens_out", lens_out)
         qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out, stream)
         return lens_out
 
@@ -280,21 +310,24 @@ class PagedCache:
         """Copies the first rows[i] rows (None: all) of page src[i] to page dst[i]
         in every layer.  See qmm_cache_copy."""
         import torch
-        n = src.shape[0]
+        shape = (src.shape[0],)
         for name, t in (("src", src), ("dst", dst), ("rows", rows)):
             if t is not None:
-                _cuda(name, t, torch.int32, (n,))
+                _need(name, t, torch.int32, shape)
                 _flat(name, t)
         qmm_cache_copy(self.handle, src, dst, rows, stream)
 
     def sync_status(self, stream=None) -> int:
         return qmm_cache_sync_status(self.handle, stream)
 
-    def _table(self, page_table, lens, B):
+    @staticmethod
+    def _table(page_table, lens, B):
         import torch
-        _cuda("page_table", page_table, torch.int32, (B, None))
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [B, pages]")
+        _need("page_table", page_table, torch.int32, (B, page_table.shape[1]))
         _rows("page_table", page_table)
-        _cuda("lens", lens, torch.int32, (B,))
+        _need("lens", lens, torch.int32, (B,))
         _flat("lens", lens)
 
     # -------------------------------------------------------------- bookkeeping
