@@ -34,9 +34,12 @@ namespace {
 
 constexpr int MAX_T = QMM_TREE_MAX_T;
 constexpr int STAT_THREADS = 256;
+constexpr int STAT_DEPTH = 8;  // steps of a thread's ring
 constexpr int WALK_THREADS = 512;
+constexpr int WALK_DEPTH = 12;  // 16-byte slots of a thread's ring: 96 KB a CTA, two CTAs on an SM
 constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_CHUNKS = 32;  // parts of a row in the eager statistics
+constexpr int AHEAD = 4;        // nodes whose rows the walk reads at a time
 
 struct SampleParams {
   const void* target;
@@ -82,94 +85,151 @@ __device__ __forceinline__ float score_at(const void* row, int64_t v) {
     return unpack16<DT == QMM_DT_BF16>(__ldg(static_cast<const uint16_t*>(row) + v));
 }
 
-// N consecutive scores from entry v: one 16-byte load, or one entry.
+// N consecutive scores from a ring's slot of 16 bytes.
 template <int DT, int N>
-__device__ __forceinline__ void load_scores(const void* row, int64_t v, float (&x)[N]) {
-  if constexpr (N == 1) {
-    x[0] = score_at<DT>(row, v);
-  } else if constexpr (DT == QMM_DT_F32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + v));
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + v));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void ring_scores(uint32_t slot, float (&x)[N]) {
+  const uint4 a = lds128(slot);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == QMM_DT_F32) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
       x[2 * i] = unpack16<DT == QMM_DT_BF16>((uint16_t)(w[i] & 0xFFFFu));
       x[2 * i + 1] = unpack16<DT == QMM_DT_BF16>((uint16_t)(w[i] >> 16));
     }
   }
 }
 
-template <int N>
-__device__ __forceinline__ void load_noise(const float* row, int64_t v, float (&x)[N]) {
-  if constexpr (N == 1) {
-    x[0] = __ldg(row + v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + v + i));
-      x[i] = a.x, x[i + 1] = a.y, x[i + 2] = a.z, x[i + 3] = a.w;
-    }
-  }
-}
-
-// Running (maximum, sum of 2^((x - maximum) c)) over a strided share of a row;
-// the maximum is of the scores themselves.  c > 0.
+// Running (base, sum of 2^(x c - base)) over a share of a row's scores x, with c =
+// log2(e) / temperature > 0 and base = max(x) c, rounded.  x c - base is one FMA;
+// because sums, probabilities and joins all use the rounded bases, that rounding
+// cancels between them.
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
   MaxSum r;
   r.m = fmaxf(a.m, b.m);
-  // a part whose maximum is -inf has no mass (its sum is 0, or NaN for NaN scores)
-  r.s = (a.m == -INFINITY ? a.s : a.s * ex2((a.m - r.m) * c)) + (b.m == -INFINITY ? b.s : b.s * ex2((b.m - r.m) * c));
+  // a part whose base is -inf has no mass (its sum is 0, or NaN for NaN scores)
+  r.s = (a.m == -INFINITY ? a.s : a.s * ex2(a.m - r.m)) + (b.m == -INFINITY ? b.s : b.s * ex2(b.m - r.m));
   return r;
 }
 
-template <int DT, int N>
-__device__ __forceinline__ MaxSum row_share(const void* row, int64_t v0, int64_t v1, int64_t step, float c) {
+// Thread-private rings in shared memory: each thread copies what it will read, a
+// few steps ahead (cp.async), so that a step waits for nothing but its own copy
+// and no barrier is needed.  A thread's slots lie THREADS * 16 bytes apart.
+template <int THREADS, int SLOTS>
+struct Ring {
+  uint32_t base, at;
+  __device__ __forceinline__ explicit Ring(uint32_t smem) : base(smem + threadIdx.x * 16), at(base) {}
+  template <int BY>
+  __device__ __forceinline__ void next() {
+    at += BY * THREADS * 16;
+    if (at == base + SLOTS * THREADS * 16) at = base;
+  }
+};
+
+// The statistics of a thread's share of a row: granules (16 bytes, counted from
+// the one that holds the row's first entry, so that any alignment will do) g,
+// g + stride, ... < end, four at a time: the maximum and the exponentials of 32
+// (16) entries overlap, where one granule at a time left the SM waiting for
+// chains of dependent instructions.
+template <int DT, int THREADS, int SLOTS>
+__device__ __forceinline__ MaxSum row_share(uint32_t smem, const void* row, int V, int g, int end, int stride,
+                                            float c) {
+  constexpr int SIZE = (int)sizeof(typename Score<DT>::type), N = 16 / SIZE, U = 4;
+  constexpr uint32_t SLOT = THREADS * 16;
+  static_assert(SLOTS % U == 0, "whole steps");
+  const int skip = (int)((uintptr_t)row & 15);
+  const int last = (int)((skip + (int64_t)V * SIZE + 15) / 16);
+  end = end < last ? end : last;
+  const char* from = reinterpret_cast<const char*>(row) - skip + (int64_t)g * 16;
+  const int64_t hop = (int64_t)stride * 16;
+  Ring<THREADS, SLOTS> in(smem), out(smem);
+  int ig = g;
+  auto issue = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ig < end) cp_async16(in.at + u * SLOT, from, 16);
+      ig += stride;
+      from += hop;
+    }
+    cp_async_commit();
+    in.template next<U>();
+  };
+#pragma unroll
+  for (int i = 0; i < SLOTS / U - 1; ++i) issue();
   MaxSum a{-INFINITY, 0.f};
-  constexpr int U = N == 1 ? 8 : 4;
-  for (int64_t v = v0; v < v1; v += step * U) {
+  for (; g < end; g += U * stride) {
+    issue();
+    cp_async_wait<SLOTS / U - 1>();
     float x[U][N];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (v + k * step < v1) {
-        load_scores<DT, N>(row, v + k * step, x[k]);
+    for (int u = 0; u < U; ++u) {
+      const int gu = g + u * stride;
+      if (gu < end) {
+        ring_scores<DT, N>(out.at + u * SLOT, x[u]);
+        if (gu == 0 || gu + 1 == last) {
+          const int v = gu * N - skip / SIZE;
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (v + e < 0 || v + e >= V) x[u][e] = -INFINITY;
+        }
       } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[k][e] = -INFINITY;
+        for (int e = 0; e < N; ++e) x[u][e] = -INFINITY;
       }
     }
-    float mx = a.m;
+    out.template next<U>();
+    float mx[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k)
+    for (int u = 0; u < U; ++u) {
+      mx[u] = x[u][0];
 #pragma unroll
-      for (int e = 0; e < N; ++e) mx = fmaxf(mx, x[k][e]);
-    if (mx > a.m) {
-      a.s = a.m == -INFINITY ? a.s : a.s * ex2((a.m - mx) * c);
-      a.m = mx;
+      for (int e = 1; e < N; ++e) mx[u] = fmaxf(mx[u], x[u][e]);
+    }
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+    if (top > a.m) {
+      a.s = a.m == -INFINITY ? a.s : a.s * ex2(a.m - top);
+      a.m = top;
     }
     const float base = a.m == -INFINITY ? 0.f : a.m;
+    const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+    float2 sum[U];
 #pragma unroll
-    for (int k = 0; k < U; ++k)
+    for (int u = 0; u < U; ++u) {
+      sum[u] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < N; ++e) a.s += ex2((x[k][e] - base) * c);
+      for (int e = 0; e < N; e += 2) {
+        float2 y = fma2(make_float2(x[u][e], x[u][e + 1]), c2, b2);
+        y.x = ex2(y.x);
+        y.y = ex2(y.y);
+        sum[u] = __fadd2_rn(sum[u], y);
+      }
+    }
+    const float2 y = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+    a.s += y.x + y.y;
   }
+  cp_async_wait<0>();
   return a;
 }
 
-__device__ __forceinline__ MaxSum warp_join(MaxSum a, float c) {
+// Granules of 16 bytes that a row of any alignment spans at most.
+__host__ __device__ constexpr int row_granules(int64_t V, int size) { return (int)((V * size + 15) / 16 + 1); }
+
+__device__ __forceinline__ MaxSum warp_join(MaxSum a) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     MaxSum o;
     o.m = __shfl_xor_sync(0xFFFFFFFFu, a.m, d);
     o.s = __shfl_xor_sync(0xFFFFFFFFu, a.s, d);
-    a = join(a, o, c);
+    a = join(a, o);
   }
   return a;
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
 
 __device__ __forceinline__ float log2e_over(const float* temperature, int b) {
   return 1.4426950408889634f / (temperature ? __ldg(temperature + b) : 1.f);
@@ -178,9 +238,9 @@ __device__ __forceinline__ float log2e_over(const float* temperature, int b) {
 // ---------------------------------------------------------------- statistics
 // CTA (chunk, row, sequence): (maximum, sum) of one part of row node = y / 2 of
 // target (y even) or draft, if the node has children.
-template <int DT, bool WIDE>
+template <int DT>
 __global__ void __launch_bounds__(STAT_THREADS) sample_stats_kernel(const __grid_constant__ SampleParams p) {
-  constexpr int N = WIDE ? Score<DT>::VEC : 1;
+  extern __shared__ __align__(16) uint8_t ring[];
   using E = typename Score<DT>::type;
   __shared__ MaxSum s_part[STAT_THREADS / 32];
   const int b = blockIdx.z, tid = threadIdx.x;
@@ -197,14 +257,14 @@ __global__ void __launch_bounds__(STAT_THREADS) sample_stats_kernel(const __grid
   const E* row = side ? static_cast<const E*>(p.draft) + b * p.d_sb + node * p.d_st
                       : static_cast<const E*>(p.target) + b * p.t_sb + node * p.t_st;
   const float c = log2e_over(p.temperature, b);
-  const int64_t groups = (p.V + N - 1) / N;
-  const int64_t g0 = groups * blockIdx.x / p.chunks, g1 = groups * (blockIdx.x + 1) / p.chunks;
-  MaxSum a = row_share<DT, N>(row, (g0 + tid) * N, g1 * N, (int64_t)STAT_THREADS * N, c);
-  a = warp_join(a, c);
+  const int64_t groups = row_granules(p.V, (int)sizeof(E));
+  const int g0 = (int)(groups * blockIdx.x / p.chunks), g1 = (int)(groups * (blockIdx.x + 1) / p.chunks);
+  MaxSum a = row_share<DT, STAT_THREADS, STAT_DEPTH>(smem_u32(ring), row, (int)p.V, g0 + tid, g1, STAT_THREADS, c);
+  a = warp_join(a);
   if ((tid & 31) == 0) s_part[tid >> 5] = a;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < STAT_THREADS / 32; ++w) a = join(a, s_part[w], c);
+    for (int w = 1; w < STAT_THREADS / 32; ++w) a = join(a, s_part[w]);
     p.stats[(((int64_t)b * p.T + node) * 2 + side) * p.chunks + blockIdx.x] = make_float2(a.m, a.s);
   }
 }
@@ -217,18 +277,19 @@ struct WalkSmem {
   float pm[MAX_T], ps[MAX_T], qm[MAX_T], qs[MAX_T];  // eager: row maxima and 1 / sums
   float rz[MAX_T], rzq[MAX_T];       // rejections at the current node: 1 / Z (0: P kept), 1 / ZQ
   int rx[MAX_T];                     // and their tokens
-  float4 part[WALK_THREADS / 32];    // per warp
-  unsigned long long best[WALK_THREADS / 32];
-  float4 cl[2];                      // this CTA's part of a cluster sum, two in turn
-  unsigned long long cl_best;
+  int list[AHEAD];                   // nodes whose rows are read together
+  float2 part[2 * AHEAD][WALK_THREADS / 32];  // per warp
+  float4 cl[2][AHEAD];               // this CTA's part of cluster sums, two in turn
 };
 
 template <int DT, bool WIDE, bool EAGER>
 __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __grid_constant__ SampleParams p,
-                                                                   int cluster) {
+                                                                      int cluster, int ahead) {
   constexpr int N = WIDE ? Score<DT>::VEC : 1;
   using E = typename Score<DT>::type;
   __shared__ WalkSmem s;
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  const uint32_t ring = smem_u32(ring_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / cluster;
   const int rank = blockIdx.x - b * cluster;
@@ -264,7 +325,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
         const float2 v = __ldcg(p.stats + (((int64_t)b * T + node) * 2 + side) * p.chunks + lane);
         a.m = v.x, a.s = v.y;
       }
-      a = warp_join(a, c);
+      a = warp_join(a);
       if (lane == 0) {
         (side ? s.qm : s.pm)[node] = a.m == -INFINITY ? 0.f : a.m;
         (side ? s.qs : s.ps)[node] = a.s != 0.f ? 1.f / a.s : 0.f;
@@ -273,124 +334,221 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
   }
   __syncthreads();
 
+  // Reductions over the cluster.  Every warp leaves a value in s.part[i]; warp i
+  // adds up the CTA's, then, after a barrier of the cluster, the ranks', each
+  // with `op` over the lanes in an order that the sizes fix.  The buffers
+  // alternate, so that one barrier a reduction is enough.
   int turn = 0;
-  // Thread 0's value of every CTA of the cluster: lane r of each warp gets
-  // rank r's, the other lanes `none`.
-  auto exchange = [&](float4 mine, float4 none) {
-    if (tid == 0) s.cl[turn] = mine;
+  constexpr int WARPS = WALK_THREADS / 32;
+  auto reduce = [&](int count, float2 none, auto op) {
+    __syncthreads();
+    float2 x = none;
+    if (warp < count) {
+      if (lane < WARPS) x = s.part[warp][lane];
+      x = op(x);
+      if (lane == 0) reinterpret_cast<float2*>(s.cl[turn])[warp] = x;
+    }
     cluster_sync_all();
-    if (lane < cluster) {
-      const uint32_t a = dsmem_map(smem_u32(&s.cl[turn]), lane);
-      none = make_float4(ld_dsmem_f32(a), ld_dsmem_f32(a + 4), ld_dsmem_f32(a + 8), ld_dsmem_f32(a + 12));
+    x = none;
+    if (warp < count) {
+      if (lane < cluster) {
+        const uint32_t a = dsmem_map(smem_u32(reinterpret_cast<float2*>(s.cl[turn]) + warp), lane);
+        x = make_float2(ld_dsmem_f32(a), ld_dsmem_f32(a + 4));
+      }
+      x = op(x);
     }
     turn ^= 1;
-    return none;
+    return x;  // of reduction `warp`, in its lanes
   };
+  static_assert(2 * AHEAD <= WARPS, "a warp for each value");
 
-  const int64_t v0 = ((int64_t)rank * WALK_THREADS + tid) * N;
-  const int64_t step = (int64_t)cluster * WALK_THREADS * N;
-  const int64_t vend = p.V;
+  const int v0 = (rank * WALK_THREADS + tid) * N, step = cluster * WALK_THREADS * N, vend = (int)p.V;
+
+  // The whole noise row is read in the end.
+  for (int v = (rank * WALK_THREADS + tid) * 32; v < vend; v += cluster * WALK_THREADS * 32)
+    prefetch_l2(noise + v);
 
   int node = 0, k = 0, rej = 0;
   float pm = 0.f, ps = 0.f, qm = 0.f, qs = 0.f;
+  uint64_t known = EAGER ? ~0ull : 0ull;  // nodes whose statistics are in s
 
-  // The statistics of `node`'s rows into pm, ps, qm, qs.
-  auto enter = [&](bool need) {
-    if constexpr (EAGER) {
-      pm = s.pm[node], ps = s.ps[node], qm = s.qm[node], qs = s.qs[node];
-    } else if (need) {
-      MaxSum a = row_share<DT, N>(target + node * p.t_st, v0, vend, step, c);
-      MaxSum q{-INFINITY, 0.f};
-      if (has_q) q = row_share<DT, N>(draft + node * p.d_st, v0, vend, step, c);
-      a = warp_join(a, c);
-      q = warp_join(q, c);
-      if (lane == 0) s.part[warp] = make_float4(a.m, a.s, q.m, q.s);
-      __syncthreads();
-      if (tid == 0)
-        for (int w = 1; w < WALK_THREADS / 32; ++w) {
-          const float4 o = s.part[w];
-          a = join(a, MaxSum{o.x, o.y}, c);
-          q = join(q, MaxSum{o.z, o.w}, c);
+  // The children of a node as bits.
+  auto children = [&](int of) {
+    return (uint64_t)__ballot_sync(0xFFFFFFFFu, s.parent[lane] == of) |
+           (uint64_t)__ballot_sync(0xFFFFFFFFu, s.parent[lane + 32] == of) << 32;
+  };
+  // The statistics of `node`'s rows into pm, ps, qm, qs.  Where they are not
+  // known, those of the nodes that follow it if every first child is accepted
+  // are taken too, `ahead` in all: their rows are read together, and the cluster
+  // meets once.
+  auto enter = [&]() {
+    if constexpr (!EAGER) {
+      if (!(known >> node & 1)) {
+        int count = 0;
+        for (int at = node; at >= 0 && count < ahead;) {
+          if (tid == 0) s.list[count] = at;
+          ++count;
+          known |= 1ull << at;
+          const uint64_t next = children(at);
+          at = next ? __ffsll((long long)next) - 1 : -1;
+          if (at >= 0 && !children(at)) at = -1;  // a leaf's statistics have no use
         }
-      const float4 o = exchange(make_float4(a.m, a.s, q.m, q.s), make_float4(-INFINITY, 0.f, -INFINITY, 0.f));
-      const MaxSum ta = warp_join(MaxSum{o.x, o.y}, c), tq = warp_join(MaxSum{o.z, o.w}, c);
-      pm = ta.m == -INFINITY ? 0.f : ta.m;
-      ps = ta.s != 0.f ? 1.f / ta.s : 0.f;
-      qm = tq.m == -INFINITY ? 0.f : tq.m;
-      qs = tq.s != 0.f ? 1.f / tq.s : 0.f;
+        __syncthreads();
+        // The rows are dealt out to the warps; each takes its share of the
+        // CTA's part of one of them.
+        const int nrows = has_q ? 2 * count : count, per = WARPS / nrows;
+        const int r = warp / per;
+        if (r < nrows) {
+          const int of = s.list[has_q ? r >> 1 : r];
+          const E* row = has_q && (r & 1) ? draft + of * p.d_st : target + of * p.t_st;
+          const int64_t groups = row_granules(p.V, (int)sizeof(E));
+          const int g0 = (int)(groups * rank / cluster), g1 = (int)(groups * (rank + 1) / cluster);
+          const MaxSum x = warp_join(row_share<DT, WALK_THREADS, WALK_DEPTH>(
+              ring, row, vend, g0 + (warp - r * per) * 32 + lane, g1, per * 32, c));
+          if (lane == 0) s.part[r][warp - r * per] = make_float2(x.m, x.s);
+        }
+        // (a value for each of the WARPS places of a row)
+        if (lane < WARPS && lane >= per && warp < nrows) s.part[warp][lane] = make_float2(-INFINITY, 0.f);
+        const float2 a = reduce(nrows, make_float2(-INFINITY, 0.f), [&](float2 x) {
+          const MaxSum y = warp_join(MaxSum{x.x, x.y});
+          return make_float2(y.m, y.s);
+        });
+        if (warp < nrows && lane == 0) {
+          const int of = s.list[has_q ? warp >> 1 : warp];
+          const bool q = has_q && (warp & 1);
+          (q ? s.qm : s.pm)[of] = a.x == -INFINITY ? 0.f : a.x;
+          (q ? s.qs : s.ps)[of] = a.y != 0.f ? 1.f / a.y : 0.f;
+        }
+        __syncthreads();
+      }
+    }
+    pm = s.pm[node], ps = s.ps[node], qm = s.qm[node], qs = s.qs[node];
+  };
+  // P and Q of M consecutive entries from v after the node's first `count`
+  // rejections, in the place of their scores.
+  auto replay = [&](int v, int count, auto& P, auto& Q) {
+    constexpr int M = sizeof(P) / sizeof(float);
+#pragma unroll
+    for (int e = 0; e < M; ++e) {
+      P[e] = ex2(fmaf(P[e], c, -pm)) * ps;
+      Q[e] = has_q ? ex2(fmaf(Q[e], c, -qm)) * qs : 0.f;
+    }
+    for (int i = 0; i < count; ++i) {
+      const int hit = s.rx[i] - v;
+      const float rz = s.rz[i], rzq = s.rzq[i];
+#pragma unroll
+      for (int e = 0; e < M; ++e) {
+        const float left = has_q ? fmaxf(P[e] - Q[e], 0.f) : (hit == e ? 0.f : P[e]);
+        if (rz > 0.f) P[e] = left * rz;
+        Q[e] = hit == e ? 0.f : Q[e] * rzq;
+      }
     }
   };
-  // P and Q of entry v after the node's rejections, from their values before any.
-  auto replay = [&](int v, float& P, float& Q) {
-    for (int i = 0; i < rej; ++i) {
-      const bool hit = v == s.rx[i];
-      const float left = has_q ? fmaxf(P - Q, 0.f) : (hit ? 0.f : P);
-      if (s.rz[i] > 0.f) P = left * s.rz[i];
-      Q = hit ? 0.f : Q * s.rzq[i];
+  // The thread's share of the vocabulary, a group of N entries at a time:
+  // f(first entry, target scores, draft scores, noise).  Groups of 16 bytes go
+  // through the ring, GROUP_DEPTH of them ahead.
+  constexpr int SLOTS = 2 + N * 4 / 16;  // of a group: target, draft, noise
+  constexpr int GROUP_DEPTH = WALK_DEPTH / (SLOTS > 3 ? 4 : 3);
+  auto share = [&](const E* trow, const E* drow, const float* nrow, auto f) {
+    if constexpr (N == 1) {
+      constexpr int U = 4;
+      for (int v = v0; v < vend; v += step * U) {
+        float a[U][1], q[U][1], w[U][1];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (v + i * step < vend) {
+            a[i][0] = score_at<DT>(trow, v + i * step);
+            if (drow) q[i][0] = score_at<DT>(drow, v + i * step);
+            if (nrow) w[i][0] = __ldg(nrow + v + i * step);
+          }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (v + i * step < vend) f(v + i * step, a[i], q[i], w[i]);
+      }
+    } else {
+      Ring<WALK_THREADS, GROUP_DEPTH * SLOTS> in(ring), out(ring);
+      constexpr uint32_t SLOT = WALK_THREADS * 16;
+      int next = v0;
+      const E *tp = trow + v0, *dp = drow + v0;
+      const float* np = nrow + v0;
+      auto issue = [&]() {
+        if (next < vend) {
+          cp_async16(in.at, tp, 16);
+          if (drow) cp_async16(in.at + SLOT, dp, 16);
+          if (nrow) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) cp_async16(in.at + (2 + i) * SLOT, np + 4 * i, 16);
+          }
+          next += step;
+          tp += step, dp += step, np += step;
+        }
+        cp_async_commit();
+        in.template next<SLOTS>();
+      };
+#pragma unroll
+      for (int i = 0; i < GROUP_DEPTH - 1; ++i) issue();
+      for (int v = v0; v < vend; v += step) {
+        issue();
+        cp_async_wait<GROUP_DEPTH - 1>();
+        float a[N], q[N], w[N];
+        ring_scores<DT, N>(out.at, a);
+        if (drow) ring_scores<DT, N>(out.at + SLOT, q);
+        if (nrow) {
+#pragma unroll
+          for (int i = 0; i < N / 4; ++i) {
+            float x[4];
+            ring_scores<QMM_DT_F32, 4>(out.at + (2 + i) * SLOT, x);
+            w[4 * i] = x[0], w[4 * i + 1] = x[1], w[4 * i + 2] = x[2], w[4 * i + 3] = x[3];
+          }
+        }
+        f(v, a, q, w);
+        out.template next<SLOTS>();
+      }
+      cp_async_wait<0>();
     }
   };
-  // The children of `node` as bits.
-  auto children = [&]() {
-    return (uint64_t)__ballot_sync(0xFFFFFFFFu, s.parent[lane] == node) |
-           (uint64_t)__ballot_sync(0xFFFFFFFFu, s.parent[lane + 32] == node) << 32;
-  };
-
-  uint64_t kids = children();
-  enter(kids != 0);
+  uint64_t kids = children(node);
+  if (kids) enter();
   while (kids) {
     const int child = __ffsll((long long)kids) - 1;
     kids &= kids - 1;
     const int x = s.token[child];
-    float P = ex2((s.tx[child] - pm) * c) * ps;
-    float Q = has_q ? ex2((s.qx[child] - qm) * c) * qs : 0.f;
-    replay(x, P, Q);
-    if (s.u[child] * (has_q ? Q : 1.f) < P) {
+    float P[1] = {s.tx[child]}, Q[1] = {s.qx[child]};
+    replay(x, rej, P, Q);
+    if (s.u[child] * (has_q ? Q[0] : 1.f) < P[0]) {
       if (tid == 0) s.path[k] = child;
       ++k;
       node = child;
       rej = 0;
-      kids = children();
-      enter(kids != 0);
+      kids = children(node);
+      if (kids) enter();
       continue;
     }
     if (kids) {
       // another sibling: Z and ZQ
       float z = 0.f, zq = 0.f;
-      const E* trow = target + node * p.t_st;
-      const E* drow = draft + node * p.d_st;
-      for (int64_t v = v0; v < vend; v += step) {
-        float a[N], q[N];
-        load_scores<DT, N>(trow, v, a);
-        if (has_q) load_scores<DT, N>(drow, v, q);
+      share(target + node * p.t_st, has_q ? draft + node * p.d_st : nullptr, nullptr,
+            [&](int v, auto& a, auto& q, auto&) {
+              replay(v, rej, a, q);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          float pv = ex2((a[e] - pm) * c) * ps;
-          float qv = has_q ? ex2((q[e] - qm) * c) * qs : 0.f;
-          replay((int)v + e, pv, qv);
-          const bool hit = (int)v + e == x;
-          z += has_q ? fmaxf(pv - qv, 0.f) : (hit ? 0.f : pv);
-          zq += hit ? 0.f : qv;
+              for (int e = 0; e < N; ++e) {
+                const bool hit = v + e == x;
+                z += has_q ? fmaxf(a[e] - q[e], 0.f) : (hit ? 0.f : a[e]);
+                zq += hit ? 0.f : q[e];
+              }
+            });
+      auto sum = [&](float2 y) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          y.x += __shfl_xor_sync(0xFFFFFFFFu, y.x, d);
+          y.y += __shfl_xor_sync(0xFFFFFFFFu, y.y, d);
         }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        z += __shfl_xor_sync(0xFFFFFFFFu, z, d);
-        zq += __shfl_xor_sync(0xFFFFFFFFu, zq, d);
-      }
-      if (lane == 0) s.part[warp] = make_float4(z, zq, 0.f, 0.f);
-      __syncthreads();
-      if (tid == 0)
-        for (int w = 1; w < WALK_THREADS / 32; ++w) {
-          z += s.part[w].x;
-          zq += s.part[w].y;
-        }
-      const float4 o = exchange(make_float4(z, zq, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f));
-      float tz = o.x, tzq = o.y;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        tz += __shfl_xor_sync(0xFFFFFFFFu, tz, d);
-        tzq += __shfl_xor_sync(0xFFFFFFFFu, tzq, d);
-      }
+        return y;
+      };
+      const float2 w = sum(make_float2(z, zq));
+      if (lane == 0) s.part[0][warp] = w;
+      const float2 t = reduce(1, make_float2(0.f, 0.f), sum);  // warp 0 holds it
+      const float tz = t.x, tzq = t.y;
       if (tid == 0) {
         s.rz[rej] = tz > 0.f ? 1.f / tz : 0.f;
         s.rzq[rej] = tzq > 0.f ? 1.f / tzq : 1.f;
@@ -407,93 +565,64 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
   }
   __syncthreads();
 
-  // The next token: argmax P / noise.  Where the last rejection leaves no mass,
-  // P stays as it was before it: both are raced, and the second counts then.
-  // Without a rejection the race is run on logarithms, (score / temperature)
-  // log2(e) - log2(noise): they need no maximum of the row, which a node
-  // without children has no other use for.
-  unsigned long long best = 0, kept = 0;
-  auto race = [](unsigned long long& to, float r, int v) {
-    if (r != r) return;
-    uint32_t o = __float_as_uint(r);
-    o = o & 0x80000000u ? ~o : o | 0x80000000u;  // the order of the values
-    const unsigned long long key = (unsigned long long)o << 32 | (0xFFFFFFFFu - (uint32_t)v);
-    to = key > to ? key : to;
-  };
+  // The next token: argmax P / noise.  Without a rejection the race is run on
+  // logarithms, (score / temperature) log2(e) - log2(noise): they need no maximum
+  // of the row, which a node without children has no other use for.  Where the
+  // last rejection leaves no mass, P stays as it was before it: that, which
+  // rounding alone brings about, is another race.
   const E* trow = target + node * p.t_st;
-  const E* drow = draft + node * p.d_st;
-  if (rej == 0) {
-    constexpr int U = N == 1 ? 8 : 2;
-    for (int64_t v = v0; v < vend; v += step * U) {
-      float a[U][N], w[U][N];
+  const E* drow = has_q ? draft + node * p.d_st : nullptr;
+  int token = 0;
+  for (int undo = 0; undo < 2; ++undo) {
+    float best = -INFINITY;
+    int at = 0x7FFFFFFF;  // a thread meets its entries in order: the first of equals stays
+    auto race = [&](float r, int v) {
+      if (r > best || (at == 0x7FFFFFFF && r == best)) best = r, at = v;
+    };
+    if (rej == 0)
+      share(trow, nullptr, noise, [&](int v, auto& a, auto&, auto& w) {
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (v + i * step < vend) {
-          load_scores<DT, N>(trow, v + i * step, a[i]);
-          load_noise<N>(noise, v + i * step, w[i]);
+        for (int e = 0; e < N; ++e) race(fmaf(a[e], c, -__log2f(w[e])), v + e);
+      });
+    else
+      share(trow, drow, noise, [&](int v, auto& a, auto& q, auto& w) {
+        replay(v, rej - 1, a, q);
+        const int hit = s.rx[rej - 1] - v;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          float pv = a[e];
+          if (!undo) pv = has_q ? fmaxf(pv - q[e], 0.f) : (hit == e ? 0.f : pv);
+          race(__fdividef(pv, w[e]), v + e);
         }
+      });
+    // the largest value, the lowest index among equals, as one 64-bit key
+    uint32_t key = __float_as_uint(best + 0.f);  // -0 is 0
+    key = key & 0x80000000u ? ~key : key | 0x80000000u;
+    auto larger = [&](float2 x) {
+      unsigned long long y = (unsigned long long)__float_as_uint(x.x) << 32 | __float_as_uint(x.y);
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (v + i * step < vend) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) race(best, fmaf(a[i][e], c, -__log2f(w[i][e])), (int)(v + i * step) + e);
-        }
-    }
-  } else {
-    for (int64_t v = v0; v < vend; v += step) {
-      float a[N], q[N], w[N];
-      load_scores<DT, N>(trow, v, a);
-      if (has_q) load_scores<DT, N>(drow, v, q);
-      load_noise<N>(noise, v, w);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const int vi = (int)v + e;
-        float pv = ex2((a[e] - pm) * c) * ps;
-        float qv = has_q ? ex2((q[e] - qm) * c) * qs : 0.f;
-        for (int i = 0; i < rej - 1; ++i) {
-          const bool hit = vi == s.rx[i];
-          const float left = has_q ? fmaxf(pv - qv, 0.f) : (hit ? 0.f : pv);
-          if (s.rz[i] > 0.f) pv = left * s.rz[i];
-          qv = hit ? 0.f : qv * s.rzq[i];
-        }
-        race(kept, __fdiv_rn(pv, w[e]), vi);
-        race(best, __fdiv_rn(has_q ? fmaxf(pv - qv, 0.f) : (vi == s.rx[rej - 1] ? 0.f : pv), w[e]), vi);
+      for (int d = 16; d > 0; d >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, y, d);
+        y = o > y ? o : y;
       }
-    }
-  }
-  auto block_max = [&](unsigned long long key) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
-      key = o > key ? o : key;
-    }
+      return make_float2(__uint_as_float((uint32_t)(y >> 32)), __uint_as_float((uint32_t)y));
+    };
+    const float2 x = larger(at == 0x7FFFFFFF ? make_float2(0.f, 0.f)
+                                             : make_float2(__uint_as_float(key), __uint_as_float(0xFFFFFFFFu - (uint32_t)at)));
     __syncthreads();
-    if (lane == 0) s.best[warp] = key;
+    if (lane == 0) s.part[0][warp] = x;
+    const float2 t = reduce(1, make_float2(0.f, 0.f), larger);
+    if (tid == 0) s.part[1][0] = t;
     __syncthreads();
-    for (int w = 0; w < WALK_THREADS / 32; ++w) key = s.best[w] > key ? s.best[w] : key;
-    return key;
-  };
-  best = block_max(best);
-  kept = rej > 0 ? block_max(kept) : 0;
-  {
-    const float4 o = exchange(make_float4(__uint_as_float((uint32_t)(best >> 32)), __uint_as_float((uint32_t)best),
-                                          __uint_as_float((uint32_t)(kept >> 32)), __uint_as_float((uint32_t)kept)),
-                              make_float4(0.f, 0.f, 0.f, 0.f));
-    best = (unsigned long long)__float_as_uint(o.x) << 32 | __float_as_uint(o.y);
-    kept = (unsigned long long)__float_as_uint(o.z) << 32 | __float_as_uint(o.w);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      const unsigned long long x = __shfl_xor_sync(0xFFFFFFFFu, best, d), y = __shfl_xor_sync(0xFFFFFFFFu, kept, d);
-      best = x > best ? x : best;
-      kept = y > kept ? y : kept;
-    }
+    const uint32_t top = __float_as_uint(s.part[1][0].x), low = __float_as_uint(s.part[1][0].y);
+    token = top ? (int)(0xFFFFFFFFu - low) : 0;
+    if (rej == 0 || top > 0x80000000u) break;  // something was left
   }
-  if (rej > 0 && (uint32_t)(best >> 32) <= 0x80000000u) best = kept;  // nothing was left
   if (rank == 0) {
     for (int i = tid; i < T; i += WALK_THREADS) p.path[(int64_t)b * T + i] = s.path[i];
     if (tid == 0) {
       p.accept[2 * b] = k;
-      p.accept[2 * b + 1] = best ? (int)(0xFFFFFFFFu - (uint32_t)best) : 0;
+      p.accept[2 * b + 1] = token;
     }
   }
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
@@ -520,11 +649,14 @@ bool sample_eager(int B, int T, int64_t V, int elem, bool has_q) {
 template <int DT, bool WIDE, bool EAGER>
 cudaError_t launch_walk(const SampleParams& p, int B, int cluster, cudaStream_t st) {
   auto kern = sample_walk_kernel<DT, WIDE, EAGER>;
+  constexpr int SMEM = WALK_THREADS * WALK_DEPTH * 16;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * cluster));
   cfg.blockDim = dim3(WALK_THREADS);
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -535,7 +667,7 @@ cudaError_t launch_walk(const SampleParams& p, int B, int cluster, cudaStream_t 
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = EAGER ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, cluster);
+  return cudaLaunchKernelEx(&cfg, kern, p, cluster, AHEAD);
 }
 
 template <int DT, bool WIDE>
@@ -544,7 +676,8 @@ cudaError_t launch_sample(SampleParams& p, int B, int elem, cudaStream_t st) {
   if (!sample_eager(B, p.T, p.V, elem, p.draft != nullptr)) return launch_walk<DT, WIDE, false>(p, B, cluster, st);
   p.chunks = sample_chunks(B, p.T, p.V);
   const int rows = (p.T - 1) * (p.draft ? 2 : 1);  // the last node has no children
-  sample_stats_kernel<DT, WIDE><<<dim3((unsigned)p.chunks, (unsigned)rows, (unsigned)B), STAT_THREADS, 0, st>>>(p);
+  sample_stats_kernel<DT><<<dim3((unsigned)p.chunks, (unsigned)rows, (unsigned)B), STAT_THREADS,
+                            STAT_THREADS * STAT_DEPTH * 16, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_walk<DT, WIDE, true>(p, B, cluster, st);
