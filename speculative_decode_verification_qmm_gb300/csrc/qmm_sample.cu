@@ -25,6 +25,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qmm.h"
 #include "qmm_attn.cuh"
 #include "qmm_attn.h"
@@ -643,15 +645,22 @@ int sample_cluster(int B, int64_t V) {
 // Eager while the rows of all nodes are read in about the time of one step of
 // the walk.
 bool sample_eager(int B, int T, int64_t V, int elem, bool has_q) {
-  return T > 1 && (int64_t)B * (T - 1) * V * elem * (has_q ? 2 : 1) <= (32ll << 20);
+  return T > 1 && (int64_t)B * (T - 1) * V * elem * (has_q ? 2 : 1) <= (48ll << 20);
 }
 
 template <int DT, bool WIDE, bool EAGER>
 cudaError_t launch_walk(const SampleParams& p, int B, int cluster, cudaStream_t st) {
   auto kern = sample_walk_kernel<DT, WIDE, EAGER>;
   constexpr int SMEM = WALK_THREADS * WALK_DEPTH * 16;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  // once on each device
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(ready.load() >> dev & 1))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev);
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * cluster));

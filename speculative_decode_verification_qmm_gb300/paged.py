@@ -18,6 +18,7 @@ which page, and how many sequences share one.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_attn_args,
@@ -64,23 +65,26 @@ def _refuse(name, t, dtype, shape):
     raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
 
 
-def _need(name, t, dtype, shape):
-    """Refuses a tensor that is not on the GPU, or of another type or shape."""
+def _flat(name, t, dtype, shape):
+    """Refuses a tensor that is not on the GPU, not contiguous, or of another type or shape."""
     if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
         _refuse(name, t, dtype, shape)
-
-
-def _flat(name, t):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(name, t):
-    """Tensors whose last dimension has to be contiguous; the strides."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+def _strided(name, t, dtype, shape):
+    """The same for one whose last dimension alone has to be contiguous."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _refuse(name, t, dtype, shape)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return st
+
+
+def _rows(name, t):
+    """Refuses a tensor whose last dimension is not contiguous."""
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
 
 
 # ------------------------------------------------------------------ raw C names
@@ -141,9 +145,10 @@ def qmm_debug_set_cache_wait_limit(h, ns: int) -> None:
     _check("qmm_debug_set_cache_wait_limit", load().qmm_debug_set_cache_wait_limit(h, ns))
 
 
+@functools.lru_cache(maxsize=256)
 def qmm_verify_sample_workspace(B: int, T: int, V: int) -> int:
-    """Bytes of device workspace qmm_verify_sample needs for those sizes."""
-    n = ctypes.c_int64(0)
+    """Bytes of device workspace qmm_verify_sample needs for those sizes (and them alone)."""
+    n = ctypes.c_int64()
     _check("qmm_verify_sample_workspace", load().qmm_verify_sample_workspace(B, T, V, ctypes.byref(n)))
     return n.value
 
@@ -179,17 +184,19 @@ def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=Non
     if draft is not None:
         if draft.dim() != 3 or draft.shape[1] not in (T, T - 1):
             raise ValueError(f"draft must hold {T} or {T - 1} rows a sequence")
-        _need("draft", draft, target.dtype, (B, draft.shape[1], V))
-        _rows("draft", draft)
+        _strided("draft", draft, target.dtype, (B, draft.shape[1], V))
         if draft.shape[1] == 0:
             draft = None
-    i32, f32 = torch.int32, torch.float32
-    for name, t, dt, shape in (("tokens", tokens, i32, (B, T)), ("u", u, f32, (B, T)), ("noise", noise, f32, (B, V)),
-                               ("parents", parents, i32, (B, T)), ("temperature", temperature, f32, (B,)),
-                               ("n_tokens", n_tokens, i32, (B,))):
-        if t is not None:
-            _need(name, t, dt, shape)
-            _flat(name, t)
+    i32, f32, nodes = torch.int32, torch.float32, (B, T)
+    _flat("tokens", tokens, i32, nodes)
+    _flat("u", u, f32, nodes)
+    _flat("noise", noise, f32, (B, V))
+    if parents is not None:
+        _flat("parents", parents, i32, nodes)
+    if temperature is not None:
+        _flat("temperature", temperature, f32, (B,))
+    if n_tokens is not None:
+        _flat("n_tokens", n_tokens, i32, (B,))
     dev = target.device
     accept = torch.empty((B, 2), dtype=i32, device=dev)
     path = torch.empty((B, T), dtype=i32, device=dev)
@@ -236,8 +243,7 @@ class PagedCache:
         for name, pool in (("k_pool", k_pool), ("v_pool", v_pool)):
             if pool is None:
                 pool = torch.zeros(shape, dtype=dtype, device=device)
-            _need(name, pool, dtype, shape)
-            _flat(name, pool)
+            _flat(name, pool, dtype, shape)
             pools.append(pool)
         self.k_pool, self.v_pool = pools
         self.n_layers, self.n_pages, self.page_size = n_layers, n_pages, page_size
@@ -260,29 +266,22 @@ class PagedCache:
         B, T = q.shape[:2]
         dt, Hq, D = self.dtype, self.n_q_heads, self.head_dim
         wide, new = (B, T, Hq, D), (B, T, self.n_kv_heads, D)
-        _need("q", q, dt, wide)
-        _rows("q", q)
-        _need("k", k, dt, new)
-        _rows("k", k)
-        _need("v", v, dt, new)
-        _rows("v", v)
+        _strided("q", q, dt, wide)
+        _strided("k", k, dt, new)
+        _strided("v", v, dt, new)
         if out is None:
             out = torch.empty(wide, dtype=dt, device=q.device)
         else:
-            _need("out", out, dt, wide)
-            _rows("out", out)
+            _strided("out", out, dt, wide)
         if lse is None:
             lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
         else:
-            _need("lse", lse, torch.float32, (B, T, Hq))
-            _flat("lse", lse)
+            _flat("lse", lse, torch.float32, (B, T, Hq))
         self._table(page_table, lens, B)
         if mask is not None:
-            _need("mask", mask, torch.int64, (B, T))
-            _rows("mask", mask)
+            _strided("mask", mask, torch.int64, (B, T))
         if n_tokens is not None:
-            _need("n_tokens", n_tokens, torch.int32, (B,))
-            _flat("n_tokens", n_tokens)
+            _flat("n_tokens", n_tokens, torch.int32, (B,))
         qmm_tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale, stream)
         return out, lse
 
@@ -294,15 +293,12 @@ class PagedCache:
         if lens_out is None:
             lens_out = torch.empty_like(lens)
         else:
-            _need("lens_out", lens_out, i32, (B,))
-            _flat("lens_out", lens_out)
+            _flat("lens_out", lens_out, i32, (B,))
         self._table(page_table, lens, B)
         if path.dim() != 2:
             raise ValueError("path must be [B, T]")
-        _need("path", path, i32, (B, path.shape[1]))
-        _rows("path", path)
-        _need("accept", accept, i32, (B, 2))
-        _flat("accept", accept)
+        _strided("path", path, i32, (B, path.shape[1]))
+        _flat("accept", accept, i32, (B, 2))
         qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out, stream)
         return lens_out
 
@@ -310,11 +306,11 @@ class PagedCache:
         """Copies the first rows[i] rows (None: all) of page src[i] to page dst[i]
         in every layer.  See qmm_cache_copy."""
         import torch
-        shape = (src.shape[0],)
-        for name, t in (("src", src), ("dst", dst), ("rows", rows)):
-            if t is not None:
-                _need(name, t, torch.int32, shape)
-                _flat(name, t)
+        shape, i32 = (src.shape[0],), torch.int32
+        _flat("src", src, i32, shape)
+        _flat("dst", dst, i32, shape)
+        if rows is not None:
+            _flat("rows", rows, i32, shape)
         qmm_cache_copy(self.handle, src, dst, rows, stream)
 
     def sync_status(self, stream=None) -> int:
@@ -325,10 +321,8 @@ class PagedCache:
         import torch
         if page_table.dim() != 2:
             raise ValueError("page_table must be [B, pages]")
-        _need("page_table", page_table, torch.int32, (B, page_table.shape[1]))
-        _rows("page_table", page_table)
-        _need("lens", lens, torch.int32, (B,))
-        _flat("lens", lens)
+        _strided("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+        _flat("lens", lens, torch.int32, (B,))
 
     # -------------------------------------------------------------- bookkeeping
     @property
