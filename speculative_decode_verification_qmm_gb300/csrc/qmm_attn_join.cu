@@ -3,9 +3,12 @@
 //
 //   m = max m_c,  l = sum l_c 2^(m_c - m),  O = sum O_c 2^(m_c - m),  out = O / l
 // over the item's CTAs c.  The partials are read from L2; what bounds the kernel
-// is latency, so a CTA takes four rows (eight at head size 64), its four warps
-// every fourth part of them, and all of a warp's loads of two parts are in
+// is latency, so a CTA takes four rows (eight at head size 64) at a time, its four
+// warps every fourth part of them, and all of a warp's loads of two parts are in
 // flight at a time; the warps' sums are added in order through shared memory.
+// An item of four parts or fewer and many rows gives each warp rows of its own.  Where
+// there are more rows than eight CTAs an SM would take, a CTA goes on to further
+// ones: finding its item costs as much as four of them.
 // Everything that does not depend on the partials is done before the wait for
 // the kernel that writes them (programmatic dependent launch).  As a tail of the
 // attention kernels' last CTA of an item the same sums took up to 30 us (64
@@ -24,7 +27,7 @@ constexpr int RU = 4;  // rows of a lane
 constexpr int U = 2;   // parts in flight
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int tk, int rows,
+__global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel(const __grid_constant__ AttnParams p, int tk, int rows,
                                                                int chunks) {
   constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp's load
   constexpr int RPC = RPW * RU;               // rows of the CTA
@@ -47,78 +50,97 @@ __global__ void __launch_bounds__(WARPS * 32) attn_join_kernel(const __grid_cons
   const int64_t u = before * p.Hkv * p.RT + (int64_t)(cur.h * p.RT + cur.rt) * nt;
   const int c0 = attn_owner(u, W, G), c1 = attn_owner(u + nt - 1, W, G);
   const int part = rows * (D + 2);
-  const int r0 = chunk * RPC, left = p.R - cur.rt * rows < rows ? p.R - cur.rt * rows : rows;
+  const int left = p.R - cur.rt * rows < rows ? p.R - cur.rt * rows : rows;
   const int sub = lane % LPR, row = lane / LPR;
   pdl_wait();  // every CTA: the call has not ended before the attention kernel has
   if (c0 == c1) return;
 
-  float4 acc[RU];
-  float mn[RU], lt[RU];
+  const bool alone = c1 - c0 < 4 && left >= 128;  // a warp joins its rows alone
+  const int from = alone ? c0 : c0 + warp, step = alone ? 1 : WARPS;
+  const int first = alone ? (chunk * WARPS + warp) * RPC : chunk * RPC;
+  const int hop = chunks * (alone ? WARPS * RPC : RPC);
+  for (int r0 = first; r0 < left; r0 += hop) {
+    float4 acc[RU];
+    float mn[RU], lt[RU];
 #pragma unroll
-  for (int k = 0; k < RU; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), mn[k] = -INFINITY, lt[k] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += WARPS * U) {
-    float4 v[U][RU];
-    float m[U][RU], l[U][RU];
+    for (int k = 0; k < RU; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), mn[k] = -INFINITY, lt[k] = 0.f;
+    for (int c = from; c <= c1; c += step * U) {
+      float4 v[U][RU];
+      float m[U][RU], l[U][RU];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int cc = c + j * WARPS;
-      const float* pp = p.ws + ((int64_t)cc * 2 + (cc == c0)) * part;
+      for (int j = 0; j < U; ++j) {
+        const int cc = c + j * step;
+        const float* pp = p.ws + ((int64_t)cc * 2 + (cc == c0)) * part;
+#pragma unroll
+        for (int k = 0; k < RU; ++k) {
+          const int r = r0 + k * RPW + row;
+          const bool have = cc <= c1;  // (rows past the item's are in the workspace too)
+          m[j][k] = have ? __ldcg(pp + rows * D + r) : -INFINITY;
+          l[j][k] = have ? __ldcg(pp + rows * D + rows + r) : 0.f;
+          v[j][k] = have ? __ldcg(reinterpret_cast<const float4*>(pp + r * D) + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int k = 0; k < RU; ++k) {
+          const float x = fmaxf(mn[k], m[j][k]);
+          const float a = attn_weight(mn[k], lt[k], x), w = attn_weight(m[j][k], l[j][k], x);
+          lt[k] = lt[k] * a + l[j][k] * w;
+          acc[k].x = acc[k].x * a + v[j][k].x * w;
+          acc[k].y = acc[k].y * a + v[j][k].y * w;
+          acc[k].z = acc[k].z * a + v[j][k].z * w;
+          acc[k].w = acc[k].w * a + v[j][k].w * w;
+          mn[k] = x;
+        }
+    }
+    if (alone) {
 #pragma unroll
       for (int k = 0; k < RU; ++k) {
         const int r = r0 + k * RPW + row;
-        const bool have = cc <= c1;
-        m[j][k] = have ? __ldcg(pp + rows * D + r) : -INFINITY;
-        l[j][k] = have ? __ldcg(pp + rows * D + rows + r) : 0.f;
-        v[j][k] = have ? __ldcg(reinterpret_cast<const float4*>(pp + r * D) + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < left) attn_store4<BF16>(p, cur, cur.rt * rows + r, sub * 4, acc[k], mn[k], lt[k]);
       }
+      continue;
     }
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-#pragma unroll
-      for (int k = 0; k < RU; ++k) {
-        const float x = fmaxf(mn[k], m[j][k]);
-        const float a = attn_weight(mn[k], lt[k], x), w = attn_weight(m[j][k], l[j][k], x);
-        lt[k] = lt[k] * a + l[j][k] * w;
-        acc[k].x = acc[k].x * a + v[j][k].x * w;
-        acc[k].y = acc[k].y * a + v[j][k].y * w;
-        acc[k].z = acc[k].z * a + v[j][k].z * w;
-        acc[k].w = acc[k].w * a + v[j][k].w * w;
-        mn[k] = x;
+    for (int k = 0; k < RU; ++k) {
+      s_acc[warp][k * RPW + row][sub] = acc[k];
+      if (sub == 0) {
+        s_m[warp][k * RPW + row] = mn[k];
+        s_l[warp][k * RPW + row] = lt[k];
       }
-  }
-#pragma unroll
-  for (int k = 0; k < RU; ++k) {
-    s_acc[warp][k * RPW + row][sub] = acc[k];
-    if (sub == 0) {
-      s_m[warp][k * RPW + row] = mn[k];
-      s_l[warp][k * RPW + row] = lt[k];
     }
-  }
-  __syncthreads();
-  // one thread a float4 of a row
-  const int rr = threadIdx.x / LPR;
-  static_assert(RPC * LPR == WARPS * 32, "a thread for each float4");
-  if (r0 + rr >= left) return;
-  float mx = -INFINITY, l = 0.f;
+    __syncthreads();
+    // one thread a float4 of a row
+    const int rr = threadIdx.x / LPR;
+    static_assert(RPC * LPR == WARPS * 32, "a thread for each float4");
+    if (r0 + rr < left) {
+      float mx = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, s_m[w][rr]);
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, s_m[w][rr]);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const float x = attn_weight(s_m[w][rr], s_l[w][rr], mx);
-    const float4 v = s_acc[w][rr][sub];
-    l += s_l[w][rr] * x;
-    a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
+      for (int w = 0; w < WARPS; ++w) {
+        const float x = attn_weight(s_m[w][rr], s_l[w][rr], mx);
+        const float4 v = s_acc[w][rr][sub];
+        l += s_l[w][rr] * x;
+        a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
+      }
+      attn_store4<BF16>(p, cur, cur.rt * rows + r0 + rr, sub * 4, a, mx, l);
+    }
+    __syncthreads();
   }
-  attn_store4<BF16>(p, cur, cur.rt * rows + r0 + rr, sub * 4, a, mx, l);
 }
 
 template <bool BF16, int D>
 cudaError_t launch(const AttnParams& p, int tk, int rows, cudaStream_t st) {
   constexpr int PER = 128 / D * RU;
-  const int chunks = ((p.R < rows ? p.R : rows) + PER - 1) / PER;
+  const int64_t items = (int64_t)p.B * p.Hkv * p.RT;
+  int chunks = ((p.R < rows ? p.R : rows) + PER - 1) / PER;
+  const int64_t most = (1216 + items - 1) / items;
+  if (chunks > most) chunks = (int)most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hkv * p.RT * chunks));
+  cfg.gridDim = dim3((unsigned)(items * chunks));
   cfg.blockDim = dim3(WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute at;
