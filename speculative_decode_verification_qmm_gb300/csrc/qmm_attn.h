@@ -24,13 +24,12 @@ cudaError_t host_pool_map(void* map, const void* base, int64_t rows, int D, int 
 // Rows of an item's tile for R rows, and cache rows of a unit.  mma.sync kernel:
 // two CTAs per SM.
 constexpr int ATTN_MMA_CTAS_PER_SM = 2;
-int attn_mma_tile_rows(int R);
+int attn_mma_tile_rows();
 int attn_mma_tile_cache_rows();
 cudaError_t prepare_attn_mma(bool bf16, int D);
 cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st);
 
-// tcgen05 kernel (more rows than the mma.sync kernel's tile holds), one CTA per
-// SM; kmap, vmap: host_pool_map with boxes of 16 rows.
+// tcgen05 kernel (more rows than the mma.sync kernel's tile), one CTA per SM; kmap, vmap: host_pool_map with boxes of 16 rows.
 int attn_tc_tile_rows(int R);
 int attn_tc_tile_cache_rows();
 cudaError_t prepare_attn_tc(bool bf16, int D);

@@ -1,4 +1,4 @@
-// qmm_attn_mma.cu -- tree attention for few rows per key/value head, on
+// qmm_attn_mma.cu -- tree attention for up to 16 rows per key/value head, on
 // mma.sync: one pass over the cached rows with a running softmax.
 //
 // Per row r and cache row j: s = q_r . K_j (m16n8k16, rows as M), then with the
@@ -6,12 +6,19 @@
 // behind the true maximum by up to 8 (p <= 256), so that O is rescaled only
 // when a row's maximum grows by more than that.
 //
-// With at most 32 rows there are at most 64 flops for each byte of the cache,
-// so the kernel is bound by the cache's stream.  Every warp of the CTA keeps a private ring of 16-row blocks of K and V in
-// shared memory (cp.async, XOR-swizzled for ldmatrix) and walks its own blocks,
-// every fourth one of the CTA's range, without any barrier between warps; the
-// ring runs across the ends of segments, so a batch of short sequences streams
-// like one long one.  Barriers and shared-memory sums are paid once a segment.
+// With at most 16 rows there are at most 32 flops for each byte of the cache, so
+// the kernel is bound by the cache's stream.  Every warp of the CTA keeps a
+// private ring of 16-row blocks of K and V in shared memory (cp.async,
+// XOR-swizzled for ldmatrix) and walks its own blocks, every fourth one of the
+// CTA's range, without any barrier between warps; the ring runs across the ends
+// of segments, so a batch of short sequences streams like one long one.  Barriers
+// and shared-memory sums are paid once a segment.
+// Measured: one sequence of 131,071 rows, 20 heads of 128, 16 rows a head, 1.34
+// GB: 203 us without the joining kernel (6.6 TB/s, 97 % of a copy), 210 with it;
+// 32 sequences of 2,048 to 8,192 rows, 8 rows a head: 115 us (6.1 TB/s).  Two row
+// tiles a warp (32 rows) took 103 us where the tcgen05 kernel takes 81 (16 x
+// 4096, 20 heads), so 17 rows and more go there.  216 registers leave room on the
+// SM for the joining kernel beside two CTAs.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -26,13 +33,13 @@ constexpr int WARPS = 4;
 constexpr int BLK = 16;            // cache rows of a warp's block
 constexpr int TK = WARPS * BLK;    // cache rows of a unit
 constexpr int STAGES = 3;
+constexpr int ROWS = 16;           // rows of an item's tile
 
-template <int D, int MT>
+template <int D>
 struct Smem {
-  static constexpr int ROWS = 16 * MT;
   static constexpr int BLK_BYTES = BLK * D * 2;             // one of K, V
   static constexpr int STAGE_BYTES = 2 * BLK_BYTES;
-  static constexpr int MC = 32 / MT;                        // columns summed at a time
+  static constexpr int MC = 32;                             // columns summed at a time
   static constexpr int PITCH = MC + 4;
   static constexpr int RING = 0;
   static constexpr int SUM = RING + WARPS * STAGES * STAGE_BYTES;
@@ -40,11 +47,10 @@ struct Smem {
   static constexpr int BYTES = ML + 2 * WARPS * ROWS * 4;
 };
 
-template <bool BF16, int D, int MT>
-__global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255) attn_mma_kernel(const __grid_constant__ AttnParams p) {
+template <bool BF16, int D>
+__global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnParams p) {
   using Op = typename std::conditional<BF16, Bf16Op, F16Op>::type;
-  using S = Smem<D, MT>;
-  constexpr int ROWS = S::ROWS;
+  using S = Smem<D>;
   constexpr int CH = D / 8;   // 16-byte chunks of a row
   constexpr int KS = D / 16;  // k steps of q . K
   constexpr int NT = D / 8;   // column tiles of O
@@ -106,10 +112,10 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
     }
   };
 
-  uint32_t qf[MT][KS][4];
-  float o[MT][NT][4];
-  float m[MT][2], l[MT][2];
-  uint64_t bits[MT][2];
+  uint32_t qf[KS][4];
+  float o[NT][4];
+  float m[2], l[2];
+  uint64_t bits[2];
   bool fresh_item = true;
   int64_t seg_u = u0;  // first unit of the segment
 
@@ -136,28 +142,24 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
       seg_u = u;
       const uint16_t* qb = p.q + cur.b * p.q_sb;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int half = 0; half < 2; ++half) {
+        const int r = cur.rt * ROWS + half * 8 + gr;
+        const bool in = r < p.R;
+        const int t = r / p.g, i = r - t * p.g;
+        const uint16_t* qr = qb + t * p.q_st + (int64_t)(cur.h * p.g + i) * p.q_sh + gt * 2;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = cur.rt * ROWS + mt * 16 + half * 8 + gr;
-          const bool in = r < p.R;
-          const int t = r / p.g, i = r - t * p.g;
-          const uint16_t* qr = qb + t * p.q_st + (int64_t)(cur.h * p.g + i) * p.q_sh + gt * 2;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            qf[mt][ks][half] = in ? *reinterpret_cast<const uint32_t*>(qr + ks * 16) : 0u;
-            qf[mt][ks][2 + half] = in ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 8) : 0u;
-          }
-          bits[mt][half] = in ? attn_bits(p, cur.b, cur.n, r) : 0;
-          m[mt][half] = -INFINITY;
-          l[mt][half] = 0.f;
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[ks][half] = in ? *reinterpret_cast<const uint32_t*>(qr + ks * 16) : 0u;
+          qf[ks][2 + half] = in ? *reinterpret_cast<const uint32_t*>(qr + ks * 16 + 8) : 0u;
         }
+        bits[half] = in ? attn_bits(p, cur.b, cur.n, r) : 0;
+        m[half] = -INFINITY;
+        l[half] = 0.f;
+      }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
     }
 
     cp_async_wait<STAGES - 1>();
@@ -205,90 +207,75 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
     }
 
     // scores
-    float s[MT][2][4];
+    float s[2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const int row = (lane & 7) + ((lane >> 4) << 3);
       const int ch = ks * 2 + ((lane >> 3) & 1);
       uint32_t b0, b1, b2, b3;
       ldmatrix_x4(kt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b0, b1, b2, b3);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        Op::mma(s[mt][0], qf[mt][ks][0], qf[mt][ks][1], qf[mt][ks][2], qf[mt][ks][3], b0, b1, s[mt][0]);
-        Op::mma(s[mt][1], qf[mt][ks][0], qf[mt][ks][1], qf[mt][ks][2], qf[mt][ks][3], b2, b3, s[mt][1]);
-      }
+      Op::mma(s[0], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b0, b1, s[0]);
+      Op::mma(s[1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b2, b3, s[1]);
     }
     if (edge) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t see = attn_seen32(bits[mt][half], j0 + gt * 2 - cur.L);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!(see >> (nt * 8 + e) & 1)) s[mt][nt][2 * half + e] = -INFINITY;
-        }
-    }
-
-    // running softmax
-    uint32_t pf[MT][4];
-    float mx[MT][2];
-    bool grow = false;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float x = fmaxf(fmaxf(s[mt][0][2 * half], s[mt][0][2 * half + 1]),
-                        fmaxf(s[mt][1][2 * half], s[mt][1][2 * half + 1]));
-        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-        mx[mt][half] = x * p.scale_log2;
-        grow |= mx[mt][half] > m[mt][half] + 8.f;
-      }
-    if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float a[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float mn = fmaxf(m[mt][half], mx[mt][half]);
-          a[half] = m[mt][half] == -INFINITY ? 0.f : ex2(m[mt][half] - mn);
-          m[mt][half] = mn;
-          l[mt][half] *= a[half];
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] *= a[e >> 1];
-      }
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float base = m[mt][half] == -INFINITY ? 0.f : m[mt][half];
+        const uint32_t see = attn_seen32(bits[half], j0 + gt * 2 - cur.L);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = s[mt][nt][2 * half + e];
-            x = ex2(fmaf(x, p.scale_log2, -base));
-            l[mt][half] += x;
-          }
+          for (int e = 0; e < 2; ++e)
+            if (!(see >> (nt * 8 + e) & 1)) s[nt][2 * half + e] = -INFINITY;
       }
-      pf[mt][0] = pack16<BF16>(s[mt][0][0], s[mt][0][1]);
-      pf[mt][1] = pack16<BF16>(s[mt][0][2], s[mt][0][3]);
-      pf[mt][2] = pack16<BF16>(s[mt][1][0], s[mt][1][1]);
-      pf[mt][3] = pack16<BF16>(s[mt][1][2], s[mt][1][3]);
     }
+
+    // running softmax
+    uint32_t pf[4];
+    float mx[2];
+    bool grow = false;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float x = fmaxf(fmaxf(s[0][2 * half], s[0][2 * half + 1]),
+                      fmaxf(s[1][2 * half], s[1][2 * half + 1]));
+      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+      mx[half] = x * p.scale_log2;
+      grow |= mx[half] > m[half] + 8.f;
+    }
+    if (__any_sync(0xFFFFFFFFu, grow)) {
+      float a[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float mn = fmaxf(m[half], mx[half]);
+        a[half] = m[half] == -INFINITY ? 0.f : ex2(m[half] - mn);
+        m[half] = mn;
+        l[half] *= a[half];
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][e] *= a[e >> 1];
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float base = m[half] == -INFINITY ? 0.f : m[half];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& x = s[nt][2 * half + e];
+          x = ex2(fmaf(x, p.scale_log2, -base));
+          l[half] += x;
+        }
+    }
+    pf[0] = pack16<BF16>(s[0][0], s[0][1]);
+    pf[1] = pack16<BF16>(s[0][2], s[0][3]);
+    pf[2] = pack16<BF16>(s[1][0], s[1][1]);
+    pf[3] = pack16<BF16>(s[1][2], s[1][3]);
 
     // O += P V
 #pragma unroll
@@ -296,11 +283,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
       const int row = lane & 15, ch = nn * 2 + (lane >> 4);
       uint32_t b0, b1, b2, b3;
       ldmatrix_x4_trans(vt + row * (D * 2) + ((ch ^ (row & 7)) << 4), b0, b1, b2, b3);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        Op::mma(o[mt][2 * nn], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], b0, b1, o[mt][2 * nn]);
-        Op::mma(o[mt][2 * nn + 1], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], b2, b3, o[mt][2 * nn + 1]);
-      }
+      Op::mma(o[2 * nn], pf[0], pf[1], pf[2], pf[3], b0, b1, o[2 * nn]);
+      Op::mma(o[2 * nn + 1], pf[0], pf[1], pf[2], pf[3], b2, b3, o[2 * nn + 1]);
     }
     if (bad) {
       // the non-finite values of V, for the rows that see their nodes
@@ -310,22 +294,20 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
         const int t = j0 + jj - cur.L;
         const int from = (lane & ~3) | ((jj & 7) >> 1);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int half = 0; half < 2; ++half) {
+          const float e0 = jj < 8 ? s[0][2 * half] : s[1][2 * half];
+          const float e1 = jj < 8 ? s[0][2 * half + 1] : s[1][2 * half + 1];
+          const float w = __shfl_sync(0xFFFFFFFFu, jj & 1 ? e1 : e0, from);
+          if (bits[half] >> t & 1) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float e0 = jj < 8 ? s[mt][0][2 * half] : s[mt][1][2 * half];
-            const float e1 = jj < 8 ? s[mt][0][2 * half + 1] : s[mt][1][2 * half + 1];
-            const float w = __shfl_sync(0xFFFFFFFFu, jj & 1 ? e1 : e0, from);
-            if (bits[mt][half] >> t & 1) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float v = unpack16<BF16>(__ldg(vn + t * p.v_st + nt * 8 + gt * 2 + e));
-                  if (!isfinite(v)) o[mt][nt][2 * half + e] += w * v;
-                }
-            }
+              for (int e = 0; e < 2; ++e) {
+                const float v = unpack16<BF16>(__ldg(vn + t * p.v_st + nt * 8 + gt * 2 + e));
+                if (!isfinite(v)) o[nt][2 * half + e] += w * v;
+              }
           }
+        }
       }
     }
     __syncwarp();
@@ -337,30 +319,26 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
       float* s_ml = reinterpret_cast<float*>(smem + S::ML);
       float* s_sum = reinterpret_cast<float*>(smem + S::SUM);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x = l[mt][half];
-          x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-          x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-          if (gt == 0) {
-            const int r = mt * 16 + half * 8 + gr;
-            s_ml[warp * ROWS + r] = m[mt][half];
-            s_ml[(WARPS + warp) * ROWS + r] = x;
-          }
+      for (int half = 0; half < 2; ++half) {
+        float x = l[half];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+        if (gt == 0) {
+          const int r = half * 8 + gr;
+          s_ml[warp * ROWS + r] = m[half];
+          s_ml[(WARPS + warp) * ROWS + r] = x;
         }
+      }
       __syncthreads();
-      float f[MT][2];
+      float f[2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int half = 0; half < 2; ++half) {
+        const int r = half * 8 + gr;
+        float mn = -INFINITY;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = mt * 16 + half * 8 + gr;
-          float mn = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < WARPS; ++w) mn = fmaxf(mn, s_ml[w * ROWS + r]);
-          f[mt][half] = attn_weight(m[mt][half], s_ml[(WARPS + warp) * ROWS + r], mn);
-        }
+        for (int w = 0; w < WARPS; ++w) mn = fmaxf(mn, s_ml[w * ROWS + r]);
+        f[half] = attn_weight(m[half], s_ml[(WARPS + warp) * ROWS + r], mn);
+      }
       const int64_t item_u = u - cur.tile;  // the item's first unit
       const bool whole = item_u == seg_u && last_tile;
       constexpr int PART = ROWS * (D + 2);
@@ -384,17 +362,15 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
 #pragma unroll
       for (int blk = 0; blk < D / S::MC; ++blk) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int k = 0; k < S::MC / 8; ++k) {
+          const int nt = blk * (S::MC / 8) + k;
 #pragma unroll
-          for (int k = 0; k < S::MC / 8; ++k) {
-            const int nt = blk * (S::MC / 8) + k;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int r = mt * 16 + half * 8 + gr;
-              float2 v = make_float2(o[mt][nt][2 * half] * f[mt][half], o[mt][nt][2 * half + 1] * f[mt][half]);
-              *reinterpret_cast<float2*>(s_sum + (warp * ROWS + r) * S::PITCH + k * 8 + gt * 2) = v;
-            }
+          for (int half = 0; half < 2; ++half) {
+            const int r = half * 8 + gr;
+            float2 v = make_float2(o[nt][2 * half] * f[half], o[nt][2 * half + 1] * f[half]);
+            *reinterpret_cast<float2*>(s_sum + (warp * ROWS + r) * S::PITCH + k * 8 + gt * 2) = v;
           }
+        }
         __syncthreads();
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -432,52 +408,39 @@ __global__ void __launch_bounds__(WARPS * 32, 2) __maxnreg__(MT == 1 ? 216 : 255
   cp_async_wait<0>();
 }
 
-template <bool BF16, int D, int MT>
+template <bool BF16, int D>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attn_mma_kernel<BF16, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Smem<D, MT>::BYTES);
+  return cudaFuncSetAttribute(attn_mma_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
 }
 
-template <bool BF16, int D, int MT>
+template <bool BF16, int D>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
   cfg.blockDim = dim3(WARPS * 32);
-  cfg.dynamicSmemBytes = Smem<D, MT>::BYTES;
+  cfg.dynamicSmemBytes = Smem<D>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_mma_kernel<BF16, D, MT>, p);
+  return cudaLaunchKernelEx(&cfg, attn_mma_kernel<BF16, D>, p);
 }
 
 }  // namespace
 
 int attn_mma_tile_cache_rows() { return TK; }
-int attn_mma_tile_rows(int R) { return R <= 16 ? 16 : 32; }
+int attn_mma_tile_rows() { return ROWS; }
 
 cudaError_t prepare_attn_mma(bool bf16, int D) {
-  cudaError_t e;
-  if (D == 128) {
-    e = bf16 ? prepare<true, 128, 1>() : prepare<false, 128, 1>();
-    if (e == cudaSuccess) e = bf16 ? prepare<true, 128, 2>() : prepare<false, 128, 2>();
-  } else {
-    e = bf16 ? prepare<true, 64, 1>() : prepare<false, 64, 1>();
-    if (e == cudaSuccess) e = bf16 ? prepare<true, 64, 2>() : prepare<false, 64, 2>();
-  }
-  return e;
+  if (D == 128) return bf16 ? prepare<true, 128>() : prepare<false, 128>();
+  return bf16 ? prepare<true, 64>() : prepare<false, 64>();
 }
 
 cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st) {
-  const bool one = attn_mma_tile_rows(p.R) == 16;
-  if (D == 128) {
-    if (bf16) return one ? launch<true, 128, 1>(p, st) : launch<true, 128, 2>(p, st);
-    return one ? launch<false, 128, 1>(p, st) : launch<false, 128, 2>(p, st);
-  }
-  if (bf16) return one ? launch<true, 64, 1>(p, st) : launch<true, 64, 2>(p, st);
-  return one ? launch<false, 64, 1>(p, st) : launch<false, 64, 2>(p, st);
+  if (D == 128) return bf16 ? launch<true, 128>(p, st) : launch<false, 128>(p, st);
+  return bf16 ? launch<true, 64>(p, st) : launch<false, 64>(p, st);
 }
 
 }  // namespace qmm

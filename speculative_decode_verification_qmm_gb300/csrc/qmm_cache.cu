@@ -228,7 +228,7 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
   const int ctas = sms * ATTN_MMA_CTAS_PER_SM;
   // two partials of a CTA's largest row tile each
-  const size_t rows_mma = (size_t)ctas * attn_mma_tile_rows(INT32_MAX);
+  const size_t rows_mma = (size_t)ctas * attn_mma_tile_rows();
   const size_t rows_tc = (size_t)sms * attn_tc_tile_rows(INT32_MAX);
   const size_t ws_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
@@ -339,8 +339,8 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
   const bool bf16 = d.dtype == QMM_DT_BF16;
-  const bool tc = p.R > attn_mma_tile_rows(p.R);
-  const int rows = tc ? attn_tc_tile_rows(p.R) : attn_mma_tile_rows(p.R);
+  const bool tc = p.R > attn_mma_tile_rows();
+  const int rows = tc ? attn_tc_tile_rows(p.R) : attn_mma_tile_rows();
   const int tk = tc ? attn_tc_tile_cache_rows() : attn_mma_tile_cache_rows();
   p.RT = (p.R + rows - 1) / rows;
   p.grid = tc ? h->sm_count : h->sm_count * ATTN_MMA_CTAS_PER_SM;

@@ -38,7 +38,7 @@ constexpr int MAX_T = QMM_TREE_MAX_T;
 constexpr int STAT_THREADS = 256;
 constexpr int STAT_DEPTH = 8;  // steps of a thread's ring
 constexpr int WALK_THREADS = 512;
-constexpr int WALK_DEPTH = 12;  // 16-byte slots of a thread's ring: 96 KB a CTA, two CTAs on an SM
+constexpr int WALK_DEPTH = 8;  // 16-byte slots of a thread's ring: 64 KB a CTA, two CTAs on an SM (12: 73 us for 69)
 constexpr int MAX_CLUSTER = 16;
 constexpr int MAX_CHUNKS = 32;  // parts of a row in the eager statistics
 constexpr int AHEAD = 4;        // nodes whose rows the walk reads at a time
