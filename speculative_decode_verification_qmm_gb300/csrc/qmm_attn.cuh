@@ -48,8 +48,8 @@ struct AttnParams {
   int R;    // rows of an item's head: T * g
   int RT;   // row tiles
   float scale_log2;  // scale * log2(e): the softmax runs in powers of two
-  float* ws;         // partials: [CTA][2][rows of a tile * (D + 2)]
-  int grid;          // CTAs of the launch
+  float* ws;         // partials: [worker][2][rows of a tile * (D + 2)]
+  int grid;          // workers that share the units: CTAs, or warps that work alone
   int64_t row0;      // first row of the layer in the pools' tensor maps
   int* status;
   uint64_t wait_limit_ns;

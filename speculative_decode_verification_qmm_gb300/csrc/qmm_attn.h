@@ -22,12 +22,13 @@ int host_cuda_fail(cudaError_t e);
 cudaError_t host_pool_map(void* map, const void* base, int64_t rows, int D, int box_rows, bool f16);
 
 // Rows of an item's tile for R rows, and cache rows of a unit.  mma.sync kernel:
-// two CTAs per SM.
+// two CTAs per SM; solo: each warp works alone, for many short items.
 constexpr int ATTN_MMA_CTAS_PER_SM = 2;
 int attn_mma_tile_rows();
-int attn_mma_tile_cache_rows();
+int attn_mma_tile_cache_rows(bool solo);
+int attn_mma_workers(int sms, bool solo);  // AttnParams::grid
 cudaError_t prepare_attn_mma(bool bf16, int D);
-cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st);
+cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, bool solo, cudaStream_t st);
 
 // tcgen05 kernel (more rows than the mma.sync kernel's tile), one CTA per SM; kmap, vmap: host_pool_map with boxes of 16 rows.
 int attn_tc_tile_rows(int R);

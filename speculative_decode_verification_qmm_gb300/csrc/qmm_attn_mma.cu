@@ -13,6 +13,8 @@
 // CTA's range, without any barrier between warps; the ring runs across the ends
 // of segments, so a batch of short sequences streams like one long one.  Barriers
 // and shared-memory sums are paid once a segment.
+// Where the segments are many and short, every warp takes units and segments of
+// its own instead (SOLO; the rule and both sides' times stand at attn_solo).
 // Measured: one sequence of 131,071 rows, 20 heads of 128, 16 rows a head, 1.34
 // GB: 203 us without the joining kernel (6.6 TB/s, 97 % of a copy), 210 with it;
 // 32 sequences of 2,048 to 8,192 rows, 8 rows a head: 115 us (6.1 TB/s).  Two row
@@ -31,7 +33,6 @@ namespace {
 
 constexpr int WARPS = 4;
 constexpr int BLK = 16;            // cache rows of a warp's block
-constexpr int TK = WARPS * BLK;    // cache rows of a unit
 constexpr int STAGES = 3;
 constexpr int ROWS = 16;           // rows of an item's tile
 
@@ -47,10 +48,16 @@ struct Smem {
   static constexpr int BYTES = ML + 2 * WARPS * ROWS * 4;
 };
 
-template <bool BF16, int D>
+// SOLO: every warp takes units of its own, of one block each, and ends its
+// segments alone; else the CTA's warps share units of four blocks.
+template <bool SOLO>
+constexpr int UNIT = SOLO ? BLK : WARPS * BLK;
+
+template <bool BF16, int D, bool SOLO>
 __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnParams p) {
   using Op = typename std::conditional<BF16, Bf16Op, F16Op>::type;
   using S = Smem<D>;
+  constexpr int TK = UNIT<SOLO>;
   constexpr int CH = D / 8;   // 16-byte chunks of a row
   constexpr int KS = D / 16;  // k steps of q . K
   constexpr int NT = D / 8;   // column tiles of O
@@ -63,7 +70,8 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
   pdl_wait();
   pdl_trigger();
   int64_t u0, u1;
-  AttnCursor cur = attn_begin<TK>(p, lane, blockIdx.x, u0, u1);
+  const int worker = SOLO ? (int)blockIdx.x * WARPS + warp : (int)blockIdx.x;  // of the p.grid that share the units
+  AttnCursor cur = attn_begin<TK>(p, lane, worker, u0, u1);
   if (u0 >= u1) return;
   AttnCursor ld = cur;
 
@@ -72,7 +80,7 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
 
   // Request the warp's block of the unit at `c` into ring slot `slot`.
   auto request = [&](const AttnCursor& c, int slot) {
-    const int j0 = c.tile * TK + warp * BLK;
+    const int j0 = c.tile * TK + (SOLO ? 0 : warp * BLK);
     const uint32_t dst = ring + slot * S::STAGE_BYTES;
     const uint16_t *kb = p.k_pool, *vb = p.v_pool;
     bool have = false;
@@ -166,7 +174,7 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
     __syncwarp();
 
     const uint32_t kt = ring + slot * S::STAGE_BYTES, vt = kt + S::BLK_BYTES;
-    const int j0 = cur.tile * TK + warp * BLK;
+    const int j0 = cur.tile * TK + (SOLO ? 0 : warp * BLK);
     const bool edge = j0 + BLK > cur.L;  // some rows are nodes, or past the end
     unsigned bad = 0;                    // nodes of the block whose V is not finite
 
@@ -316,107 +324,142 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
     const bool last_tile = cur.tile + 1 == cur.ntiles;
     if (last_tile || u + 1 == u1) {
       // ------------------------------------------------ end of the segment
-      float* s_ml = reinterpret_cast<float*>(smem + S::ML);
-      float* s_sum = reinterpret_cast<float*>(smem + S::SUM);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x = l[half];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
-        if (gt == 0) {
-          const int r = half * 8 + gr;
-          s_ml[warp * ROWS + r] = m[half];
-          s_ml[(WARPS + warp) * ROWS + r] = x;
-        }
-      }
-      __syncthreads();
-      float f[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = half * 8 + gr;
-        float mn = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) mn = fmaxf(mn, s_ml[w * ROWS + r]);
-        f[half] = attn_weight(m[half], s_ml[(WARPS + warp) * ROWS + r], mn);
-      }
       const int64_t item_u = u - cur.tile;  // the item's first unit
       const bool whole = item_u == seg_u && last_tile;
       constexpr int PART = ROWS * (D + 2);
-      const int my_slot = item_u >= u0 ? 1 : 0;  // the item begins in this CTA
-      float* part = p.ws + ((int64_t)blockIdx.x * 2 + my_slot) * PART;
-      // each thread sums one float4 of a column block over the warps
-      const int cr = tid / (S::MC / 4), cc = (tid % (S::MC / 4)) * 4;
-      float cm = -INFINITY, cl = 0.f;
+      // slot 1: the item begins in this worker's range
+      float* part = p.ws + ((int64_t)worker * 2 + (item_u >= u0 ? 1 : 0)) * PART;
+      if constexpr (SOLO) {
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) cm = fmaxf(cm, s_ml[w * ROWS + cr]);
+        for (int half = 0; half < 2; ++half) {
+          float x = l[half];
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+          const int lr = half * 8 + gr, r = cur.rt * ROWS + lr;
+          if (whole) {
+            const int t = r / p.g, i = r - t * p.g;
+            if (r >= p.R) continue;
+            const bool live = t < cur.n;
+            const float inv = live && x != 0.f ? 1.f / x : 0.f;
+            uint16_t* to = p.out + cur.b * p.o_sb + t * p.o_st + (int64_t)(cur.h * p.g + i) * p.o_sh + gt * 2;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float lw = s_ml[(WARPS + w) * ROWS + cr];
-        cl += lw * attn_weight(s_ml[w * ROWS + cr], lw, cm);
-      }
-      const int r_out = cur.rt * ROWS + cr;
-      const int t_out = r_out / p.g, i_out = r_out - t_out * p.g;
-      const bool in_out = r_out < p.R, live_out = in_out && t_out < cur.n;
-      uint16_t* orow = p.out + cur.b * p.o_sb + t_out * p.o_st + (int64_t)(cur.h * p.g + i_out) * p.o_sh;
-      const float inv = live_out && cl != 0.f ? 1.f / cl : 0.f;
+            for (int nt = 0; nt < NT; ++nt)
+              *reinterpret_cast<uint32_t*>(to + nt * 8) =
+                  inv != 0.f ? pack16<BF16>(o[nt][2 * half] * inv, o[nt][2 * half + 1] * inv) : 0u;
+            if (p.lse && gt == 0)
+              p.lse[((int64_t)cur.b * p.T + t) * p.Hq + cur.h * p.g + i] =
+                  live ? (m[half] + log2f(x)) * 0.69314718055994531f : -INFINITY;
+          } else {
 #pragma unroll
-      for (int blk = 0; blk < D / S::MC; ++blk) {
+            for (int nt = 0; nt < NT; ++nt)
+              *reinterpret_cast<float2*>(part + lr * D + nt * 8 + gt * 2) =
+                  make_float2(o[nt][2 * half], o[nt][2 * half + 1]);
+            if (gt == 0) {
+              part[ROWS * D + lr] = m[half];
+              part[ROWS * D + ROWS + lr] = x;
+            }
+          }
+        }
+        fresh_item = true;
+      } else {
+        float* s_ml = reinterpret_cast<float*>(smem + S::ML);
+        float* s_sum = reinterpret_cast<float*>(smem + S::SUM);
 #pragma unroll
-        for (int k = 0; k < S::MC / 8; ++k) {
-          const int nt = blk * (S::MC / 8) + k;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < 2; ++half) {
+          float x = l[half];
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+          x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+          if (gt == 0) {
             const int r = half * 8 + gr;
-            float2 v = make_float2(o[nt][2 * half] * f[half], o[nt][2 * half + 1] * f[half]);
-            *reinterpret_cast<float2*>(s_sum + (warp * ROWS + r) * S::PITCH + k * 8 + gt * 2) = v;
+            s_ml[warp * ROWS + r] = m[half];
+            s_ml[(WARPS + warp) * ROWS + r] = x;
           }
         }
         __syncthreads();
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float f[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = half * 8 + gr;
+          float mn = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) mn = fmaxf(mn, s_ml[w * ROWS + r]);
+          f[half] = attn_weight(m[half], s_ml[(WARPS + warp) * ROWS + r], mn);
+        }
+        // each thread sums one float4 of a column block over the warps
+        const int cr = tid / (S::MC / 4), cc = (tid % (S::MC / 4)) * 4;
+        float cm = -INFINITY, cl = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) cm = fmaxf(cm, s_ml[w * ROWS + cr]);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(s_sum + (w * ROWS + cr) * S::PITCH + cc);
-          a.x += v.x;
-          a.y += v.y;
-          a.z += v.z;
-          a.w += v.w;
+          const float lw = s_ml[(WARPS + w) * ROWS + cr];
+          cl += lw * attn_weight(s_ml[w * ROWS + cr], lw, cm);
         }
-        if (!whole) {
-          *reinterpret_cast<float4*>(part + cr * D + blk * S::MC + cc) = a;
-        } else if (in_out) {
-          uint2 v = make_uint2(0u, 0u);
-          if (inv != 0.f) v = make_uint2(pack16<BF16>(a.x * inv, a.y * inv), pack16<BF16>(a.z * inv, a.w * inv));
-          *reinterpret_cast<uint2*>(orow + blk * S::MC + cc) = v;
+        const int r_out = cur.rt * ROWS + cr;
+        const int t_out = r_out / p.g, i_out = r_out - t_out * p.g;
+        const bool in_out = r_out < p.R, live_out = in_out && t_out < cur.n;
+        uint16_t* orow = p.out + cur.b * p.o_sb + t_out * p.o_st + (int64_t)(cur.h * p.g + i_out) * p.o_sh;
+        const float inv = live_out && cl != 0.f ? 1.f / cl : 0.f;
+#pragma unroll
+        for (int blk = 0; blk < D / S::MC; ++blk) {
+#pragma unroll
+          for (int k = 0; k < S::MC / 8; ++k) {
+            const int nt = blk * (S::MC / 8) + k;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int r = half * 8 + gr;
+              float2 v = make_float2(o[nt][2 * half] * f[half], o[nt][2 * half + 1] * f[half]);
+              *reinterpret_cast<float2*>(s_sum + (warp * ROWS + r) * S::PITCH + k * 8 + gt * 2) = v;
+            }
+          }
+          __syncthreads();
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(s_sum + (w * ROWS + cr) * S::PITCH + cc);
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+          }
+          if (!whole) {
+            *reinterpret_cast<float4*>(part + cr * D + blk * S::MC + cc) = a;
+          } else if (in_out) {
+            uint2 v = make_uint2(0u, 0u);
+            if (inv != 0.f) v = make_uint2(pack16<BF16>(a.x * inv, a.y * inv), pack16<BF16>(a.z * inv, a.w * inv));
+            *reinterpret_cast<uint2*>(orow + blk * S::MC + cc) = v;
+          }
+          __syncthreads();
+        }
+        if (whole) {
+          if (p.lse && in_out && cc == 0)
+            p.lse[((int64_t)cur.b * p.T + t_out) * p.Hq + cur.h * p.g + i_out] =
+                live_out ? (cm + log2f(cl)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          if (cc == 0) {
+            part[ROWS * D + cr] = cm;
+            part[ROWS * D + ROWS + cr] = cl;
+          }
         }
         __syncthreads();
+        fresh_item = true;
       }
-      if (whole) {
-        if (p.lse && in_out && cc == 0)
-          p.lse[((int64_t)cur.b * p.T + t_out) * p.Hq + cur.h * p.g + i_out] =
-              live_out ? (cm + log2f(cl)) * 0.69314718055994531f : -INFINITY;
-      } else {
-        if (cc == 0) {
-          part[ROWS * D + cr] = cm;
-          part[ROWS * D + ROWS + cr] = cl;
-        }
-      }
-      __syncthreads();
-      fresh_item = true;
     }
     attn_next<TK>(p, cur);
   }
   cp_async_wait<0>();
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool SOLO>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attn_mma_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
+  return cudaFuncSetAttribute(attn_mma_kernel<BF16, D, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Smem<D>::BYTES);
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool SOLO>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.grid);
+  cfg.gridDim = dim3((unsigned)(SOLO ? p.grid / WARPS : p.grid));
   cfg.blockDim = dim3(WARPS * 32);
   cfg.dynamicSmemBytes = Smem<D>::BYTES;
   cfg.stream = st;
@@ -425,22 +468,34 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_mma_kernel<BF16, D>, p);
+  return cudaLaunchKernelEx(&cfg, attn_mma_kernel<BF16, D, SOLO>, p);
+}
+
+template <bool BF16, int D>
+cudaError_t prepare_both() {
+  const cudaError_t e = prepare<BF16, D, true>();
+  return e == cudaSuccess ? prepare<BF16, D, false>() : e;
+}
+
+template <bool BF16, int D>
+cudaError_t launch_one(const AttnParams& p, bool solo, cudaStream_t st) {
+  return solo ? launch<BF16, D, true>(p, st) : launch<BF16, D, false>(p, st);
 }
 
 }  // namespace
 
-int attn_mma_tile_cache_rows() { return TK; }
+int attn_mma_tile_cache_rows(bool solo) { return solo ? UNIT<true> : UNIT<false>; }
 int attn_mma_tile_rows() { return ROWS; }
+int attn_mma_workers(int sms, bool solo) { return sms * ATTN_MMA_CTAS_PER_SM * (solo ? WARPS : 1); }
 
 cudaError_t prepare_attn_mma(bool bf16, int D) {
-  if (D == 128) return bf16 ? prepare<true, 128>() : prepare<false, 128>();
-  return bf16 ? prepare<true, 64>() : prepare<false, 64>();
+  if (D == 128) return bf16 ? prepare_both<true, 128>() : prepare_both<false, 128>();
+  return bf16 ? prepare_both<true, 64>() : prepare_both<false, 64>();
 }
 
-cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, cudaStream_t st) {
-  if (D == 128) return bf16 ? launch<true, 128>(p, st) : launch<false, 128>(p, st);
-  return bf16 ? launch<true, 64>(p, st) : launch<false, 64>(p, st);
+cudaError_t launch_attn_mma(const AttnParams& p, bool bf16, int D, bool solo, cudaStream_t st) {
+  if (D == 128) return bf16 ? launch_one<true, 128>(p, solo, st) : launch_one<false, 128>(p, solo, st);
+  return bf16 ? launch_one<true, 64>(p, solo, st) : launch_one<false, 64>(p, solo, st);
 }
 
 }  // namespace qmm

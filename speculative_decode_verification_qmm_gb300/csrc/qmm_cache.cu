@@ -196,6 +196,20 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const __grid_constan
   }
 }
 
+// Whether the mma.sync kernel's warps work alone (p.R within its tile).  A warp
+// alone ends a segment without the CTA's barriers and sums, but has one block of
+// the cache in every unit where four warps share one.  So it is for many short
+// sequences: more than three items of 128 values (six of 64) for each CTA, and at
+// most SOLO_MAX rows.  Measured, alone against shared, in us: 128 sequences of up
+// to 30 / 120 / 300 / 600 rows, 8 nodes, 20 heads of 128, two rows a node: 47 : 59,
+// 61 : 91, 83 : 117, 120 : 145; 8 heads, one row: 16 : 23, 23 : 32, 31 : 41, 46 :
+// 54.  Past the limits: 48 sequences of up to 1,500 and 4,000 rows, 20 heads: 101 :
+// 100, 223 : 216; 16 sequences of up to 120 and 600 rows: 23 : 17, 35 : 29.
+constexpr int SOLO_MAX = 1024;
+bool attn_solo(const AttnParams& p, int64_t cap, int ctas, int D) {
+  return cap <= SOLO_MAX && (int64_t)p.B * p.Hkv * D >= (int64_t)3 * 128 * ctas;
+}
+
 }  // namespace
 
 extern "C" {
@@ -226,9 +240,8 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   h->sm_count = sms;
   while ((1 << h->page_shift) < d->page_size) ++h->page_shift;
   cudaStream_t st = (cudaStream_t)stream;
-  const int ctas = sms * ATTN_MMA_CTAS_PER_SM;
   // two partials of a CTA's largest row tile each
-  const size_t rows_mma = (size_t)ctas * attn_mma_tile_rows();
+  const size_t rows_mma = (size_t)attn_mma_workers(sms, true) * attn_mma_tile_rows();
   const size_t rows_tc = (size_t)sms * attn_tc_tile_rows(INT32_MAX);
   const size_t ws_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
@@ -340,14 +353,16 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   p.wait_limit_ns = h->wait_limit_ns;
   const bool bf16 = d.dtype == QMM_DT_BF16;
   const bool tc = p.R > attn_mma_tile_rows();
+  const bool solo = !tc && attn_solo(p, (int64_t)a->table_width << h->page_shift, attn_mma_workers(h->sm_count, false),
+                                     d.head_dim);
   const int rows = tc ? attn_tc_tile_rows(p.R) : attn_mma_tile_rows();
-  const int tk = tc ? attn_tc_tile_cache_rows() : attn_mma_tile_cache_rows();
+  const int tk = tc ? attn_tc_tile_cache_rows() : attn_mma_tile_cache_rows(solo);
   p.RT = (p.R + rows - 1) / rows;
-  p.grid = tc ? h->sm_count : h->sm_count * ATTN_MMA_CTAS_PER_SM;
+  p.grid = tc ? h->sm_count : attn_mma_workers(h->sm_count, solo);
   p.row0 = (int64_t)a->layer * d.n_pages * d.n_kv_heads * d.page_size;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = tc ? launch_attn_tc(p, bf16, d.head_dim, &h->kmap, &h->vmap, st)
-                     : launch_attn_mma(p, bf16, d.head_dim, st);
+                     : launch_attn_mma(p, bf16, d.head_dim, solo, st);
   if (e == cudaSuccess) e = launch_attn_join(p, bf16, d.head_dim, tk, rows, st);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }

@@ -235,6 +235,93 @@ def test_bad_lengths_and_pages_are_reported(T, Hq):
         check(out[::2], lse[::2], ref[::2], lref[::2], tol[::2], ltol[::2])
 
 
+def _many(B, T, seed=20, **kw):
+    """Sequences enough for every warp of the GPU to work alone: B * 8 heads of 128, 16 * B of 64."""
+    rng = np.random.default_rng(seed)
+    lens = [EDGES[i % len(EDGES)] for i in range(B)]
+    counts = [int(x) for x in rng.integers(0, T + 1, B)]
+    return Attention("bf16", 128, kw.pop("Hq", 8), 8, T, kw.pop("page", 16), lens, counts, tree=True, seed=seed, **kw)
+
+
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,T,page,B", [
+    ("bf16", 128, 8, 8, 1, 16, 120),
+    ("f16", 128, 16, 8, 8, 32, 120),    # 16 rows
+    ("bf16", 128, 24, 8, 5, 64, 120),   # 15 rows
+    ("f16", 128, 64, 8, 1, 128, 120),
+    ("bf16", 64, 40, 20, 7, 16, 100),   # 14 rows
+    ("f16", 64, 20, 20, 2, 16, 100),
+])
+def test_many_sequences(dtype, D, Hq, Hkv, T, page, B):
+    rng = np.random.default_rng(T)
+    lens = [EDGES[i % len(EDGES)] for i in range(B - 1)] + [900]
+    counts = [int(x) for x in rng.integers(0, T + 1, B)]
+    a = Attention(dtype, D, Hq, Hkv, T, page, lens, counts, tree=True, seed=D + T, sigma=1.5)
+    cache = a.make_cache(q)
+    first = assert_attention(a, cache, q)
+    again = a.call(cache)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
+def test_many_sequences_unseen_rows_hold_anything(fill):
+    T, bad = 6, 2
+    a = _many(120, T, seed=21, fill=fill)
+    seen = a.seen.copy()
+    seen[:, :, bad] = False
+    seen[:, bad, bad] = True
+    seen[:, 3] = False  # a row that sees no node
+    a.set_seen(seen)
+    a.k[:, bad, :, 3] = fill
+    a.v[:, bad, :, 5::7] = fill
+    for b, n in enumerate(a.counts):
+        a.q[b, n:], a.k[b, n:], a.v[b, n:] = fill, fill, fill
+    out, lse = a.call(a.make_cache(q))
+    a.k[:, bad], a.v[:, bad] = 0, 0
+    for b, n in enumerate(a.counts):
+        a.q[b, n:], a.k[b, n:], a.v[b, n:] = 0, 0, 0
+    ref, lref, tol, ltol = a.reference()
+    rows = [t for t in range(T) if t != bad]
+    check(out[:, rows], lse[:, rows], ref[:, rows], lref[:, rows], tol[:, rows], ltol[:, rows])
+
+
+def test_many_sequences_seen_nonfinite_values_arrive():
+    a = _many(120, 6, seed=22)
+    a.counts = [6] * 120
+    a.v[:, 1, :, 9] = float("inf")
+    a.v[:, 3, :, 20] = float("nan")
+    out, _ = a.call(a.make_cache(q))
+    sees1, sees3 = torch.from_numpy(a.seen[:, :, 1]).cuda(), torch.from_numpy(a.seen[:, :, 3]).cuda()
+    assert torch.equal(torch.isinf(out[..., 9]), sees1[:, :, None].expand(-1, -1, 8))
+    assert torch.equal(torch.isnan(out[..., 20]), sees3[:, :, None].expand(-1, -1, 8))
+
+
+def test_many_sequences_strides():
+    a = _many(120, 5, seed=23, Hq=16, page=32, strided=True)
+    assert not a.q.is_contiguous() and not a.v.is_contiguous()
+    wide = torch.full((120, 5, 17, 136), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert_attention(a, a.make_cache(q), q, out=wide[:, :, :16, :128])
+    assert (wide[:, :, 16] == 7).all() and (wide[:, :, :, 128:] == 7).all()
+
+
+def test_many_sequences_bad_lengths_and_pages_are_reported():
+    a = _many(120, 3, seed=24)
+    ref, lref, tol, ltol = a.reference()
+    good_table, good_lens = a.table.clone(), list(a.lens)
+    cache = a.make_cache(q)
+    for table_edit, lens_edit in (((2, 0, 10 ** 6), None), ((4, 0, -1), None), (None, -5), (None, 10 ** 6)):
+        a.table, a.lens = good_table.clone(), list(good_lens)
+        at = table_edit[0] if table_edit else 1
+        if table_edit:
+            a.table[at, table_edit[1]] = table_edit[2]
+        else:
+            a.lens[at] = lens_edit
+        out, lse = a.call(cache)
+        assert cache.sync_status() == q.QMM_ERR_INDEX
+        assert cache.sync_status() == q.QMM_OK
+        keep = [b for b in range(120) if b != at]
+        check(out[keep], lse[keep], ref[keep], lref[keep], tol[keep], ltol[keep])
+
+
 @pytest.mark.parametrize("T,Hq", [(16, 8), (64, 8)])
 def test_expired_waits_are_reported(T, Hq):
     """Waits that give up at once: the call ends, the status says so, and the
