@@ -176,7 +176,9 @@ def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=Non
     qmm_verify_sample.  accept[:, 0] nodes are accepted, path[b, :accept[b, 0]]
     names them, accept[:, 1] is the token that follows them."""
     import torch
-    import torch
+    if stream is not None:  # the results are allocated on the stream that writes them
+        with torch.cuda.stream(stream):
+            return verify_sample(target, draft, tokens, u, noise, parents, temperature, n_tokens)
     if target.dim() != 3 or not target.is_cuda:
         raise ValueError("target must be a CUDA tensor [B, T, V]")
     B, T, V = target.shape
@@ -201,9 +203,7 @@ def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=Non
     accept = torch.empty((B, 2), dtype=i32, device=dev)
     path = torch.empty((B, T), dtype=i32, device=dev)
     ws = torch.empty(qmm_verify_sample_workspace(B, T, V), dtype=torch.uint8, device=dev)
-    qmm_verify_sample(target, draft, tokens, u, noise, accept, path, ws, parents, temperature, n_tokens, stream)
-    if stream is not None:
-        ws.record_stream(stream)
+    qmm_verify_sample(target, draft, tokens, u, noise, accept, path, ws, parents, temperature, n_tokens)
     return accept, path
 
 
@@ -260,7 +260,9 @@ class PagedCache:
         """(out, lse): the nodes' attention over cache and tree; their keys and
         values are written behind the cached rows.  See qmm_tree_attention."""
         import torch
-        import torch
+        if stream is not None:  # the results are allocated on the stream that writes them
+            with torch.cuda.stream(stream):
+                return self.attend(layer, q, k, v, page_table, lens, mask, n_tokens, scale, out, lse)
         if q.dim() != 4:
             raise ValueError("q must be [B, T, n_q_heads, head_dim]")
         B, T = q.shape[:2]
@@ -282,13 +284,16 @@ class PagedCache:
             _strided("mask", mask, torch.int64, (B, T))
         if n_tokens is not None:
             _flat("n_tokens", n_tokens, torch.int32, (B,))
-        qmm_tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale, stream)
+        qmm_tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale)
         return out, lse
 
     def commit(self, page_table, lens, path, accept, lens_out=None, stream=None):
         """The new lengths: the accepted branches' rows move behind the cached ones
         in every layer.  See qmm_cache_commit."""
         import torch
+        if stream is not None:  # lens_out is allocated on the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.commit(page_table, lens, path, accept, lens_out)
         B, i32 = lens.shape[0], torch.int32
         if lens_out is None:
             lens_out = torch.empty_like(lens)
@@ -299,7 +304,7 @@ class PagedCache:
             raise ValueError("path must be [B, T]")
         _strided("path", path, i32, (B, path.shape[1]))
         _flat("accept", accept, i32, (B, 2))
-        qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out, stream)
+        qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out)
         return lens_out
 
     def copy_pages(self, src, dst, rows=None, stream=None):
