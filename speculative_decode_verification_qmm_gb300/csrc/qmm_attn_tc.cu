@@ -1,4 +1,4 @@
-// qmm_attn_tc.cu -- tree attention for more than 32 rows per key/value head, on
+// qmm_attn_tc.cu -- tree attention for more than 16 rows per key/value head, on
 // the tcgen05 tensor cores: one pass over the cached rows with a running
 // softmax.
 //
@@ -12,7 +12,7 @@
 // behind the true maximum by up to 8 (P <= 256): O is rescaled, by the softmax
 // warps and through their registers, only when a row of the warp grows more.
 //   warps 0 .. 4 NQ - 1   softmax, rescaling, output (four warps a row tile)
-//   two warps             issue the MMAs: one all Q K^T, the other all P V
+//   two warps             issue the MMAs
 //   two warps             load K and V tiles, one ring each: tensor copies of 16
 //                         rows, which lie in one page; cp.async for the tree's
 //                         nodes, from the caller's rows (and on to the cache), and
@@ -21,17 +21,19 @@
 // SM's share of the HBM stream, and its two products 0.55 us of the tensor cores
 // and its 16,384 exponentials about as long: with one row tile the stream is the
 // bound, and S is double-buffered so that Q K^T of the next tile runs under the
-// softmax.  With two, each tile of K and V serves 256 rows, and the products of
-// one row tile run under the softmax of the other.  The issue of an MMA blocks
-// until the one before it is nearly done, so that a barrier test between two
-// products leaves the tensor cores idle for its 130 cycles, and a product whose
-// operands are ready waits behind one whose are not: hence two issuers.
-// S is computed SW cache rows at a time into two buffers, so that the next
-// Q K^T runs under the softmax of the last; SW is the whole tile for NQ = 1, and
-// half of it for NQ = 2, whose tensor memory (512 columns) would not hold two
-// whole S and O of both row tiles.  With one whole S each, a step took 5,700
-// cycles of which the tensor cores worked 2,048.  P overwrites the first half of
-// its S.
+// softmax.  One warp then issues all Q K^T, another all P V: the issue of an MMA
+// blocks until the one before it is nearly done, and a product whose operands are
+// ready would wait behind one whose are not.
+// With two row tiles each tile of K and V serves 256 rows, and tensor memory (512
+// columns) holds one S and O of each.  One warp issues everything: P V of a row
+// tile and Q K^T of its next cache tile back to back, which MMAs of one thread may
+// without a barrier between them, then the same for the other row tile, whose
+// softmax ran meanwhile.  The softmax hands P over in two steps of SW columns, so
+// that P V of the first runs under the softmax of the second; a step's P
+// overwrites the first half of its S.  Q K^T over all 128 columns at once: over
+// 64 it takes as long.  Before, two issuers and S in two buffers of 64 columns
+// took 130 us for 4 sequences x 16,384 rows, 64 nodes, 64 heads on 8, this 125 us
+// (1,100 TFLOP/s).
 // Every wait is bounded; on a timeout the CTA records it, its roles run out of
 // their loops without waiting, its copies and MMAs in flight are drained and
 // tensor memory is freed.
@@ -115,11 +117,12 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
                    const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D, NQ>;
   constexpr int ROWS = NQ * 128;
-  constexpr int SW = TK / NQ, SUB = TK / SW;  // columns of S, steps of a tile
-  constexpr uint32_t IDESC_S = tc_idesc_n(BF16 ? 1u : 0u, SW);
+  constexpr int SW = TK / NQ, SUB = TK / SW;  // columns of a step's P, steps of a tile
+  constexpr int NB = 2 / NQ;                  // buffers of S of a row tile
+  constexpr uint32_t IDESC_S = tc_idesc_n(BF16 ? 1u : 0u, TK);
   constexpr uint32_t IDESC_O = tc_idesc_n(BF16 ? 1u : 0u, D) | (1u << 16);  // B along N
-  // tensor memory columns: S twice, then O, of each row tile
-  constexpr uint32_t COL_O = 2 * SW;
+  // tensor memory columns: NB times S, then O, of each row tile
+  constexpr uint32_t COL_O = NB * TK;
   constexpr uint32_t COL_Q = 256;  // of the second row tile
   constexpr int MMA_WARP = NQ * 4, LOAD_WARP = MMA_WARP + 2;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -352,61 +355,90 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         }
         return ok;
       };
-      int n = 0, seg = 0;          // steps and segments so far (n: parities only)
+      // S of row tile q and the K tile in `slot`, into column d
+      auto product_s = [&](int q, int slot, uint32_t d) {
+        const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + slot * S::TILE);
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (uint32_t)(kk >> 2) * (S::HALF >> 4) + (uint32_t)(kk & 3) * (32 >> 4);
+            mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
+          }
+        }
+      };
+      // O of row tile q += P of a step (its part of the V tile in `slot`)
+      auto product_o = [&](int q, int slot, int step, bool first) {
+        const uint32_t a = tmem + q * COL_Q + (step & 1) * SW, d = tmem + q * COL_Q + COL_O;
+        const uint32_t b = desc_lo_mn(base + S::V + slot * S::TILE + step % SUB * SW * 128, S::HALF);
+        tc_fence_after();
+        if (leader) {
+          mma_ts(d, a, b, IDESC_O, !first);
+#pragma unroll
+          for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
+          tc_commit(b_odone + 8 * q);
+        }
+      };
+      int n = 0, seg = 0;          // tiles and segments so far (n: parities only)
       int slot = 0, round = 0;     // of the tile of K or V
+      int vslot = 0, vround = 0;   // of the tile of V, where one warp issues both
       for (int64_t u = u0; u < u1 && ok; ++seg) {
-        const int count = segment(u), steps = count * SUB;
-        if (who == 0) {
-          if (!need(b_qfull, seg)) break;
-          for (int j = 0; j < steps && ok; ++j, ++n) {
-            const int sub = j % SUB;
-            if (sub == 0 && !need(b_kfull + 8 * slot, round)) break;
-            const uint32_t b = desc_lo(base + S::K + slot * S::TILE + sub * SW * 128);
+        const int count = segment(u);
+        if constexpr (NQ == 2) {
+          // O += P V of a row tile, then S of its next tile, then the other row tile
+          for (int j = -1; who == 0 && j < count && ok; ++j) {
+            if (j < 0 && !need(b_qfull, seg)) break;
+            for (int q = 0; q < 2 && ok; ++q) {
+              if (j >= 0) {
+                if (q == 0 && !need(b_vfull + 8 * vslot, vround)) break;
+                if (j == 0 && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) break;
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              const int buf = 2 * q + (n & 1);
-              // its S held P of two steps ago until that product was done
-              if (n >= 2 && !need(b_sfree + 8 * buf, (n >> 1) - 1)) break;
-              const uint32_t a = desc_lo(base + S::Q + q * S::TILE), d = tmem + q * COL_Q + (n & 1) * SW;
-              tc_fence_after();
-              if (leader) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t o = (uint32_t)(kk >> 2) * (S::HALF >> 4) + (uint32_t)(kk & 3) * (32 >> 4);
-                  mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
+                for (int sub = 0; sub < SUB; ++sub) {
+                  if (!need(b_pfull + 8 * (2 * q + sub), n)) break;
+                  product_o(q, vslot, sub, j == 0 && sub == 0);
                 }
-                tc_commit(b_sfull + 8 * buf);
+                if (!ok) break;
+                if (leader && j + 1 == count) tc_commit(b_olast + 8 * q);
+              }
+              if (j + 1 < count) {
+                if (q == 0 && !need(b_kfull + 8 * slot, round)) break;
+                product_s(q, slot, tmem + q * COL_Q);
+                if (leader) tc_commit(b_sfull + 8 * (2 * q));
               }
             }
             if (!ok) break;
-            if (leader && sub == SUB - 1) tc_commit(b_kempty + 8 * slot);
-            if (leader && j + 1 == steps) tc_commit(b_qempty);
-            if (sub == SUB - 1 && ++slot == S::KS) slot = 0, ++round;
+            if (j >= 0) {
+              if (leader) tc_commit(b_vempty + 8 * vslot);
+              if (++vslot == S::VS) vslot = 0, ++vround;
+              ++n;
+            }
+            if (j + 1 < count) {
+              if (leader) tc_commit(b_kempty + 8 * slot);
+              if (leader && j + 2 == count) tc_commit(b_qempty);
+              if (++slot == S::KS) slot = 0, ++round;
+            }
+          }
+        } else if (who == 0) {
+          if (!need(b_qfull, seg)) break;
+          for (int j = 0; j < count; ++j, ++n) {
+            if (!need(b_kfull + 8 * slot, round)) break;
+            // its S held P of two tiles ago until the product of that was done
+            if (n >= 2 && !need(b_sfree + 8 * (n & 1), (n >> 1) - 1)) break;
+            product_s(0, slot, tmem + (n & 1) * TK);
+            if (leader) tc_commit(b_sfull + 8 * (n & 1));
+            if (leader) tc_commit(b_kempty + 8 * slot);
+            if (leader && j + 1 == count) tc_commit(b_qempty);
+            if (++slot == S::KS) slot = 0, ++round;
           }
         } else {
-          for (int j = 0; j < steps && ok; ++j, ++n) {
-            const int sub = j % SUB;
-            if (sub == 0 && !need(b_vfull + 8 * slot, round)) break;
-            const uint32_t b = desc_lo_mn(base + S::V + slot * S::TILE + sub * SW * 128, S::HALF);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              const int buf = 2 * q + (n & 1);
-              if (!need(b_pfull + 8 * buf, n >> 1)) break;
-              if (j == 0 && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) break;
-              const uint32_t a = tmem + q * COL_Q + (n & 1) * SW, d = tmem + q * COL_Q + COL_O;
-              tc_fence_after();
-              if (leader) {
-                mma_ts(d, a, b, IDESC_O, j > 0);
-#pragma unroll
-                for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
-                tc_commit(b_odone + 8 * q);
-                tc_commit(b_sfree + 8 * buf);
-                if (j + 1 == steps) tc_commit(b_olast + 8 * q);
-              }
-            }
-            if (!ok) break;
-            if (leader && sub == SUB - 1) tc_commit(b_vempty + 8 * slot);
-            if (sub == SUB - 1 && ++slot == S::VS) slot = 0, ++round;
+          for (int j = 0; j < count; ++j, ++n) {
+            if (!need(b_vfull + 8 * slot, round) || !need(b_pfull + 8 * (n & 1), n >> 1)) break;
+            if (j == 0 && seg > 0 && !need(b_oempty, seg - 1)) break;
+            product_o(0, slot, n, j == 0);
+            if (leader) tc_commit(b_sfree + 8 * (n & 1));
+            if (leader && j + 1 == count) tc_commit(b_olast);
+            if (leader) tc_commit(b_vempty + 8 * slot);
+            if (++slot == S::VS) slot = 0, ++round;
           }
         }
         cur.tile += count - 1;
@@ -448,7 +480,8 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         const int n = done + j;
         const int buf = 2 * q + (n & 1);
         const uint32_t t_s = tl + (n & 1) * SW;
-        if (!need(b_sfull + 8 * buf, n >> 1)) continue;
+        if (n % SUB == 0) need(b_sfull + 8 * (2 * q + n / SUB % NB), n / SUB / NB);
+        if (!ok) continue;
         if (idle) {  // no row of the warp is the item's: whatever P is, nobody looks
           if (lane == 0) mbar_arrive(b_pfull + 8 * buf);
           continue;
