@@ -12,7 +12,7 @@
 // behind the true maximum by up to 8 (P <= 256): O is rescaled, by the softmax
 // warps and through their registers, only when a row of the warp grows more.
 //   warps 0 .. 4 NQ - 1   softmax, rescaling, output (four warps a row tile)
-//   two warps             issue the MMAs
+//   two warps (NQ = 2: one) issue the MMAs
 //   two warps             load K and V tiles, one ring each: tensor copies of 16
 //                         rows, which lie in one page; cp.async for the tree's
 //                         nodes, from the caller's rows (and on to the cache), and
@@ -112,7 +112,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
 }
 
 template <bool BF16, int D, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 128, 1)
+__global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
     attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D, NQ>;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
   // tensor memory columns: NB times S, then O, of each row tile
   constexpr uint32_t COL_O = NB * TK;
   constexpr uint32_t COL_Q = 256;  // of the second row tile
-  constexpr int MMA_WARP = NQ * 4, LOAD_WARP = MMA_WARP + 2;
+  constexpr int MMA_WARP = NQ * 4, MMA_WARPS = 2 / NQ, LOAD_WARP = MMA_WARP + MMA_WARPS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = smem_u32(smem);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
       mbar_init(b_olast + 8 * i, 1);
       mbar_init(b_oempty + 8 * i, 4);
     }
-    mbar_init(b_drain, 2);
+    mbar_init(b_drain, MMA_WARPS);
     for (int i = 0; i < BAD_BUFS; ++i) s_bad[i] = 0;
     s_flag[0] = 0;
     if (base & 1023u) {
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(NQ * 128 + 128, 1)
         const int count = segment(u);
         if constexpr (NQ == 2) {
           // O += P V of a row tile, then S of its next tile, then the other row tile
-          for (int j = -1; who == 0 && j < count && ok; ++j) {
+          for (int j = -1; j < count && ok; ++j) {
             if (j < 0 && !need(b_qfull, seg)) break;
             for (int q = 0; q < 2 && ok; ++q) {
               if (j >= 0) {
@@ -668,7 +668,7 @@ template <bool BF16, int D, int NQ>
 cudaError_t launch(const AttnParams& p, const void* kmap, const void* vmap, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.grid);
-  cfg.blockDim = dim3(NQ * 128 + 128);
+  cfg.blockDim = dim3(NQ * 128 + 64 / NQ + 64);
   cfg.dynamicSmemBytes = Smem<D, NQ>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute at;
