@@ -363,7 +363,9 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = tc ? launch_attn_tc(p, bf16, d.head_dim, &h->kmap, &h->vmap, st)
                      : launch_attn_mma(p, bf16, d.head_dim, solo, st);
-  if (e == cudaSuccess) e = launch_attn_join(p, bf16, d.head_dim, tk, rows, st);
+  // items of one unit each are never cut: nothing to join
+  if (e == cudaSuccess && ((int64_t)a->table_width << h->page_shift) > tk)
+    e = launch_attn_join(p, bf16, d.head_dim, tk, rows, st);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }
 

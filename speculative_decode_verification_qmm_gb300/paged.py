@@ -113,15 +113,19 @@ def qmm_tree_attention(h, layer, q, k_new, v_new, page_table, lens, out, lse=Non
     """q, out CUDA [B, T, Hq, D]; k_new, v_new [B, T, Hkv, D]; page_table int32
     [B, pages]; lens, n_tokens int32 [B]; mask int64 [B, T]; lse fp32 [B, T, Hq]
     or None; asynchronous."""
+    _tree_attention(h, layer, q, k_new, v_new, page_table, lens, out, lse, mask, n_tokens, scale, stream, q.stride(),
+                    k_new.stride(), v_new.stride(), out.stride(), page_table.stride(0))
+
+
+def _tree_attention(h, layer, q, k, v, table, lens, out, lse, mask, n_tokens, scale, stream, qs, ks, vs, os, ld_table):
     B, T, _, D = q.shape
-    qs, ks, vs, os = q.stride(), k_new.stride(), v_new.stride(), out.stride()
-    args = _ATTN.pack(
-        _ATTN.size, layer, B, T, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), out.data_ptr(),
+    rc = load().qmm_tree_attention(h, _ATTN.pack(
+        _ATTN.size, layer, B, T, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
         qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], os[0], os[1], os[2],
-        0 if lse is None else lse.data_ptr(), page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+        0 if lse is None else lse.data_ptr(), table.data_ptr(), ld_table, table.shape[1],
         D ** -0.5 if scale is None else scale, lens.data_ptr(), 0 if n_tokens is None else n_tokens.data_ptr(),
-        0 if mask is None else mask.data_ptr(), 0 if mask is None else mask.stride(0))
-    rc = load().qmm_tree_attention(h, args, _stream_ptr(stream, q.device.index))
+        0 if mask is None else mask.data_ptr(), 0 if mask is None else mask.stride(0)),
+        _stream_ptr(stream, q.device.index))
     if rc:
         _check("qmm_tree_attention", rc)
 
@@ -160,12 +164,12 @@ def qmm_verify_sample(target, draft, tokens, u, noise, accept, path, workspace, 
     B, T, V = target.shape
     ts = target.stride()
     ds = (0, 0) if draft is None else draft.stride()
-    opt = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    args = _SAMPLE.pack(
-        _SAMPLE.size, _dtype(target.dtype), B, T, V, target.data_ptr(), ts[0], ts[1], opt(draft), ds[0], ds[1],
-        tokens.data_ptr(), opt(parents), opt(n_tokens), u.data_ptr(), noise.data_ptr(), opt(temperature),
-        accept.data_ptr(), path.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    rc = load().qmm_verify_sample(args, _stream_ptr(stream, target.device.index))
+    rc = load().qmm_verify_sample(_SAMPLE.pack(
+        _SAMPLE.size, _dtype(target.dtype), B, T, V, target.data_ptr(), ts[0], ts[1],
+        0 if draft is None else draft.data_ptr(), ds[0], ds[1], tokens.data_ptr(),
+        0 if parents is None else parents.data_ptr(), 0 if n_tokens is None else n_tokens.data_ptr(), u.data_ptr(),
+        noise.data_ptr(), 0 if temperature is None else temperature.data_ptr(), accept.data_ptr(), path.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size()), _stream_ptr(stream, target.device.index))
     if rc:
         _check("qmm_verify_sample", rc)
 
@@ -190,9 +194,13 @@ def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=Non
         if draft.shape[1] == 0:
             draft = None
     i32, f32, nodes = torch.int32, torch.float32, (B, T)
-    _flat("tokens", tokens, i32, nodes)
-    _flat("u", u, f32, nodes)
-    _flat("noise", noise, f32, (B, V))
+    # the usual call's checks in one expression; what fails is named after it
+    if (tokens.shape != nodes or tokens.dtype is not i32 or not tokens.is_cuda or not tokens.is_contiguous()
+            or u.shape != nodes or u.dtype is not f32 or not u.is_cuda or not u.is_contiguous()
+            or noise.shape != (B, V) or noise.dtype is not f32 or not noise.is_cuda or not noise.is_contiguous()):
+        _flat("tokens", tokens, i32, nodes)
+        _flat("u", u, f32, nodes)
+        _flat("noise", noise, f32, (B, V))
     if parents is not None:
         _flat("parents", parents, i32, nodes)
     if temperature is not None:
@@ -265,12 +273,24 @@ class PagedCache:
                 return self.attend(layer, q, k, v, page_table, lens, mask, n_tokens, scale, out, lse)
         if q.dim() != 4:
             raise ValueError("q must be [B, T, n_q_heads, head_dim]")
-        B, T = q.shape[:2]
-        dt, Hq, D = self.dtype, self.n_q_heads, self.head_dim
-        wide, new = (B, T, Hq, D), (B, T, self.n_kv_heads, D)
-        _strided("q", q, dt, wide)
-        _strided("k", k, dt, new)
-        _strided("v", v, dt, new)
+        B, T, _, _ = q.shape
+        dt, Hq, D, i32 = self.dtype, self.n_q_heads, self.head_dim, torch.int32
+        wide, new, seqs = (B, T, Hq, D), (B, T, self.n_kv_heads, D), (B,)
+        qs, ks, vs, table = q.stride(), k.stride(), v.stride(), page_table.shape
+        # all of a usual call's checks in one expression; what fails is named after it
+        if (q.shape != wide or k.shape != new or v.shape != new or q.dtype is not dt or k.dtype is not dt
+                or v.dtype is not dt or not q.is_cuda or not k.is_cuda or not v.is_cuda or qs[3] != 1 or ks[3] != 1
+                or vs[3] != 1 or len(table) != 2 or table[0] != B or page_table.dtype is not i32
+                or not page_table.is_cuda or page_table.stride(1) != 1 or lens.shape != seqs or lens.dtype is not i32
+                or not lens.is_cuda or not lens.is_contiguous()):
+            _strided("q", q, dt, wide)
+            _strided("k", k, dt, new)
+            _strided("v", v, dt, new)
+            self._table(page_table, lens, B)
+        if mask is not None:
+            _strided("mask", mask, torch.int64, (B, T))
+        if n_tokens is not None:
+            _flat("n_tokens", n_tokens, i32, seqs)
         if out is None:
             out = torch.empty(wide, dtype=dt, device=q.device)
         else:
@@ -279,12 +299,8 @@ class PagedCache:
             lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
         else:
             _flat("lse", lse, torch.float32, (B, T, Hq))
-        self._table(page_table, lens, B)
-        if mask is not None:
-            _strided("mask", mask, torch.int64, (B, T))
-        if n_tokens is not None:
-            _flat("n_tokens", n_tokens, torch.int32, (B,))
-        qmm_tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale)
+        _tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale, None, qs, ks,
+                        vs, out.stride(), page_table.stride(0))
         return out, lse
 
     def commit(self, page_table, lens, path, accept, lens_out=None, stream=None):
