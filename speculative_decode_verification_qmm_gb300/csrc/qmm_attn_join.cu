@@ -6,9 +6,12 @@
 // is latency, so a CTA takes four rows (eight at head size 64) at a time, its four
 // warps every fourth part of them, and all of a warp's loads of two parts are in
 // flight at a time; the warps' sums are added in order through shared memory.
-// An item of four parts or fewer and many rows gives each warp rows of its own.  Where
-// there are more rows than eight CTAs an SM would take, a CTA goes on to further
-// ones: finding its item costs as much as four of them.
+// An item of four parts or fewer and many rows gives each warp rows of its own (4 x
+// 16,384 rows, 512 rows a head: 120 us instead of 127 with the attention kernel).
+// Where there are more rows than eight CTAs an SM would take, a CTA goes on to
+// further ones: finding its item costs as much as four of them (four CTAs an SM:
+// 124 us, 32: 125 us).  What it adds to the attention kernel: 5 to 10 us where all
+// items are cut, 2 where none is.
 // Everything that does not depend on the partials is done before the wait for
 // the kernel that writes them (programmatic dependent launch).  As a tail of the
 // attention kernels' last CTA of an item the same sums took up to 30 us (64

@@ -19,7 +19,8 @@
 // GB: 203 us without the joining kernel (6.6 TB/s, 97 % of a copy), 210 with it;
 // 32 sequences of 2,048 to 8,192 rows, 8 rows a head: 115 us (6.1 TB/s).  Two row
 // tiles a warp (32 rows) took 103 us where the tcgen05 kernel takes 81 (16 x
-// 4096, 20 heads), so 17 rows and more go there.  216 registers leave room on the
+// 4096, 20 heads), so 17 rows and more go there.  P is rounded to 16 bits, as the
+// product needs it; l sums what was not rounded.  216 registers leave room on the
 // SM for the joining kernel beside two CTAs.
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -33,7 +33,14 @@
 // overwrites the first half of its S.  Q K^T over all 128 columns at once: over
 // 64 it takes as long.  Before, two issuers and S in two buffers of 64 columns
 // took 130 us for 4 sequences x 16,384 rows, 64 nodes, 64 heads on 8, one 125 us
-// and, with the stores of partials below, 122 us (1,130 TFLOP/s).
+// and, with the stores of partials below, 120 us (1,150 TFLOP/s; 1,620 cycles a
+// row tile and cache tile, of which the tensor cores work 1,024: a softmax of
+// 1,500 cycles and its hand-overs do not fit under the other row tile's products.
+// Two softmax warps a row, half of the columns each, need 96 registers a thread,
+// spilled, and took 231 us).
+// With one row tile: 16 x 8,192 rows, 128 rows a head: 106 us (650 TFLOP/s, 5.2
+// TB/s); one sequence of 131,072, 64 rows a head: 95 us (5.7 TB/s).
+// P is rounded to 16 bits, as the product needs it; l sums what was not rounded.
 // Every wait is bounded; on a timeout the CTA records it, its roles run out of
 // their loops without waiting, its copies and MMAs in flight are drained and
 // tensor memory is freed.
@@ -683,6 +690,10 @@ cudaError_t launch(const AttnParams& p, const void* kmap, const void* vmap, cuda
 }  // namespace
 
 int attn_tc_tile_cache_rows() { return TK; }
+// One row tile of 128 or two.  Two read K and V once for 256 rows, one has S
+// double-buffered and its idle warps cost less.  Measured, one against two, in us:
+// 128 rows, 16 x 8,192 cached: 106 : 111; 64 rows, 131,072: 95 : 101; 32 rows, 16 x
+// 4,096: 77 : 88; 512 rows, 4 x 16,384: 177 : 119; 192 rows of 64, 8 x 8,000: 49 : 43.
 int attn_tc_tile_rows(int R) { return R <= 128 ? 128 : 256; }
 
 cudaError_t prepare_attn_tc(bool bf16, int D) {

@@ -21,7 +21,16 @@
 // With few bytes in the batch's rows a first kernel takes the statistics of
 // every row that could be visited, over the whole GPU, and the walk needs no
 // pass until its end (EAGER); with many, the walk reads the rows of its own
-// nodes only.  sample_eager() holds the rule.
+// nodes only, four nodes ahead along the first children.  sample_eager() holds
+// the rule.
+// What bounds it: a chain of dependent steps.  Measured, target and drafter
+// scores of 151,936 entries: one sequence, chain of 8, fp32: 10.5 us, two launches
+// of which the first reads 8.5 MB; 32 sequences, chains of 16, 16 bits: 70 us, the
+// steps of the longest walks, where the visited rows of all sequences take 14 at
+// the copy rate: the busiest SMs issue in 93 % of their cycles, all of them in 30 %
+// on average; 4 trees of 64, 50,257 fp32: 12.8 us.
+// 16-byte copies where rows lie on 16-byte boundaries (WIDE), else single entries
+// in the passes over whole rows of a walk: 70 us against 81 for the batch above.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -630,22 +639,33 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
-// Parts of a row in the eager statistics, and CTAs of a walk.
+// Parts of a row in the eager statistics: about four CTAs per SM.
 int sample_chunks(int B, int T, int64_t V) {
-  int64_t c = 608 / (2ll * B * (T > 1 ? T - 1 : 1));  // about four CTAs per SM
+  int64_t c = 608 / (2ll * B * (T > 1 ? T - 1 : 1));
   const int64_t most = (V + 4095) / 4096;
   c = c < most ? c : most;
   return (int)(c < 1 ? 1 : (c > MAX_CHUNKS ? MAX_CHUNKS : c));
 }
+// CTAs of a walk: all that two on each SM allow, while each has two entries a
+// thread and more.  Measured, 151,936 entries of 16 bits, blocks of 16: with at
+// most 152 / 304 / 608 CTAs 12 sequences took 45 / 42 / 42 us, 20 took 76 / 60 /
+// 57, 32 took 78 / 70 / 81; 8 sequences of 1,000 entries 9.8 us, and 10.4 with
+// clusters of 16.
 int sample_cluster(int B, int64_t V) {
   int c = MAX_CLUSTER;
   while (c > 1 && ((int64_t)B * c > 304 || (int64_t)c * WALK_THREADS * 4 > 2 * V)) c /= 2;
   return c;
 }
-// Eager while the rows of all nodes are read in about the time of one step of
-// the walk.
-bool sample_eager(int B, int T, int64_t V, int elem, bool has_q) {
-  return T > 1 && (int64_t)B * (T - 1) * V * elem * (has_q ? 2 : 1) <= (48ll << 20);
+// Eager while reading the rows of all nodes costs less than the walk's own steps,
+// one after the other, of the longest of its sequences: of a tree, or a long
+// chain, most nodes are not visited, of a short chain they may all be.  Measured,
+// eager against not, in us, 151,936 entries of 16 bits: 17 MB: 14 : 23; 34 MB: 21 :
+// 26; chains of 8, 68 MB: 34 : 44; chains of 16, 109 MB: 37 : 42; 182 MB: 52 : 60;
+// 292 MB: 71 : 70; chains of 32, 75 MB: 29 : 22; trees of 8, 85 MB: 38 : 34; of 16,
+// 73 MB: 32 : 24; of 64 (50,257 entries of 32 bits), 101 MB: 28 : 13.
+bool sample_eager(int B, int T, int64_t V, int elem, bool has_q, bool chain) {
+  const int64_t most = (chain && T <= 16 ? 192ll : 48ll) << 20;
+  return T > 1 && (int64_t)B * (T - 1) * V * elem * (has_q ? 2 : 1) <= most;
 }
 
 template <int DT, bool WIDE, bool EAGER>
@@ -682,7 +702,7 @@ cudaError_t launch_walk(const SampleParams& p, int B, int cluster, cudaStream_t 
 template <int DT, bool WIDE>
 cudaError_t launch_sample(SampleParams& p, int B, int elem, cudaStream_t st) {
   const int cluster = sample_cluster(B, p.V);
-  if (!sample_eager(B, p.T, p.V, elem, p.draft != nullptr)) return launch_walk<DT, WIDE, false>(p, B, cluster, st);
+  if (!sample_eager(B, p.T, p.V, elem, p.draft != nullptr, p.parents == nullptr)) return launch_walk<DT, WIDE, false>(p, B, cluster, st);
   p.chunks = sample_chunks(B, p.T, p.V);
   const int rows = (p.T - 1) * (p.draft ? 2 : 1);  // the last node has no children
   sample_stats_kernel<DT><<<dim3((unsigned)p.chunks, (unsigned)rows, (unsigned)B), STAT_THREADS,
@@ -708,7 +728,8 @@ int qmm_verify_sample_workspace(int B, int T, int64_t V, int64_t* bytes) {
   *bytes = 0;
   const int rc = check_sizes(B, T, V);
   if (rc != QMM_OK) return rc;
-  *bytes = sample_eager(B, T, V, 2, false) ? (int64_t)B * T * 2 * sample_chunks(B, T, V) * (int64_t)sizeof(float2) : 256;
+  // the most that any type, with or without drafter scores and parents, takes
+  *bytes = sample_eager(B, T, V, 2, false, true) ? (int64_t)B * T * 2 * sample_chunks(B, T, V) * (int64_t)sizeof(float2) : 256;
   return QMM_OK;
 }
 

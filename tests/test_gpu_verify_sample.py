@@ -117,6 +117,16 @@ def test_large_vocabulary(T, V):
     d.check(d.call())
 
 
+def test_chains_with_and_without_parents_agree():
+    """90 MB of scores: a chain without parents has its statistics taken first, one
+    whose parents are given is read as the walk meets its rows."""
+    d = Drafted("f32", 40, 8, 40000, False, True, seed=12)
+    first = [x.cpu() for x in d.call()]
+    d.check(first)
+    walked = [x.cpu() for x in d.call(parents=torch.from_numpy(d.parents).cuda())]
+    assert torch.equal(first[0], walked[0]) and torch.equal(first[1], walked[1])
+
+
 def test_read_ahead_and_walked_rows_agree():
     """The same sequences alone (statistics of all rows taken first) and in a batch
     large enough for rows to be read as the walk meets them."""
