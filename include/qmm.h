@@ -45,6 +45,10 @@
  * qmm_prefill computes the same product for a prompt's worth of rows (any M)
  * on an FP8 handle, as a tensor-core GEMM (see its comment below).
  *
+ * Around the product, for steps that draft a tree: a paged key/value cache, the
+ * nodes' attention over it, acceptance for sampled decoding, and the compaction
+ * of the accepted branch (qmm_cache_create and what follows it below).
+ *
  * Conventions for every entry point:
  *   - Return value: QMM_OK (0) or one of the QMM_ERR_* codes below.  No call
  *     throws, aborts or prints.  qmm_strerror() names a code.
@@ -53,9 +57,10 @@
  *   - stream is a cudaStream_t passed as void* (NULL = the legacy default
  *     stream).  Calls documented as asynchronous only enqueue work on it.
  *   - The caller owns every buffer it passes; the library never frees caller
- *     memory and keeps no pointer to it after the call returns (the one
- *     exception is the stamp buffer of the profiling hook qmm_debug_set_trace,
- *     kept until it is switched off or the handle is destroyed).
+ *     memory and keeps no pointer to it after the call returns (the exceptions
+ *     are the pools of a paged cache, kept until its handle is destroyed, and
+ *     the stamp buffer of the profiling hook qmm_debug_set_trace, kept until it
+ *     is switched off or the handle is destroyed).
  *   - bf16 activations are passed as uint16_t bit patterns.
  */
 #ifndef QMM_H_

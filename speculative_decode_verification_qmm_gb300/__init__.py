@@ -9,6 +9,10 @@ stream); every step of the computation runs in ``libqmm.so``'s kernels.
 with W in Q4_0 (32-element blocks, fp16 scale, 4-bit codes offset by 8) or
 FP8 E4M3 with 128x128 fp32 scales, optionally with the 32-point Hadamard
 rotation of the activations for weights rotated offline.
+
+Around that product, for a step of tree-drafted decoding (``paged``):
+``PagedCache`` with ``attend``, ``commit`` and ``copy_pages``, and
+``verify_sample``.
 """
 from __future__ import annotations
 
