@@ -1,5 +1,5 @@
-// qmm_attn_mma.cu -- tree attention for up to 16 rows per key/value head, on
-// mma.sync: one pass over the cached rows with a running softmax.
+// qmm_attn_mma.cu -- tree attention for up to 16 rows per key/value head (32 in
+// many short sequences), on mma.sync: one pass over the cached rows with a running softmax.
 //
 // Per row r and cache row j: s = q_r . K_j (m16n8k16, rows as M), then with the
 // running maximum m, p = 2^(c s - m), l += p, O += p V_j, all fp32.  m may lag

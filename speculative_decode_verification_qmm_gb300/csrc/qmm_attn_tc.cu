@@ -1,4 +1,5 @@
-// qmm_attn_tc.cu -- tree attention for more than 16 rows per key/value head, on
+// qmm_attn_tc.cu -- tree attention for more than 16 rows per key/value head (but
+// for 17 to 32 in many short sequences, see attn_solo), on
 // the tcgen05 tensor cores: one pass over the cached rows with a running
 // softmax.
 //

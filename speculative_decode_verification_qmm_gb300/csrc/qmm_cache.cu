@@ -201,18 +201,24 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const __grid_constan
   }
 }
 
-// Whether the mma.sync kernel's warps work alone (p.R within its tile).  A warp
-// alone ends a segment without the CTA's barriers and sums, but has one block of
-// the cache in every unit where four warps share one.  So it is for many short
-// sequences: more than three items of 128 values (six of 64) for each CTA, and at
-// most SOLO_MAX rows.  Measured, alone against shared, in us: 128 sequences of up
-// to 30 / 120 / 300 / 600 rows, 8 nodes, 20 heads of 128, two rows a node: 47 : 59,
-// 61 : 91, 83 : 117, 120 : 145; 8 heads, one row: 16 : 23, 23 : 32, 31 : 41, 46 :
-// 54.  Past the limits: 48 sequences of up to 1,500 and 4,000 rows, 20 heads: 101 :
-// 100, 223 : 216; 16 sequences of up to 120 and 600 rows: 23 : 17, 35 : 29.
+// Whether the mma.sync kernel's warps work alone.  A warp alone ends a segment
+// without the CTA's barriers and sums, but has one block of the cache in every
+// unit where four warps share one.  So it is for many short sequences: more than
+// three (sequence, head) pairs of 128 values (six of 64) for each CTA, and at most
+// SOLO_MAX rows.  Measured, alone against shared, in us: 128 sequences of up to 30
+// / 120 / 300 / 600 rows, 8 nodes, 20 heads of 128, two rows a node: 47 : 59, 61 :
+// 91, 83 : 117, 120 : 145; 8 heads, one row: 16 : 23, 23 : 32, 31 : 41, 46 : 54.
+// Past the limits: 48 sequences of up to 1,500 and 4,000 rows, 20 heads: 101 : 100,
+// 223 : 216; 16 sequences of up to 120 and 600 rows: 23 : 17, 35 : 29.
+// With 17 to 32 rows a head a warp walks the cache twice, and still ends before the
+// tcgen05 kernel, whose segments are a longer chain, up to half as many rows: 128
+// sequences of up to 30 / 120 / 300 / 800 rows, 20 heads of 128, 32 rows: 76 : 93,
+// 103 : 122, 143 : 187, 265 : 223; 24 rows, 8 heads: 35 : 42, 46 : 43, 60 : 80, 107 :
+// 96; with 64 rows a head and 10 heads 73 : 55, 100 : 81, 131 : 124, 249 : 144.
 constexpr int SOLO_MAX = 1024;
 bool attn_solo(const AttnParams& p, int64_t cap, int ctas, int D) {
-  return cap <= SOLO_MAX && (int64_t)p.B * p.Hkv * D >= (int64_t)3 * 128 * ctas;
+  const int tiles = (p.R + attn_mma_tile_rows() - 1) / attn_mma_tile_rows();
+  return tiles <= 2 && cap <= SOLO_MAX / tiles && (int64_t)p.B * p.Hkv * D >= (int64_t)3 * 128 * ctas;
 }
 
 }  // namespace
@@ -357,9 +363,9 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
   const bool bf16 = d.dtype == QMM_DT_BF16;
-  const bool tc = p.R > attn_mma_tile_rows();
-  const bool solo = !tc && attn_solo(p, (int64_t)a->table_width << h->page_shift, attn_mma_workers(h->sm_count, false),
-                                     d.head_dim);
+  const bool solo = attn_solo(p, (int64_t)a->table_width << h->page_shift, attn_mma_workers(h->sm_count, false),
+                              d.head_dim);
+  const bool tc = !solo && p.R > attn_mma_tile_rows();
   const int rows = tc ? attn_tc_tile_rows(p.R) : attn_mma_tile_rows();
   const int tk = tc ? attn_tc_tile_cache_rows() : attn_mma_tile_cache_rows(solo);
   p.RT = (p.R + rows - 1) / rows;

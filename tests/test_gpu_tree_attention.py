@@ -262,9 +262,25 @@ def test_many_sequences(dtype, D, Hq, Hkv, T, page, B):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
-@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf")])
-def test_many_sequences_unseen_rows_hold_anything(fill):
-    T, bad = 6, 2
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,T,page,B", [
+    ("bf16", 128, 24, 8, 7, 16, 120),   # 21 rows
+    ("f16", 128, 16, 8, 16, 32, 120),   # 32 rows
+    ("bf16", 64, 40, 20, 16, 16, 100),  # 32 rows
+])
+def test_many_sequences_two_row_tiles(dtype, D, Hq, Hkv, T, page, B):
+    rng = np.random.default_rng(T)
+    lens = [EDGES[i % len(EDGES)] for i in range(B - 1)] + [400]
+    counts = [int(x) for x in rng.integers(0, T + 1, B)]
+    a = Attention(dtype, D, Hq, Hkv, T, page, lens, counts, tree=True, seed=D + T, sigma=1.5)
+    cache = a.make_cache(q)
+    first = assert_attention(a, cache, q)
+    again = a.call(cache)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("T,fill", [(6, float("nan")), (6, float("inf")), (6, -float("inf")), (20, float("nan"))])
+def test_many_sequences_unseen_rows_hold_anything(T, fill):
+    bad = 2
     a = _many(120, T, seed=21, fill=fill)
     seen = a.seen.copy()
     seen[:, :, bad] = False
