@@ -50,6 +50,7 @@ struct AttnParams {
   float scale_log2;  // scale * log2(e): the softmax runs in powers of two
   float* ws;         // partials: [worker][2][rows of a tile * (D + 2)]
   int grid;          // workers that share the units: CTAs, or warps that work alone
+  int4* cuts;        // [worker]: sequence, head, row tile of its last unit, and attn_cut of it
   int64_t row0;      // first row of the layer in the pools' tensor maps
   int* status;
   uint64_t wait_limit_ns;
@@ -232,6 +233,10 @@ __device__ __forceinline__ void attn_next(const AttnParams& p, AttnCursor& c) {
 __device__ __forceinline__ int attn_owner(int64_t u, int64_t W, int G) {
   return (int)(((u + 1) * G - 1) / W);
 }
+
+// Whether the item of a worker's last unit goes on in the next worker's range: 0
+// no, 1 yes, having begun in this one, 2 yes, having begun before.
+__device__ __forceinline__ int attn_cut(bool goes_on, bool began_here) { return goes_on ? (began_here ? 1 : 2) : 0; }
 
 // The weight of a partial sum with maximum m and sum l when it is joined to
 // others under the maximum mn: 0 for a part that saw nothing (and not for one

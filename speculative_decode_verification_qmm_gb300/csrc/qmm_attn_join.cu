@@ -12,6 +12,9 @@
 // further ones: finding its item costs as much as four of them (four CTAs an SM:
 // 124 us, 32: 125 us).  What it adds to the attention kernel: 5 to 10 us where all
 // items are cut, 2 where none is.
+// Most of more items than that are not cut.  The CTAs are then for the workers:
+// each reads what its worker left (AttnParams::cuts) and joins the item that goes
+// on behind the worker's range, if one began in it.
 // Everything that does not depend on the partials is done before the wait for
 // the kernel that writes them (programmatic dependent launch).  As a tail of the
 // attention kernels' last CTA of an item the same sums took up to 30 us (64
@@ -28,8 +31,9 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int RU = 4;  // rows of a lane
 constexpr int U = 2;   // parts in flight
+constexpr int JOIN_CTAS = 1216;  // eight an SM
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool CUTS>
 __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel(const __grid_constant__ AttnParams p, int tk, int rows,
                                                                int chunks) {
   constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp's load
@@ -38,27 +42,38 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
   __shared__ float s_m[WARPS][RPC], s_l[WARPS][RPC];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
+  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
   AttnCursor cur{};
-  cur.b = item / (p.Hkv * p.RT);
-  cur.h = item / p.RT % p.Hkv;
-  cur.rt = item % p.RT;
-  attn_sizes(p, cur.b, cur.L, cur.n);
-  int nt = (cur.L + cur.n + tk - 1) / tk;
-  nt = nt < 1 ? 1 : nt;
-  int64_t before, all;
-  attn_count(p, tk, lane, cur.b, before, all);
-  const int64_t W = all * p.Hkv * p.RT;
-  const int G = W < p.grid ? (int)W : p.grid;
-  const int64_t u = before * p.Hkv * p.RT + (int64_t)(cur.h * p.RT + cur.rt) * nt;
-  const int c0 = attn_owner(u, W, G), c1 = attn_owner(u + nt - 1, W, G);
+  int c0 = unit, c1 = unit;
+  if constexpr (!CUTS) {
+    cur.b = unit / (p.Hkv * p.RT);
+    cur.h = unit / p.RT % p.Hkv;
+    cur.rt = unit % p.RT;
+    attn_sizes(p, cur.b, cur.L, cur.n);
+    int nt = (cur.L + cur.n + tk - 1) / tk;
+    nt = nt < 1 ? 1 : nt;
+    int64_t before, all;
+    attn_count(p, tk, lane, cur.b, before, all);
+    const int64_t W = all * p.Hkv * p.RT;
+    const int G = W < p.grid ? (int)W : p.grid;
+    const int64_t u = before * p.Hkv * p.RT + (int64_t)(cur.h * p.RT + cur.rt) * nt;
+    c0 = attn_owner(u, W, G);
+    c1 = attn_owner(u + nt - 1, W, G);
+  }
+  pdl_wait();  // every CTA: the call has not ended before the attention kernel has
+  if constexpr (CUTS) {
+    const int4 cut = __ldcg(p.cuts + c0);
+    if (cut.w == 1)
+      for (c1 = c0 + 1; c1 + 1 < p.grid && __ldcg(&p.cuts[c1].w) == 2;) ++c1;
+    cur.b = cut.x, cur.h = cut.y, cur.rt = cut.z;
+  }
+  if (c0 == c1) return;
+  if constexpr (CUTS) attn_sizes(p, cur.b, cur.L, cur.n);
   const int part = rows * (D + 2);
   const int left = p.R - cur.rt * rows < rows ? p.R - cur.rt * rows : rows;
   const int sub = lane % LPR, row = lane / LPR;
-  pdl_wait();  // every CTA: the call has not ended before the attention kernel has
-  if (c0 == c1) return;
 
-  const bool alone = c1 - c0 < 4 && left >= 128;  // a warp joins its rows alone
+  const bool alone = c1 - c0 < 4 && (CUTS || left >= 128);  // a warp joins its rows alone
   const int from = alone ? c0 : c0 + warp, step = alone ? 1 : WARPS;
   const int first = alone ? (chunk * WARPS + warp) * RPC : chunk * RPC;
   const int hop = chunks * (alone ? WARPS * RPC : RPC);
@@ -135,15 +150,15 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
   }
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool CUTS>
 cudaError_t launch(const AttnParams& p, int tk, int rows, cudaStream_t st) {
-  constexpr int PER = 128 / D * RU;
-  const int64_t items = (int64_t)p.B * p.Hkv * p.RT;
+  constexpr int PER = 128 / D * RU * (CUTS ? WARPS : 1);
+  const int64_t units = CUTS ? p.grid - 1 : (int64_t)p.B * p.Hkv * p.RT;
   int chunks = ((p.R < rows ? p.R : rows) + PER - 1) / PER;
-  const int64_t most = (1216 + items - 1) / items;
+  const int64_t most = (JOIN_CTAS + units - 1) / units;
   if (chunks > most) chunks = (int)most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * chunks));
+  cfg.gridDim = dim3((unsigned)(units * chunks));
   cfg.blockDim = dim3(WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -151,14 +166,25 @@ cudaError_t launch(const AttnParams& p, int tk, int rows, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF16, D>, p, tk, rows, chunks);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF16, D, CUTS>, p, tk, rows, chunks);
+}
+
+template <bool BF16, int D>
+cudaError_t launch_one(const AttnParams& p, int tk, int rows, cudaStream_t st) {
+  // Measured, CTAs by cuts against by items, in us with the attention kernel:
+  // 2,560 items (128 sequences of up to 120 / 600 / 4,000 rows, head size 64): 36 :
+  // 43, 68 : 78, 296 : 299; 5,120 (head size 128, up to 120 / 300 / 800): 87 : 103, 128
+  // : 143, 212 : 222; 320 (16 sequences, up to 120 / 600 / 4,000): 18 : 17, 30 : 29,
+  // 91 : 89; 384 (48 sequences, 8 heads): 13.6 : 13.1, 28 : 27, 90 : 88.
+  const bool cuts = (int64_t)p.B * p.Hkv * p.RT > JOIN_CTAS;
+  return cuts ? launch<BF16, D, true>(p, tk, rows, st) : launch<BF16, D, false>(p, tk, rows, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, cudaStream_t st) {
-  if (D == 128) return bf16 ? launch<true, 128>(p, tk, rows, st) : launch<false, 128>(p, tk, rows, st);
-  return bf16 ? launch<true, 64>(p, tk, rows, st) : launch<false, 64>(p, tk, rows, st);
+  if (D == 128) return bf16 ? launch_one<true, 128>(p, tk, rows, st) : launch_one<false, 128>(p, tk, rows, st);
+  return bf16 ? launch_one<true, 64>(p, tk, rows, st) : launch_one<false, 64>(p, tk, rows, st);
 }
 
 }  // namespace qmm

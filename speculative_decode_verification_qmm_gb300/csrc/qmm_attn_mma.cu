@@ -73,7 +73,10 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
   int64_t u0, u1;
   const int worker = SOLO ? (int)blockIdx.x * WARPS + warp : (int)blockIdx.x;  // of the p.grid that share the units
   AttnCursor cur = attn_begin<TK>(p, lane, worker, u0, u1);
-  if (u0 >= u1) return;
+  if (u0 >= u1) {
+    if (lane == 0 && (SOLO || warp == 0)) p.cuts[worker] = make_int4(0, 0, 0, 0);
+    return;
+  }
   AttnCursor ld = cur;
 
   const uint32_t ring = smem_u32(smem) + S::RING + warp * STAGES * S::STAGE_BYTES;
@@ -327,6 +330,8 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
       // ------------------------------------------------ end of the segment
       const int64_t item_u = u - cur.tile;  // the item's first unit
       const bool whole = item_u == seg_u && last_tile;
+      if (u + 1 == u1 && lane == 0 && (SOLO || warp == 0))
+        p.cuts[worker] = make_int4(cur.b, cur.h, cur.rt, attn_cut(!last_tile, item_u >= u0));
       constexpr int PART = ROWS * (D + 2);
       // slot 1: the item begins in this worker's range
       float* part = p.ws + ((int64_t)worker * 2 + (item_u >= u0 ? 1 : 0)) * PART;

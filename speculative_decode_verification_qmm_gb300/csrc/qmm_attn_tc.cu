@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
 
+  if (tid == 0 && u0 >= u1) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   const uint64_t lim = p.wait_limit_ns;
   auto fail = [&](int code) {
     if (!s_flag[0]) atomicOr(p.status, code);
@@ -572,6 +573,8 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
       const int64_t item_u = u - cur.tile;  // the item's first unit
       const bool last_tile = cur.tile + count == cur.ntiles;
       const bool whole = cur.tile == 0 && last_tile;
+      if (tid == 0 && u + count == u1)
+        p.cuts[blockIdx.x] = make_int4(cur.b, cur.h, cur.rt, attn_cut(!last_tile, item_u >= u0));
       constexpr int PART = ROWS * (D + 2);
       float* part = p.ws + ((int64_t)blockIdx.x * 2 + (item_u >= u0 ? 1 : 0)) * PART;
       const int t_row = r / p.g, i_row = r - t_row * p.g;

@@ -23,6 +23,7 @@ struct qmm_cache {
   int page_shift = 0;
   CUtensorMap kmap, vmap;   // the pools' rows
   float* ws = nullptr;      // partials of split attention items
+  int4* cuts = nullptr;     // which items are split (behind ws)
   int* status = nullptr;    // device error word
   uint64_t wait_limit_ns = 2000000000ull;  // 2 s
 };
@@ -207,14 +208,16 @@ __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const __grid_constan
 // three (sequence, head) pairs of 128 values (six of 64) for each CTA, and at most
 // SOLO_MAX rows.  Measured, alone against shared, in us: 128 sequences of up to 30
 // / 120 / 300 / 600 rows, 8 nodes, 20 heads of 128, two rows a node: 47 : 59, 61 :
-// 91, 83 : 117, 120 : 145; 8 heads, one row: 16 : 23, 23 : 32, 31 : 41, 46 : 54.
+// 91, 83 : 117, 120 : 145 (and since, with a shorter join, 120 rows: 51); 8 heads,
+// one row: 16 : 23, 23 : 32, 31 : 41, 46 : 54.
 // Past the limits: 48 sequences of up to 1,500 and 4,000 rows, 20 heads: 101 : 100,
 // 223 : 216; 16 sequences of up to 120 and 600 rows: 23 : 17, 35 : 29.
 // With 17 to 32 rows a head a warp walks the cache twice, and still ends before the
 // tcgen05 kernel, whose segments are a longer chain, up to half as many rows: 128
-// sequences of up to 30 / 120 / 300 / 800 rows, 20 heads of 128, 32 rows: 76 : 93,
-// 103 : 122, 143 : 187, 265 : 223; 24 rows, 8 heads: 35 : 42, 46 : 43, 60 : 80, 107 :
-// 96; with 64 rows a head and 10 heads 73 : 55, 100 : 81, 131 : 124, 249 : 144.
+// sequences of up to 30 / 120 / 300 rows, 20 heads of 128, 32 rows: 62 : 93, 87 :
+// 122, 128 : 187; 24 rows, 8 heads: 29 : 42, 39 : 43, 54 : 80.  Past it: 800 rows,
+// 265 : 223 and 107 : 96; with 64 rows a head and 10 heads, 30 / 120 / 300 rows: 73 :
+// 55, 100 : 81, 131 : 124.
 constexpr int SOLO_MAX = 1024;
 bool attn_solo(const AttnParams& p, int64_t cap, int ctas, int D) {
   const int tiles = (p.R + attn_mma_tile_rows() - 1) / attn_mma_tile_rows();
@@ -254,7 +257,8 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   // two partials of a CTA's largest row tile each
   const size_t rows_mma = (size_t)attn_mma_workers(sms, true) * attn_mma_tile_rows();
   const size_t rows_tc = (size_t)sms * attn_tc_tile_rows(INT32_MAX);
-  const size_t ws_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
+  const size_t part_bytes = 2 * (rows_mma > rows_tc ? rows_mma : rows_tc) * (d->head_dim + 2) * sizeof(float);
+  const size_t ws_bytes = part_bytes + (size_t)attn_mma_workers(sms, true) * sizeof(int4);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
   if (e == cudaSuccess) e = prepare_attn_tc(d->dtype == QMM_DT_BF16, d->head_dim);
   const bool f16 = d->dtype == QMM_DT_F16;
@@ -262,7 +266,7 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   if (e == cudaSuccess) e = host_pool_map(&h->vmap, d->v_pool, pool_rows, d->head_dim, 16, f16);
   void* ptr = nullptr;
   if (e == cudaSuccess && (e = host_dev_alloc(&ptr, ws_bytes)) == cudaSuccess)
-    h->ws = static_cast<float*>(ptr);
+    h->ws = static_cast<float*>(ptr), h->cuts = reinterpret_cast<int4*>(static_cast<char*>(ptr) + part_bytes);
   if (e == cudaSuccess && (e = host_dev_alloc(&ptr, sizeof(int))) == cudaSuccess)
     h->status = static_cast<int*>(ptr);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, sizeof(int), st);
@@ -360,6 +364,7 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   p.R = p.T * p.g;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.ws = h->ws;
+  p.cuts = h->cuts;
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
   const bool bf16 = d.dtype == QMM_DT_BF16;

@@ -278,6 +278,24 @@ def test_many_sequences_two_row_tiles(dtype, D, Hq, Hkv, T, page, B):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,T,B", [
+    ("bf16", 128, 8, 8, 3, 160),    # 3 rows
+    ("f16", 64, 24, 8, 16, 160),    # 48 rows
+    ("bf16", 64, 12, 4, 50, 310),   # 150 rows: two row tiles
+])
+def test_one_long_among_many_sequences(dtype, D, Hq, Hkv, T, B):
+    """More items than a CTA each, and one that is cut between many CTAs."""
+    rng = np.random.default_rng(T)
+    lens = [EDGES[i % len(EDGES)] for i in range(B)]
+    lens[B // 2] = 30001
+    counts = [int(x) for x in rng.integers(0, T + 1, B)]
+    a = Attention(dtype, D, Hq, Hkv, T, 16, lens, counts, tree=True, seed=D + T)
+    cache = a.make_cache(q)
+    first = assert_attention(a, cache, q)
+    again = a.call(cache)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 @pytest.mark.parametrize("T,fill", [(6, float("nan")), (6, float("inf")), (6, -float("inf")), (20, float("nan"))])
 def test_many_sequences_unseen_rows_hold_anything(T, fill):
     bad = 2
