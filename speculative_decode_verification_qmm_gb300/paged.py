@@ -133,9 +133,11 @@ def _tree_attention(h, layer, q, k, v, table, lens, out, lse, mask, n_tokens, sc
 def qmm_cache_commit(h, page_table, lens, path, accept, lens_out, stream=None) -> None:
     """Compacts the accepted branches (path int32 [B, T], accept int32 [B, 2]); asynchronous."""
     B, T = path.shape
-    _check("qmm_cache_commit", load().qmm_cache_commit(
+    rc = load().qmm_cache_commit(
         h, B, T, page_table.data_ptr(), page_table.stride(0), page_table.shape[1], lens.data_ptr(), path.data_ptr(),
-        path.stride(0), accept.data_ptr(), lens_out.data_ptr(), _stream_ptr(stream, lens.device.index)))
+        path.stride(0), accept.data_ptr(), lens_out.data_ptr(), _stream_ptr(stream, lens.device.index))
+    if rc:
+        _check("qmm_cache_commit", rc)
 
 
 def qmm_cache_copy(h, src, dst, rows=None, stream=None) -> None:
@@ -310,16 +312,23 @@ class PagedCache:
         if stream is not None:  # lens_out is allocated on the stream that writes it
             with torch.cuda.stream(stream):
                 return self.commit(page_table, lens, path, accept, lens_out)
-        B, i32 = lens.shape[0], torch.int32
+        i32, seqs, table, nodes = torch.int32, lens.shape, page_table.shape, path.shape
+        B = seqs[0]
+        # the usual call's checks in one expression; what fails is named after it
+        if (len(seqs) != 1 or lens.dtype is not i32 or not lens.is_cuda or not lens.is_contiguous() or len(table) != 2
+                or table[0] != B or page_table.dtype is not i32 or not page_table.is_cuda
+                or page_table.stride(1) != 1 or len(nodes) != 2 or nodes[0] != B or path.dtype is not i32
+                or not path.is_cuda or path.stride(1) != 1 or accept.shape != (B, 2) or accept.dtype is not i32
+                or not accept.is_cuda or not accept.is_contiguous()):
+            self._table(page_table, lens, B)
+            if path.dim() != 2:
+                raise ValueError("path must be [B, T]")
+            _strided("path", path, i32, (B, path.shape[1]))
+            _flat("accept", accept, i32, (B, 2))
         if lens_out is None:
             lens_out = torch.empty_like(lens)
         else:
             _flat("lens_out", lens_out, i32, (B,))
-        self._table(page_table, lens, B)
-        if path.dim() != 2:
-            raise ValueError("path must be [B, T]")
-        _strided("path", path, i32, (B, path.shape[1]))
-        _flat("accept", accept, i32, (B, 2))
         qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out)
         return lens_out
 
