@@ -348,7 +348,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
   // Reductions over the cluster.  Every warp leaves a value in s.part[i]; warp i
   // adds up the CTA's, then, after a barrier of the cluster, the ranks', each
   // with `op` over the lanes in an order that the sizes fix.  The buffers
-  // alternate, so that one barrier a reduction is enough.
+  // alternate, so that one barrier a reduction is enough.  These barriers have no
+  // limit: every thread of the cluster meets them in the same order because each
+  // decides alike, from values in its own CTA's memory that were computed from
+  // the same inputs in the same order and are not written while any warp reads them.
   int turn = 0;
   constexpr int WARPS = WALK_THREADS / 32;
   auto reduce = [&](int count, float2 none, auto op) {
@@ -530,6 +533,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
       if (tid == 0) s.path[k] = child;
       ++k;
       node = child;
+      // the next node's rejections overwrite this one's, which a slower warp may
+      // still be reading above; a node whose statistics are known has no other barrier
+      if (rej) __syncthreads();
       rej = 0;
       kids = children(node);
       if (kids) enter();

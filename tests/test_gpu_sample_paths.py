@@ -1,0 +1,73 @@
+"""Sampled walks on the paths that small cases do not take: shapes of trees that
+reject and accept at one node, and batches whose rows are read as the walk meets
+them, in every type, alignment and with no drafter scores.  Compared with the
+64-bit walk of paged_util where its margin says that rounding cannot turn it."""
+import numpy as np
+import pytest
+
+import speculative_decode_verification_qmm_gb300 as q
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+from paged_util import sample_reference  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib_built():
+    q.load(build_if_missing=True)
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+
+
+def _cuda(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+def _compare(got, target, draft, tokens, parents, u, noise, most_skipped):
+    """Every sequence against its 64-bit walk; margins below 1e-3 are not compared."""
+    accept, path = (x.cpu().numpy() for x in got)
+    B, T = tokens.shape
+    skipped = 0
+    for b in range(B):
+        nodes, token, margin = sample_reference(target[b].double().numpy(), None if draft is None else draft[b].double().numpy(),
+                                                tokens[b], parents[b], u[b].astype(np.float64),
+                                                noise[b].astype(np.float64), 1.0, T)
+        if margin < 1e-3:
+            skipped += 1
+            continue
+        assert accept[b].tolist() == [len(nodes), token], (b, margin)
+        assert path[b].tolist() == nodes + [-1] * (T - len(nodes)), b
+    assert skipped <= most_skipped * B
+
+
+@pytest.mark.parametrize("B,V", [(600, 300),    # the statistics of all rows are taken first
+                                 (300, 8000)])  # 58 MB: rows are read as the walk meets them
+@pytest.mark.parametrize("rejected", [1, 3])
+def test_accepted_after_rejections_then_an_only_child_rejected(B, V, rejected):
+    """Root -> some rejected children, then an accepted one -> one child, rejected.
+    The lists of rejections of the two nodes follow each other at once.  The
+    rejected tokens are those by which Q exceeds P most, the accepted one (u = 0)
+    that by which P exceeds Q most, so that nearly every walk is of this kind."""
+    T = rejected + 3
+    r = np.random.default_rng(V + rejected)
+    target = torch.from_numpy(r.standard_normal((B, T, V)).astype(np.float32) * 2)
+    draft = torch.from_numpy(r.standard_normal((B, T, V)).astype(np.float32) * 2)
+    parents = np.zeros((B, T), np.int32)
+    parents[:, 0], parents[:, T - 1] = -1, T - 2
+    more = torch.softmax(draft, 2) - torch.softmax(target, 2)  # Q - P
+    tokens = np.zeros((B, T), np.int32)
+    tokens[:, 1:T - 2] = more[:, 0].topk(rejected, 1).indices.numpy()
+    tokens[:, T - 2] = more[:, 0].argmin(1).numpy()
+    tokens[:, T - 1] = more[:, T - 2].argmax(1).numpy()
+    u = np.full((B, T), 0.999, np.float32)
+    u[:, T - 2] = 0.0
+    noise = r.exponential(size=(B, V)).astype(np.float32) + np.float32(1e-30)
+    args = (target.cuda(), draft.cuda(), _cuda(tokens), _cuda(u), _cuda(noise))
+    got = q.verify_sample(*args, parents=_cuda(parents))
+    assert (got[1][:, 0] == T - 2).float().mean() > 0.98 and (got[0][:, 0] <= 1).all()
+    _compare(got, target, draft, tokens, parents, u, noise, 0.1)
+    for _ in range(5):
+        again = q.verify_sample(*args, parents=_cuda(parents))
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
