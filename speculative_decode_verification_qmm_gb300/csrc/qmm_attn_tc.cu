@@ -340,10 +340,11 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
       u += count;
     }
     cp_async_wait<0>();
-    // tensor copies in flight land before the CTA leaves: the last tile of every slot
+    // Tensor copies in flight land before the CTA leaves: the last tile of every
+    // slot.  Always: another role can give up after this one's last look at the flag.
     for (int i = 0; i < slots; ++i) {
       const int rounds = i < slot ? round + 1 : round;
-      if (rounds > 0 && s_flag[0] && lane == 0 && !mbar_wait_bounded(full + 8 * i, (rounds - 1) & 1, 1000000000ull))
+      if (rounds > 0 && lane == 0 && !mbar_wait_bounded(full + 8 * i, (rounds - 1) & 1, 1000000000ull))
         atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
     }
   } else if (warp >= MMA_WARP) {
