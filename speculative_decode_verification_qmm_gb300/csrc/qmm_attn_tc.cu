@@ -20,25 +20,25 @@
 //                         the rows around them; Q, once a segment, by both
 // Why this split.  At 128 rows a tile of K and V (64 KB) takes 1.5 us of an
 // SM's share of the HBM stream, and its two products 0.55 us of the tensor cores
-// and its 16,384 exponentials about as long: with one row tile the stream is the
+// and its softmax of 16,384 scores 0.8: with one row tile the stream is the
 // bound, and S is double-buffered so that Q K^T of the next tile runs under the
 // softmax.  One warp then issues all Q K^T, another all P V: the issue of an MMA
 // blocks until the one before it is nearly done, and a product whose operands are
 // ready would wait behind one whose are not.
 // With two row tiles each tile of K and V serves 256 rows, and tensor memory (512
 // columns) holds one S and O of each.  One warp issues everything: P V of a row
-// tile and Q K^T of its next cache tile back to back, which MMAs of one thread may
-// without a barrier between them, then the same for the other row tile, whose
-// softmax ran meanwhile.  The softmax hands P over in two steps of SW columns, so
+// tile and, when that has ended, Q K^T of its next cache tile, whose S lies where P
+// did, then the same for the other row tile, whose softmax ran meanwhile.  (MMAs with
+// different accumulators have no promised order, so the wait is needed; without it
+// the case below took 120 us.)  The softmax hands P over in two steps of SW columns, so
 // that P V of the first runs under the softmax of the second; a step's P
 // overwrites the first half of its S.  Q K^T over all 128 columns at once: over
 // 64 it takes as long.  Before, two issuers and S in two buffers of 64 columns
-// took 130 us for 4 sequences x 16,384 rows, 64 nodes, 64 heads on 8, one 125 us
-// and, with the stores of partials below, 120 us (1,150 TFLOP/s; 1,620 cycles a
-// row tile and cache tile, of which the tensor cores work 1,024: a softmax of
-// 1,500 cycles and its hand-overs do not fit under the other row tile's products.
-// Two softmax warps a row, half of the columns each, need 96 registers a thread,
-// spilled, and took 231 us).
+// took 130 us for 4 sequences x 16,384 rows, 64 nodes, 64 heads on 8; this takes
+// 126 us (1,097 TFLOP/s; 1,700 cycles a row tile and cache tile, of which the tensor
+// cores work 1,024: a softmax of 1,500 cycles and its hand-overs do not fit under
+// the other row tile's products.  Two softmax warps a row, half of the columns
+// each, need 96 registers a thread, spilled, and took 231 us).
 // With one row tile: 16 x 8,192 rows, 128 rows a head: 106 us (650 TFLOP/s, 5.2
 // TB/s); one sequence of 131,072, 64 rows a head: 95 us (5.7 TB/s).
 // P is rounded to 16 bits, as the product needs it; l sums what was not rounded.
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
           tc_commit(b_odone + 8 * q);
         }
       };
-      int n = 0, seg = 0;          // tiles and segments so far (n: parities only)
+      int n = 0, seg = 0;          // tiles and segments so far (n: parities, and whether there was one)
       int slot = 0, round = 0;     // of the tile of K or V
       int vslot = 0, vround = 0;   // of the tile of V, where one warp issues both
       for (int64_t u = u0; u < u1 && ok; ++seg) {
@@ -408,10 +408,14 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
                   product_o(q, vslot, sub, j == 0 && sub == 0);
                 }
                 if (!ok) break;
+                if (leader) tc_commit(b_sfree + 8 * q);
                 if (leader && j + 1 == count) tc_commit(b_olast + 8 * q);
               }
               if (j + 1 < count) {
                 if (q == 0 && !need(b_kfull + 8 * slot, round)) break;
+                // S goes where P of the tile before lies, until its products have ended
+                const int before = j >= 0 ? n : n - 1;
+                if (before >= 0 && !need(b_sfree + 8 * q, before)) break;
                 product_s(q, slot, tmem + q * COL_Q);
                 if (leader) tc_commit(b_sfull + 8 * (2 * q));
               }

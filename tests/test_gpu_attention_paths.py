@@ -40,3 +40,19 @@ def test_waits_that_give_up_under_copies_in_flight(D, T, Hq, lens):
         assert cache.sync_status() == q.QMM_ERR_TIMEOUT
         assert cache.sync_status() == q.QMM_OK
         check(out, lse, ref, lref, tol, ltol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,T,Hq", [(64, 64, 8), (128, 64, 8), (128, 43, 6)])
+def test_two_row_tiles_over_many_cache_tiles(dtype, D, T, Hq):
+    """129 rows a head and more: scores of a cache tile take the place of the tile
+    before's probabilities, over long segments and from one segment to the next.
+    Equal calls give equal bits."""
+    a = Attention(dtype, D, Hq, 2, T, 32, [9000, 130, 2000, 0, 5000], tree=True, seed=18, sigma=1.5)
+    ref, lref, tol, ltol = a.reference()
+    cache = a.make_cache(q)
+    out, lse = a.call(cache)
+    check(out, lse, ref, lref, tol, ltol)
+    for _ in range(10):
+        again = a.call(cache)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
