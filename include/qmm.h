@@ -398,7 +398,8 @@ typedef struct {
  * it, whatever they hold, NaN and infinities included; nothing past row
  * L + n - 1 is read.
  * Scores, softmax statistics and sums are fp32; the exponentials are rounded
- * to the 16-bit type for the product with V, as the outputs are at the end.
+ * to the 16-bit type for the product with V, as the outputs are at the end (in
+ * f16 one below 2^-32 of the row's largest counts in the sum of exponentials alone).
  * All pointers to 16-bit data are 16-byte aligned.  Asynchronous on `stream`
  * (the attention kernel, and one that adds up the parts of rows that it cut
  * between CTAs, in a fixed order: equal calls give equal bits).

@@ -114,6 +114,14 @@ __device__ __forceinline__ uint32_t zero_nonfinite(uint32_t w) {
   return w;
 }
 
+// The kernels' running maximum m, the base of P = 2^(c s - m), is the row's largest
+// c s less this: 0 in bf16, whose range P needs no part of.  In f16 what lies below
+// 2^-25 is lost from P V (not from the sum l): with the largest P between 2^7 and,
+// as m may lag by 8, 2^15, that is 2^-32 of the largest, or 3e-5 over 131,072 rows
+// instead of 4e-3.
+template <bool BF16>
+constexpr float ATTN_BASE_BELOW = BF16 ? 0.f : 7.f;
+
 // Cached rows L and nodes n of sequence b, brought into the range that the
 // page table can hold (what is out of range is reported, not followed).
 __device__ __forceinline__ bool attn_sizes(const AttnParams& p, int b, int& L, int& n) {

@@ -3,8 +3,8 @@
 //
 // Per row r and cache row j: s = q_r . K_j (m16n8k16, rows as M), then with the
 // running maximum m, p = 2^(c s - m), l += p, O += p V_j, all fp32.  m may lag
-// behind the true maximum by up to 8 (p <= 256), so that O is rescaled only
-// when a row's maximum grows by more than that.
+// behind the true maximum by up to 8 (p <= 2^8; in f16 2^15, ATTN_BASE_BELOW), so
+// that O is rescaled only when a row's maximum grows by more than that.
 //
 // With at most 16 rows there are at most 32 flops for each byte of the cache, so
 // the kernel is bound by the cache's stream.  Every warp of the CTA keeps a
@@ -255,7 +255,7 @@ __global__ void __maxnreg__(216) attn_mma_kernel(const __grid_constant__ AttnPar
                       fmaxf(s[1][2 * half], s[1][2 * half + 1]));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-      mx[half] = x * p.scale_log2;
+      mx[half] = x * p.scale_log2 - ATTN_BASE_BELOW<BF16>;
       grow |= mx[half] > m[half] + 8.f;
     }
     if (__any_sync(0xFFFFFFFFu, grow)) {

@@ -10,8 +10,9 @@
 //   O += P V      A = P in tensor memory (16 bits), B = V in shared memory
 // with S, O and the statistics in fp32.  One thread owns one row (a lane of
 // tensor memory), so the softmax needs no exchange between threads.  m may lag
-// behind the true maximum by up to 8 (P <= 256): O is rescaled, by the softmax
-// warps and through their registers, only when a row of the warp grows more.
+// behind the true maximum by up to 8 (P <= 2^8; in f16 2^15, ATTN_BASE_BELOW): O is
+// rescaled, by the softmax warps and through their registers, only when a row of
+// the warp grows more.
 //   warps 0 .. 4 NQ - 1   softmax, rescaling, output (four warps a row tile)
 //   two warps (NQ = 2: one) issue the MMAs
 //   two warps             load K and V tiles, one ring each: tensor copies of 16
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
               x[(i >> 1) & 3] = fmaxf(x[(i >> 1) & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
           mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
-        mx *= p.scale_log2;
+        mx = mx * p.scale_log2 - ATTN_BASE_BELOW<BF16>;
         // (rows past the item's hold anything and must not decide for the others)
         if (__any_sync(0xFFFFFFFFu, in && mx > m + 8.f)) {
           const float mn = fmaxf(m, mx);

@@ -56,3 +56,32 @@ def test_two_row_tiles_over_many_cache_tiles(dtype, D, T, Hq):
     for _ in range(10):
         again = a.call(cache)
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("B,L,T,Hq,Hkv", [
+    (1, 20000, 3, 2, 1),      # 6 rows a head
+    (2, 20000, 16, 4, 2),     # 32 rows
+    (1, 20000, 64, 8, 2),     # 256 rows
+    (120, 900, 2, 16, 16),    # many short sequences
+    (120, 400, 10, 32, 16),   # the same, 20 rows
+])
+def test_f16_tails_far_below_the_peaks(B, L, T, Hq, Hkv):
+    """Every 16th cached row scores highest and has values of 0; all others weigh
+    e^-17.5 = 2^-25.2 of it, with values of 1000: they alone make the output.  With
+    a base at least 2^7 below a row's maximum, an f16 probability loses at most
+    2^-25 of 2^7 of the largest, so the bound's term 2^-25 sum |v| becomes 2^-32
+    sum |v| over the number of the largest."""
+    a = Attention("f16", 64, Hq, Hkv, T, 32, [L] * B, seed=19)
+    a.q.zero_(), a.k.zero_(), a.k_pool.zero_()
+    a.q[..., 0] = 8.0  # scores are k[0]
+    a.k_pool[..., 0], a.k[..., 0] = -17.5, -17.5
+    a.v_pool.fill_(1000.0), a.v.fill_(1000.0)
+    a.k_pool[:, :, :, ::16, 0], a.v_pool[:, :, :, ::16] = 0.0, 0.0
+    ref, lref, tol, ltol = a.reference()
+    assert ref.min() > 1000 * 14 * 2.0 ** -25.3
+    peaks = (L + 15) // 16
+    total = 1000.0 * (L - peaks + 1 + torch.arange(T, device="cuda"))[:, None, None].double()  # sum |v| of what node t sees
+    tol -= 2.0 ** -25 * (total + 1)
+    tol += 2.0 ** -32 * total / peaks + 2.0 ** -25
+    out, lse = a.call(a.make_cache(q), ragged=False)
+    check(out, lse, ref, lref, tol, ltol)
