@@ -71,3 +71,23 @@ def test_accepted_after_rejections_then_an_only_child_rejected(B, V, rejected):
     for _ in range(5):
         again = q.verify_sample(*args, parents=_cuda(parents))
         assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
+@pytest.mark.parametrize("B,T,V", [(300, 1, 3000), (100, 4, 3000), (300, 4, 8000)])
+@pytest.mark.parametrize("offset", [2.0 ** 20, -2.0 ** 20])
+def test_scores_with_a_large_common_offset(B, T, V, offset):
+    """A softmax does not depend on an offset.  2^20 is a multiple of the scores' own
+    spacing of 1/8 there, so differences of scores are exact in fp32, and so is the
+    definition's walk to 64-bit rounding; margins below 1e-3 are not compared."""
+    r = np.random.default_rng(V + T)
+    target = torch.from_numpy((r.standard_normal((B, T, V)) * 2 + offset).astype(np.float32))
+    draft = torch.from_numpy((r.standard_normal((B, T, V)) * 2 + offset).astype(np.float32))
+    parents = np.tile(np.arange(-1, T - 1, dtype=np.int32), (B, 1))
+    tokens = np.zeros((B, T), np.int32)
+    tokens[:, 1:] = target[:, :-1].argmax(2).numpy()  # accepted most often
+    u = r.random((B, T)).astype(np.float32)
+    noise = r.exponential(size=(B, V)).astype(np.float32) + np.float32(1e-30)
+    got = q.verify_sample(target.cuda(), draft.cuda(), _cuda(tokens), _cuda(u), _cuda(noise), parents=_cuda(parents))
+    if T > 1:
+        assert (got[0][:, 0] == T - 1).float().mean() > 0.25  # nodes without children are reached
+    _compare(got, target, draft, tokens, parents, u, noise, 0.1)
