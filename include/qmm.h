@@ -405,8 +405,9 @@ typedef struct {
  * between CTAs, in a fixed order: equal calls give equal bits).
  * Errors: STATE, INVALID_ARG (NULL pointers, bad struct_size or scale), SHAPE
  * (layer, B, T or table_width out of range), ALIGN (pointers, strides,
- * ld_table < table_width, ld_mask < T), DEVICE, CUDA.  Lengths and page ids
- * are checked on the device (qmm_cache_sync_status). */
+ * ld_table < table_width, ld_mask < T; not strides of dimensions of one entry),
+ * DEVICE, CUDA.  Lengths and page ids are checked on the device
+ * (qmm_cache_sync_status). */
 int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* args, void* stream);
 
 /* Keep one branch of every sequence's drafted nodes: in every layer and both
@@ -420,7 +421,7 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* args, void* stream);
  *   path: device, int32 [B][T], row stride ld_path.  accept: device, int32 [B][2].
  *   lens_out: device, int32 [B]; not lens, which every CTA of the call reads.
  * Asynchronous.  Errors: STATE, INVALID_ARG (NULL, lens_out is lens), SHAPE (B, T, table_width),
- * ALIGN (ld_path < T, ld_table < table_width), DEVICE, CUDA. */
+ * ALIGN (ld_path < T or ld_table < table_width with B > 1), DEVICE, CUDA. */
 int qmm_cache_commit(qmm_cache_t h, int B, int T, const int32_t* page_table, int64_t ld_table,
                      int table_width, const int32_t* lens, const int32_t* path, int64_t ld_path,
                      const int32_t* accept, int32_t* lens_out, void* stream);

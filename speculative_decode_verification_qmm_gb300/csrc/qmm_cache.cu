@@ -328,9 +328,13 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   if ((((uintptr_t)a->lse | (uintptr_t)a->page_table | (uintptr_t)a->lens | (uintptr_t)a->n_tokens) & 3) ||
       ((uintptr_t)a->mask & 7))
     return QMM_ERR_ALIGN;
+  // strides of dimensions with one entry are not followed
+  const int dims[3][2] = {{a->B, a->B}, {a->T, a->T}, {d.n_q_heads, d.n_kv_heads}};
   for (int i = 0; i < 3; ++i)
-    if ((a->q_stride[i] | a->k_stride[i] | a->v_stride[i] | a->out_stride[i]) & 7) return QMM_ERR_ALIGN;
-  if (a->ld_table < a->table_width || (a->mask && a->ld_mask < a->T)) return QMM_ERR_ALIGN;
+    if ((dims[i][0] > 1 && ((a->q_stride[i] | a->out_stride[i]) & 7)) ||
+        (dims[i][1] > 1 && ((a->k_stride[i] | a->v_stride[i]) & 7)))
+      return QMM_ERR_ALIGN;
+  if (a->B > 1 && (a->ld_table < a->table_width || (a->mask && a->ld_mask < a->T))) return QMM_ERR_ALIGN;
   int rc = check_current(h);
   if (rc != QMM_OK) return rc;
 
@@ -392,7 +396,7 @@ int qmm_cache_commit(qmm_cache_t h, int B, int T, const int32_t* page_table, int
   if (!page_table || !lens || !path || !accept || !lens_out || lens_out == lens) return QMM_ERR_INVALID_ARG;
   if (B < 1 || B > h->d.max_batch || T < 1 || T > QMM_TREE_MAX_T || table_width < 1) return QMM_ERR_SHAPE;
   if (((int64_t)table_width << h->page_shift) > INT32_MAX - 4096) return QMM_ERR_SHAPE;
-  if (ld_path < T || ld_table < table_width) return QMM_ERR_ALIGN;
+  if (B > 1 && (ld_path < T || ld_table < table_width)) return QMM_ERR_ALIGN;
   if (((uintptr_t)page_table | (uintptr_t)lens | (uintptr_t)path | (uintptr_t)accept | (uintptr_t)lens_out) & 3)
     return QMM_ERR_ALIGN;
   const int rc = check_current(h);

@@ -85,3 +85,27 @@ def test_f16_tails_far_below_the_peaks(B, L, T, Hq, Hkv):
     tol += 2.0 ** -32 * total / peaks + 2.0 ** -25
     out, lse = a.call(a.make_cache(q), ragged=False)
     check(out, lse, ref, lref, tol, ltol)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv", [(1, 5, 4, 2), (3, 1, 4, 2), (2, 3, 1, 1), (1, 1, 1, 1), (1, 20, 4, 1)])
+def test_strides_that_are_never_used(B, T, Hq, Hkv):
+    """A dimension of one entry has any stride: it is neither checked nor followed."""
+    a = Attention("bf16", 64, Hq, Hkv, T, 16, [33, 5, 60][:B], tree=True, seed=24)
+    ref, lref, tol, ltol = a.reference()
+    cache = a.make_cache(q)
+
+    def odd(x, stride=3):
+        return x.as_strided(x.shape, [stride if n == 1 else s for n, s in zip(x.shape, x.stride())])
+
+    table, lens, mask = a.table.cuda(), torch.tensor(a.lens, dtype=torch.int32).cuda(), a.mask.cuda()
+    out = odd(torch.empty(B, T, Hq, 64, dtype=torch.bfloat16, device="cuda"))
+    _, lse = cache.attend(0, odd(a.q), odd(a.k), odd(a.v), odd(table, 1), lens, mask=odd(mask, 1), out=out)
+    check(out, lse, ref, lref, tol, ltol)
+    path = torch.arange(1, T + 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+    accept = torch.tensor([[T - 1, 0]] * B, dtype=torch.int32, device="cuda")
+    got = cache.commit(odd(table, 1), lens, odd(path, 1), accept)
+    assert got.tolist() == [n + T for n in a.lens] and cache.sync_status() == q.QMM_OK
+    if B > 1:  # and where there are several entries it is
+        with pytest.raises(q.QmmError) as e:
+            cache.commit(table.as_strided(table.shape, (1, 1)), lens, path, accept)
+        assert e.value.code == q.QMM_ERR_ALIGN
