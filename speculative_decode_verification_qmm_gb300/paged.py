@@ -21,7 +21,7 @@ import ctypes
 import functools
 import struct
 
-from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_attn_args,
+from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_ERR_DEVICE, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_attn_args,
                    qmm_cache_desc, qmm_sample_args)
 
 
@@ -59,24 +59,26 @@ def _dtype(dtype):
     return _CODES[dtype]
 
 
-def _refuse(name, t, dtype, shape):
+def _refuse(name, t, dtype, shape, device):
     if not t.is_cuda or t.dtype != dtype:
         raise TypeError(f"{name} must be a CUDA tensor of {dtype}, not {t.dtype} on {t.device}")
-    raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be on cuda:{device}, not {t.device}")
 
 
-def _flat(name, t, dtype, shape):
-    """Refuses a tensor that is not on the GPU, not contiguous, or of another type or shape."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        _refuse(name, t, dtype, shape)
+def _flat(name, t, dtype, shape, device):
+    """Refuses a tensor that is not on that GPU, not contiguous, or of another type or shape."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _refuse(name, t, dtype, shape, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _strided(name, t, dtype, shape):
+def _strided(name, t, dtype, shape, device):
     """The same for one whose last dimension alone has to be contiguous."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        _refuse(name, t, dtype, shape)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _refuse(name, t, dtype, shape, device)
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
 
@@ -188,27 +190,31 @@ def verify_sample(target, draft, tokens, u, noise, parents=None, temperature=Non
     if target.dim() != 3 or not target.is_cuda:
         raise ValueError("target must be a CUDA tensor [B, T, V]")
     B, T, V = target.shape
+    at = target.get_device()
     _rows("target", target)
     if draft is not None:
         if draft.dim() != 3 or draft.shape[1] not in (T, T - 1):
             raise ValueError(f"draft must hold {T} or {T - 1} rows a sequence")
-        _strided("draft", draft, target.dtype, (B, draft.shape[1], V))
+        _strided("draft", draft, target.dtype, (B, draft.shape[1], V), at)
         if draft.shape[1] == 0:
             draft = None
     i32, f32, nodes = torch.int32, torch.float32, (B, T)
     # the usual call's checks in one expression; what fails is named after it
-    if (tokens.shape != nodes or tokens.dtype is not i32 or not tokens.is_cuda or not tokens.is_contiguous()
-            or u.shape != nodes or u.dtype is not f32 or not u.is_cuda or not u.is_contiguous()
-            or noise.shape != (B, V) or noise.dtype is not f32 or not noise.is_cuda or not noise.is_contiguous()):
-        _flat("tokens", tokens, i32, nodes)
-        _flat("u", u, f32, nodes)
-        _flat("noise", noise, f32, (B, V))
+    if (tokens.shape != nodes or tokens.dtype is not i32 or tokens.get_device() != at or not tokens.is_contiguous()
+            or u.shape != nodes or u.dtype is not f32 or u.get_device() != at or not u.is_contiguous()
+            or noise.shape != (B, V) or noise.dtype is not f32 or noise.get_device() != at
+            or not noise.is_contiguous()):
+        _flat("tokens", tokens, i32, nodes, at)
+        _flat("u", u, f32, nodes, at)
+        _flat("noise", noise, f32, (B, V), at)
     if parents is not None:
-        _flat("parents", parents, i32, nodes)
+        _flat("parents", parents, i32, nodes, at)
     if temperature is not None:
-        _flat("temperature", temperature, f32, (B,))
+        _flat("temperature", temperature, f32, (B,), at)
     if n_tokens is not None:
-        _flat("n_tokens", n_tokens, i32, (B,))
+        _flat("n_tokens", n_tokens, i32, (B,), at)
+    if torch._C._cuda_getDevice() != at:
+        _check("verify_sample", QMM_ERR_DEVICE)
     dev = target.device
     accept = torch.empty((B, 2), dtype=i32, device=dev)
     path = torch.empty((B, T), dtype=i32, device=dev)
@@ -253,12 +259,15 @@ class PagedCache:
         for name, pool in (("k_pool", k_pool), ("v_pool", v_pool)):
             if pool is None:
                 pool = torch.zeros(shape, dtype=dtype, device=device)
-            _flat(name, pool, dtype, shape)
+            _flat(name, pool, dtype, shape, pools[0].get_device() if pools else max(0, pool.get_device()))
             pools.append(pool)
         self.k_pool, self.v_pool = pools
         self.n_layers, self.n_pages, self.page_size = n_layers, n_pages, page_size
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.dtype = n_q_heads, n_kv_heads, head_dim, dtype
         self.handle = None
+        self._device = pools[0].get_device()
+        if torch._C._cuda_getDevice() != self._device:
+            _check("PagedCache", QMM_ERR_DEVICE)
         self.handle = qmm_cache_create(_dtype(dtype), n_layers, n_pages, page_size, n_q_heads, n_kv_heads, head_dim,
                                        max_batch, self.k_pool, self.v_pool, stream)
         self._users = [0] * n_pages
@@ -276,31 +285,32 @@ class PagedCache:
         if q.dim() != 4:
             raise ValueError("q must be [B, T, n_q_heads, head_dim]")
         B, T, _, _ = q.shape
-        dt, Hq, D, i32 = self.dtype, self.n_q_heads, self.head_dim, torch.int32
+        dt, Hq, D, i32, at = self.dtype, self.n_q_heads, self.head_dim, torch.int32, self._device
         wide, new, seqs = (B, T, Hq, D), (B, T, self.n_kv_heads, D), (B,)
         qs, ks, vs, table = q.stride(), k.stride(), v.stride(), page_table.shape
         # all of a usual call's checks in one expression; what fails is named after it
         if (q.shape != wide or k.shape != new or v.shape != new or q.dtype is not dt or k.dtype is not dt
-                or v.dtype is not dt or not q.is_cuda or not k.is_cuda or not v.is_cuda or qs[3] != 1 or ks[3] != 1
-                or vs[3] != 1 or len(table) != 2 or table[0] != B or page_table.dtype is not i32
-                or not page_table.is_cuda or page_table.stride(1) != 1 or lens.shape != seqs or lens.dtype is not i32
-                or not lens.is_cuda or not lens.is_contiguous()):
-            _strided("q", q, dt, wide)
-            _strided("k", k, dt, new)
-            _strided("v", v, dt, new)
+                or v.dtype is not dt or q.get_device() != at or k.get_device() != at or v.get_device() != at
+                or qs[3] != 1 or ks[3] != 1 or vs[3] != 1 or len(table) != 2 or table[0] != B
+                or page_table.dtype is not i32 or page_table.get_device() != at or page_table.stride(1) != 1
+                or lens.shape != seqs or lens.dtype is not i32 or lens.get_device() != at
+                or not lens.is_contiguous()):
+            _strided("q", q, dt, wide, at)
+            _strided("k", k, dt, new, at)
+            _strided("v", v, dt, new, at)
             self._table(page_table, lens, B)
         if mask is not None:
-            _strided("mask", mask, torch.int64, (B, T))
+            _strided("mask", mask, torch.int64, (B, T), at)
         if n_tokens is not None:
-            _flat("n_tokens", n_tokens, i32, seqs)
+            _flat("n_tokens", n_tokens, i32, seqs, at)
         if out is None:
             out = torch.empty(wide, dtype=dt, device=q.device)
         else:
-            _strided("out", out, dt, wide)
+            _strided("out", out, dt, wide, at)
         if lse is None:
             lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
         else:
-            _flat("lse", lse, torch.float32, (B, T, Hq))
+            _flat("lse", lse, torch.float32, (B, T, Hq), at)
         _tree_attention(self.handle, layer, q, k, v, page_table, lens, out, lse, mask, n_tokens, scale, None, qs, ks,
                         vs, out.stride(), page_table.stride(0))
         return out, lse
@@ -312,23 +322,23 @@ class PagedCache:
         if stream is not None:  # lens_out is allocated on the stream that writes it
             with torch.cuda.stream(stream):
                 return self.commit(page_table, lens, path, accept, lens_out)
-        i32, seqs, table, nodes = torch.int32, lens.shape, page_table.shape, path.shape
+        i32, seqs, table, nodes, at = torch.int32, lens.shape, page_table.shape, path.shape, self._device
         B = seqs[0]
         # the usual call's checks in one expression; what fails is named after it
-        if (len(seqs) != 1 or lens.dtype is not i32 or not lens.is_cuda or not lens.is_contiguous() or len(table) != 2
-                or table[0] != B or page_table.dtype is not i32 or not page_table.is_cuda
+        if (len(seqs) != 1 or lens.dtype is not i32 or lens.get_device() != at or not lens.is_contiguous()
+                or len(table) != 2 or table[0] != B or page_table.dtype is not i32 or page_table.get_device() != at
                 or page_table.stride(1) != 1 or len(nodes) != 2 or nodes[0] != B or path.dtype is not i32
-                or not path.is_cuda or path.stride(1) != 1 or accept.shape != (B, 2) or accept.dtype is not i32
-                or not accept.is_cuda or not accept.is_contiguous()):
+                or path.get_device() != at or path.stride(1) != 1 or accept.shape != (B, 2)
+                or accept.dtype is not i32 or accept.get_device() != at or not accept.is_contiguous()):
             self._table(page_table, lens, B)
             if path.dim() != 2:
                 raise ValueError("path must be [B, T]")
-            _strided("path", path, i32, (B, path.shape[1]))
-            _flat("accept", accept, i32, (B, 2))
+            _strided("path", path, i32, (B, path.shape[1]), at)
+            _flat("accept", accept, i32, (B, 2), at)
         if lens_out is None:
             lens_out = torch.empty_like(lens)
         else:
-            _flat("lens_out", lens_out, i32, (B,))
+            _flat("lens_out", lens_out, i32, (B,), at)
         qmm_cache_commit(self.handle, page_table, lens, path, accept, lens_out)
         return lens_out
 
@@ -336,23 +346,22 @@ class PagedCache:
         """Copies the first rows[i] rows (None: all) of page src[i] to page dst[i]
         in every layer.  See qmm_cache_copy."""
         import torch
-        shape, i32 = (src.shape[0],), torch.int32
-        _flat("src", src, i32, shape)
-        _flat("dst", dst, i32, shape)
+        shape, i32, at = (src.numel(),), torch.int32, self._device
+        _flat("src", src, i32, shape, at)
+        _flat("dst", dst, i32, shape, at)
         if rows is not None:
-            _flat("rows", rows, i32, shape)
+            _flat("rows", rows, i32, shape, at)
         qmm_cache_copy(self.handle, src, dst, rows, stream)
 
     def sync_status(self, stream=None) -> int:
         return qmm_cache_sync_status(self.handle, stream)
 
-    @staticmethod
-    def _table(page_table, lens, B):
+    def _table(self, page_table, lens, B):
         import torch
         if page_table.dim() != 2:
             raise ValueError("page_table must be [B, pages]")
-        _strided("page_table", page_table, torch.int32, (B, page_table.shape[1]))
-        _flat("lens", lens, torch.int32, (B,))
+        _strided("page_table", page_table, torch.int32, (B, page_table.shape[1]), self._device)
+        _flat("lens", lens, torch.int32, (B,), self._device)
 
     # -------------------------------------------------------------- bookkeeping
     @property
