@@ -379,10 +379,12 @@ class PagedCache:
             self._users[p] = 1
         return pages
 
-    def reserve(self, seqs, rows: int) -> None:
+    def reserve(self, seqs, rows: int, stream=None) -> None:
         """Pages of their own for `rows` more rows of every sequence: fresh ones
         where more are needed, and a copy of a partly filled last page that
-        others share.  Nothing is taken when there are too few."""
+        others share, made on `stream` (None: the current one), which has to be the
+        one that writes the sequences' rows.  Nothing is taken when there are too
+        few."""
         need, shared, left = [], [], list(self._users)
         for s in seqs:
             tail = s.length // self.page_size
@@ -405,13 +407,16 @@ class PagedCache:
                 self._users[s.pages[i]] -= 1
                 s.pages[i] = fresh
             s.pages += self._take(n)
-        self._copy(copies)
+        self._copy(copies, stream)
 
     def _copy(self, copies, stream=None):
         import torch
+        if stream is not None:  # the page ids are allocated on the stream that reads them
+            with torch.cuda.stream(stream):
+                return self._copy(copies)
         if copies:
             t = torch.tensor(copies, dtype=torch.int32).t().contiguous().to(self.k_pool.device)
-            self.copy_pages(t[0], t[1], t[2], stream)
+            self.copy_pages(t[0], t[1], t[2])
 
     def advance(self, seqs, counts) -> None:
         """The host's record of `counts` committed rows a sequence."""
@@ -438,9 +443,13 @@ class PagedCache:
                 self._free.append(p)
         seq.pages, seq.length = [], 0
 
-    def tables(self, seqs):
-        """(page_table, lens) CUDA tensors for a call over `seqs`."""
+    def tables(self, seqs, stream=None):
+        """(page_table, lens) CUDA tensors for calls over `seqs` on `stream` (None: the
+        current one)."""
         import torch
+        if stream is not None:  # allocated on the stream that reads them
+            with torch.cuda.stream(stream):
+                return self.tables(seqs)
         width = max(1, max(len(s.pages) for s in seqs))
         rows = [s.pages + [0] * (width - len(s.pages)) for s in seqs]
         dev = self.k_pool.device

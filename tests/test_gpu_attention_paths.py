@@ -109,3 +109,44 @@ def test_strides_that_are_never_used(B, T, Hq, Hkv):
         with pytest.raises(q.QmmError) as e:
             cache.commit(table.as_strided(table.shape, (1, 1)), lens, path, accept)
         assert e.value.code == q.QMM_ERR_ALIGN
+
+
+def test_a_step_on_a_side_stream():
+    """attend, fork, reserve (which copies the shared last page) and attend again, all
+    on one stream that is behind the host and the current stream: the fork's copy
+    holds the rows that the first call wrote."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(25)
+    cache = q.PagedCache(2, 8, 16, 4, 2, 64)
+    x = [torch.randn(1, 5, 8, 64, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    s = torch.cuda.Stream()
+
+    def attend(seq, layer, part, stream):
+        table, lens = cache.tables([seq], stream)
+        return cache.attend(layer, part[:, :, :4], part[:, :, 4:6], part[:, :, 6:], table, lens, stream=stream)[0]
+
+    def step(stream):
+        a = cache.new_sequence()
+        cache.reserve([a], 5, stream)
+        for layer in range(2):
+            attend(a, layer, x[0], stream)
+        cache.advance([a], [5])
+        b = cache.fork(a)
+        cache.reserve([b], 5, stream)
+        assert b.pages != a.pages
+        return a, b, [attend(b, layer, x[1], stream) for layer in range(2)]
+
+    a, b, want = step(None)
+    pages, length = [a.pages[0], b.pages[0]], a.length
+    torch.cuda.synchronize()
+    rows = cache.k_pool[:, pages].clone()
+    cache.free(a), cache.free(b)
+    cache.k_pool.zero_(), cache.v_pool.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+    a, b, got = step(s)
+    s.synchronize()
+    assert length == a.length == 5 and cache.sync_status() == q.QMM_OK
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(cache.k_pool[:, [a.pages[0], b.pages[0]]][:, :, :, :5], rows[:, :, :, :5])
