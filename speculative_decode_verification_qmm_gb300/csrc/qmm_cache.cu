@@ -169,36 +169,38 @@ struct CopyParams {
   const int32_t* dst;
   const int32_t* rows;
   int32_t* status;
-  int Hkv, page_shift, chunks;
+  int Hkv, page_shift, chunks, pools;  // pools: of single layers, two each
 };
 
-// CTA (i, layer and pool): the rows of a head are contiguous, rows * chunks
+// CTA (i, layer and pool; past 65,535 of these the next so many): the rows of a head are contiguous, rows * chunks
 // 16-byte chunks; heads follow each other a page of rows apart.
 __global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const __grid_constant__ CopyParams p) {
-  const int i = blockIdx.x, lp = blockIdx.y;
+  const int i = blockIdx.x;
   const int s = p.src[i], d = p.dst[i], page = 1 << p.page_shift;
   const int rows = p.rows ? p.rows[i] : page;
   if (s < 0 || s >= p.n_pages || d < 0 || d >= p.n_pages || rows < 0 || rows > page) {
-    if (threadIdx.x == 0 && lp == 0) atomicOr(p.status, DEV_ERR_INDEX);
+    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, DEV_ERR_INDEX);
     return;
   }
   if (s == d) return;
-  uint16_t* base = (lp & 1 ? p.v_pool : p.k_pool) + (lp >> 1) * p.layer_stride;
-  const uint4* from = reinterpret_cast<const uint4*>(base + s * p.page_stride);
-  uint4* to = reinterpret_cast<uint4*>(base + d * p.page_stride);
   const int per = rows * p.chunks, head = p.chunks << p.page_shift, total = p.Hkv * per;
-  for (int at = threadIdx.x; at < total; at += COPY_THREADS * COPY_BATCH) {
-    uint4 v[COPY_BATCH];
-    int off[COPY_BATCH];
+  for (int lp = blockIdx.y; lp < p.pools; lp += gridDim.y) {
+    uint16_t* base = (lp & 1 ? p.v_pool : p.k_pool) + (lp >> 1) * p.layer_stride;
+    const uint4* from = reinterpret_cast<const uint4*>(base + s * p.page_stride);
+    uint4* to = reinterpret_cast<uint4*>(base + d * p.page_stride);
+    for (int at = threadIdx.x; at < total; at += COPY_THREADS * COPY_BATCH) {
+      uint4 v[COPY_BATCH];
+      int off[COPY_BATCH];
 #pragma unroll
-    for (int u = 0; u < COPY_BATCH; ++u) {
-      const int x = at + u * COPY_THREADS;
-      off[u] = x / per * head + x % per;
-      if (x < total) v[u] = from[off[u]];
+      for (int u = 0; u < COPY_BATCH; ++u) {
+        const int x = at + u * COPY_THREADS;
+        off[u] = x / per * head + x % per;
+        if (x < total) v[u] = from[off[u]];
+      }
+#pragma unroll
+      for (int u = 0; u < COPY_BATCH; ++u)
+        if (at + u * COPY_THREADS < total) to[off[u]] = v[u];
     }
-#pragma unroll
-    for (int u = 0; u < COPY_BATCH; ++u)
-      if (at + u * COPY_THREADS < total) to[off[u]] = v[u];
   }
 }
 
@@ -452,7 +454,9 @@ int qmm_cache_copy(qmm_cache_t h, int n, const int32_t* src, const int32_t* dst,
   p.Hkv = h->d.n_kv_heads;
   p.page_shift = h->page_shift;
   p.chunks = h->d.head_dim / 8;
-  copy_kernel<<<dim3((unsigned)n, (unsigned)(2 * h->d.n_layers)), COPY_THREADS, 0, (cudaStream_t)stream>>>(p);
+  p.pools = 2 * h->d.n_layers;
+  const unsigned y = p.pools < 65535 ? p.pools : 65535;
+  copy_kernel<<<dim3((unsigned)n, y), COPY_THREADS, 0, (cudaStream_t)stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }

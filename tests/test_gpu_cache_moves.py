@@ -185,3 +185,21 @@ def test_refusals():
     p.cache.close()
     assert L.qmm_cache_copy(h, 0, None, None, None, None) == q.QMM_ERR_STATE
     assert L.qmm_cache_sync_status(h, None) == q.QMM_ERR_STATE
+
+
+def test_more_layers_than_a_grid_dimension_holds():
+    """What qmm_cache_create accepts can be copied and committed: 40,000 layers, 80,000
+    pools of a layer."""
+    layers = 40000
+    p = Pools(layers, 3, 16, 1, 64, seed=3)
+    want = p.bits()
+    for pool in want:
+        pool[:, 2, :, :9] = pool[:, 0, :, :9]
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    p.cache.copy_pages(dev([0]), dev([2]), dev([9]))
+    assert p.equals(want)
+    for pool in want:
+        pool[:, 2, :, 3] = pool[:, 2, :, 6]
+    out = p.cache.commit(dev([[2]]), dev([2]), dev([[4, 0, 0, 0, 0]]), dev([[1, 0]]))
+    assert out.tolist() == [4] and p.equals(want)
+    assert p.cache.sync_status() == q.QMM_OK
