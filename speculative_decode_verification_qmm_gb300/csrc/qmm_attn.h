@@ -38,6 +38,6 @@ cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, const void* km
                            cudaStream_t st);
 
 // Sums of the partials that a launch with those tiles left (qmm_attn_join.cu).
-cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, cudaStream_t st);
+cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, int sms, cudaStream_t st);
 
 }  // namespace qmm

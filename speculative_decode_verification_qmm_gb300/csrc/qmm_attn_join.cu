@@ -31,7 +31,7 @@ namespace {
 constexpr int WARPS = 4;
 constexpr int RU = 4;  // rows of a lane
 constexpr int U = 2;   // parts in flight
-constexpr int JOIN_CTAS = 1216;  // eight an SM
+constexpr int CTAS_PER_SM = 8;
 
 template <bool BF16, int D, bool CUTS>
 __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel(const __grid_constant__ AttnParams p, int tk, int rows,
@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
 }
 
 template <bool BF16, int D, bool CUTS>
-cudaError_t launch(const AttnParams& p, int tk, int rows, cudaStream_t st) {
+cudaError_t launch(const AttnParams& p, int tk, int rows, int ctas, cudaStream_t st) {
   constexpr int PER = 128 / D * RU * (CUTS ? WARPS : 1);
   const int64_t units = CUTS ? p.grid - 1 : (int64_t)p.B * p.Hkv * p.RT;
   int chunks = ((p.R < rows ? p.R : rows) + PER - 1) / PER;
-  const int64_t most = (JOIN_CTAS + units - 1) / units;
+  const int64_t most = (ctas + units - 1) / units;
   if (chunks > most) chunks = (int)most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * chunks));
@@ -170,21 +170,22 @@ cudaError_t launch(const AttnParams& p, int tk, int rows, cudaStream_t st) {
 }
 
 template <bool BF16, int D>
-cudaError_t launch_one(const AttnParams& p, int tk, int rows, cudaStream_t st) {
+cudaError_t launch_one(const AttnParams& p, int tk, int rows, int sms, cudaStream_t st) {
   // Measured, CTAs by cuts against by items, in us with the attention kernel:
   // 2,560 items (128 sequences of up to 120 / 600 / 4,000 rows, head size 64): 36 :
   // 43, 68 : 78, 296 : 299; 5,120 (head size 128, up to 120 / 300 / 800): 87 : 103, 128
   // : 143, 212 : 222; 320 (16 sequences, up to 120 / 600 / 4,000): 18 : 17, 30 : 29,
   // 91 : 89; 384 (48 sequences, 8 heads): 13.6 : 13.1, 28 : 27, 90 : 88.
-  const bool cuts = (int64_t)p.B * p.Hkv * p.RT > JOIN_CTAS;
-  return cuts ? launch<BF16, D, true>(p, tk, rows, st) : launch<BF16, D, false>(p, tk, rows, st);
+  const int ctas = CTAS_PER_SM * sms;
+  const bool cuts = (int64_t)p.B * p.Hkv * p.RT > ctas;
+  return cuts ? launch<BF16, D, true>(p, tk, rows, ctas, st) : launch<BF16, D, false>(p, tk, rows, ctas, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, cudaStream_t st) {
-  if (D == 128) return bf16 ? launch_one<true, 128>(p, tk, rows, st) : launch_one<false, 128>(p, tk, rows, st);
-  return bf16 ? launch_one<true, 64>(p, tk, rows, st) : launch_one<false, 64>(p, tk, rows, st);
+cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, int sms, cudaStream_t st) {
+  if (D == 128) return bf16 ? launch_one<true, 128>(p, tk, rows, sms, st) : launch_one<false, 128>(p, tk, rows, sms, st);
+  return bf16 ? launch_one<true, 64>(p, tk, rows, sms, st) : launch_one<false, 64>(p, tk, rows, sms, st);
 }
 
 }  // namespace qmm

@@ -387,7 +387,7 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
                      : launch_attn_mma(p, bf16, d.head_dim, solo, st);
   // items of one unit each are never cut: nothing to join
   if (e == cudaSuccess && ((int64_t)a->table_width << h->page_shift) > tk)
-    e = launch_attn_join(p, bf16, d.head_dim, tk, rows, st);
+    e = launch_attn_join(p, bf16, d.head_dim, tk, rows, h->sm_count, st);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }
 

@@ -680,21 +680,25 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
-// Parts of a row in the eager statistics: about four CTAs per SM.
-int sample_chunks(int B, int T, int64_t V) {
-  int64_t c = 608 / (2ll * B * (T > 1 ? T - 1 : 1));
+// Parts of a row in the eager statistics: about four CTAs per SM; the most there are
+// on any GPU.
+int sample_chunks_most(int64_t V) {
   const int64_t most = (V + 4095) / 4096;
-  c = c < most ? c : most;
-  return (int)(c < 1 ? 1 : (c > MAX_CHUNKS ? MAX_CHUNKS : c));
+  return (int)(most < MAX_CHUNKS ? most : MAX_CHUNKS);
+}
+int sample_chunks(int B, int T, int64_t V, int sms) {
+  const int64_t c = 4ll * sms / (2ll * B * (T > 1 ? T - 1 : 1));
+  const int most = sample_chunks_most(V);
+  return (int)(c < 1 ? 1 : (c > most ? most : c));
 }
 // CTAs of a walk: all that two on each SM allow, while each has two entries a
-// thread and more.  Measured, 151,936 entries of 16 bits, blocks of 16: with at
+// thread and more.  Measured on 152 SMs, 151,936 entries of 16 bits, blocks of 16: with at
 // most 152 / 304 / 608 CTAs 12 sequences took 45 / 42 / 42 us, 20 took 76 / 60 /
 // 57, 32 took 78 / 70 / 81; 8 sequences of 1,000 entries 9.8 us, and 10.4 with
 // clusters of 16.
-int sample_cluster(int B, int64_t V) {
+int sample_cluster(int B, int64_t V, int sms) {
   int c = MAX_CLUSTER;
-  while (c > 1 && ((int64_t)B * c > 304 || (int64_t)c * WALK_THREADS * 4 > 2 * V)) c /= 2;
+  while (c > 1 && ((int64_t)B * c > 2ll * sms || (int64_t)c * WALK_THREADS * 4 > 2 * V)) c /= 2;
   return c;
 }
 // Eager while reading the rows of all nodes costs less than the walk's own steps,
@@ -741,10 +745,10 @@ cudaError_t launch_walk(const SampleParams& p, int B, int cluster, cudaStream_t 
 }
 
 template <int DT, bool WIDE>
-cudaError_t launch_sample(SampleParams& p, int B, int elem, cudaStream_t st) {
-  const int cluster = sample_cluster(B, p.V);
+cudaError_t launch_sample(SampleParams& p, int B, int elem, int sms, cudaStream_t st) {
+  const int cluster = sample_cluster(B, p.V, sms);
   if (!sample_eager(B, p.T, p.V, elem, p.draft != nullptr, p.parents == nullptr)) return launch_walk<DT, WIDE, false>(p, B, cluster, st);
-  p.chunks = sample_chunks(B, p.T, p.V);
+  p.chunks = sample_chunks(B, p.T, p.V, sms);
   const int rows = (p.T - 1) * (p.draft ? 2 : 1);  // the last node has no children
   sample_stats_kernel<DT><<<dim3((unsigned)p.chunks, (unsigned)rows, (unsigned)B), STAT_THREADS,
                             STAT_THREADS * STAT_DEPTH * 16, st>>>(p);
@@ -769,8 +773,8 @@ int qmm_verify_sample_workspace(int B, int T, int64_t V, int64_t* bytes) {
   *bytes = 0;
   const int rc = check_sizes(B, T, V);
   if (rc != QMM_OK) return rc;
-  // the most that any type, with or without drafter scores and parents, takes
-  *bytes = sample_eager(B, T, V, 2, false, true) ? (int64_t)B * T * 2 * sample_chunks(B, T, V) * (int64_t)sizeof(float2) : 256;
+  // the most that any type, with or without drafter scores and parents, takes on any GPU
+  *bytes = sample_eager(B, T, V, 2, false, true) ? (int64_t)B * T * 2 * sample_chunks_most(V) * (int64_t)sizeof(float2) : 256;
   return QMM_OK;
 }
 
@@ -820,13 +824,13 @@ int qmm_verify_sample(const qmm_sample_args* a, void* stream) {
   cudaError_t e;
   switch (a->dtype) {
     case QMM_DT_F32:
-      e = wide ? launch_sample<QMM_DT_F32, true>(p, a->B, elem, st) : launch_sample<QMM_DT_F32, false>(p, a->B, elem, st);
+      e = wide ? launch_sample<QMM_DT_F32, true>(p, a->B, elem, sms, st) : launch_sample<QMM_DT_F32, false>(p, a->B, elem, sms, st);
       break;
     case QMM_DT_BF16:
-      e = wide ? launch_sample<QMM_DT_BF16, true>(p, a->B, elem, st) : launch_sample<QMM_DT_BF16, false>(p, a->B, elem, st);
+      e = wide ? launch_sample<QMM_DT_BF16, true>(p, a->B, elem, sms, st) : launch_sample<QMM_DT_BF16, false>(p, a->B, elem, sms, st);
       break;
     default:
-      e = wide ? launch_sample<QMM_DT_F16, true>(p, a->B, elem, st) : launch_sample<QMM_DT_F16, false>(p, a->B, elem, st);
+      e = wide ? launch_sample<QMM_DT_F16, true>(p, a->B, elem, sms, st) : launch_sample<QMM_DT_F16, false>(p, a->B, elem, sms, st);
   }
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }

@@ -178,3 +178,12 @@ def test_tree_mask():
     assert chain[0, 63] == -1 and chain[0, 62] == (1 << 63) - 1
     with pytest.raises(ValueError):
         q.tree_mask(torch.tensor([[0]]))
+
+
+def test_sample_workspace_holds_for_any_gpu(L):
+    """Every row has room for all of its parts, 4,096 entries each and 32 at most,
+    whatever share of them a GPU's number of SMs makes a call use."""
+    for V, parts in ((1, 1), (4097, 2), (151936, 32)):
+        one = q.qmm_verify_sample_workspace(1, 8, V)
+        assert one == 8 * 2 * parts * 8
+        assert q.qmm_verify_sample_workspace(40, 8, V) == 40 * one
