@@ -63,8 +63,19 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
   pdl_wait();  // every CTA: the call has not ended before the attention kernel has
   if constexpr (CUTS) {
     const int4 cut = __ldcg(p.cuts + c0);
-    if (cut.w == 1)
-      for (c1 = c0 + 1; c1 + 1 < p.grid && __ldcg(&p.cuts[c1].w) == 2;) ++c1;
+    if (cut.w == 1) {
+      // the first worker from the next one on whose last unit is not of this item,
+      // 32 at a time: one after the other, 1,300 sequences of 16 rows and one
+      // of 131,072 with one head took 120 us, and take 91
+      for (c1 = c0 + 1;; c1 += 32) {
+        const bool on = c1 + lane + 1 < p.grid && __ldcg(&p.cuts[c1 + lane].w) == 2;
+        const unsigned end = __ballot_sync(0xFFFFFFFFu, !on);
+        if (end) {
+          c1 += __ffs(end) - 1;
+          break;
+        }
+      }
+    }
     cur.b = cut.x, cur.h = cut.y, cur.rt = cut.z;
   }
   if (c0 == c1) return;

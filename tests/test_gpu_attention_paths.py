@@ -150,3 +150,16 @@ def test_a_step_on_a_side_stream():
     assert length == a.length == 5 and cache.sync_status() == q.QMM_OK
     assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert torch.equal(cache.k_pool[:, [a.pages[0], b.pages[0]]][:, :, :, :5], rows[:, :, :, :5])
+
+
+@pytest.mark.parametrize("D,T,Hq", [(128, 1, 1), (64, 3, 2), (128, 9, 4)])
+def test_one_item_over_most_of_the_grid_among_many(D, T, Hq):
+    """More items than the join has CTAs for by item, and one that goes on through more
+    workers than a warp has lanes."""
+    B = 1300
+    lens = [i % 19 for i in range(B)]
+    lens[700] = 70001
+    a = Attention("bf16", D, Hq, 1, T, 16, lens, tree=True, seed=26)
+    ref, lref, tol, ltol = a.reference()
+    out, lse = a.call(a.make_cache(q))
+    check(out, lse, ref, lref, tol, ltol)
