@@ -163,3 +163,49 @@ def test_one_item_over_most_of_the_grid_among_many(D, T, Hq):
     ref, lref, tol, ltol = a.reference()
     out, lse = a.call(a.make_cache(q))
     check(out, lse, ref, lref, tol, ltol)
+
+
+@pytest.mark.parametrize("T,Hq", [(16, 16), (48, 16), (64, 32)])
+def test_offsets_past_32_bits_with_many_rows(T, Hq):
+    """32, 96 and 256 rows a head in the last layer of pools of more than 2^32
+    elements: copied rows and written nodes are addressed in 64 bits."""
+    layers, page, Hkv, D = 9, 1024, 8, 128
+    n_pages = (1 << 32) // (8 * page * Hkv * D) + 1
+    k_pool = torch.zeros(layers, n_pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    v_pool = torch.zeros_like(k_pool)
+    assert k_pool.numel() > 1 << 32
+    a = Attention("bf16", D, Hq, Hkv, T, page, [700, 1010], [T, T - 1], tree=True, seed=27, extra_pages=0)
+    last = [n_pages - 1 - i for i in range(a.k_pool.shape[1])]
+    k_pool[layers - 1, last] = a.k_pool[0]
+    v_pool[layers - 1, last] = a.v_pool[0]
+    ref, lref, tol, ltol = a.reference()
+    want = a.expect_pools()
+    cache = q.PagedCache(layers, n_pages, page, Hq, Hkv, D, max_batch=2, k_pool=k_pool, v_pool=v_pool)
+    a.table = n_pages - 1 - a.table
+    a.layer = layers - 1
+    out, lse = a.call(cache)
+    assert cache.sync_status() == q.QMM_OK
+    check(out, lse, ref, lref, tol, ltol)
+    for pool, w in zip((k_pool, v_pool), want):
+        assert torch.equal(pool[layers - 1, last], w[0])
+        assert not pool[:layers - 1].any()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (8, 2)])
+def test_prompt_in_chains_of_64(Hq, Hkv):
+    """A prompt of 150 tokens as chains of 64, 64 and 22: every chunk attends to those
+    before it, which its own calls have written."""
+    whole = Attention("bf16", 128, Hq, Hkv, 150, 16, [0], seed=28)
+    cache = whole.make_cache(q)
+    at = 0
+    while at < 150:
+        n = min(64, 150 - at)
+        a = Attention("bf16", 128, Hq, Hkv, n, 16, [at], seed=29)
+        a.table, a.k_pool, a.v_pool = whole.table, whole.k_pool, whole.v_pool
+        a.q, a.k, a.v = (x[:, at:at + n] for x in (whole.q, whole.k, whole.v))
+        out, lse = a.call(cache)
+        check(out, lse, *a.reference())
+        at += n
+    for pool, new in ((whole.k_pool, whole.k), (whole.v_pool, whole.v)):
+        ids = whole.table[0].long().cuda()
+        assert torch.equal(pool[0, ids].transpose(0, 1).reshape(Hkv, -1, 128)[:, :150], new[0].transpose(0, 1))

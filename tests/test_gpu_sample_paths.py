@@ -11,6 +11,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from paged_util import sample_reference  # noqa: E402
+from test_gpu_verify_sample import Drafted  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -91,3 +92,69 @@ def test_scores_with_a_large_common_offset(B, T, V, offset):
     if T > 1:
         assert (got[0][:, 0] == T - 1).float().mean() > 0.25  # nodes without children are reached
     _compare(got, target, draft, tokens, parents, u, noise, 0.1)
+
+
+@pytest.mark.parametrize("dtype,draft,B,T,V,tree", [
+    ("bf16", True, 48, 8, 40000, False),   # 16-byte rows
+    ("f16", True, 48, 8, 40008, True),
+    ("bf16", True, 48, 8, 40001, True),    # rows of any alignment
+    ("f16", True, 48, 8, 40003, False),
+    ("f32", True, 24, 8, 40001, True),
+    ("bf16", False, 96, 8, 40000, True),   # tokens drafted without probabilities
+    ("f16", False, 96, 8, 40001, False),
+    ("f32", False, 48, 8, 40004, True),
+    ("f32", False, 48, 8, 40001, True),
+])
+def test_rows_read_as_the_walk_meets_them(dtype, draft, B, T, V, tree):
+    """More than 48 MB of scores, parents given: no statistics are taken ahead."""
+    d = Drafted(dtype, B, T, V, tree, draft, seed=V + B)
+    assert B * (T - 1) * V * d.target.element_size() * (2 if draft else 1) > 48 << 20
+    parents = torch.from_numpy(d.parents).cuda()
+    d.check(d.call(parents=parents))
+    d.check(d.call(ragged=True, parents=parents), ragged=True)
+
+
+@pytest.mark.parametrize("B", [2, 300])  # statistics first; rows read as the walk meets them
+def test_sampling_and_moves_in_a_graph(B):
+    """verify_sample, commit and copy_pages captured together and replayed over new
+    inputs in the same buffers."""
+    T, V, page = 6, 8000, 16
+    first, second = (Drafted("f32", B, T, V, True, True, seed=B + i) for i in range(2))
+    cache = q.PagedCache(2, 2 * B, page, 1, 1, 64, max_batch=B)
+    cache.k_pool.normal_(), cache.v_pool.normal_()
+    start = cache.k_pool.clone(), cache.v_pool.clone()
+    dev = lambda x: _cuda(np.asarray(x, np.int32))  # noqa: E731
+    table, lens, src, dst = dev(np.arange(B)[:, None]), dev([3] * B), dev([0]), dev([2 * B - 1])
+    bufs = dict(target=first.target.cuda(), draft=first.draft.cuda(), tokens=_cuda(first.tokens), u=_cuda(first.u),
+                noise=_cuda(first.noise), parents=_cuda(first.parents), temperature=_cuda(first.temperature))
+
+    def step():
+        accept, path = q.verify_sample(**bufs)
+        new = cache.commit(table, lens, path, accept)
+        cache.copy_pages(src, dst)
+        return accept, path, new
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            captured = step()
+    torch.cuda.synchronize()
+    for d in (first, second):
+        for name, buf in bufs.items():
+            x = getattr(d, name)
+            buf.copy_(x if isinstance(x, torch.Tensor) else torch.from_numpy(x))
+        for pool, old in zip((cache.k_pool, cache.v_pool), start):
+            pool.copy_(old)
+        want = [x.clone() for x in step()]
+        pools = cache.k_pool.clone(), cache.v_pool.clone()
+        for pool, old in zip((cache.k_pool, cache.v_pool), start):
+            pool.copy_(old)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(captured, want))
+        assert torch.equal(cache.k_pool, pools[0]) and torch.equal(cache.v_pool, pools[1])
+        d.check(want[:2])
+    assert cache.sync_status() == q.QMM_OK
