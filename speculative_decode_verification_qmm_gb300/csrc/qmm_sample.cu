@@ -295,7 +295,7 @@ struct WalkSmem {
 
 template <int DT, bool WIDE, bool EAGER>
 __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __grid_constant__ SampleParams p,
-                                                                      int cluster, int ahead) {
+                                                                      int cluster) {
   constexpr int N = WIDE ? Score<DT>::VEC : 1;
   using E = typename Score<DT>::type;
   __shared__ WalkSmem s;
@@ -398,13 +398,13 @@ __global__ void __launch_bounds__(WALK_THREADS, 2) sample_walk_kernel(const __gr
   };
   // The statistics of `node`'s rows into pm, ps, qm, qs.  Where they are not
   // known, those of the nodes that follow it if every first child is accepted
-  // are taken too, `ahead` in all: their rows are read together, and the cluster
+  // are taken too, AHEAD in all: their rows are read together, and the cluster
   // meets once.
   auto enter = [&]() {
     if constexpr (!EAGER) {
       if (!(known >> node & 1)) {
         int count = 0;
-        for (int at = node; at >= 0 && count < ahead;) {
+        for (int at = node; at >= 0 && count < AHEAD;) {
           if (tid == 0) s.list[count] = at;
           ++count;
           known |= 1ull << at;
@@ -741,7 +741,7 @@ cudaError_t launch_walk(const SampleParams& p, int B, int cluster, cudaStream_t 
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = EAGER ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, cluster, AHEAD);
+  return cudaLaunchKernelEx(&cfg, kern, p, cluster);
 }
 
 template <int DT, bool WIDE>
