@@ -400,7 +400,10 @@ typedef struct {
  * Scores, softmax statistics and sums are fp32; the exponentials are rounded
  * to the 16-bit type for the product with V, as the outputs are at the end (in
  * f16 one below 2^-32 of the row's largest counts in the sum of exponentials alone).
- * All pointers to 16-bit data are 16-byte aligned.  Asynchronous on `stream`
+ * All pointers to 16-bit data are 16-byte aligned.  What a call costs depends on
+ * table_width too: a table no wider than the sequences need lets short batches
+ * take shorter paths (at most 1,024 rows a sequence; no joining launch where one
+ * cache tile, 16 to 128 rows, holds all).  Asynchronous on `stream`
  * (the attention kernel, and one that adds up the parts of rows that it cut
  * between CTAs, in a fixed order: equal calls give equal bits).
  * Errors: STATE, INVALID_ARG (NULL pointers, bad struct_size or scale), SHAPE
@@ -477,7 +480,8 @@ typedef struct {
  * would have them.  Scores of -inf have probability 0.  Nodes whose token is
  * outside [0, V) are never accepted and change nothing.  The next token is in
  * [0, V) whatever the inputs.  Arithmetic in fp32; sums in an order fixed by the
- * sizes, so equal inputs give equal results.  Asynchronous.
+ * sizes, so equal inputs give equal results.  Rows are read in whole aligned
+ * groups of 16 bytes, which at a row's ends may hold other values.  Asynchronous.
  * Errors: INVALID_ARG (NULL, bad struct_size or dtype, workspace too small),
  * SHAPE (B, T, V), ALIGN (pointers not aligned to their element, workspace),
  * DEVICE, CUDA. */

@@ -40,8 +40,8 @@
 // cores work 1,024: a softmax of 1,500 cycles and its hand-overs do not fit under
 // the other row tile's products.  Two softmax warps a row, half of the columns
 // each, need 96 registers a thread, spilled, and took 231 us).
-// With one row tile: 16 x 8,192 rows, 128 rows a head: 106 us (650 TFLOP/s, 5.2
-// TB/s); one sequence of 131,072, 64 rows a head: 95 us (5.7 TB/s).
+// With one row tile, 64/8 heads: 16 x 8,192 rows, 128 rows a head: 107 us (645
+// TFLOP/s, 5.1 TB/s); one sequence of 131,072, 64 rows a head: 91 us (5.9 TB/s).
 // P is rounded to 16 bits, as the product needs it; l sums what was not rounded.
 // Every wait is bounded; on a timeout the CTA records it, its roles run out of
 // their loops without waiting, its copies and MMAs in flight are drained and
@@ -702,8 +702,10 @@ cudaError_t launch(const AttnParams& p, const void* kmap, const void* vmap, cuda
 int attn_tc_tile_cache_rows() { return TK; }
 // One row tile of 128 or two.  Two read K and V once for 256 rows, one has S
 // double-buffered and its idle warps cost less.  Measured, one against two, in us:
-// 128 rows, 16 x 8,192 cached: 106 : 111; 64 rows, 131,072: 95 : 101; 32 rows, 16 x
-// 4,096: 77 : 88; 512 rows, 4 x 16,384: 177 : 119; 192 rows of 64, 8 x 8,000: 49 : 43.
+// 128 rows, 16 x 8,192 cached, 64/8 heads of 128: 106 : 117; 64 rows, 131,072: 91 :
+// 108; 32 rows, 16 x 4,096, 40/20: 119 : 141; 512 rows, 4 x 16,384, 64/8: 175 : 125;
+// alike for 160 rows, 8 x 2,000, 40/8: 35 : 36, and 192 rows, 8 x 8,000, 24/8 of 64:
+// 62 : 62.
 int attn_tc_tile_rows(int R) { return R <= 128 ? 128 : 256; }
 
 cudaError_t prepare_attn_tc(bool bf16, int D) {

@@ -24,11 +24,11 @@
 // nodes only, four nodes ahead along the first children.  sample_eager() holds
 // the rule.
 // What bounds it: a chain of dependent steps.  Measured, target and drafter
-// scores of 151,936 entries: one sequence, chain of 8, fp32: 10.5 us, two launches
-// of which the first reads 8.5 MB; 32 sequences, chains of 16, 16 bits: 70 us, the
+// scores of 151,936 entries: one sequence, chain of 8, fp32: 10.3 us, two launches
+// of which the first reads 8.5 MB; 32 sequences, chains of 16, 16 bits: 69 us, the
 // steps of the longest walks, where the visited rows of all sequences take 14 at
 // the copy rate: the busiest SMs issue in 93 % of their cycles, all of them in 30 %
-// on average; 4 trees of 64, 50,257 fp32: 12.8 us.
+// on average; 4 trees of 64, 50,257 fp32: 13.1 us.
 // 16-byte copies where rows lie on 16-byte boundaries (WIDE), else single entries
 // in the passes over whole rows of a walk: 70 us against 81 for the batch above.
 #include <cuda_runtime.h>
@@ -707,7 +707,7 @@ int sample_cluster(int B, int64_t V, int sms) {
 // eager against not, in us, 151,936 entries of 16 bits: 17 MB: 14 : 23; 34 MB: 21 :
 // 26; chains of 8, 68 MB: 34 : 44; chains of 16, 109 MB: 37 : 42; 182 MB: 52 : 60;
 // 292 MB: 71 : 70; chains of 32, 75 MB: 29 : 22; trees of 8, 85 MB: 38 : 34; of 16,
-// 73 MB: 32 : 24; of 64 (50,257 entries of 32 bits), 101 MB: 28 : 13.
+// 73 MB: 32 : 24; of 64 (50,257 entries of 32 bits), 101 MB: 28 : 13.  Chains of 17 to 31 were not measured.
 bool sample_eager(int B, int T, int64_t V, int elem, bool has_q, bool chain) {
   const int64_t most = (chain && T <= 16 ? 192ll : 48ll) << 20;
   return T > 1 && (int64_t)B * (T - 1) * V * elem * (has_q ? 2 : 1) <= most;
