@@ -331,7 +331,7 @@ typedef struct {
   int32_t n_layers;
   int32_t page_size;    /* rows of a page: a power of two, 16 to 1024           */
   int32_t n_q_heads;    /* a multiple of n_kv_heads, at most 64 times it        */
-  int32_t n_kv_heads;
+  int32_t n_kv_heads;   /* 1 to 1024                                            */
   int32_t head_dim;     /* 64 or 128                                            */
   int32_t max_batch;    /* sequences of one call, 1 to QMM_CACHE_MAX_BATCH      */
   int64_t n_pages;      /* pages of one layer; a pool has at most 2^31 - 1 rows
@@ -421,6 +421,7 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* args, void* stream);
  * a sequence with other entries is refused on the device: its rows stay and
  * lens_out[b] = lens[b].
  * Rows that are in place already cost nothing.
+ * Every sequence of the call has at least its root: leave those without nodes out.
  *   path: device, int32 [B][T], row stride ld_path.  accept: device, int32 [B][2].
  *   lens_out: device, int32 [B]; not lens, which every CTA of the call reads.
  * Asynchronous.  Errors: STATE, INVALID_ARG (NULL, lens_out is lens), SHAPE (B, T, table_width),
