@@ -440,6 +440,229 @@ int qmm_cache_commit(qmm_cache_t h, int B, int T, const int32_t* page_table, int
 int qmm_cache_copy(qmm_cache_t h, int n, const int32_t* src, const int32_t* dst,
                    const int32_t* rows, void* stream);
 
+/* ---- prompts: rotary positions, appended rows, their attention -------------------- */
+
+/* A prompt of any length reaches the cache in one call a layer: qmm_cache_append
+ * turns its queries and keys by their positions and writes keys and values behind
+ * the cached rows; qmm_prompt_attention then attends with the queries.  Rows of
+ * all sequences are packed: rows starts[b] .. starts[b + 1] - 1 of q, k and v are
+ * the new rows of sequence b, in order, as a product over all of them gives them.
+ * qmm_rotate is the turning alone, for the nodes of a drafted tree, whose keys and
+ * values qmm_tree_attention writes. */
+#define QMM_ROPE_MAX_DIM 1024
+#define QMM_ROPE_MAX_HEADS 65536
+#define QMM_CACHE_MAX_ROWS (1 << 24) /* of one call */
+
+typedef enum { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 } qmm_rope_layout;
+
+/* Rotary positions.  Of the first `dims` dimensions of a head, pair i is (i, i +
+ * dims / 2) in the half layout, (2 i, 2 i + 1) in the interleaved one; a pair
+ * (x, y) at position p becomes
+ *     amplitude (x cos w - y sin w),  amplitude (x sin w + y cos w)
+ * with w = 2 pi p turns[i] / 2^64: a frequency is its turns a position as a 64-bit
+ * fraction, whole turns left out, so that p turns[i] modulo 2^64 is the angle
+ * without error for every p, negative ones too.  Dimensions past `dims` stay.
+ * Arithmetic in fp32, one rounding at the end. */
+typedef struct {
+  uint32_t struct_size;  /* = sizeof(qmm_rope)                                  */
+  uint32_t layout;       /* qmm_rope_layout                                     */
+  int32_t dims;          /* even, 2 .. head_dim                                 */
+  float amplitude;       /* finite                                              */
+  const uint64_t* turns; /* device, [dims / 2]                                  */
+} qmm_rope;
+
+typedef struct {
+  uint32_t struct_size;     /* = sizeof(qmm_rotate_args)                        */
+  uint32_t in_dtype;        /* QMM_DT_* of x                                    */
+  uint32_t out_dtype;       /* QMM_DT_* of out                                  */
+  int32_t B;                /* B * T rows, 1 .. 2^31 - 1                        */
+  int32_t T;
+  int32_t heads;            /* 1 .. QMM_ROPE_MAX_HEADS                          */
+  int32_t turned_heads;     /* the first of them, 0 .. heads; the others are
+                               converted only                                   */
+  int32_t head_dim;         /* 2 .. QMM_ROPE_MAX_DIM                            */
+  const void* x;            /* [B][T][heads][head_dim], strides below           */
+  void* out;                /* the same; x itself where type and strides agree  */
+  int64_t x_stride[3];      /* in elements: sequence, row, head; any            */
+  int64_t out_stride[3];
+  const int32_t* positions; /* [B][T], contiguous                               */
+  qmm_rope rope;
+} qmm_rotate_args;
+
+/* Rotary positions of the rows of x.  Asynchronous.  Errors: INVALID_ARG (NULL,
+ * bad struct_size, dtype, layout or amplitude, out == x with other strides or
+ * element size), SHAPE, ALIGN (a pointer not aligned to its element), DEVICE,
+ * CUDA. */
+int qmm_rotate(const qmm_rotate_args* args, void* stream);
+
+typedef struct {
+  uint32_t struct_size;      /* = sizeof(qmm_append_args)                       */
+  uint32_t dtype;            /* QMM_DT_* of q, k and v                          */
+  int32_t layer;             /* 0 .. n_layers - 1                               */
+  int32_t B;                 /* sequences, 1 .. max_batch                       */
+  int64_t N;                 /* rows of q, k, v and q_out, 0 .. QMM_CACHE_MAX_ROWS */
+  const void* q;             /* [N][n_q_heads][head_dim]; NULL: keys and values alone */
+  const void* k;             /* [N][n_kv_heads][head_dim]                       */
+  const void* v;
+  void* q_out;               /* [N][n_q_heads][head_dim] in the cache's type    */
+  int64_t q_stride[2];       /* in elements: row, head; any                     */
+  int64_t k_stride[2];
+  int64_t v_stride[2];
+  int64_t q_out_stride[2];
+  const int32_t* page_table; /* [B][table_width], row stride ld_table           */
+  int64_t ld_table;
+  int32_t table_width;
+  const int32_t* lens;       /* [B]: cached rows of every sequence              */
+  const int32_t* starts;     /* [B + 1], increasing from 0, starts[B] <= N      */
+  const int32_t* positions;  /* [N]; NULL: lens[b] + i for row i of sequence b  */
+  const qmm_rope* rope;      /* host; NULL: nothing is turned                   */
+} qmm_append_args;
+
+/* Appends rows to `layer` of the cache: key and value of row i of sequence b are
+ * written to row lens[b] + i of the cache, the key turned, and q_out gets the
+ * turned query; all rounded once to the cache's type.  Rows starts[B] .. N - 1
+ * belong to no sequence: nothing is written for them.  A row whose place or page
+ * is out of range is skipped and reported (qmm_cache_sync_status).  The caller
+ * sees to it that no two rows of a call have the same place.  Asynchronous.
+ * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), q or q_out NULL alone,
+ * bad struct_size, dtype or rope), SHAPE (layer, B, N, table_width, rope->dims), ALIGN (a pointer
+ * not aligned to its element, ld_table < table_width with B > 1), DEVICE, CUDA. */
+int qmm_cache_append(qmm_cache_t h, const qmm_append_args* args, void* stream);
+
+typedef struct {
+  uint32_t struct_size;      /* = sizeof(qmm_prompt_args)                       */
+  int32_t layer;             /* 0 .. n_layers - 1                               */
+  int32_t B;                 /* sequences, 1 .. max_batch                       */
+  int32_t table_width;
+  int64_t N;                 /* rows of q, out and lse, 0 .. QMM_CACHE_MAX_ROWS */
+  const void* q;             /* [N][n_q_heads][head_dim], 16-byte aligned       */
+  void* out;                 /* [N][n_q_heads][head_dim], 16-byte aligned       */
+  int64_t q_stride[2];       /* in elements: row, head; multiples of 8          */
+  int64_t out_stride[2];
+  float* lse;                /* [N][n_q_heads], contiguous, or NULL             */
+  const int32_t* page_table; /* [B][table_width], row stride ld_table           */
+  int64_t ld_table;
+  const int32_t* lens;       /* [B]: rows of every sequence that precede its new ones */
+  const int32_t* starts;     /* [B + 1], increasing from 0, starts[B] <= N      */
+  float scale;               /* of the scores; finite and > 0                   */
+} qmm_prompt_args;
+
+/* Attention of a prompt's rows over the paged cache, which holds them already.
+ * For row i of sequence b (row r = starts[b] + i of q), L = lens[b], and query head
+ * h (key/value head h / (n_q_heads / n_kv_heads))
+ *     s_j = scale * dot(q[r][h], K_j),  j = 0 .. L + i
+ *     out[r][h] = sum_j exp(s_j) V_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
+ * Later rows do not influence it, whatever they or the rest of the last page
+ * hold, NaN and infinities included.  Rows of q past starts[B], and their outputs,
+ * are not touched.  Numerics as in qmm_tree_attention; equal calls give equal
+ * bits.  Asynchronous.
+ * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), bad struct_size or scale), SHAPE
+ * (layer, B, N or table_width out of range), ALIGN (pointers, strides, ld_table <
+ * table_width; not strides of dimensions of one entry), DEVICE, CUDA.  Lengths,
+ * starts and page ids are checked on the device (qmm_cache_sync_status): a sequence
+ * that the table or N cannot hold is left alone, and a page that does not exist is
+ * read as page 0. */
+int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* args, void* stream);
+
+/* ---- residual sums and norms -------------------------------------------------------- */
+
+#define QMM_NORM_MAX_N 32768
+#define QMM_NORM_CENTERED 1u /* flag: subtract the mean before the mean square  */
+
+typedef struct {
+  uint32_t struct_size;     /* = sizeof(qmm_norm_args)                          */
+  uint32_t flags;           /* QMM_NORM_CENTERED or 0                           */
+  int64_t M;                /* rows, 1 .. 2^31 - 1                              */
+  int64_t N;                /* entries of a row, 1 .. QMM_NORM_MAX_N            */
+  uint32_t res_dtype;       /* QMM_DT_* of residual and residual_out            */
+  uint32_t y_dtype;         /* of y                                             */
+  uint32_t out_dtype;       /* of out                                           */
+  float eps;                /* >= 0, added to the mean square                   */
+  const void* residual;     /* [M][N], row stride ld_residual                   */
+  int64_t ld_residual;
+  const void* y;            /* the block's output, or NULL                      */
+  int64_t ld_y;
+  void* residual_out;       /* may be residual itself; with y only              */
+  int64_t ld_residual_out;
+  void* out;                /* or NULL: the residual sum alone                  */
+  int64_t ld_out;
+  const float* weight;      /* [N] of the norm; with out                        */
+  const float* bias;        /* [N], or NULL                                     */
+  const float* post_weight; /* [N] of the norm of y, or NULL: y as it is        */
+  const float* post_bias;   /* [N], or NULL                                     */
+  const float* gate;        /* [M][N], row stride ld_gate (0: one row for all), or NULL: 1 */
+  int64_t ld_gate;
+  float scale;              /* of what is added; finite                         */
+} qmm_norm_args;
+
+/* What stands between two blocks of a layer:
+ *     z = y, or norm(y) post_weight + post_bias
+ *     r' = residual + scale gate z             -> residual_out
+ *     out = norm(r') weight + bias
+ * with norm(x) = x / sqrt(mean(x^2) + eps), or, QMM_NORM_CENTERED, the same of
+ * x - mean(x).  Without y, r' is the residual and residual_out is not written.
+ * Arithmetic and sums in fp32, the sums in an order fixed by N; out is of the
+ * unrounded r'.  Asynchronous.  Errors: INVALID_ARG (NULL, bad struct_size, flags,
+ * dtype, eps or scale; neither y nor out), SHAPE, ALIGN (a pointer not aligned to
+ * its element, a row stride below N), DEVICE, CUDA. */
+int qmm_residual_norm(const qmm_norm_args* args, void* stream);
+
+/* ---- adjustment of scores before sampling -------------------------------------------- */
+
+typedef struct {
+  uint32_t struct_size;     /* = sizeof(qmm_adjust_args)                        */
+  uint32_t dtype;           /* QMM_DT_* of scores and out                       */
+  int32_t B;                /* sequences, 1 .. 65535                            */
+  int32_t T;                /* nodes per sequence, 1 .. QMM_TREE_MAX_T          */
+  int64_t V;                /* vocabulary, 1 .. 2^24                            */
+  const void* scores;       /* [B][T][V], entries of a row contiguous           */
+  int64_t stride[2];        /* in elements: sequence, node                      */
+  void* out;                /* may be scores itself, with its strides           */
+  int64_t out_stride[2];
+  const int32_t* tokens;    /* [B][T], contiguous; NULL: no node counts         */
+  const int32_t* parents;   /* [B][T], contiguous; NULL: a chain (t - 1)        */
+  const int32_t* n_tokens;  /* [B]; NULL: all T                                 */
+  const int32_t* counts;    /* [B][V], row stride ld_counts: how often each token
+                               was emitted, the root included; NULL: never      */
+  int64_t ld_counts;
+  const uint32_t* prompt;   /* [B][ceil(V / 32)], row stride ld_prompt: bit v % 32 of
+                               word v / 32: token v is in the prompt; NULL: none */
+  int64_t ld_prompt;
+  const float* repetition;  /* [B], > 0; NULL: 1                                */
+  const float* frequency;   /* [B]; NULL: 0                                     */
+  const float* presence;    /* [B]; NULL: 0                                     */
+  const float* bias;        /* [B][V], row stride ld_bias (0: one row for all); NULL: 0 */
+  int64_t ld_bias;
+  const uint32_t* mask;     /* [B][T][ceil(V / 32)], strides in words: bits of the
+                               tokens that may follow the node; NULL: all       */
+  int64_t mask_stride[2];
+} qmm_adjust_args;
+
+/* Penalties, biases and grammar masks on the scores after every node of a drafted
+ * tree, ahead of qmm_verify_sample: row t of sequence b is adjusted as if the nodes
+ * on the path to t, t itself included, had been emitted.  With c = counts[b][v] +
+ * the number of those nodes (the root, counted already, left out) with token v:
+ *     x = scores[b][t][v]
+ *     c > 0 or v in the prompt:  x = x / repetition for x > 0, else x repetition
+ *     x = x - frequency c - presence [c > 0] + bias[v]
+ *     x = -inf where the node's mask bit is 0
+ * in fp32, rounded once.  Rows t >= n_tokens[b] of out are not touched.  Nodes whose
+ * token is outside [0, V) count for nothing; a parent that does not come before its
+ * node ends the path.  Asynchronous.
+ * Errors: INVALID_ARG (NULL scores or out, bad struct_size or dtype, out == scores
+ * with other strides), SHAPE (B, T, V), ALIGN (a pointer not aligned to its
+ * element, ld_counts < V, ld_prompt < V / 32 with B > 1), DEVICE, CUDA. */
+int qmm_adjust_scores(const qmm_adjust_args* args, void* stream);
+
+/* After a step: counts[b][v] += 1 for every token that sequence b emitted, the
+ * accepted nodes' tokens[b][path[b][j]], j < accept[2 b], and the next token
+ * accept[2 b + 1] (the layouts of qmm_verify_sample).  Tokens outside [0, V) and path entries outside
+ * [0, T) are skipped.  tokens, path: device, int32 [B][T], contiguous.
+ * Asynchronous.  Errors: INVALID_ARG (NULL), SHAPE (B, T, V as above), ALIGN
+ * (pointers, ld_counts < V with B > 1), DEVICE, CUDA. */
+int qmm_count_tokens(int32_t* counts, int64_t ld_counts, int B, int T, int64_t V, const int32_t* tokens,
+                     const int32_t* path, const int32_t* accept, void* stream);
+
 /* ---- verification of drafted tokens by rejection sampling ------------------------ */
 
 typedef struct {

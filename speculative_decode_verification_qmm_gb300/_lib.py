@@ -33,6 +33,9 @@ QMM_DT_BF16 = 0
 QMM_DT_F16 = 1
 QMM_DT_F32 = 2
 QMM_TREE_MAX_T = 64
+QMM_ROPE_HALF = 0
+QMM_ROPE_INTERLEAVED = 1
+QMM_NORM_CENTERED = 1
 
 
 class qmm_desc(ctypes.Structure):
@@ -136,6 +139,136 @@ class qmm_sample_args(ctypes.Structure):
     ]
 
 
+class qmm_rope(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("layout", ctypes.c_uint32),
+        ("dims", ctypes.c_int32),
+        ("amplitude", ctypes.c_float),
+        ("turns", ctypes.c_void_p),
+    ]
+
+
+class qmm_rotate_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("in_dtype", ctypes.c_uint32),
+        ("out_dtype", ctypes.c_uint32),
+        ("B", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("turned_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64 * 3),
+        ("out_stride", ctypes.c_int64 * 3),
+        ("positions", ctypes.c_void_p),
+        ("rope", qmm_rope),
+    ]
+
+
+class qmm_append_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+        ("layer", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("k_stride", ctypes.c_int64 * 2),
+        ("v_stride", ctypes.c_int64 * 2),
+        ("q_out_stride", ctypes.c_int64 * 2),
+        ("page_table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("table_width", ctypes.c_int32),
+        ("lens", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("rope", ctypes.c_void_p),
+    ]
+
+
+class qmm_prompt_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("layer", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("table_width", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("out_stride", ctypes.c_int64 * 2),
+        ("lse", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("ld_table", ctypes.c_int64),
+        ("lens", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class qmm_norm_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("flags", ctypes.c_uint32),
+        ("M", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("res_dtype", ctypes.c_uint32),
+        ("y_dtype", ctypes.c_uint32),
+        ("out_dtype", ctypes.c_uint32),
+        ("eps", ctypes.c_float),
+        ("residual", ctypes.c_void_p),
+        ("ld_residual", ctypes.c_int64),
+        ("y", ctypes.c_void_p),
+        ("ld_y", ctypes.c_int64),
+        ("residual_out", ctypes.c_void_p),
+        ("ld_residual_out", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("post_weight", ctypes.c_void_p),
+        ("post_bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("ld_gate", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class qmm_adjust_args(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+        ("B", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("V", ctypes.c_int64),
+        ("scores", ctypes.c_void_p),
+        ("stride", ctypes.c_int64 * 2),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64 * 2),
+        ("tokens", ctypes.c_void_p),
+        ("parents", ctypes.c_void_p),
+        ("n_tokens", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("ld_counts", ctypes.c_int64),
+        ("prompt", ctypes.c_void_p),
+        ("ld_prompt", ctypes.c_int64),
+        ("repetition", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p),
+        ("presence", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("ld_bias", ctypes.c_int64),
+        ("mask", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64 * 2),
+    ]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
@@ -158,6 +291,12 @@ SIGNATURES = {
     "qmm_tree_attention": (_INT, [_P, _P, _P]),
     "qmm_cache_commit": (_INT, [_P, _INT, _INT, _P, _I64, _INT, _P, _P, _I64, _P, _P, _P]),
     "qmm_cache_copy": (_INT, [_P, _INT, _P, _P, _P, _P]),
+    "qmm_cache_append": (_INT, [_P, _P, _P]),
+    "qmm_prompt_attention": (_INT, [_P, _P, _P]),
+    "qmm_rotate": (_INT, [_P, _P]),
+    "qmm_residual_norm": (_INT, [_P, _P]),
+    "qmm_adjust_scores": (_INT, [_P, _P]),
+    "qmm_count_tokens": (_INT, [_P, _I64, _INT, _INT, _I64, _P, _P, _P, _P]),
     "qmm_verify_sample": (_INT, [_P, _P]),
     "qmm_verify_sample_workspace": (_INT, [_INT, _INT, _I64, ctypes.POINTER(_I64)]),
     "qmm_sync_status": (_INT, [_P, _P]),

@@ -15,6 +15,8 @@
 // Most of more items than that are not cut.  The CTAs are then for the workers:
 // each reads what its worker left (AttnParams::cuts) and joins the item that goes
 // on behind the worker's range, if one began in it.
+// Items of the prompt attention (qmm_prompt.cu) are joined by cuts always; there a cut
+// holds the item's first row among the packed ones, its head and its number of rows.
 // Everything that does not depend on the partials is done before the wait for
 // the kernel that writes them (programmatic dependent launch).  As a tail of the
 // attention kernels' last CTA of an item the same sums took up to 30 us (64
@@ -32,12 +34,14 @@ constexpr int WARPS = 4;
 constexpr int RU = 4;  // rows of a lane
 constexpr int U = 2;   // parts in flight
 constexpr int CTAS_PER_SM = 8;
+enum { ITEMS, CUTS_OF_TREES, CUTS_OF_PROMPTS };
 
-template <bool BF16, int D, bool CUTS>
+template <bool BF16, int D, int MODE>
 __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel(const __grid_constant__ AttnParams p, int tk, int rows,
                                                                int chunks) {
   constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes of a row, rows of a warp's load
   constexpr int RPC = RPW * RU;               // rows of the CTA
+  constexpr bool CUTS = MODE != ITEMS, PROMPT = MODE == CUTS_OF_PROMPTS;
   __shared__ float4 s_acc[WARPS][RPC][LPR];
   __shared__ float s_m[WARPS][RPC], s_l[WARPS][RPC];
   pdl_trigger();
@@ -79,9 +83,16 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
     cur.b = cut.x, cur.h = cut.y, cur.rt = cut.z;
   }
   if (c0 == c1) return;
-  if constexpr (CUTS) attn_sizes(p, cur.b, cur.L, cur.n);
   const int part = rows * (D + 2);
-  const int left = p.R - cur.rt * rows < rows ? p.R - cur.rt * rows : rows;
+  int left, first_row;  // the item's rows, and the first one's place among the head's
+  if constexpr (PROMPT) {
+    first_row = cur.b * p.g, left = cur.rt;
+    cur.b = 0, cur.n = INT32_MAX;
+  } else {
+    if constexpr (CUTS) attn_sizes(p, cur.b, cur.L, cur.n);
+    first_row = cur.rt * rows;
+    left = p.R - first_row < rows ? p.R - first_row : rows;
+  }
   const int sub = lane % LPR, row = lane / LPR;
 
   const bool alone = c1 - c0 < 4 && (CUTS || left >= 128);  // a warp joins its rows alone
@@ -127,7 +138,7 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
 #pragma unroll
       for (int k = 0; k < RU; ++k) {
         const int r = r0 + k * RPW + row;
-        if (r < left) attn_store4<BF16>(p, cur, cur.rt * rows + r, sub * 4, acc[k], mn[k], lt[k]);
+        if (r < left) attn_store4<BF16>(p, cur, first_row + r, sub * 4, acc[k], mn[k], lt[k]);
       }
       continue;
     }
@@ -155,14 +166,15 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
         l += s_l[w][rr] * x;
         a.x += v.x * x, a.y += v.y * x, a.z += v.z * x, a.w += v.w * x;
       }
-      attn_store4<BF16>(p, cur, cur.rt * rows + r0 + rr, sub * 4, a, mx, l);
+      attn_store4<BF16>(p, cur, first_row + r0 + rr, sub * 4, a, mx, l);
     }
     __syncthreads();
   }
 }
 
-template <bool BF16, int D, bool CUTS>
+template <bool BF16, int D, int MODE>
 cudaError_t launch(const AttnParams& p, int tk, int rows, int ctas, cudaStream_t st) {
+  constexpr bool CUTS = MODE != ITEMS;
   constexpr int PER = 128 / D * RU * (CUTS ? WARPS : 1);
   const int64_t units = CUTS ? p.grid - 1 : (int64_t)p.B * p.Hkv * p.RT;
   int chunks = ((p.R < rows ? p.R : rows) + PER - 1) / PER;
@@ -177,7 +189,7 @@ cudaError_t launch(const AttnParams& p, int tk, int rows, int ctas, cudaStream_t
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF16, D, CUTS>, p, tk, rows, chunks);
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<BF16, D, MODE>, p, tk, rows, chunks);
 }
 
 template <bool BF16, int D>
@@ -189,10 +201,20 @@ cudaError_t launch_one(const AttnParams& p, int tk, int rows, int sms, cudaStrea
   // 91 : 89; 384 (48 sequences, 8 heads): 13.6 : 13.1, 28 : 27, 90 : 88.
   const int ctas = CTAS_PER_SM * sms;
   const bool cuts = (int64_t)p.B * p.Hkv * p.RT > ctas;
-  return cuts ? launch<BF16, D, true>(p, tk, rows, ctas, st) : launch<BF16, D, false>(p, tk, rows, ctas, st);
+  return cuts ? launch<BF16, D, CUTS_OF_TREES>(p, tk, rows, ctas, st) : launch<BF16, D, ITEMS>(p, tk, rows, ctas, st);
+}
+
+template <bool BF16, int D>
+cudaError_t launch_prompts(const AttnParams& p, int rows, int sms, cudaStream_t st) {
+  return p.grid > 1 ? launch<BF16, D, CUTS_OF_PROMPTS>(p, 0, rows, CTAS_PER_SM * sms, st) : cudaSuccess;
 }
 
 }  // namespace
+
+cudaError_t launch_prompt_join(const AttnParams& p, bool bf16, int D, int rows, int sms, cudaStream_t st) {
+  if (D == 128) return bf16 ? launch_prompts<true, 128>(p, rows, sms, st) : launch_prompts<false, 128>(p, rows, sms, st);
+  return bf16 ? launch_prompts<true, 64>(p, rows, sms, st) : launch_prompts<false, 64>(p, rows, sms, st);
+}
 
 cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, int sms, cudaStream_t st) {
   if (D == 128) return bf16 ? launch_one<true, 128>(p, tk, rows, sms, st) : launch_one<false, 128>(p, tk, rows, sms, st);

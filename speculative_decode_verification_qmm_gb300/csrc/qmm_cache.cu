@@ -13,6 +13,8 @@
 #include "qmm.h"
 #include "qmm_attn.cuh"
 #include "qmm_attn.h"
+#include "qmm_prompt.cuh"
+#include "qmm_rope.cuh"
 
 using namespace qmm;
 
@@ -263,6 +265,7 @@ int qmm_cache_create(qmm_cache_t* out, const qmm_cache_desc* d, void* stream) {
   const size_t ws_bytes = part_bytes + (size_t)attn_mma_workers(sms, true) * sizeof(int4);
   cudaError_t e = prepare_attn_mma(d->dtype == QMM_DT_BF16, d->head_dim);
   if (e == cudaSuccess) e = prepare_attn_tc(d->dtype == QMM_DT_BF16, d->head_dim);
+  if (e == cudaSuccess) e = prepare_prompt(d->dtype == QMM_DT_BF16, d->head_dim);
   const bool f16 = d->dtype == QMM_DT_F16;
   if (e == cudaSuccess) e = host_pool_map(&h->kmap, d->k_pool, pool_rows, d->head_dim, 16, f16);
   if (e == cudaSuccess) e = host_pool_map(&h->vmap, d->v_pool, pool_rows, d->head_dim, 16, f16);
@@ -388,6 +391,121 @@ int qmm_tree_attention(qmm_cache_t h, const qmm_attn_args* a, void* stream) {
   // items of one unit each are never cut: nothing to join
   if (e == cudaSuccess && ((int64_t)a->table_width << h->page_shift) > tk)
     e = launch_attn_join(p, bf16, d.head_dim, tk, rows, h->sm_count, st);
+  return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
+}
+
+int qmm_cache_append(qmm_cache_t h, const qmm_append_args* a, void* stream) {
+  if (!is_live(h)) return QMM_ERR_STATE;
+  if (!a || a->struct_size != sizeof(qmm_append_args)) return QMM_ERR_INVALID_ARG;
+  if (a->dtype > QMM_DT_F32 || (a->N != 0 && (!a->k || !a->v || !a->q != !a->q_out)) || !a->page_table || !a->lens || !a->starts)
+    return QMM_ERR_INVALID_ARG;
+  const qmm_cache_desc& d = h->d;
+  if (a->layer < 0 || a->layer >= d.n_layers || a->B < 1 || a->B > d.max_batch || a->N < 0 || a->N > QMM_CACHE_MAX_ROWS ||
+      a->table_width < 1 || ((int64_t)a->table_width << h->page_shift) > INT32_MAX - 4096)
+    return QMM_ERR_SHAPE;
+  int rc = a->rope ? rope_check(a->rope, d.head_dim) : QMM_OK;
+  if (rc != QMM_OK) return rc;
+  const int elem = a->dtype == QMM_DT_F32 ? 4 : 2;
+  if ((((uintptr_t)a->q | (uintptr_t)a->k | (uintptr_t)a->v) & (elem - 1)) || ((uintptr_t)a->q_out & 1) ||
+      (((uintptr_t)a->page_table | (uintptr_t)a->lens | (uintptr_t)a->starts | (uintptr_t)a->positions) & 3) ||
+      (a->B > 1 && a->ld_table < a->table_width))
+    return QMM_ERR_ALIGN;
+  rc = check_current(h);
+  if (rc != QMM_OK) return rc;
+  if (a->N == 0) return QMM_OK;
+  RopeParams p = {};
+  p.page_stride = (int64_t)d.n_kv_heads * d.page_size * d.head_dim;
+  auto add = [&](const void* src, const int64_t* s, void* dst, int64_t d_row, int64_t d_head, int heads, bool turned, bool pool) {
+    RopeHeads& t = p.part[p.parts++];
+    t.src = src, t.dst = dst;
+    // strides of dimensions with one entry are not followed
+    t.s_row = a->N > 1 ? s[0] : 0, t.s_head = heads > 1 ? s[1] : 0;
+    t.d_row = a->N > 1 ? d_row : 0, t.d_head = heads > 1 ? d_head : 0;
+    t.heads = heads, t.turned = turned && a->rope, t.pool = pool;
+    p.heads += heads;
+  };
+  const int64_t layer = a->layer * d.n_pages * p.page_stride, head = (int64_t)d.page_size * d.head_dim;
+  add(a->k, a->k_stride, static_cast<uint16_t*>(d.k_pool) + layer, 0, head, d.n_kv_heads, true, true);
+  add(a->v, a->v_stride, static_cast<uint16_t*>(d.v_pool) + layer, 0, head, d.n_kv_heads, false, true);
+  if (a->q) add(a->q, a->q_stride, a->q_out, a->q_out_stride[0], a->q_out_stride[1], d.n_q_heads, true, false);
+  p.D = d.head_dim;
+  p.m = a->rope ? a->rope->dims / 2 : 0;
+  p.half = !a->rope || a->rope->layout == QMM_ROPE_HALF;
+  p.amplitude = a->rope ? a->rope->amplitude : 1.f;
+  p.turns = a->rope ? a->rope->turns : nullptr;
+  p.positions = a->positions;
+  p.rows = a->N;
+  p.B = a->B;
+  p.starts = a->starts;
+  p.lens = a->lens;
+  p.table = a->page_table;
+  p.ld_table = a->ld_table;
+  p.table_width = a->table_width;
+  p.page_shift = h->page_shift;
+  p.n_pages = d.n_pages;
+  p.status = h->status;
+  const cudaError_t e = launch_rope(p, a->dtype, d.dtype, true, h->sm_count, (cudaStream_t)stream);
+  return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
+}
+
+int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* a, void* stream) {
+  if (!is_live(h)) return QMM_ERR_STATE;
+  if (!a || a->struct_size != sizeof(qmm_prompt_args)) return QMM_ERR_INVALID_ARG;
+  if ((a->N != 0 && (!a->q || !a->out)) || !a->page_table || !a->lens || !a->starts) return QMM_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f) || !isfinite(a->scale)) return QMM_ERR_INVALID_ARG;
+  const qmm_cache_desc& d = h->d;
+  if (a->layer < 0 || a->layer >= d.n_layers || a->B < 1 || a->B > d.max_batch || a->N < 0 || a->N > QMM_CACHE_MAX_ROWS ||
+      a->table_width < 1 || ((int64_t)a->table_width << h->page_shift) > INT32_MAX - 4096)
+    return QMM_ERR_SHAPE;
+  if ((((uintptr_t)a->q | (uintptr_t)a->out) & 15) ||
+      (((uintptr_t)a->lse | (uintptr_t)a->page_table | (uintptr_t)a->lens | (uintptr_t)a->starts) & 3))
+    return QMM_ERR_ALIGN;
+  // strides of dimensions with one entry are not followed
+  if ((a->N > 1 && ((a->q_stride[0] | a->out_stride[0]) & 7)) || (d.n_q_heads > 1 && ((a->q_stride[1] | a->out_stride[1]) & 7)) ||
+      (a->B > 1 && a->ld_table < a->table_width))
+    return QMM_ERR_ALIGN;
+  const int rc = check_current(h);
+  if (rc != QMM_OK) return rc;
+  if (a->N == 0) return QMM_OK;
+  PromptParams pp = {};
+  AttnParams& p = pp.a;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.out = static_cast<uint16_t*>(a->out);
+  p.q_st = a->N > 1 ? a->q_stride[0] : 0, p.q_sh = d.n_q_heads > 1 ? a->q_stride[1] : 0;
+  p.o_st = a->N > 1 ? a->out_stride[0] : 0, p.o_sh = d.n_q_heads > 1 ? a->out_stride[1] : 0;
+  p.lse = a->lse;
+  p.page_stride = (int64_t)d.n_kv_heads * d.page_size * d.head_dim;
+  p.n_pages = d.n_pages;
+  p.k_pool = static_cast<uint16_t*>(d.k_pool) + a->layer * d.n_pages * p.page_stride;
+  p.v_pool = static_cast<uint16_t*>(d.v_pool) + a->layer * d.n_pages * p.page_stride;
+  p.table = a->page_table;
+  p.ld_table = a->ld_table;
+  p.table_width = a->table_width;
+  p.page_shift = h->page_shift;
+  p.lens = a->lens;
+  p.B = a->B;
+  p.Hq = d.n_q_heads;
+  p.Hkv = d.n_kv_heads;
+  p.g = d.n_q_heads / d.n_kv_heads;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.ws = h->ws;
+  p.cuts = h->cuts;
+  p.status = h->status;
+  p.wait_limit_ns = h->wait_limit_ns;
+  p.grid = h->sm_count;
+  p.row0 = (int64_t)a->layer * d.n_pages * d.n_kv_heads * d.page_size;
+  pp.starts = a->starts;
+  pp.N = (int)a->N;
+  // a row tile of 128 where a sequence's rows of a head are no more on average
+  pp.rows = a->N * p.g <= (int64_t)128 * a->B ? 128 : 256;
+  pp.per = pp.rows / p.g;
+  p.R = pp.rows;
+  const bool bf16 = d.dtype == QMM_DT_BF16;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = launch_prompt(pp, bf16, d.head_dim, &h->kmap, &h->vmap, st);
+  // items of one cache tile each are never cut: nothing to join
+  if (e == cudaSuccess && ((int64_t)a->table_width << h->page_shift) > prompt_tile_cache_rows())
+    e = launch_prompt_join(p, bf16, d.head_dim, pp.rows, h->sm_count, st);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }
 

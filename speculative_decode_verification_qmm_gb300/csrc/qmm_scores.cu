@@ -1,0 +1,325 @@
+// qmm_scores.cu -- penalties, biases and grammar masks on the scores of a drafted
+// tree (qmm_adjust_scores in include/qmm.h), and the counts that they go by
+// (qmm_count_tokens).
+//
+// Mathematics.  With c(v) the times that token v was emitted, the node's own path
+// included: x -> x / r (x > 0) or x r where v was seen; x - f c - p [c > 0] + bias; -inf
+// where the grammar bit is 0.
+//
+// A CTA takes a range of the vocabulary of one sequence and walks its nodes: the
+// counts, prompt bits and biases of the range are read once, for all nodes.  Which
+// nodes lie on a node's path is one bit each of a 64-bit word; a node's tokens that
+// fall into the range, mostly none, are added to the counts.
+// What bounds it: memory.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "qmm.h"
+#include "qmm_attn.cuh"
+#include "qmm_attn.h"
+
+namespace qmm {
+namespace {
+
+constexpr int MAX_T = QMM_TREE_MAX_T;
+constexpr int THREADS = 256;
+constexpr int E = 8;  // entries of a thread
+constexpr int RANGE = THREADS * E;
+
+struct AdjustParams {
+  const void* scores;
+  void* out;
+  int64_t s_sb, s_st, o_sb, o_st;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* n_tokens;
+  const int32_t* counts;
+  const uint32_t* prompt;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const float* bias;
+  const uint32_t* mask;
+  int64_t ld_counts, ld_prompt, ld_bias, m_sb, m_st;
+  int64_t V;
+  int T;
+  int per;  // nodes of a CTA
+};
+
+// Entry e of thread t lies at RANGE's place place(e, t): 8 side by side, or every 256th.
+template <bool WIDE>
+__device__ __forceinline__ int place(int e, int t) {
+  return WIDE ? t * E + e : e * THREADS + t;
+}
+
+template <int DT, bool WIDE>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t left, float (&x)[E]) {
+  const int t = threadIdx.x;
+  if constexpr (WIDE && DT == QMM_DT_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + t * E);
+    const bool a = t * E < left, b = t * E + 4 < left;
+    const float4 u = a ? __ldcs(p) : make_float4(0.f, 0.f, 0.f, 0.f), v = b ? __ldcs(p + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  } else if constexpr (WIDE) {
+    const uint4 v = t * E < left ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + t * E))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = unpack16<DT == QMM_DT_BF16>((uint16_t)w[i]);
+      x[2 * i + 1] = unpack16<DT == QMM_DT_BF16>((uint16_t)(w[i] >> 16));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int k = place<false>(e, t);
+      if constexpr (DT == QMM_DT_F32)
+        x[e] = k < left ? __ldcs(static_cast<const float*>(base) + at + k) : 0.f;
+      else
+        x[e] = k < left ? unpack16<DT == QMM_DT_BF16>(static_cast<const uint16_t*>(base)[at + k]) : 0.f;
+    }
+  }
+}
+
+template <int DT, bool WIDE>
+__device__ __forceinline__ void store8(void* base, int64_t at, int64_t left, const float (&x)[E]) {
+  const int t = threadIdx.x;
+  if constexpr (WIDE && DT == QMM_DT_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at + t * E);
+    if (t * E < left) __stcs(p, make_float4(x[0], x[1], x[2], x[3]));
+    if (t * E + 4 < left) __stcs(p + 1, make_float4(x[4], x[5], x[6], x[7]));
+  } else if constexpr (WIDE) {
+    constexpr bool BF = DT == QMM_DT_BF16;
+    if (t * E < left)
+      __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at + t * E),
+             make_uint4(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]), pack16<BF>(x[4], x[5]), pack16<BF>(x[6], x[7])));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int k = place<false>(e, t);
+      if (k >= left) continue;
+      if constexpr (DT == QMM_DT_F32)
+        static_cast<float*>(base)[at + k] = x[e];
+      else
+        static_cast<uint16_t*>(base)[at + k] = (uint16_t)pack16<DT == QMM_DT_BF16>(x[e], 0.f);
+    }
+  }
+}
+
+// The bits of a thread's eight entries in words that begin with bit 0 of the range
+// (a range is whole words).
+template <bool WIDE>
+__device__ __forceinline__ uint32_t bits8(const uint32_t* words, int64_t left) {
+  const int t = threadIdx.x;
+  if constexpr (WIDE) return t * E < left ? __ldg(words + t / 4) >> (8 * (t & 3)) & 255u : 0u;
+  uint32_t r = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int k = place<false>(e, t);
+    if (k < left) r |= (__ldg(words + k / 32) >> (k & 31) & 1u) << e;
+  }
+  return r;
+}
+
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(THREADS) adjust_kernel(const __grid_constant__ AdjustParams p) {
+  __shared__ int s_token[MAX_T];               // place in the range, or -1
+  __shared__ unsigned long long s_path[MAX_T];  // the nodes on a node's path that lie in the range
+  const int t = threadIdx.x, b = blockIdx.y;
+  const int64_t v0 = (int64_t)blockIdx.x * RANGE, left = p.V - v0;
+  int n = p.T;
+  if (p.n_tokens) {
+    n = __ldg(p.n_tokens + b);
+    n = n < 0 ? 0 : (n > p.T ? p.T : n);
+  }
+  const int first = blockIdx.z * p.per, end = first + p.per < n ? first + p.per : n;
+  if (first >= end) return;
+  const bool penal = p.repetition || p.frequency || p.presence;
+  float c[E], bias[E];
+  uint32_t asked = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) c[e] = 0.f, bias[e] = 0.f;
+  float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
+  if (penal) {
+    if (p.repetition) rep = __ldg(p.repetition + b), inv = 1.f / rep;
+    if (p.frequency) freq = __ldg(p.frequency + b);
+    if (p.presence) pres = __ldg(p.presence + b);
+    if (p.counts) {
+      const int32_t* row = p.counts + b * p.ld_counts + v0;
+      if constexpr (WIDE) {
+        const int4* q = reinterpret_cast<const int4*>(row + t * E);
+        const int4 u = t * E < left ? __ldg(q) : make_int4(0, 0, 0, 0), w = t * E + 4 < left ? __ldg(q + 1) : make_int4(0, 0, 0, 0);
+        c[0] = (float)u.x, c[1] = (float)u.y, c[2] = (float)u.z, c[3] = (float)u.w;
+        c[4] = (float)w.x, c[5] = (float)w.y, c[6] = (float)w.z, c[7] = (float)w.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) c[e] = place<false>(e, t) < left ? (float)__ldg(row + place<false>(e, t)) : 0.f;
+      }
+    }
+    if (p.prompt) asked = bits8<WIDE>(p.prompt + b * p.ld_prompt + v0 / 32, left);
+    if (t < MAX_T) {
+      int64_t x = -1;
+      if (p.tokens && t < n) x = __ldg(p.tokens + (int64_t)b * p.T + t) - v0;
+      s_token[t] = x >= 0 && x < RANGE && x < left ? (int)x : -1;
+    }
+    __syncthreads();
+    if (t < MAX_T && t < n) {
+      unsigned long long path = 0;
+      int node = t;
+      while (node > 0) {
+        if (s_token[node] >= 0) path |= 1ull << node;
+        const int up = p.parents ? __ldg(p.parents + (int64_t)b * p.T + node) : node - 1;
+        if (up >= node) break;
+        node = up;
+      }
+      s_path[t] = path;
+    }
+    __syncthreads();
+  }
+  if (p.bias) {
+    const float* row = p.bias + b * p.ld_bias + v0;
+    if constexpr (WIDE) {
+      const float4* q = reinterpret_cast<const float4*>(row + t * E);
+      const float4 u = t * E < left ? __ldg(q) : make_float4(0.f, 0.f, 0.f, 0.f),
+                   w = t * E + 4 < left ? __ldg(q + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      bias[0] = u.x, bias[1] = u.y, bias[2] = u.z, bias[3] = u.w, bias[4] = w.x, bias[5] = w.y, bias[6] = w.z, bias[7] = w.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) bias[e] = place<false>(e, t) < left ? __ldg(row + place<false>(e, t)) : 0.f;
+    }
+  }
+  const uint32_t* mask = p.mask ? p.mask + b * p.m_sb + v0 / 32 : nullptr;
+#pragma unroll 2
+  for (int i = first; i < end; ++i) {
+    float x[E];
+    load8<DT, WIDE>(p.scores, b * p.s_sb + i * p.s_st + v0, left, x);
+    const uint32_t may = mask ? bits8<WIDE>(mask + i * p.m_st, left) : 255u;
+    if (penal) {
+      float k[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) k[e] = c[e];
+      for (unsigned long long path = s_path[i]; path; path &= path - 1) {
+        const int at = s_token[__ffsll((long long)path) - 1];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (place<WIDE>(e, t) == at) k[e] += 1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool some = k[e] > 0.f;
+        if (some || (asked >> e & 1)) x[e] *= x[e] > 0.f ? inv : rep;
+        x[e] = x[e] - freq * k[e] - (some ? pres : 0.f);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = may >> e & 1 ? x[e] + bias[e] : -INFINITY;
+    store8<DT, WIDE>(p.out, b * p.o_sb + i * p.o_st + v0, left, x);
+  }
+}
+
+template <int DT>
+cudaError_t launch_adjust(const AdjustParams& p, int B, bool wide, int sms, cudaStream_t st) {
+  AdjustParams q = p;
+  const int64_t ranges = (p.V + RANGE - 1) / RANGE, ctas = ranges * B;
+  // all nodes of a sequence in one CTA, unless that leaves SMs idle
+  int64_t parts = (4ll * sms + ctas - 1) / ctas;
+  if (parts > p.T) parts = p.T;
+  q.per = (int)((p.T + parts - 1) / parts);
+  const dim3 grid((unsigned)ranges, (unsigned)B, (unsigned)((p.T + q.per - 1) / q.per));
+  if (wide)
+    adjust_kernel<DT, true><<<grid, THREADS, 0, st>>>(q);
+  else
+    adjust_kernel<DT, false><<<grid, THREADS, 0, st>>>(q);
+  return cudaGetLastError();
+}
+
+__global__ void count_kernel(int32_t* counts, int64_t ld, int T, int64_t V, const int32_t* tokens, const int32_t* path,
+                             const int32_t* accept) {
+  const int b = blockIdx.x, j = threadIdx.x;
+  const int k = __ldg(accept + 2 * b);
+  int x = -1;
+  if (j < T && j < k) {
+    const int node = __ldg(path + (int64_t)b * T + j);
+    if (node >= 0 && node < T) x = __ldg(tokens + (int64_t)b * T + node);
+  } else if (j == MAX_T) {
+    x = __ldg(accept + 2 * b + 1);
+  }
+  if (x >= 0 && x < V) atomicAdd(counts + b * ld + x, 1);
+}
+
+int check_sizes(int B, int T, int64_t V) {
+  return B < 1 || B > 65535 || T < 1 || T > MAX_T || V < 1 || V > (1 << 24) ? QMM_ERR_SHAPE : QMM_OK;
+}
+
+}  // namespace
+}  // namespace qmm
+
+using namespace qmm;
+
+extern "C" {
+
+int qmm_adjust_scores(const qmm_adjust_args* a, void* stream) {
+  if (!a || a->struct_size != sizeof(qmm_adjust_args)) return QMM_ERR_INVALID_ARG;
+  if (a->dtype > QMM_DT_F32 || !a->scores || !a->out) return QMM_ERR_INVALID_ARG;
+  int rc = check_sizes(a->B, a->T, a->V);
+  if (rc != QMM_OK) return rc;
+  const int64_t words = (a->V + 31) / 32;
+  const int elem = a->dtype == QMM_DT_F32 ? 4 : 2;
+  const uintptr_t small = (uintptr_t)a->tokens | (uintptr_t)a->parents | (uintptr_t)a->n_tokens | (uintptr_t)a->counts |
+                          (uintptr_t)a->prompt | (uintptr_t)a->repetition | (uintptr_t)a->frequency |
+                          (uintptr_t)a->presence | (uintptr_t)a->bias | (uintptr_t)a->mask;
+  if ((((uintptr_t)a->scores | (uintptr_t)a->out) & (elem - 1)) || (small & 3)) return QMM_ERR_ALIGN;
+  if (a->B > 1 && ((a->counts && a->ld_counts < a->V) || (a->prompt && a->ld_prompt < words) ||
+                   (a->bias && a->ld_bias && a->ld_bias < a->V)))
+    return QMM_ERR_ALIGN;
+  AdjustParams p;
+  // strides of dimensions with one entry are not followed
+  const bool bs = a->B > 1, ts = a->T > 1;
+  p.s_sb = bs ? a->stride[0] : 0, p.s_st = ts ? a->stride[1] : 0;
+  p.o_sb = bs ? a->out_stride[0] : 0, p.o_st = ts ? a->out_stride[1] : 0;
+  p.m_sb = bs ? a->mask_stride[0] : 0, p.m_st = ts ? a->mask_stride[1] : 0;
+  if (a->out == a->scores && (p.s_sb != p.o_sb || p.s_st != p.o_st)) return QMM_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  rc = host_check_device(&dev, &sms);
+  if (rc != QMM_OK) return rc;
+  p.scores = a->scores, p.out = a->out;
+  p.tokens = a->tokens, p.parents = a->parents, p.n_tokens = a->n_tokens;
+  p.counts = a->counts, p.prompt = a->prompt;
+  p.repetition = a->repetition, p.frequency = a->frequency, p.presence = a->presence;
+  p.bias = a->bias, p.mask = a->mask;
+  p.ld_counts = bs ? a->ld_counts : 0, p.ld_prompt = bs ? a->ld_prompt : 0, p.ld_bias = bs ? a->ld_bias : 0;
+  p.V = a->V;
+  p.T = a->T;
+  p.per = a->T;
+  // 16-byte loads where every row of every tensor starts on a boundary and holds
+  // whole groups of eight scores (and so of eight bits)
+  const bool wide = !((a->V | p.s_sb | p.s_st | p.o_sb | p.o_st) & 7) && !(((uintptr_t)a->scores | (uintptr_t)a->out) & 15) &&
+                    !(a->counts && (((uintptr_t)a->counts & 15) || (p.ld_counts & 3))) &&
+                    !(a->bias && (((uintptr_t)a->bias & 15) || (p.ld_bias & 3)));
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+  switch (a->dtype) {
+    case QMM_DT_F32: e = launch_adjust<QMM_DT_F32>(p, a->B, wide, sms, st); break;
+    case QMM_DT_BF16: e = launch_adjust<QMM_DT_BF16>(p, a->B, wide, sms, st); break;
+    default: e = launch_adjust<QMM_DT_F16>(p, a->B, wide, sms, st); break;
+  }
+  return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
+}
+
+int qmm_count_tokens(int32_t* counts, int64_t ld_counts, int B, int T, int64_t V, const int32_t* tokens,
+                     const int32_t* path, const int32_t* accept, void* stream) {
+  if (!counts || !tokens || !path || !accept) return QMM_ERR_INVALID_ARG;
+  int rc = check_sizes(B, T, V);
+  if (rc != QMM_OK) return rc;
+  if ((((uintptr_t)counts | (uintptr_t)tokens | (uintptr_t)path | (uintptr_t)accept) & 3) || (B > 1 && ld_counts < V))
+    return QMM_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  rc = host_check_device(&dev, &sms);
+  if (rc != QMM_OK) return rc;
+  count_kernel<<<B, MAX_T + 32, 0, (cudaStream_t)stream>>>(counts, ld_counts, T, V, tokens, path, accept);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
+}
+
+}  // extern "C"

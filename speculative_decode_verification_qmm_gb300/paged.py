@@ -10,8 +10,18 @@
     cache.advance([seq], accepted)           # once the host knows the counts
     other = cache.fork(seq)
 
-The arithmetic runs in libqmm.so's kernels (qmm_tree_attention,
-qmm_cache_commit, qmm_cache_copy, qmm_verify_sample of include/qmm.h).  What
+A prompt of any length, its rows packed with other prompts':
+
+    cache.reserve([seq], n)
+    table, lens = cache.tables([seq])
+    starts = cache.starts([n])
+    q = cache.append(layer, q, k, v, table, lens, starts, rope=rope)
+    out, lse = cache.attend_prompt(layer, q, table, lens, starts)
+    cache.advance([seq], [n])                # after the last layer
+
+The arithmetic runs in libqmm.so's kernels (qmm_tree_attention, qmm_cache_append,
+qmm_prompt_attention, qmm_cache_commit, qmm_cache_copy, qmm_verify_sample of
+include/qmm.h).  What
 stays on the host is bookkeeping: which pages are free, which sequence holds
 which page, and how many sequences share one.
 """
@@ -21,15 +31,18 @@ import ctypes
 import functools
 import struct
 
-from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_ERR_DEVICE, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_attn_args,
-                   qmm_cache_desc, qmm_sample_args)
+from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_ERR_DEVICE, QMM_OK, QMM_TREE_MAX_T, QmmError, load, qmm_append_args,
+                   qmm_attn_args, qmm_cache_desc, qmm_prompt_args, qmm_sample_args)
 
 
 # The argument structs of the C calls, packed in one go: filling a ctypes
 # structure field by field costs more than a small kernel.
 _ATTN = struct.Struct("@IiiiPPPP12qPPqifPPPq")
 _SAMPLE = struct.Struct("@IIiiqPqqPqqPPPPPPPPPq")
+_APPEND = struct.Struct("@IIiiqPPPP8qPqiPPPP")
+_PROMPT = struct.Struct("@IiiiqPP4qPPqPPf0q")
 assert _ATTN.size == ctypes.sizeof(qmm_attn_args) and _SAMPLE.size == ctypes.sizeof(qmm_sample_args)
+assert _APPEND.size == ctypes.sizeof(qmm_append_args) and _PROMPT.size == ctypes.sizeof(qmm_prompt_args)
 _raw_stream = None
 _CODES = {}
 
@@ -130,6 +143,36 @@ def _tree_attention(h, layer, q, k, v, table, lens, out, lse, mask, n_tokens, sc
         _stream_ptr(stream, q.device.index))
     if rc:
         _check("qmm_tree_attention", rc)
+
+
+def qmm_cache_append(h, layer, q, k, v, q_out, page_table, lens, starts, rope=None, positions=None, stream=None) -> None:
+    """q CUDA [N, Hq, D] (or None), k, v [N, Hkv, D] in fp32, bf16 or f16, q_out
+    [N, Hq, D] in the cache's type; page_table int32 [B, pages]; lens int32 [B];
+    starts int32 [B + 1]; positions int32 [N]; rope: a Rope; asynchronous."""
+    qs = os = (0, 0, 0)
+    if q is not None:
+        qs, os = q.stride(), q_out.stride()
+    ks, vs = k.stride(), v.stride()
+    rc = load().qmm_cache_append(h, _APPEND.pack(
+        _APPEND.size, _dtype(k.dtype), layer, lens.shape[0], k.shape[0], 0 if q is None else q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), 0 if q is None else q_out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1],
+        page_table.data_ptr(), page_table.stride(0), page_table.shape[1], lens.data_ptr(), starts.data_ptr(),
+        0 if positions is None else positions.data_ptr(), 0 if rope is None else rope.address),
+        _stream_ptr(stream, k.device.index))
+    if rc:
+        _check("qmm_cache_append", rc)
+
+
+def qmm_prompt_attention(h, layer, q, page_table, lens, starts, out, lse=None, scale=None, stream=None) -> None:
+    """q, out CUDA [N, Hq, D]; page_table int32 [B, pages]; lens int32 [B]; starts
+    int32 [B + 1]; lse fp32 [N, Hq] or None; asynchronous."""
+    qs, os = q.stride(), out.stride()
+    rc = load().qmm_prompt_attention(h, _PROMPT.pack(
+        _PROMPT.size, layer, lens.shape[0], page_table.shape[1], q.shape[0], q.data_ptr(), out.data_ptr(), qs[0], qs[1],
+        os[0], os[1], 0 if lse is None else lse.data_ptr(), page_table.data_ptr(), page_table.stride(0), lens.data_ptr(),
+        starts.data_ptr(), q.shape[2] ** -0.5 if scale is None else scale), _stream_ptr(stream, q.device.index))
+    if rc:
+        _check("qmm_prompt_attention", rc)
 
 
 def qmm_cache_commit(h, page_table, lens, path, accept, lens_out, stream=None) -> None:
@@ -315,6 +358,72 @@ class PagedCache:
                         vs, out.stride(), page_table.stride(0))
         return out, lse
 
+    def append(self, layer: int, q, k, v, page_table, lens, starts, rope=None, positions=None, out=None, stream=None):
+        """Writes the packed rows' keys, turned by their positions, and values behind
+        the cached rows, and returns their turned queries in the cache's type (None
+        where q is None).  See qmm_cache_append."""
+        import torch
+        if stream is not None:  # the result is allocated on the stream that writes it
+            with torch.cuda.stream(stream):
+                return self.append(layer, q, k, v, page_table, lens, starts, rope, positions, out)
+        if k.dim() != 3:
+            raise ValueError("k must be [N, n_kv_heads, head_dim]")
+        dt, at, i32 = k.dtype, self._device, torch.int32
+        N, D = k.shape[0], self.head_dim
+        new, wide = (N, self.n_kv_heads, D), (N, self.n_q_heads, D)
+        _dtype(dt)
+        _strided("k", k, dt, new, at)
+        _strided("v", v, dt, new, at)
+        self._packed(page_table, lens, starts)
+        if positions is not None:
+            _flat("positions", positions, i32, (N,), at)
+        if rope is not None and rope.device_index != at:
+            raise ValueError(f"rope must be on cuda:{at}, not cuda:{rope.device_index}")
+        if q is None:
+            if out is not None:
+                raise ValueError("out without q")
+        else:
+            _strided("q", q, dt, wide, at)
+            if out is None:
+                out = torch.empty(wide, dtype=self.dtype, device=k.device)
+            else:
+                _strided("out", out, self.dtype, wide, at)
+        qmm_cache_append(self.handle, layer, q, k, v, out, page_table, lens, starts, rope, positions)
+        return out
+
+    def attend_prompt(self, layer: int, q, page_table, lens, starts, scale=None, out=None, lse=None, stream=None):
+        """(out, lse): causal attention of packed rows that the cache holds already, as
+        append() leaves them; lens are the rows before them.  See
+        qmm_prompt_attention."""
+        import torch
+        if stream is not None:  # the results are allocated on the stream that writes them
+            with torch.cuda.stream(stream):
+                return self.attend_prompt(layer, q, page_table, lens, starts, scale, out, lse)
+        if q.dim() != 3:
+            raise ValueError("q must be [N, n_q_heads, head_dim]")
+        N, Hq, at = q.shape[0], self.n_q_heads, self._device
+        wide = (N, Hq, self.head_dim)
+        _strided("q", q, self.dtype, wide, at)
+        self._packed(page_table, lens, starts)
+        if out is None:
+            out = torch.empty(wide, dtype=self.dtype, device=q.device)
+        else:
+            _strided("out", out, self.dtype, wide, at)
+        if lse is None:
+            lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
+        else:
+            _flat("lse", lse, torch.float32, (N, Hq), at)
+        qmm_prompt_attention(self.handle, layer, q, page_table, lens, starts, out, lse, scale)
+        return out, lse
+
+    def _packed(self, page_table, lens, starts):
+        import torch
+        if lens.dim() != 1:
+            raise ValueError("lens must be [B]")
+        B = lens.shape[0]
+        self._table(page_table, lens, B)
+        _flat("starts", starts, torch.int32, (B + 1,), self._device)
+
     def commit(self, page_table, lens, path, accept, lens_out=None, stream=None):
         """The new lengths: the accepted branches' rows move behind the cached ones
         in every layer.  See qmm_cache_commit."""
@@ -455,6 +564,19 @@ class PagedCache:
         dev = self.k_pool.device
         return (torch.tensor(rows, dtype=torch.int32).to(dev),
                 torch.tensor([s.length for s in seqs], dtype=torch.int32).to(dev))
+
+    def starts(self, counts, stream=None):
+        """CUDA int32 [B + 1]: where each sequence's rows begin among `counts` packed ones."""
+        import torch
+        if stream is not None:  # allocated on the stream that reads it
+            with torch.cuda.stream(stream):
+                return self.starts(counts)
+        ends = [0]
+        for n in counts:
+            if n < 0:
+                raise ValueError(f"{n} rows of a sequence")
+            ends.append(ends[-1] + int(n))
+        return torch.tensor(ends, dtype=torch.int32).to(self.k_pool.device)
 
     def close(self):
         if self.handle:
