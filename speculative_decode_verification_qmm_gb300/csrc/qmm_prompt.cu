@@ -31,6 +31,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "qmm_attn.cuh"
 #include "qmm_attn.h"
 #include "qmm_prompt.cuh"
@@ -43,6 +45,15 @@ namespace {
 constexpr int TK = 128;      // cache rows of a tile
 constexpr int BAD_BUFS = 16; // more than twice the segments that the rings hold
 constexpr int BAD_WORDS = 8; // an item's tokens after its first: at most 255
+constexpr int ITEM_WEIGHT = 3;
+
+// Two MMA warps and two loading warps beside four softmax warps; with two row tiles an MMA
+// warp and three loading warps beside eight.
+constexpr int threads_of(int NQ) { return NQ == 1 ? 256 : 384; }
+// Registers a thread with two row tiles: what three groups of four warps are launched with, and
+// what the two softmax groups and the third one go on with.
+constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
+static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * REGS_LAUNCH, "registers of a CTA");
 
 template <int D, int NQ>
 struct Smem {
@@ -59,7 +70,8 @@ struct Smem {
   static constexpr int NBAR = 2 * KS + 3 * VS + 16;
   static constexpr int BAD = BAR + NBAR * 8;        // rows with non-finite V, by segment
   static constexpr int FLAG = BAD + BAD_BUFS * BAD_WORDS * 4;  // [0] abort, [1] tensor memory
-  static constexpr int BYTES = FLAG + 16;
+  static constexpr int START = FLAG + 16;           // the CTA's share, and the cursor at its start
+  static constexpr int BYTES = START + 48;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
@@ -99,7 +111,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
 }
 
 // ---------------------------------------------------------------- division of the work
-// sum of floor((a i + b) / m) over i < n, by Euclid's algorithm.
+// sum of floor((a i + b) / m) over i < n <= 2^24, by Euclid's algorithm; m at most 128, b below 2^32.
 __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t sum = 0;
   while (n > 0) {
@@ -111,10 +123,10 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
       sum += (int64_t)n * (b / m);
       b %= m;
     }
-    const uint64_t y = (uint64_t)a * n + b;
+    const uint32_t y = a * n + b;  // below 128 * 2^24 + 128
     if (y < m) break;
-    n = (uint32_t)(y / m);
-    b = (uint32_t)(y % m);
+    n = y / m;
+    b = y % m;
     const uint32_t t = m;
     m = a;
     a = t;
@@ -143,44 +155,53 @@ __device__ __forceinline__ bool prompt_sizes(const PromptParams& p, int b, int& 
   return ok;
 }
 
+// A place in the call's work: an item (sequence, head, row tile) weighs its cache tiles
+// and ITEM_WEIGHT more, which lie before the first tile, for what it costs to begin and
+// end.
 struct Cursor {
-  int b, h, rt, tile;  // the unit
-  int tiles;           // cache tiles of the row tile
+  int b, h, rt;
+  int w;               // weight of the item that lies before the place
+  int tiles;           // cache tiles of the item
   int L, n, first;     // of the sequence
 };
+
+__device__ __forceinline__ int64_t weight_before(const PromptParams& p, int L, int n, int count) {
+  return units_before(L, n, p.per, count) + (int64_t)ITEM_WEIGHT * count;
+}
 
 __device__ __forceinline__ int tiles_of(const PromptParams& p, const Cursor& c) {
   const int end = (c.rt + 1) * p.per;
   return (c.L + (end < c.n ? end : c.n) + TK - 1) / TK;
 }
 
-// The cursor at the first unit of CTA c's range [u0, u1), for every lane of a warp.
-__device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, int64_t& u0, int64_t& u1) {
+// The start of CTA c's share of the work, and the share's weight, for every lane of a warp.
+__device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, int64_t& left) {
   int64_t W = 0;
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
     int64_t w = 0;
     if (b0 + lane < p.a.B) {
       int L, n, first;
       if (!prompt_sizes(p, b0 + lane, L, n, first) && c == 0) atomicOr(p.a.status, DEV_ERR_INDEX);
-      w = units_before(L, n, p.per, (n + p.per - 1) / p.per) * p.a.Hkv;
+      w = weight_before(p, L, n, (n + p.per - 1) / p.per) * p.a.Hkv;
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
     W += w;
   }
+  // no CTA without a share between two that have one: the joining kernel counts on it
   const int G = W < p.a.grid ? (int)W : p.a.grid;
   Cursor cur{};
-  u0 = u1 = 0;
+  left = 0;
   if (c >= G) return cur;
-  u0 = W * c / G;
-  u1 = W * (c + 1) / G;
+  const int64_t u0 = W * c / G;
+  left = W * (c + 1) / G - u0;
   int64_t before = 0;
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
     int L = 0, n = 0, first = 0;
     int64_t w = 0;
     if (b0 + lane < p.a.B) {
       prompt_sizes(p, b0 + lane, L, n, first);
-      w = units_before(L, n, p.per, (n + p.per - 1) / p.per) * p.a.Hkv;
+      w = weight_before(p, L, n, (n + p.per - 1) / p.per) * p.a.Hkv;
     }
     int64_t inc = w;
 #pragma unroll
@@ -201,28 +222,39 @@ __device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, 
     before += __shfl_sync(0xFFFFFFFFu, inc, 31);
   }
   const int all = (cur.n + p.per - 1) / p.per;
-  const int64_t a_head = units_before(cur.L, cur.n, p.per, all);
+  const int64_t a_head = weight_before(p, cur.L, cur.n, all);
   const int64_t rem = u0 - before;
   cur.h = (int)(rem / a_head);
   const int64_t in_head = rem - cur.h * a_head;
-  // the last row tile that begins at or before the unit, 32 places at a time
+  // the last row tile that begins at or before the place, 32 candidates at a time
   int lo = 0, hi = all;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const bool le = at < hi && units_before(cur.L, cur.n, p.per, at) <= in_head;
+    const bool le = at < hi && weight_before(p, cur.L, cur.n, at) <= in_head;
     const int k = __popc(__ballot_sync(0xFFFFFFFFu, le));
     lo += k * step;
     hi = hi < lo + step ? hi : lo + step;
   }
   cur.rt = lo;
-  cur.tile = (int)(in_head - units_before(cur.L, cur.n, p.per, lo));
+  cur.w = (int)(in_head - weight_before(p, cur.L, cur.n, lo));
   cur.tiles = tiles_of(p, cur);
   return cur;
 }
 
-// On to the first cache tile of the next row tile.
+// Takes what the share has of the cursor's item: its cache tiles from `tile` on, and how
+// many.  The cursor moves behind them.
+__device__ __forceinline__ int take(Cursor& c, int64_t& left, int& tile) {
+  const int64_t rest = c.tiles + ITEM_WEIGHT - c.w;
+  const int w = rest < left ? (int)rest : (int)left;
+  tile = c.w > ITEM_WEIGHT ? c.w - ITEM_WEIGHT : 0;
+  c.w += w;
+  left -= w;
+  return c.w > ITEM_WEIGHT ? c.w - ITEM_WEIGHT - tile : 0;
+}
+
+// On to the next item.
 __device__ __forceinline__ void next(const PromptParams& p, Cursor& c) {
-  c.tile = 0;
+  c.w = 0;
   if ((int64_t)++c.rt * p.per >= c.n) {
     c.rt = 0;
     if (++c.h == p.a.Hkv) {
@@ -236,8 +268,37 @@ __device__ __forceinline__ void next(const PromptParams& p, Cursor& c) {
   c.tiles = tiles_of(p, c);
 }
 
+// Rows r0 .. left - 1 of a V tile without what is not finite (each row that has some is told
+// to `found`), and zeros in the rows from `left` on, by a warp.
+template <bool BF16, int D, typename F>
+__device__ __forceinline__ void clean(uint32_t tile, int r0, int left, int lane, F found) {
+  constexpr int CH = D / 8, HALF = TK * 128, BATCH = 8;
+  const int ch = lane % CH, end = left * CH;
+  auto place = [&](int id) {
+    const int row = id / CH;
+    return tile + (ch >> 3) * HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+  };
+  auto put = [](uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  };
+  for (int id = r0 * CH + lane; id < end; id += 32 * BATCH) {
+    uint4 v[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (id + 32 * i < end) v[i] = lds128(place(id + 32 * i));
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (id + 32 * i < end && any_nonfinite<BF16>(v[i])) {
+        put(place(id + 32 * i), make_uint4(zero_nonfinite<BF16>(v[i].x), zero_nonfinite<BF16>(v[i].y),
+                                           zero_nonfinite<BF16>(v[i].z), zero_nonfinite<BF16>(v[i].w)));
+        found((id + 32 * i) / CH);
+      }
+  }
+  for (int id = (left > 0 ? left : 0) * CH + lane; id < TK * CH; id += 32) put(place(id), make_uint4(0u, 0u, 0u, 0u));
+}
+
 template <bool BF16, int D, int NQ>
-__global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
+__global__ void __launch_bounds__(threads_of(NQ), 1)
     prompt_kernel(const __grid_constant__ PromptParams pp, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D, NQ>;
@@ -251,6 +312,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
   constexpr uint32_t COL_O = NB * TK;
   constexpr uint32_t COL_Q = 256;  // of the second row tile
   constexpr int MMA_WARP = NQ * 4, MMA_WARPS = 2 / NQ, LOAD_WARP = MMA_WARP + MMA_WARPS;
+  constexpr int Q_WARP = NQ == 2 ? LOAD_WARP + 2 : -1;  // (NQ = 1: both loading warps)
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = smem_u32(smem);
@@ -272,7 +334,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
       mbar_init(b_vempty + 8 * i, 1);
       mbar_init(b_vland + 8 * i, 1);
     }
-    mbar_init(b_qfull, 2);
+    mbar_init(b_qfull, NQ == 1 ? 2 : 1);
     mbar_init(b_qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
@@ -296,23 +358,27 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
   // then may the joining kernel take its place.
   pdl_wait();
   pdl_trigger();
-  int64_t u0, u1;
-  Cursor cur = begin(pp, lane, blockIdx.x, u0, u1);
+  int64_t share;
+  Cursor cur;
+  if (warp == 0) {
+    cur = begin(pp, lane, blockIdx.x, share);
+    if (lane == 0) {
+      *reinterpret_cast<int64_t*>(smem + S::START) = share;
+      *reinterpret_cast<Cursor*>(smem + S::START + 8) = cur;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  share = *reinterpret_cast<const int64_t*>(smem + S::START);
+  cur = *reinterpret_cast<const Cursor*>(smem + S::START + 8);
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
 
-  if (tid == 0 && u0 >= u1) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   const uint64_t lim = p.wait_limit_ns;
   auto fail = [&](int code) {
     if (!s_flag[0]) atomicOr(p.status, code);
     s_flag[0] = 1;
-  };
-  // The cache tiles of the segment that starts at unit u.
-  auto segment = [&](int64_t u) {
-    const int64_t left = cur.tiles - cur.tile;
-    return (int)(left < u1 - u ? left : u1 - u);
   };
   // Tokens and rows of the cursor's row tile.
   auto tokens = [&] {
@@ -320,10 +386,34 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
     return left < pp.per ? left : pp.per;
   };
 
+  // Rows of Q, by threads `id` of `STEP` CH; rows past the item's stay as they are, and so do
+  // their results.
+  auto load_q = [&](int id, auto step) {
+    constexpr int CH = D / 8, STEP = decltype(step)::value / CH;  // 16-byte chunks of a row, rows at a time
+    const int rows = tokens() * p.g, ch = id % CH;
+    const int dt = STEP / p.g, dh = STEP % p.g;
+    int row = id / CH, t = row / p.g, h = row % p.g;
+    const uint16_t* src = p.q + (int64_t)(cur.first + cur.rt * pp.per) * p.q_st + (int64_t)cur.h * p.g * p.q_sh + ch * 8;
+#pragma unroll 8
+    for (; row < rows; row += STEP) {
+      cp_async16(base + S::Q + (row >> 7) * S::TILE + (ch >> 3) * S::HALF + (row & 127) * 128 +
+                     (((ch & 7) ^ (row & 7)) << 4),
+                 src + t * p.q_st + h * p.q_sh, 16);
+      t += dt, h += dh;
+      if (h >= p.g) h -= p.g, ++t;
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_qfull);
+  };
+
+  if (warp >= MMA_WARP) {
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------------ load
     const bool is_v = warp > LOAD_WARP;
-    constexpr int CH = D / 8;  // 16-byte chunks of a row
     const uint32_t full = is_v ? b_vfull : b_kfull, empty = is_v ? b_vempty : b_kempty;
     const uint32_t ring = base + (is_v ? S::V : S::K);
     const int slots = is_v ? S::VS : S::KS;
@@ -336,30 +426,25 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
     };
     int slot = 0, round = 0, seg = 0;
     unsigned landing = 0, landed = 0;  // bits by slot: a copy counts on vland; vland's parity
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const int count = segment(u);
-      // Q, by both warps; rows past the item's stay as they are, and so do their results
-      if (seg > 0) wait(b_qempty, (uint32_t)((seg - 1) & 1));
-      if (!ok) break;
-      const int rows = tokens() * p.g;
-      {
-        constexpr int STEP = 64 / CH;  // rows of both warps at a time
-        const int id = (warp - LOAD_WARP) * 32 + lane, ch = id % CH;
-        const int dt = STEP / p.g, dh = STEP % p.g;
-        int row = id / CH, t = row / p.g, h = row % p.g;
-        const uint16_t* src = p.q + (int64_t)(cur.first + cur.rt * pp.per) * p.q_st + (int64_t)cur.h * p.g * p.q_sh + ch * 8;
-#pragma unroll 4
-        for (; row < rows; row += STEP) {
-          cp_async16(base + S::Q + (row >> 7) * S::TILE + (ch >> 3) * S::HALF + (row & 127) * 128 +
-                         (((ch & 7) ^ (row & 7)) << 4),
-                     src + t * p.q_st + h * p.q_sh, 16);
-          t += dt, h += dh;
-          if (h >= p.g) h -= p.g, ++t;
+    while (share > 0 && ok) {
+      int tile;
+      const int count = take(cur, share, tile);
+      if (count > 0) {
+        if (NQ == 1 || warp == Q_WARP) {
+          if (seg > 0) wait(b_qempty, (uint32_t)((seg - 1) & 1));
+          if (!ok) break;
+          if constexpr (NQ == 1)
+            load_q((warp - LOAD_WARP) * 32 + lane, std::integral_constant<int, 64>());
+          else
+            load_q(lane, std::integral_constant<int, 32>());
         }
+        ++seg;
       }
       // Lane i < BLOCKS looks up the page of the tile's block i, a tile ahead.  An
       // id out of range is reported; rows of page 0 take its place.
-      const int end = cur.L + cur.n;
+      const int first_token = cur.rt * pp.per;
+      const int end = cur.L + first_token + tokens();  // rows that a row of the item sees
+      const int all_see = cur.L + first_token;         // the last row that every one sees
       int ahead = 0;
       auto lookup = [&](int j) {
         const int jb = j * TK + lane * 16;
@@ -372,20 +457,15 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
           }
         }
       };
-      lookup(cur.tile);
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_qfull);
-      const int all_see = cur.L + cur.rt * pp.per;  // the last row that every row of the item sees
-      for (int j = 0; j < count; ++j) {
-        const int j0 = (cur.tile + j) * TK;
+      const int copies = NQ == 2 && warp == Q_WARP ? 0 : count;
+      if (copies > 0) lookup(tile);
+      for (int j = 0; j < copies; ++j) {
+        const int j0 = (tile + j) * TK;
         const int pid = ahead;
-        if (j + 1 < count) lookup(cur.tile + j + 1);
+        if (j + 1 < count) lookup(tile + j + 1);
         if (round > 0) wait(empty + 8 * slot, (uint32_t)((round - 1) & 1));
         if (!ok) break;
-        const int left = end - j0 < TK ? end - j0 : TK;  // rows of the tile that exist
+        const int left = end - j0 < TK ? end - j0 : TK;  // rows of the tile that count
         const int blocks = (left + 15) / 16;
         const bool masked = is_v && j0 + TK - 1 > all_see;
         const uint32_t bar = (masked ? b_vland : full) + 8 * slot, dst = ring + slot * S::TILE;
@@ -407,30 +487,17 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
           }
           landed ^= 1u << slot;
           landing &= ~(1u << slot);
-          const int r0 = all_see + 1 > j0 ? all_see + 1 - j0 : 0;
-          for (int id = r0 * CH + lane; id < TK * CH; id += 32) {
-            const int row = id / CH, ch = id % CH;
-            const uint32_t at = dst + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (row < left) {
-              v = lds128(at);
-              if (!any_nonfinite<BF16>(v)) continue;
-              v = make_uint4(zero_nonfinite<BF16>(v.x), zero_nonfinite<BF16>(v.y), zero_nonfinite<BF16>(v.z),
-                             zero_nonfinite<BF16>(v.w));
-              const int k = j0 + row - all_see - 1;
-              if (k < 32 * BAD_WORDS) atomicOr(s_bad + (seg & (BAD_BUFS - 1)) * BAD_WORDS + (k >> 5), 1u << (k & 31));
-            }
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
+          clean<BF16, D>(dst, all_see + 1 > j0 ? all_see + 1 - j0 : 0, left, lane, [&](int row) {
+            const int k = j0 + row - all_see - 1;
+            atomicOr(s_bad + ((seg - 1) & (BAD_BUFS - 1)) * BAD_WORDS + (k >> 5), 1u << (k & 31));
+          });
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(full + 8 * slot);
         }
         if (++slot == slots) slot = 0, ++round;
       }
-      u += count;
-      if (u < u1) next(pp, cur);
+      if (share > 0) next(pp, cur);
     }
     cp_async_wait<0>();
     // Tensor copies in flight land before the CTA leaves: the last tile of every
@@ -444,7 +511,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
           atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
       }
     }
-  } else if (warp >= MMA_WARP) {
+  } else {
     // ------------------------------------------------------------ MMA issue
     // The warp stays together and one elected lane issues (see qmm_attn_tc.cu).
     uint32_t leader;
@@ -484,8 +551,13 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
     int n = 0, seg = 0;         // tiles and segments so far (parities, and whether there was one)
     int slot = 0, round = 0;    // of the tile of K or V
     int vslot = 0, vround = 0;  // of the tile of V, where one warp issues both
-    for (int64_t u = u0; u < u1 && ok; ++seg) {
-      const int count = segment(u);
+    while (share > 0 && ok) {
+      int tile;
+      const int count = take(cur, share, tile);
+      if (count == 0) {  // (a share can end before an item's first tile)
+        if (share > 0) next(pp, cur);
+        continue;
+      }
       if constexpr (NQ == 2) {
         // O += P V of a row tile, then S of its next cache tile, then the other row tile
         for (int j = -1; j < count && ok; ++j) {
@@ -548,16 +620,19 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
           if (++slot == S::VS) slot = 0, ++round;
         }
       }
-      u += count;
-      if (u < u1) next(pp, cur);
+      ++seg;
+      if (share > 0) next(pp, cur);
     }
     // all MMAs of the CTA have ended before tensor memory is given back
     if (leader) {
       tc_commit(b_drain);
       if (!mbar_wait_bounded(b_drain, 0, 1000000000ull)) atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax
+    // a thread holds a row's 128 scores: registers of the other warps go to these
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
     const int q = warp >> 2;
     const int row = q * 128 + (warp & 3) * 32 + lane;
     const int t_in = row / p.g, i_row = row - t_in * p.g;  // token in the row tile, query head
@@ -575,8 +650,13 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
       return ok;
     };
     int done = 0, seg = 0;  // done: parities only
-    for (int64_t u = u0; u < u1; ++seg) {
-      const int count = segment(u);
+    while (share > 0) {
+      int tile;
+      const int count = take(cur, share, tile);
+      if (count == 0) {
+        if (share > 0) next(pp, cur);
+        continue;
+      }
       const int toks = tokens();
       const bool in = t_in < toks, idle = !__any_sync(0xFFFFFFFFu, in);
       const int t_row = cur.rt * pp.per + t_in;
@@ -595,7 +675,7 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
           continue;
         }
         tc_fence_after();
-        const int j0 = (cur.tile + j) * TK;
+        const int j0 = (tile + j) * TK;
         uint32_t v[TK / 32][32];  // the row's scores
 #pragma unroll
         for (int c = 0; c < TK / 32; ++c) tmem_ld32(t_s + c * 32, v[c]);
@@ -668,13 +748,11 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
       // ------------------------------------------------ end of the segment
       need(b_olast + 8 * q, seg);
       tc_fence_after();
-      const int64_t item_u = u - cur.tile;  // the item's first unit
-      const bool last_tile = cur.tile + count == cur.tiles;
-      const bool whole = cur.tile == 0 && last_tile;
-      if (tid == 0 && u + count == u1)
-        p.cuts[blockIdx.x] = make_int4(cur.first + cur.rt * pp.per, cur.h, toks * p.g, attn_cut(!last_tile, item_u >= u0));
+      const bool last_tile = tile + count == cur.tiles, whole = tile == 0 && last_tile;
+      if (tid == 0 && !last_tile)
+        p.cuts[blockIdx.x] = make_int4(cur.first + cur.rt * pp.per, cur.h, toks * p.g, attn_cut(true, tile == 0));
       constexpr int PART = ROWS * (D + 2);
-      float* part = p.ws + ((int64_t)blockIdx.x * 2 + (item_u >= u0 ? 1 : 0)) * PART;
+      float* part = p.ws + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * PART;
       const unsigned* bad = s_bad + (seg & (BAD_BUFS - 1)) * BAD_WORDS;
       unsigned any_bad = 0;
 #pragma unroll
@@ -684,6 +762,55 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
       const int64_t at = cur.first + t_row;  // the row in q, out and lse
       const float inv = in && l != 0.f ? 1.f / l : 0.f;
       uint16_t* const to16 = p.out + at * p.o_st + (int64_t)(cur.h * p.g + i_row) * p.o_sh;
+      if (whole && !any_bad && !idle) {
+        // The rows' outputs are taken out of tensor memory, which is then free for the
+        // next item, before they are stored.
+        uint32_t w[D / 2];
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(t_o + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            w[(c + i) / 2] = pack16<BF16>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_oempty + 8 * q);
+        // Four lanes exchange their rows' 32 columns, so that they store a row's 64 bytes at a time.
+        uint16_t* rows[4];
+        bool have[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          rows[k] = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)to16, (lane & 28) + k)) + (lane & 3) * 8;
+          have[k] = __shfl_sync(0xFFFFFFFFu, in && ok, (lane & 28) + k);
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t* x = w + c / 2;
+#pragma unroll
+          for (int h = 2; h > 0; h >>= 1)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!(k & h))
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t &lo = x[k * 4 + e], &hi = x[(k | h) * 4 + e];
+                  const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, lane & h ? lo : hi, h);
+                  (lane & h ? lo : hi) = y;
+                }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (have[k])
+              *reinterpret_cast<uint4*>(rows[k] + c) = make_uint4(x[k * 4], x[k * 4 + 1], x[k * 4 + 2], x[k * 4 + 3]);
+        }
+        if (ok && in && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
+        done += count;
+        ++seg;
+        if (share > 0) next(pp, cur);
+        continue;
+      }
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
@@ -751,8 +878,8 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
         part[ROWS * D + ROWS + row] = l;
       }
       done += count;
-      u += count;
-      if (u < u1) next(pp, cur);
+      ++seg;
+      if (share > 0) next(pp, cur);
     }
   }
 
@@ -765,6 +892,13 @@ __global__ void __launch_bounds__(NQ * 128 + 64 / NQ + 64, 1)
 
 template <bool BF16, int D, int NQ>
 cudaError_t prepare() {
+  if (NQ == 2) {
+    // a CTA launched with fewer registers than its groups ask for would wait for them
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, prompt_kernel<BF16, D, NQ>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < REGS_LAUNCH) return cudaErrorInvalidKernelImage;
+  }
   return cudaFuncSetAttribute(prompt_kernel<BF16, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, NQ>::BYTES);
 }
 
@@ -772,7 +906,7 @@ template <bool BF16, int D, int NQ>
 cudaError_t launch(const PromptParams& p, const void* kmap, const void* vmap, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.a.grid);
-  cfg.blockDim = dim3(NQ * 128 + 64 / NQ + 64);
+  cfg.blockDim = dim3(threads_of(NQ));
   cfg.dynamicSmemBytes = Smem<D, NQ>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute at;
