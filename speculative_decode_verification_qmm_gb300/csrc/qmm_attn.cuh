@@ -95,15 +95,12 @@ __device__ __forceinline__ float unpack16(uint16_t v) {
   if constexpr (BF16) return __uint_as_float((uint32_t)v << 16);
   return __half2float(__ushort_as_half(v));
 }
-// Whether any of the eight 16-bit values is an infinity or a NaN: exponent bits all ones.
+// Whether any of the eight 16-bit values is an infinity or a NaN: exponent bits all ones,
+// so that one more carries into the sign's place.
 template <bool BF16>
 __device__ __forceinline__ bool any_nonfinite(const uint4& v) {
-  constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || ((w[i] >> 16) & E) == E;
-  return bad;
+  constexpr uint32_t E = BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = BF16 ? 0x00800080u : 0x04000400u;
+  return (((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u;
 }
 // The same pair-wise: zero in the place of every non-finite value.
 template <bool BF16>

@@ -47,14 +47,8 @@ constexpr int BAD_BUFS = 16; // more than twice the segments that the rings hold
 constexpr int BAD_WORDS = 8; // an item's tokens after its first: at most 255
 constexpr int ITEM_WEIGHT = 3;
 
-// Two MMA warps and two loading warps beside four softmax warps; with two row tiles an MMA
-// warp and three loading warps beside eight.
-constexpr int threads_of(int NQ) { return NQ == 1 ? 256 : 384; }
-// Registers a thread with two row tiles: what three groups of four warps are launched with, and
-// what the two softmax groups and the third one go on with.
-constexpr int REGS_LAUNCH = 168, REGS_SOFTMAX = 216, REGS_OTHER = 72;
-static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * REGS_LAUNCH, "registers of a CTA");
-
+// Four softmax warps a row tile, two MMA warps, two loading warps.
+constexpr int threads_of(int NQ) { return NQ * 128 + 128; }
 template <int D, int NQ>
 struct Smem {
   static constexpr int TILE = TK * D * 2;           // one of K, V; also 128 rows of Q
@@ -65,9 +59,9 @@ struct Smem {
   static constexpr int K = Q + NQ * TILE;
   static constexpr int V = K + KS * TILE;
   static constexpr int BAR = V + VS * TILE;
-  // kfull[KS], kempty[KS], vfull[VS], vempty[VS], vland[VS], qfull, qempty, sfull[2],
-  // sfree[2], pfull[4], odone, olast[2], oempty[2], drain
-  static constexpr int NBAR = 2 * KS + 3 * VS + 16;
+  // kfull[KS], kempty[KS], vfull[VS], vempty[VS], vland[VS], sfull[2], sfree[2],
+  // pfull[4], odone[2], olast[2], oempty[2], qfull, qempty, drain
+  static constexpr int NBAR = 2 * KS + 3 * VS + 17;
   static constexpr int BAD = BAR + NBAR * 8;        // rows with non-finite V, by segment
   static constexpr int FLAG = BAD + BAD_BUFS * BAD_WORDS * 4;  // [0] abort, [1] tensor memory
   static constexpr int START = FLAG + 16;           // the CTA's share, and the cursor at its start
@@ -98,15 +92,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_t, uint32_t a_t, uint32_t b_lo
       : "memory");
 }
 
-// Bounded wait that also gives up when another role did.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint64_t lim, volatile int* abort) {
-  if (lim == 0) return false;
-  if (mbar_try_wait(bar, parity)) return true;
+// A warp's bounded wait for a phase of a barrier; it gives up too when another role did.  All
+// branches are the warp's, not a lane's: with loops of single lanes and an error path of
+// one lane behind them, a pair of cache tiles took 2,950 cycles in a model of the kernel
+// below, and takes 2,490.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t lim, volatile int* flag) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
   const long long limit = (long long)(lim < (1ull << 40) ? lim : (1ull << 40)) * 2;
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort || clock64() - t0 > limit) return false;
-  }
+  while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+    if (__any_sync(0xFFFFFFFFu, *flag || clock64() - t0 > limit)) return false;
   return true;
 }
 
@@ -174,35 +169,39 @@ __device__ __forceinline__ int tiles_of(const PromptParams& p, const Cursor& c) 
   return (c.L + (end < c.n ? end : c.n) + TK - 1) / TK;
 }
 
+// Quotients of whole numbers that mostly fit into 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The start of CTA c's share of the work, and the share's weight, for every lane of a warp.
 __device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, int64_t& left) {
-  int64_t W = 0;
+  Cursor cur{};
+  int64_t W = 0, head = 0;  // of a key/value head of the lane's sequence
+  auto look = [&](int b0) {
+    cur.L = cur.n = cur.first = 0;
+    bool ok = true;
+    if (b0 + lane < p.a.B) ok = prompt_sizes(p, b0 + lane, cur.L, cur.n, cur.first);
+    head = weight_before(p, cur.L, cur.n, (cur.n + p.per - 1) / p.per);
+    return ok;
+  };
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-    int64_t w = 0;
-    if (b0 + lane < p.a.B) {
-      int L, n, first;
-      if (!prompt_sizes(p, b0 + lane, L, n, first) && c == 0) atomicOr(p.a.status, DEV_ERR_INDEX);
-      w = weight_before(p, L, n, (n + p.per - 1) / p.per) * p.a.Hkv;
-    }
+    if (!look(b0) && c == 0) atomicOr(p.a.status, DEV_ERR_INDEX);
+    int64_t w = head * p.a.Hkv;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
     W += w;
   }
   // no CTA without a share between two that have one: the joining kernel counts on it
   const int G = W < p.a.grid ? (int)W : p.a.grid;
-  Cursor cur{};
   left = 0;
   if (c >= G) return cur;
-  const int64_t u0 = W * c / G;
-  left = W * (c + 1) / G - u0;
+  const int64_t u0 = quotient(W * c, G);
+  left = quotient(W * (c + 1), G) - u0;
   int64_t before = 0;
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-    int L = 0, n = 0, first = 0;
-    int64_t w = 0;
-    if (b0 + lane < p.a.B) {
-      prompt_sizes(p, b0 + lane, L, n, first);
-      w = weight_before(p, L, n, (n + p.per - 1) / p.per) * p.a.Hkv;
-    }
+    if (p.a.B > 32) look(b0);
+    const int64_t w = head * p.a.Hkv;
     int64_t inc = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -213,30 +212,31 @@ __device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, 
     if (past) {
       const int who = __ffs(past) - 1;
       cur.b = b0 + who;
-      cur.L = __shfl_sync(0xFFFFFFFFu, L, who);
-      cur.n = __shfl_sync(0xFFFFFFFFu, n, who);
-      cur.first = __shfl_sync(0xFFFFFFFFu, first, who);
+      cur.L = __shfl_sync(0xFFFFFFFFu, cur.L, who);
+      cur.n = __shfl_sync(0xFFFFFFFFu, cur.n, who);
+      cur.first = __shfl_sync(0xFFFFFFFFu, cur.first, who);
+      head = __shfl_sync(0xFFFFFFFFu, head, who);
       before += __shfl_sync(0xFFFFFFFFu, inc - w, who);
       break;
     }
     before += __shfl_sync(0xFFFFFFFFu, inc, 31);
   }
-  const int all = (cur.n + p.per - 1) / p.per;
-  const int64_t a_head = weight_before(p, cur.L, cur.n, all);
   const int64_t rem = u0 - before;
-  cur.h = (int)(rem / a_head);
-  const int64_t in_head = rem - cur.h * a_head;
+  cur.h = (int)quotient(rem, head);
+  const int64_t in_head = rem - cur.h * head;
   // the last row tile that begins at or before the place, 32 candidates at a time
-  int lo = 0, hi = all;
+  int lo = 0, hi = (cur.n + p.per - 1) / p.per;
+  int64_t at_lo = 0;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const bool le = at < hi && weight_before(p, cur.L, cur.n, at) <= in_head;
-    const int k = __popc(__ballot_sync(0xFFFFFFFFu, le));
+    const int64_t w = weight_before(p, cur.L, cur.n, at < hi ? at : hi);
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, at < hi && w <= in_head));
+    if (k > 0) at_lo = __shfl_sync(0xFFFFFFFFu, w, k - 1);
     lo += k * step;
     hi = hi < lo + step ? hi : lo + step;
   }
   cur.rt = lo;
-  cur.w = (int)(in_head - weight_before(p, cur.L, cur.n, lo));
+  cur.w = (int)(in_head - at_lo);
   cur.tiles = tiles_of(p, cur);
   return cur;
 }
@@ -310,47 +310,53 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   constexpr uint32_t IDESC_O = tc_idesc_n(BF16 ? 1u : 0u, D) | (1u << 16);  // B along N
   // tensor memory columns: NB times S, then O, of each row tile
   constexpr uint32_t COL_O = NB * TK;
-  constexpr uint32_t COL_Q = 256;  // of the second row tile
-  constexpr int MMA_WARP = NQ * 4, MMA_WARPS = 2 / NQ, LOAD_WARP = MMA_WARP + MMA_WARPS;
-  constexpr int Q_WARP = NQ == 2 ? LOAD_WARP + 2 : -1;  // (NQ = 1: both loading warps)
+  constexpr uint32_t COL_Q = D == 128 ? 256 : 192;  // of the second row tile
+  // With two row tiles P lies where its S did, or, heads of 64, in columns of its own: then
+  // the next S need not wait for the product of P and V, but for the softmax to have read S.
+  constexpr bool APART = NQ == 2 && D == 64;
+  constexpr uint32_t COL_P = 384;  // APART, 64 columns a row tile
+  // NQ = 1: one warp issues all Q K^T, the other all P V.  APART: each issues both for its row
+  // tile.  Else one issues everything (the commits of two would wait behind each other's
+  // products), and the other loads Q.
+  constexpr bool ONE = NQ == 2 && !APART;
+  constexpr int ISSUERS = APART ? 2 : 1;  // that use a tile of K, or of V
+  constexpr int MMA_WARP = NQ * 4, MMA_WARPS = 2, LOAD_WARP = MMA_WARP + MMA_WARPS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = smem_u32(smem);
-  const uint32_t b_kfull = base + S::BAR, b_kempty = b_kfull + S::KS * 8, b_vfull = b_kempty + S::KS * 8,
-                 b_vempty = b_vfull + S::VS * 8, b_vland = b_vempty + S::VS * 8, b_qfull = b_vland + S::VS * 8,
-                 b_qempty = b_qfull + 8, b_sfull = b_qempty + 8, b_sfree = b_sfull + 16, b_pfull = b_sfree + 16,
-                 b_odone = b_pfull + 32, b_olast = b_odone + 8, b_oempty = b_olast + 16, b_drain = b_oempty + 16;
+  // (constant distances from base: nothing to keep in registers)
+  constexpr uint32_t O_KFULL = S::BAR, O_KEMPTY = O_KFULL + S::KS * 8, O_VFULL = O_KEMPTY + S::KS * 8,
+                     O_VEMPTY = O_VFULL + S::VS * 8, O_VLAND = O_VEMPTY + S::VS * 8, O_SFULL = O_VLAND + S::VS * 8,
+                     O_SFREE = O_SFULL + 16, O_PFULL = O_SFREE + 16, O_ODONE = O_PFULL + 32, O_OLAST = O_ODONE + 16,
+                     O_OEMPTY = O_OLAST + 16, O_QFULL = O_OEMPTY + 16, O_QEMPTY = O_QFULL + 8, O_DRAIN = O_QEMPTY + 8;
   // sfull, sfree: [row tile], NQ = 1: [buffer]; pfull: [row tile][step], NQ = 1: [buffer]
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::FLAG);
   unsigned* s_bad = reinterpret_cast<unsigned*>(smem + S::BAD);
 
   if (tid == 0) {
     for (int i = 0; i < S::KS; ++i) {
-      mbar_init(b_kfull + 8 * i, 1);
-      mbar_init(b_kempty + 8 * i, 1);
+      mbar_init(base + O_KFULL + 8 * i, 1);
+      mbar_init(base + O_KEMPTY + 8 * i, ISSUERS);
     }
     for (int i = 0; i < S::VS; ++i) {
-      mbar_init(b_vfull + 8 * i, 1);
-      mbar_init(b_vempty + 8 * i, 1);
-      mbar_init(b_vland + 8 * i, 1);
+      mbar_init(base + O_VFULL + 8 * i, 1);
+      mbar_init(base + O_VEMPTY + 8 * i, ISSUERS);
+      mbar_init(base + O_VLAND + 8 * i, 1);
     }
-    mbar_init(b_qfull, NQ == 1 ? 2 : 1);
-    mbar_init(b_qempty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(b_sfull + 8 * i, 1);
-      mbar_init(b_sfree + 8 * i, 1);
-      mbar_init(b_olast + 8 * i, 1);
-      mbar_init(b_oempty + 8 * i, 4);
+      mbar_init(base + O_SFULL + 8 * i, 1);
+      mbar_init(base + O_SFREE + 8 * i, APART ? 4 : 1);
+      mbar_init(base + O_ODONE + 8 * i, 1);
+      mbar_init(base + O_OLAST + 8 * i, 1);
+      mbar_init(base + O_OEMPTY + 8 * i, 4);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(b_pfull + 8 * i, 4);
-    mbar_init(b_odone, 1);
-    mbar_init(b_drain, MMA_WARPS);
+    for (int i = 0; i < 4; ++i) mbar_init(base + O_PFULL + 8 * i, 4);
+    mbar_init(base + O_QFULL, 1);
+    mbar_init(base + O_QEMPTY, 1);
+    mbar_init(base + O_DRAIN, MMA_WARPS);
     for (int i = 0; i < BAD_BUFS * BAD_WORDS; ++i) s_bad[i] = 0;
-    s_flag[0] = 0;
-    if (base & 1023u) {
-      atomicOr(p.status, DEV_ERR_SMEM_ALIGN);
-      s_flag[0] = 1;
-    }
+    // a limit of 0 makes every wait give up
+    s_flag[0] = base & 1023u ? DEV_ERR_SMEM_ALIGN : (p.wait_limit_ns == 0 ? DEV_ERR_TIMEOUT_EMPTY : 0);
     fence_mbar_init();
   }
   if (warp == MMA_WARP) tmem_alloc(base + S::FLAG + 4, 512);
@@ -358,10 +364,9 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   // then may the joining kernel take its place.
   pdl_wait();
   pdl_trigger();
-  int64_t share;
-  Cursor cur;
   if (warp == 0) {
-    cur = begin(pp, lane, blockIdx.x, share);
+    int64_t share;
+    const Cursor cur = begin(pp, lane, blockIdx.x, share);
     if (lane == 0) {
       *reinterpret_cast<int64_t*>(smem + S::START) = share;
       *reinterpret_cast<Cursor*>(smem + S::START + 8) = cur;
@@ -370,80 +375,48 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  share = *reinterpret_cast<const int64_t*>(smem + S::START);
-  cur = *reinterpret_cast<const Cursor*>(smem + S::START + 8);
-  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
 
   if (tid == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   const uint64_t lim = p.wait_limit_ns;
-  auto fail = [&](int code) {
-    if (!s_flag[0]) atomicOr(p.status, code);
-    s_flag[0] = 1;
+  auto fail = [&](int code) { s_flag[0] = code; };  // by all lanes of a warp
+  // Each role reads the CTA's share anew, for registers of its own.
+  auto start = [&](Cursor& c) {
+    c = *reinterpret_cast<const Cursor*>(smem + S::START + 8);
+    return *reinterpret_cast<const int64_t*>(smem + S::START);
   };
-  // Tokens and rows of the cursor's row tile.
-  auto tokens = [&] {
-    const int left = cur.n - cur.rt * pp.per;
+  // Tokens of the cursor's row tile.
+  auto tokens = [&](const Cursor& c) {
+    const int left = c.n - c.rt * pp.per;
     return left < pp.per ? left : pp.per;
   };
 
-  // Rows of Q, by threads `id` of `STEP` CH; rows past the item's stay as they are, and so do
-  // their results.
-  auto load_q = [&](int id, auto step) {
-    constexpr int CH = D / 8, STEP = decltype(step)::value / CH;  // 16-byte chunks of a row, rows at a time
-    const int rows = tokens() * p.g, ch = id % CH;
-    const int dt = STEP / p.g, dh = STEP % p.g;
-    int row = id / CH, t = row / p.g, h = row % p.g;
-    const uint16_t* src = p.q + (int64_t)(cur.first + cur.rt * pp.per) * p.q_st + (int64_t)cur.h * p.g * p.q_sh + ch * 8;
-#pragma unroll 8
-    for (; row < rows; row += STEP) {
-      cp_async16(base + S::Q + (row >> 7) * S::TILE + (ch >> 3) * S::HALF + (row & 127) * 128 +
-                     (((ch & 7) ^ (row & 7)) << 4),
-                 src + t * p.q_st + h * p.q_sh, 16);
-      t += dt, h += dh;
-      if (h >= p.g) h -= p.g, ++t;
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(b_qfull);
-  };
-
-  if (warp >= MMA_WARP) {
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------------ load
+    Cursor cur;
+    int64_t share = start(cur);
     const bool is_v = warp > LOAD_WARP;
-    const uint32_t full = is_v ? b_vfull : b_kfull, empty = is_v ? b_vempty : b_kempty;
+    const uint32_t full = base + (is_v ? O_VFULL : O_KFULL), empty = base + (is_v ? O_VEMPTY : O_KEMPTY);
     const uint32_t ring = base + (is_v ? S::V : S::K);
     const int slots = is_v ? S::VS : S::KS;
     const CUtensorMap* map = is_v ? &vmap : &kmap;
     constexpr int BLOCKS = TK / 16;  // 16 rows, one tensor copy a half
     bool ok = s_flag[0] == 0;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      ok = __all_sync(0xFFFFFFFFu, ok && wait_or_abort(bar, parity, lim, s_flag));
-      if (!ok && lane == 0) fail(DEV_ERR_TIMEOUT_EMPTY);
+      if (ok && !warp_wait(bar, parity, lim, s_flag)) {
+        fail(DEV_ERR_TIMEOUT_EMPTY);
+        ok = false;
+      }
     };
     int slot = 0, round = 0, seg = 0;
     unsigned landing = 0, landed = 0;  // bits by slot: a copy counts on vland; vland's parity
     while (share > 0 && ok) {
       int tile;
       const int count = take(cur, share, tile);
-      if (count > 0) {
-        if (NQ == 1 || warp == Q_WARP) {
-          if (seg > 0) wait(b_qempty, (uint32_t)((seg - 1) & 1));
-          if (!ok) break;
-          if constexpr (NQ == 1)
-            load_q((warp - LOAD_WARP) * 32 + lane, std::integral_constant<int, 64>());
-          else
-            load_q(lane, std::integral_constant<int, 32>());
-        }
-        ++seg;
-      }
+      if (count > 0) ++seg;
       // Lane i < BLOCKS looks up the page of the tile's block i, a tile ahead.  An
       // id out of range is reported; rows of page 0 take its place.
       const int first_token = cur.rt * pp.per;
-      const int end = cur.L + first_token + tokens();  // rows that a row of the item sees
+      const int end = cur.L + first_token + tokens(cur);  // rows that a row of the item sees
       const int all_see = cur.L + first_token;         // the last row that every one sees
       int ahead = 0;
       auto lookup = [&](int j) {
@@ -457,9 +430,8 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
           }
         }
       };
-      const int copies = NQ == 2 && warp == Q_WARP ? 0 : count;
-      if (copies > 0) lookup(tile);
-      for (int j = 0; j < copies; ++j) {
+      if (count > 0) lookup(tile);
+      for (int j = 0; j < count; ++j) {
         const int j0 = (tile + j) * TK;
         const int pid = ahead;
         if (j + 1 < count) lookup(tile + j + 1);
@@ -468,7 +440,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         const int left = end - j0 < TK ? end - j0 : TK;  // rows of the tile that count
         const int blocks = (left + 15) / 16;
         const bool masked = is_v && j0 + TK - 1 > all_see;
-        const uint32_t bar = (masked ? b_vland : full) + 8 * slot, dst = ring + slot * S::TILE;
+        const uint32_t bar = (masked ? base + O_VLAND : full) + 8 * slot, dst = ring + slot * S::TILE;
         landing = masked ? landing | 1u << slot : landing & ~(1u << slot);
         if (lane == 0) mbar_arrive_expect_tx(bar, blocks * 16 * D * 2);
         __syncwarp();
@@ -499,35 +471,89 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       }
       if (share > 0) next(pp, cur);
     }
-    cp_async_wait<0>();
     // Tensor copies in flight land before the CTA leaves: the last tile of every
     // slot.  Always: another role can give up after this one's last look at the flag.
     for (int i = 0; i < slots; ++i) {
       const int rounds = i < slot ? round + 1 : round;
       if (rounds > 0 && lane == 0) {
         const bool on_land = landing >> i & 1u;
-        if (!mbar_wait_bounded(on_land ? b_vland + 8 * i : full + 8 * i, on_land ? landed >> i & 1u : (rounds - 1) & 1,
+        if (!mbar_wait_bounded(on_land ? base + O_VLAND + 8 * i : full + 8 * i, on_land ? landed >> i & 1u : (rounds - 1) & 1,
                                1000000000ull))
           atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
       }
     }
-  } else {
+  } else if (warp >= MMA_WARP) {
     // ------------------------------------------------------------ MMA issue
     // The warp stays together and one elected lane issues (see qmm_attn_tc.cu).
     uint32_t leader;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
-    const int who = warp - MMA_WARP;  // NQ = 1: 0 Q K^T, 1 P V
+    Cursor cur_next;
+    int64_t share = start(cur_next);
+    // What the products' operands come from is made uniform: they then live in uniform
+    // registers.
+    auto uniform = [](uint32_t x) { return __reduce_max_sync(0xFFFFFFFFu, x); };
+    const uint32_t tmem = uniform((uint32_t)s_flag[1]);
+    const int who = (int)uniform((uint32_t)(warp - MMA_WARP));
     bool ok = s_flag[0] == 0;
     auto need = [&](uint32_t bar, int phase) {
-      if (ok && !__all_sync(0xFFFFFFFFu, wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag))) {
-        if (leader) fail(DEV_ERR_TIMEOUT_FULL);
+      if (!warp_wait(bar, (uint32_t)(phase & 1), lim, s_flag)) {
+        fail(DEV_ERR_TIMEOUT_FULL);
         ok = false;
       }
       return ok;
     };
-    // S of row tile q and the K tile in `slot`, into column d
-    auto product_s = [&](int q, int slot, uint32_t d) {
-      const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + slot * S::TILE);
+    // Requests row tile q's rows of Q of the item at c; rows past the item's stay as they are,
+    // and so do their results.
+    auto request_q = [&](int q, const Cursor& c) {
+      constexpr int CH = D / 8, STEP = 32 / CH;  // 16-byte chunks of a row, rows at a time
+      const int left = tokens(c) * p.g - q * 128, rows = left < 128 ? left : 128, ch = lane % CH;
+      const int dt = STEP / p.g, dh = STEP % p.g;
+      int row = lane / CH, t = (q * 128 + row) / p.g, h = (q * 128 + row) % p.g;
+      const uint16_t* src = p.q + (int64_t)(c.first + c.rt * pp.per) * p.q_st + (int64_t)c.h * p.g * p.q_sh + ch * 8;
+#pragma unroll 4
+      for (; row < rows; row += STEP) {
+        cp_async16(base + S::Q + q * S::TILE + (ch >> 3) * S::HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                   src + t * p.q_st + h * p.q_sh, 16);
+        t += dt, h += dh;
+        if (h >= p.g) h -= p.g, ++t;
+      }
+      cp_async_commit();
+    };
+    auto q_landed = [&] {
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    int n = 0, seg = 0;         // tiles and segments so far (parities, and whether there was one)
+    int slot = 0, round = 0;    // of the tile of K
+    int vslot = 0, vround = 0;  // of the tile of V
+    // Barriers and columns of row tile q and tile n
+    auto s_index = [&](int q, int n) { return (uint32_t)(NQ == 2 ? q : n & 1); };
+    auto s_phase = [&](int n) { return NQ == 2 ? n : n >> 1; };
+    auto s_column = [&](int q, int n) { return tmem + (NQ == 2 ? q * COL_Q : (n & 1) * TK); };
+    // The segments one after the other; the next one is looked up ahead, for its Q.
+    int count = 0, count_next = 0;
+    auto look_ahead = [&] {
+      count_next = 0;
+      while (share > 0 && count_next == 0) {  // (a share can end before an item's first tile)
+        if (cur_next.w == cur_next.tiles + ITEM_WEIGHT) next(pp, cur_next);
+        int from;
+        count_next = take(cur_next, share, from);
+      }
+      count_next = (int)uniform((uint32_t)count_next);
+    };
+    // S of row tile q and the segment's cache tile j, the call's n-th; `takes` and `leaves`: is
+    // the first, the last to use the tile of K
+    auto issue_s = [&](int q, int j, int n, bool takes, bool leaves) {
+      if (ONE && j == 0 && takes && !need(base + O_QFULL, seg)) return false;
+      if (!ONE && j == 0) q_landed();
+      if (takes && !need(base + O_KFULL + 8 * slot, round)) return false;
+      // S goes where S, or P, of the last tile but NB lies: until that one was read (APART), or
+      // its product with V has ended
+      if (n >= NB && !need(base + O_SFREE + 8 * s_index(q, n), s_phase(n) - 1)) return false;
+      // (operands are worked out before the branch on the lane: in it, each would go to a
+      // uniform register for every product anew, three times as slow)
+      const uint32_t a = desc_lo(base + S::Q + q * S::TILE), b = desc_lo(base + S::K + slot * S::TILE), d = s_column(q, n);
       tc_fence_after();
       if (leader) {
 #pragma unroll
@@ -536,116 +562,101 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
           mma_ss(d, a + o, b + o, IDESC_S, kk > 0);
         }
       }
-    };
-    // O of row tile q += a step's P (at column a) times its rows of the V tile in `slot`
-    auto product_o = [&](int q, int slot, int sub, uint32_t a, bool first) {
-      const uint32_t d = tmem + q * COL_Q + COL_O;
-      const uint32_t b = desc_lo_mn(base + S::V + slot * S::TILE + sub * SW * 128, S::HALF);
-      tc_fence_after();
-      if (leader) {
-        mma_ts(d, a, b, IDESC_O, !first);
-#pragma unroll
-        for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
+      if (leader) tc_commit(base + O_SFULL + 8 * s_index(q, n));
+      if (leader && leaves) tc_commit(base + O_KEMPTY + 8 * slot);
+      if (leader && ONE && leaves && j + 1 == count) tc_commit(base + O_QEMPTY);
+      if (leaves && ++slot == S::KS) slot = 0, ++round;
+      if (!ONE && j + 1 == count && count_next > 0) {  // Q makes way for the next one
+        if (!need(base + O_SFULL + 8 * s_index(q, n), s_phase(n))) return false;
+        request_q(q, cur_next);
       }
+      return true;
     };
-    int n = 0, seg = 0;         // tiles and segments so far (parities, and whether there was one)
-    int slot = 0, round = 0;    // of the tile of K or V
-    int vslot = 0, vround = 0;  // of the tile of V, where one warp issues both
-    while (share > 0 && ok) {
-      int tile;
-      const int count = take(cur, share, tile);
-      if (count == 0) {  // (a share can end before an item's first tile)
-        if (share > 0) next(pp, cur);
-        continue;
-      }
-      if constexpr (NQ == 2) {
-        // O += P V of a row tile, then S of its next cache tile, then the other row tile
-        for (int j = -1; j < count && ok; ++j) {
-          if (j < 0 && !need(b_qfull, seg)) break;
-          for (int q = 0; q < 2 && ok; ++q) {
-            if (j >= 0) {
-              if (q == 0 && !need(b_vfull + 8 * vslot, vround)) break;
-              if (j == 0 && seg > 0 && !need(b_oempty + 8 * q, seg - 1)) break;
+    // O of row tile q += P times V, in the steps that P comes in
+    auto issue_o = [&](int q, int j, int n, bool takes, bool leaves) {
+      if (takes && !need(base + O_VFULL + 8 * vslot, vround)) return false;
+      if (j == 0 && seg > 0 && !need(base + O_OEMPTY + 8 * q, seg - 1)) return false;
 #pragma unroll
-              for (int sub = 0; sub < SUB; ++sub) {
-                if (!need(b_pfull + 8 * (2 * q + sub), n)) break;
-                product_o(q, vslot, sub, tmem + q * COL_Q + sub * (SW / 2), j == 0 && sub == 0);
-              }
-              if (!ok) break;
-              if (leader) tc_commit(b_sfree + 8 * q);
-              if (leader && j + 1 == count) tc_commit(b_olast + 8 * q);
-            }
-            if (j + 1 < count) {
-              if (q == 0 && !need(b_kfull + 8 * slot, round)) break;
-              // S goes where P of the tile before lies, until its products have ended
-              const int before = j >= 0 ? n : n - 1;
-              if (before >= 0 && !need(b_sfree + 8 * q, before)) break;
-              product_s(q, slot, tmem + q * COL_Q);
-              if (leader) tc_commit(b_sfull + 8 * q);
-            }
-          }
-          if (!ok) break;
-          if (j >= 0) {
-            if (leader) tc_commit(b_vempty + 8 * vslot);
-            if (++vslot == S::VS) vslot = 0, ++vround;
-            ++n;
-          }
-          if (j + 1 < count) {
-            if (leader) tc_commit(b_kempty + 8 * slot);
-            if (leader && j + 2 == count) tc_commit(b_qempty);
-            if (++slot == S::KS) slot = 0, ++round;
-          }
+      for (int sub = 0; sub < SUB; ++sub) {
+        if (!need(base + O_PFULL + 8 * (NQ == 2 ? 2 * q + sub : n & 1), s_phase(n))) return false;
+        const uint32_t a = (APART ? tmem + COL_P + q * 64 : s_column(q, n)) + sub * (SW / 2), d = tmem + q * COL_Q + COL_O;
+        const uint32_t b = desc_lo_mn(base + S::V + vslot * S::TILE + sub * SW * 128, S::HALF);
+        tc_fence_after();
+        if (leader) {
+          mma_ts(d, a, b, IDESC_O, sub > 0 || j > 0);
+#pragma unroll
+          for (int kk = 1; kk < SW / 16; ++kk) mma_ts(d, a + kk * 8, b + kk * (2048 >> 4), IDESC_O, 1);
         }
-      } else if (who == 0) {
-        if (!need(b_qfull, seg)) break;
-        for (int j = 0; j < count; ++j, ++n) {
-          if (!need(b_kfull + 8 * slot, round)) break;
-          // its S held P of two tiles ago until the product of that was done
-          if (n >= 2 && !need(b_sfree + 8 * (n & 1), (n >> 1) - 1)) break;
-          product_s(0, slot, tmem + (n & 1) * TK);
-          if (leader) tc_commit(b_sfull + 8 * (n & 1));
-          if (leader) tc_commit(b_kempty + 8 * slot);
-          if (leader && j + 1 == count) tc_commit(b_qempty);
-          if (++slot == S::KS) slot = 0, ++round;
+      }
+      if (!ONE && leader) tc_commit(base + O_ODONE + 8 * q);
+      if (!APART && leader) tc_commit(base + O_SFREE + 8 * s_index(q, n));
+      if (leader && j + 1 == count) tc_commit(base + O_OLAST + 8 * q);
+      if (leader && leaves) tc_commit(base + O_VEMPTY + 8 * vslot);
+      if (leaves && ++vslot == S::VS) vslot = 0, ++vround;
+      return true;
+    };
+    look_ahead();
+    if (!ONE && (NQ == 2 || who == 0) && count_next > 0) request_q(who, cur_next);
+    while (count_next > 0 && ok) {
+      count = count_next;
+      if constexpr (ONE) {
+        if (who == 0) {
+          // P V of a row tile, S of its next cache tile, then the other row tile
+          for (int j = -1; j < count && ok; ++j) {
+            for (int q = 0; q < 2 && ok; ++q) {
+              if (j >= 0 && !issue_o(q, j, n, q == 0, q == 1)) break;
+              if (j + 1 < count) issue_s(q, j + 1, j < 0 ? n : n + 1, q == 0, q == 1);
+            }
+            if (j >= 0) ++n;
+          }
+        } else {
+          // Q, when the products with the last one have ended
+          if (seg > 0 && !need(base + O_QEMPTY, seg - 1)) break;
+          for (int q = 0; q < 2; ++q) request_q(q, cur_next);
+          q_landed();
+          if (lane == 0) mbar_arrive(base + O_QFULL);
         }
+        look_ahead();
       } else {
-        for (int j = 0; j < count; ++j, ++n) {
-          if (!need(b_vfull + 8 * slot, round) || !need(b_pfull + 8 * (n & 1), n >> 1)) break;
-          if (j == 0 && seg > 0 && !need(b_oempty, seg - 1)) break;
-          product_o(0, slot, 0, tmem + (n & 1) * TK, j == 0);
-          if (leader) tc_commit(b_odone);
-          if (leader) tc_commit(b_sfree + 8 * (n & 1));
-          if (leader && j + 1 == count) tc_commit(b_olast);
-          if (leader) tc_commit(b_vempty + 8 * slot);
-          if (++slot == S::VS) slot = 0, ++round;
+        look_ahead();
+        if constexpr (NQ == 1) {
+          for (int j = 0; j < count && ok; ++j, ++n)
+            if (who == 0)
+              issue_s(0, j, n, true, true);
+            else
+              issue_o(0, j, n, true, true);
+        } else if (issue_s(who, 0, n, true, true)) {
+          // the next S first: its place is free long before P is there
+          for (int j = 0; j < count; ++j, ++n) {
+            if (j + 1 < count && !issue_s(who, j + 1, n + 1, true, true)) break;
+            if (!issue_o(who, j, n, true, true)) break;
+          }
         }
       }
       ++seg;
-      if (share > 0) next(pp, cur);
     }
+    cp_async_wait<0>();
     // all MMAs of the CTA have ended before tensor memory is given back
     if (leader) {
-      tc_commit(b_drain);
-      if (!mbar_wait_bounded(b_drain, 0, 1000000000ull)) atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
+      tc_commit(base + O_DRAIN);
+      if (!mbar_wait_bounded(base + O_DRAIN, 0, 1000000000ull)) atomicOr(p.status, DEV_ERR_TIMEOUT_DRAIN);
     }
-  }
   } else {
     // ------------------------------------------------------------ softmax
-    // a thread holds a row's 128 scores: registers of the other warps go to these
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+    Cursor cur;
+    int64_t share = start(cur);
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
     const int q = warp >> 2;
     const int row = q * 128 + (warp & 3) * 32 + lane;
     const int t_in = row / p.g, i_row = row - t_in * p.g;  // token in the row tile, query head
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + q * COL_Q;
     const uint32_t t_o = tl + COL_O;
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = s_flag[0] == 0;
     auto need = [&](uint32_t bar, int phase) {
-      if (ok) {
-        const bool got = __all_sync(0xFFFFFFFFu, wait_or_abort(bar, (uint32_t)(phase & 1), lim, s_flag));
-        if (!got) {
-          if (lane == 0) fail(DEV_ERR_TIMEOUT_FULL);
-          ok = false;
-        }
+      if (ok && !warp_wait(bar, (uint32_t)(phase & 1), lim, s_flag)) {
+        fail(DEV_ERR_TIMEOUT_FULL);
+        ok = false;
       }
       return ok;
     };
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         if (share > 0) next(pp, cur);
         continue;
       }
-      const int toks = tokens();
+      const int toks = tokens(cur);
       const bool in = t_in < toks, idle = !__any_sync(0xFFFFFFFFu, in);
       const int t_row = cur.rt * pp.per + t_in;
       const int all_see = cur.L + cur.rt * pp.per;
@@ -666,12 +677,16 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       for (int j = 0; j < count; ++j) {
         const int n = done + j;
         const uint32_t t_s = tl + (NB == 2 ? (n & 1) * TK : 0);
-        const uint32_t pfull = b_pfull + 8 * (NQ == 2 ? 2 * q : n & 1);
-        need(b_sfull + 8 * (NQ == 2 ? q : n & 1), NQ == 2 ? n : n >> 1);
+        const uint32_t pfull = base + O_PFULL + 8 * (NQ == 2 ? 2 * q : n & 1);
+        need(base + O_SFULL + 8 * (NQ == 2 ? q : n & 1), NQ == 2 ? n : n >> 1);
         if (!ok) continue;
         if (idle) {  // no row of the warp is the item's: whatever P is, nobody looks
-          if (lane == 0)
+          if (lane == 0 && APART) mbar_arrive(base + O_SFREE + 8 * q);
+          // (the next S can be there before the other warps have handed over this P)
+          if (APART && j > 0 && !need(base + O_ODONE + 8 * q, n - 1)) continue;
+          if (lane == 0) {
             for (int sub = 0; sub < SUB; ++sub) mbar_arrive(pfull + 8 * sub);
+          }
           continue;
         }
         tc_fence_after();
@@ -680,6 +695,11 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
 #pragma unroll
         for (int c = 0; c < TK / 32; ++c) tmem_ld32(t_s + c * 32, v[c]);
         tmem_wait_ld();
+        if constexpr (APART) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(base + O_SFREE + 8 * q);
+        }
         if (j0 + TK - 1 > all_see) {
           const int last = sees - j0;
 #pragma unroll
@@ -688,6 +708,18 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
             for (int i = 0; i < 32; ++i)
               if (c * 32 + i > last) v[c][i] = 0xFF800000u;  // -inf
         }
+        // P of 32 columns, in pairs, and their sum
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, m2 = make_float2(0.f, 0.f);
+        auto powers = [&](int c, uint32_t (&w)[16]) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float2 e = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), c2, m2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
+            w[i / 2] = pack16<BF16>(e.x, e.y);
+          }
+        };
         float mx;
         {
           float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -699,16 +731,19 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
           mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         }
         mx = mx * p.scale_log2 - ATTN_BASE_BELOW<BF16>;
-        // (rows past the item's hold anything and must not decide for the others)
-        if (__any_sync(0xFFFFFFFFu, in && mx > m + 8.f)) {
+        // P's place, and O, are free when the last product with V has ended: with P in the
+        // place of S, this S was computed after it
+        const bool grows = __any_sync(0xFFFFFFFFu, in && mx > m + 8.f);  // (rows past the item's hold anything)
+        if ((APART || (NQ == 1 && grows)) && j > 0) {
+          if (!need(base + O_ODONE + 8 * q, n - 1)) continue;
+          tc_fence_after();
+        }
+        if (grows) {
           const float mn = fmaxf(m, mx);
           const float a = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;
           l *= a;
           if (j > 0) {
-            // NQ = 2: this S was computed after the last product with V had ended
-            if (NQ == 1 && !need(b_odone, n - 1)) continue;
-            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               uint32_t x[16];
@@ -720,21 +755,13 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
             }
           }
         }
-        const float mb = m == -INFINITY ? 0.f : m;
-        const float2 c2 = make_float2(p.scale_log2, p.scale_log2), m2 = make_float2(-mb, -mb);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        m2.x = m2.y = m == -INFINITY ? 0.f : -m;
+        const uint32_t t_p = APART ? tmem + ((uint32_t)((warp & 3) * 32) << 16) + COL_P + q * 64 : t_s;
 #pragma unroll
         for (int c = 0; c < TK / 32; ++c) {
           uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float2 e = fma2(make_float2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])), c2, m2);
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-            sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], e);
-            w[i / 2] = pack16<BF16>(e.x, e.y);
-          }
-          tmem_st16(t_s + c * 16, w);
+          powers(c, w);
+          tmem_st16(t_p + c * 16, w);
           if ((c + 1) % (SW / 32) == 0) {
             tmem_wait_st();
             tc_fence_before();
@@ -746,7 +773,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       }
 
       // ------------------------------------------------ end of the segment
-      need(b_olast + 8 * q, seg);
+      need(base + O_OLAST + 8 * q, seg);
       tc_fence_after();
       const bool last_tile = tile + count == cur.tiles, whole = tile == 0 && last_tile;
       if (tid == 0 && !last_tile)
@@ -777,7 +804,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_oempty + 8 * q);
+        if (lane == 0) mbar_arrive(base + O_OEMPTY + 8 * q);
         // Four lanes exchange their rows' 32 columns, so that they store a row's 64 bytes at a time.
         uint16_t* rows[4];
         bool have[4];
@@ -870,7 +897,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_oempty + 8 * q);
+      if (lane == 0) mbar_arrive(base + O_OEMPTY + 8 * q);
       if (whole) {
         if (ok && in && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
       } else if (ok) {
@@ -884,21 +911,15 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   }
 
   __syncthreads();
+  if (tid == 0 && s_flag[0]) atomicOr(p.status, s_flag[0]);
   if (warp == MMA_WARP) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(__shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0), 512);
   }
 }
 
 template <bool BF16, int D, int NQ>
 cudaError_t prepare() {
-  if (NQ == 2) {
-    // a CTA launched with fewer registers than its groups ask for would wait for them
-    cudaFuncAttributes at;
-    const cudaError_t e = cudaFuncGetAttributes(&at, prompt_kernel<BF16, D, NQ>);
-    if (e != cudaSuccess) return e;
-    if (at.numRegs < REGS_LAUNCH) return cudaErrorInvalidKernelImage;
-  }
   return cudaFuncSetAttribute(prompt_kernel<BF16, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, NQ>::BYTES);
 }
 
