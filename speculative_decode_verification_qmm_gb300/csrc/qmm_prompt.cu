@@ -129,10 +129,24 @@ __device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a,
   return sum;
 }
 
+// The same for m = TK and a power of two.
+__device__ __forceinline__ int64_t floor_sum_pow2(uint32_t n, uint32_t a, uint32_t b) {
+  if (a >= TK) return ((int64_t)n * (n - 1) >> 1) * (a / TK) + (int64_t)n * (b / TK);
+  const int sa = 31 - __clz(a), sk = 31 - __clz(TK / a);
+  auto steps = [&](uint32_t x) {  // sum of floor(i a / TK) over i < x
+    const int64_t q = x >> sk;
+    return (q * (q - 1) >> 1 << sk) + q * (x & ((1u << sk) - 1));
+  };
+  const uint32_t c = b >> sa;
+  return steps(n + c) - steps(c);
+}
+
 // Cache tiles of the first `count` row tiles of a sequence with L earlier and n new rows.
 __device__ __forceinline__ int64_t units_before(int L, int n, int per, int count) {
-  const int full = n / per < count ? n / per : count;
-  int64_t u = floor_sum((uint32_t)full, TK, (uint32_t)per, (uint32_t)L + per + TK - 1);
+  const bool pow2 = (per & (per - 1)) == 0;
+  const int most = pow2 ? n >> (31 - __clz(per)) : n / per, full = most < count ? most : count;
+  const uint32_t b = (uint32_t)L + per + TK - 1;
+  int64_t u = pow2 ? floor_sum_pow2((uint32_t)full, (uint32_t)per, b) : floor_sum((uint32_t)full, TK, (uint32_t)per, b);
   if (count > full) u += ((int64_t)L + n + TK - 1) / TK;
   return u;
 }
@@ -269,32 +283,41 @@ __device__ __forceinline__ void next(const PromptParams& p, Cursor& c) {
 }
 
 // Rows r0 .. left - 1 of a V tile without what is not finite (each row that has some is told
-// to `found`), and zeros in the rows from `left` on, by a warp.
+// to `found`), and zeros in the rows from `left` on, by a warp.  (Batches whose branch is
+// the warp's: with one for each chunk a tile's 128 rows took 10,000 cycles.)
 template <bool BF16, int D, typename F>
 __device__ __forceinline__ void clean(uint32_t tile, int r0, int left, int lane, F found) {
-  constexpr int CH = D / 8, HALF = TK * 128, BATCH = 8;
-  const int ch = lane % CH, end = left * CH;
-  auto place = [&](int id) {
-    const int row = id / CH;
-    return tile + (ch >> 3) * HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-  };
+  constexpr int CH = D / 8, HALF = TK * 128, BATCH = 8, ROWS = 32 * BATCH / CH;  // rows of a batch
+  const int ch = lane % CH;
+  auto place = [&](int row) { return tile + (ch >> 3) * HALF + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
   auto put = [](uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
   };
-  for (int id = r0 * CH + lane; id < end; id += 32 * BATCH) {
+  int row = r0 + lane / CH;
+  for (int first = r0; first < left; first += ROWS, row += ROWS) {
     uint4 v[BATCH];
+    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (id + 32 * i < end) v[i] = lds128(place(id + 32 * i));
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (id + 32 * i < end && any_nonfinite<BF16>(v[i])) {
-        put(place(id + 32 * i), make_uint4(zero_nonfinite<BF16>(v[i].x), zero_nonfinite<BF16>(v[i].y),
-                                           zero_nonfinite<BF16>(v[i].z), zero_nonfinite<BF16>(v[i].w)));
-        found((id + 32 * i) / CH);
+    for (int i = 0; i < BATCH; ++i) {
+      // (past the end the last row again)
+      v[i] = lds128(place(row + i * (32 / CH) < left ? row + i * (32 / CH) : left - 1));
+      bad |= any_nonfinite<BF16>(v[i]);
+    }
+    if (__any_sync(0xFFFFFFFFu, bad)) {
+#pragma unroll 1
+      for (int i = 0; i < BATCH; ++i) {
+        const int r = row + i * (32 / CH);
+        if (r >= left) break;
+        const uint4 x = lds128(place(r));
+        if (!any_nonfinite<BF16>(x)) continue;
+        put(place(r), make_uint4(zero_nonfinite<BF16>(x.x), zero_nonfinite<BF16>(x.y), zero_nonfinite<BF16>(x.z),
+                                 zero_nonfinite<BF16>(x.w)));
+        found(r);
       }
+      __syncwarp();
+    }
   }
-  for (int id = (left > 0 ? left : 0) * CH + lane; id < TK * CH; id += 32) put(place(id), make_uint4(0u, 0u, 0u, 0u));
+  for (int r = left + lane / CH; r < TK; r += 32 / CH) put(place(r), make_uint4(0u, 0u, 0u, 0u));
 }
 
 template <bool BF16, int D, int NQ>
@@ -602,12 +625,12 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       if constexpr (ONE) {
         if (who == 0) {
           // P V of a row tile, S of its next cache tile, then the other row tile
-          for (int j = -1; j < count && ok; ++j) {
-            for (int q = 0; q < 2 && ok; ++q) {
-              if (j >= 0 && !issue_o(q, j, n, q == 0, q == 1)) break;
-              if (j + 1 < count) issue_s(q, j + 1, j < 0 ? n : n + 1, q == 0, q == 1);
-            }
-            if (j >= 0) ++n;
+          if (!issue_s(0, 0, n, true, false) || !issue_s(1, 0, n, false, true)) break;
+          for (int j = 0; j < count; ++j, ++n) {
+            if (!issue_o(0, j, n, true, false)) break;
+            if (j + 1 < count && !issue_s(0, j + 1, n + 1, true, false)) break;
+            if (!issue_o(1, j, n, false, true)) break;
+            if (j + 1 < count && !issue_s(1, j + 1, n + 1, false, true)) break;
           }
         } else {
           // Q, when the products with the last one have ended
@@ -794,13 +817,14 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         // next item, before they are stored.
         uint32_t w[D / 2];
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(t_o + c, v);
+        for (int c = 0; c < D; c += 64) {
+          uint32_t v[2][32];
+          tmem_ld32(t_o + c, v[0]);
+          tmem_ld32(t_o + c + 32, v[1]);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            w[(c + i) / 2] = pack16<BF16>(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+          for (int i = 0; i < 64; i += 2)
+            w[(c + i) / 2] = pack16<BF16>(__uint_as_float(v[i >> 5][i & 31]) * inv, __uint_as_float(v[i >> 5][(i & 31) + 1]) * inv);
         }
         tc_fence_before();
         __syncwarp();
