@@ -450,7 +450,7 @@ int qmm_cache_copy(qmm_cache_t h, int n, const int32_t* src, const int32_t* dst,
  * qmm_rotate is the turning alone, for the nodes of a drafted tree, whose keys and
  * values qmm_tree_attention writes. */
 #define QMM_ROPE_MAX_DIM 1024
-#define QMM_ROPE_MAX_HEADS 65536
+#define QMM_ROPE_MAX_HEADS 8192
 #define QMM_CACHE_MAX_ROWS (1 << 24) /* of one call */
 
 typedef enum { QMM_ROPE_HALF = 0, QMM_ROPE_INTERLEAVED = 1 } qmm_rope_layout;

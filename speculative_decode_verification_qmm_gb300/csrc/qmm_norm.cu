@@ -5,13 +5,17 @@
 // norm(x) = x rsqrt(mean x^2 + eps), or of x - mean x: the mean first, then the mean
 // square of the differences, which does not cancel.
 //
-// A group of threads (a warp for short rows, else the CTA) holds a whole row in
-// registers, E entries a thread, so that every input is read once and r' is
-// normalised unrounded.
-// What bounds it: memory for many rows, the chain load -> sum -> load for few.
+// Rows of up to SHORT entries: a warp each, straight from memory.  Longer ones: a CTA each,
+// which holds a whole row in registers, E entries a thread, so that r' is normalised
+// unrounded; the inputs of its next rows are on their way into shared memory meanwhile.
+// They are copied in whole 16-byte groups, which at a row's ends may hold other values,
+// so that rows need no alignment.
+// What bounds it: memory for many rows, the chain load -> sum -> sum for few.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "qmm.h"
 #include "qmm_attn.cuh"
@@ -38,42 +42,54 @@ struct NormParams {
   float eps, scale, inv_n;
 };
 
-// Entries of a thread: vectors of V, a group's threads side by side.
-template <int E, int V>
-__device__ __forceinline__ void load_row(int dt, const void* base, int64_t at, int t, int threads, int n, float (&x)[E]) {
+constexpr int SHORT = 512;
+constexpr int MAX_DEVICES = 64;
+
+// Entries of a thread: vectors of V, a group's threads side by side.  FRESH: read once.
+template <int E, int V, bool FRESH>
+__device__ __forceinline__ void load_row(int dt, const void* row, int t, int threads, int n, float (&x)[E]) {
   if (dt == QMM_DT_F32) {
-    const float* p = static_cast<const float*>(base) + at;
+    const float* p = static_cast<const float*>(row);
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
       const int k = (i * threads + t) * V;
       if constexpr (V == 4) {
-        const float4 v = k < n ? *reinterpret_cast<const float4*>(p + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* q = reinterpret_cast<const float4*>(p + k);
+        const float4 v = k < n ? (FRESH ? __ldcs(q) : *q) : make_float4(0.f, 0.f, 0.f, 0.f);
         x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
       } else {
-        x[i] = k < n ? p[k] : 0.f;
+        x[i] = k < n ? (FRESH ? __ldcs(p + k) : p[k]) : 0.f;
       }
     }
     return;
   }
-  const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-  const bool bf = dt == QMM_DT_BF16;
-  auto wide = [&](uint32_t v) { return bf ? unpack16<true>((uint16_t)v) : unpack16<false>((uint16_t)v); };
+  const uint16_t* p = static_cast<const uint16_t*>(row);
+  uint32_t w[(E + 1) / 2];
 #pragma unroll
   for (int i = 0; i < E / V; ++i) {
     const int k = (i * threads + t) * V;
     if constexpr (V == 4) {
-      const uint2 v = k < n ? *reinterpret_cast<const uint2*>(p + k) : make_uint2(0u, 0u);
-      x[4 * i] = wide(v.x), x[4 * i + 1] = wide(v.x >> 16), x[4 * i + 2] = wide(v.y), x[4 * i + 3] = wide(v.y >> 16);
+      const uint2* q = reinterpret_cast<const uint2*>(p + k);
+      const uint2 v = k < n ? (FRESH ? __ldcs(q) : *q) : make_uint2(0u, 0u);
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
     } else {
-      x[i] = k < n ? wide(p[k]) : 0.f;
+      const uint32_t v = k < n ? (FRESH ? __ldcs(p + k) : p[k]) : 0;
+      w[i / 2] = i & 1 ? w[i / 2] | v << 16 : v;
     }
+  }
+  if (dt == QMM_DT_BF16) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = unpack16<true>((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = unpack16<false>((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]));
   }
 }
 
 template <int E, int V>
-__device__ __forceinline__ void store_row(int dt, void* base, int64_t at, int t, int threads, int n, const float (&x)[E]) {
+__device__ __forceinline__ void store_row(int dt, void* row, int t, int threads, int n, const float (&x)[E]) {
   if (dt == QMM_DT_F32) {
-    float* p = static_cast<float*>(base) + at;
+    float* p = static_cast<float*>(row);
 #pragma unroll
     for (int i = 0; i < E / V; ++i) {
       const int k = (i * threads + t) * V;
@@ -85,112 +101,199 @@ __device__ __forceinline__ void store_row(int dt, void* base, int64_t at, int t,
     }
     return;
   }
-  uint16_t* p = static_cast<uint16_t*>(base) + at;
-  const bool bf = dt == QMM_DT_BF16;
-  auto pack = [&](float a, float b) { return bf ? pack16<true>(a, b) : pack16<false>(a, b); };
+  uint16_t* p = static_cast<uint16_t*>(row);
+  uint32_t w[(E + 1) / 2];
+#pragma unroll
+  for (int i = 0; i < E; i += 2)
+    w[i / 2] = dt == QMM_DT_BF16 ? pack16<true>(x[i], i + 1 < E ? x[i + 1] : 0.f) : pack16<false>(x[i], i + 1 < E ? x[i + 1] : 0.f);
 #pragma unroll
   for (int i = 0; i < E / V; ++i) {
     const int k = (i * threads + t) * V;
     if (k >= n) continue;
     if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(p + k) = make_uint2(pack(x[4 * i], x[4 * i + 1]), pack(x[4 * i + 2], x[4 * i + 3]));
+      *reinterpret_cast<uint2*>(p + k) = make_uint2(w[2 * i], w[2 * i + 1]);
     else
-      p[k] = (uint16_t)pack(x[i], 0.f);
+      p[k] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
   }
 }
 
-template <bool WARP, int E, int V>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s_sum[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int threads = WARP ? 32 : blockDim.x, t = WARP ? lane : threadIdx.x;
-  const int64_t rows = WARP ? (int64_t)gridDim.x * (blockDim.x / 32) : gridDim.x;
-  auto sum_all = [&](float v) {
+__device__ __forceinline__ int size_of(int dt) { return dt == QMM_DT_F32 ? 4 : 2; }
+__device__ __forceinline__ const char* row_of(const void* base, int64_t m, int64_t ld, int dt) {
+  return static_cast<const char*>(base) + m * ld * size_of(dt);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    if constexpr (!WARP) {
-      __syncthreads();  // the sums before were read
-      if (lane == 0) s_sum[warp] = v;
-      __syncthreads();
-      v = lane < (int)(blockDim.x / 32) ? s_sum[lane] : 0.f;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    }
-    return v;
-  };
-  // x <- norm(x) w + b; entries past the row stay zero
-  auto normed = [&](float (&x)[E], const float* w, const float* b) {
-    if (p.centered) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) s += x[i];
-      const float mean = sum_all(s) * p.inv_n;
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (((i / V) * threads + t) * V + i % V < p.N) x[i] -= mean;
-    }
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+// x <- norm(x) w + b; entries past the row stay zero.
+template <int E, int V, typename S>
+__device__ __forceinline__ void normed(const NormParams& p, float (&x)[E], const float* w, const float* b, int t, int threads,
+                                       S sum_all) {
+  if (p.centered) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(x[i], x[i], s);
-    const float f = rsqrtf(fmaf(sum_all(s), p.inv_n, p.eps));
-    float wv[E];
-    load_row<E, V>(QMM_DT_F32, w, 0, t, threads, p.N, wv);
+    for (int i = 0; i < E; ++i) s += x[i];
+    const float mean = sum_all(s) * p.inv_n;
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = x[i] * f * wv[i];
-    if (b) {
-      load_row<E, V>(QMM_DT_F32, b, 0, t, threads, p.N, wv);
+    for (int i = 0; i < E; ++i)
+      if (((i / V) * threads + t) * V + i % V < p.N) x[i] -= mean;
+  }
+  float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] += wv[i];
+  for (int i = 0; i < E; ++i) s = fmaf(x[i], x[i], s);
+  float wv[E];
+  load_row<E, V, false>(QMM_DT_F32, w, t, threads, p.N, wv);
+  const float f = rsqrtf(fmaf(sum_all(s), p.inv_n, p.eps));
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = x[i] * f * wv[i];
+  if (b) {
+    load_row<E, V, false>(QMM_DT_F32, b, t, threads, p.N, wv);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] += wv[i];
+  }
+}
+
+// One row, from where y, the residual and the gate lie.
+template <int E, int V, bool FRESH, typename S>
+__device__ __forceinline__ void one_row(const NormParams& p, int64_t m, const void* y, const void* res, const void* gate, int t,
+                                        int threads, S sum_all) {
+  float r[E];
+  load_row<E, V, FRESH>(p.res_dt, res, t, threads, p.N, r);
+  if (p.y) {
+    float z[E];
+    load_row<E, V, FRESH>(p.y_dt, y, t, threads, p.N, z);
+    if (p.post_weight) normed<E, V>(p, z, p.post_weight, p.post_bias, t, threads, sum_all);
+    if (p.gate) {
+      float g[E];
+      load_row<E, V, false>(QMM_DT_F32, gate, t, threads, p.N, g);
+#pragma unroll
+      for (int i = 0; i < E; ++i) z[i] *= g[i];
     }
+#pragma unroll
+    for (int i = 0; i < E; ++i) r[i] = fmaf(p.scale, z[i], r[i]);
+    store_row<E, V>(p.res_dt, const_cast<char*>(row_of(p.res_out, m, p.ld_res_out, p.res_dt)), t, threads, p.N, r);
+  }
+  if (p.out) {
+    normed<E, V>(p, r, p.weight, p.bias, t, threads, sum_all);
+    store_row<E, V>(p.out_dt, const_cast<char*>(row_of(p.out, m, p.ld_out, p.out_dt)), t, threads, p.N, r);
+  }
+}
+
+// Short rows: a warp each.
+template <int E, int V>
+__global__ void __launch_bounds__(256) norm_short_kernel(const __grid_constant__ NormParams p) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < p.M; m += (int64_t)gridDim.x * 8)
+    one_row<E, V, true>(p, m, row_of(p.y, m, p.ld_y, p.y_dt), row_of(p.res, m, p.ld_res, p.res_dt),
+                        row_of(p.gate, m, p.ld_gate, QMM_DT_F32), lane, 32, warp_sum);
+}
+
+// Longer rows: a CTA each, `stages` of them in shared memory; 0: straight from memory.
+template <int E, int V>
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams p, int stages, int stage_bytes) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float s_sum[2][32];
+  const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5;
+  int turn = 0;
+  // (sums alternate between two places: a barrier after the writes is enough)
+  auto sum_all = [&](float v) {
+    v = warp_sum(v);
+    if (lane == 0) s_sum[turn][warp] = v;
+    __syncthreads();
+    v = warp_sum(lane < threads >> 5 ? s_sum[turn][lane] : 0.f);
+    turn ^= 1;
+    return v;
   };
-  for (int64_t m = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + warp : blockIdx.x; m < p.M; m += rows) {
-    float r[E];
-    load_row<E, V>(p.res_dt, p.res, m * p.ld_res, t, threads, p.N, r);
-    if (p.y) {
-      float z[E];
-      load_row<E, V>(p.y_dt, p.y, m * p.ld_y, t, threads, p.N, z);
-      if (p.post_weight) normed(z, p.post_weight, p.post_bias);
-      if (p.gate) {
-        float g[E];
-        load_row<E, V>(QMM_DT_F32, p.gate, m * p.ld_gate, t, threads, p.N, g);
-#pragma unroll
-        for (int i = 0; i < E; ++i) z[i] *= g[i];
-      }
-#pragma unroll
-      for (int i = 0; i < E; ++i) r[i] = fmaf(p.scale, z[i], r[i]);
-      store_row<E, V>(p.res_dt, p.res_out, m * p.ld_res_out, t, threads, p.N, r);
+  const int y_room = p.y ? (p.N * size_of(p.y_dt) + 31) & ~15 : 0, r_room = (p.N * size_of(p.res_dt) + 31) & ~15;
+  // where a row begins behind the boundary that its copy starts from
+  auto skew = [](const char* row) { return (int)((uintptr_t)row & 15); };
+  auto request = [&](int64_t m, int stage) {
+    if (m < p.M) {
+      const uint32_t to = smem_u32(smem) + stage * stage_bytes;
+      auto copy = [&](uint32_t dst, const char* row, int bytes) {
+        const int groups = (skew(row) + bytes + 15) >> 4;
+        for (int c = t; c < groups; c += threads) cp_async16(dst + c * 16, row - skew(row) + c * 16, 16);
+      };
+      if (p.y) copy(to, row_of(p.y, m, p.ld_y, p.y_dt), p.N * size_of(p.y_dt));
+      copy(to + y_room, row_of(p.res, m, p.ld_res, p.res_dt), p.N * size_of(p.res_dt));
+      if (p.gate && p.ld_gate) copy(to + y_room + r_room, row_of(p.gate, m, p.ld_gate, QMM_DT_F32), p.N * 4);
     }
-    if (p.out) {
-      normed(r, p.weight, p.bias);
-      store_row<E, V>(p.out_dt, p.out, m * p.ld_out, t, threads, p.N, r);
+    cp_async_commit();
+  };
+  int64_t ahead = blockIdx.x;
+  for (int s = 0; s + 1 < stages; ++s, ahead += gridDim.x) request(ahead, s);
+  int stage = 0;
+  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    const char *y = row_of(p.y, m, p.ld_y, p.y_dt), *res = row_of(p.res, m, p.ld_res, p.res_dt),
+               *gate = row_of(p.gate, m, p.ld_gate, QMM_DT_F32);
+    if (stages) {
+      // the row has come, and the last one's place is free
+      if (stages == 3)
+        cp_async_wait<1>();
+      else if (stages == 2)
+        cp_async_wait<0>();
+      else
+        cp_async_wait<2>();
+      __syncthreads();
+      request(ahead, stage == 0 ? stages - 1 : stage - 1);
+      ahead += gridDim.x;
+      const char* from = smem + stage * stage_bytes;
+      y = from + skew(y);
+      res = from + y_room + skew(res);
+      if (p.ld_gate) gate = from + y_room + r_room + skew(gate);
+      if (++stage == stages) stage = 0;
     }
+    one_row<E, V, false>(p, m, y, res, gate, t, threads, sum_all);
   }
 }
 
 template <int V>
-cudaError_t launch(const NormParams& p, int sms, cudaStream_t st) {
-  if (p.N <= 1024) {
-    const int64_t need = (p.M + 7) / 8, most = 8ll * sms;
-    const unsigned grid = (unsigned)(need < most ? need : most);
-    if (p.N <= 128)
-      norm_kernel<true, 4, V><<<grid, 256, 0, st>>>(p);
-    else if (p.N <= 512)
-      norm_kernel<true, 16, V><<<grid, 256, 0, st>>>(p);
-    else
-      norm_kernel<true, 32, V><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
-  }
-  const int E = p.N <= 8192 ? 8 : (p.N <= 16384 ? 16 : 32);
-  const int threads = ((p.N + E - 1) / E + 31) / 32 * 32;
-  const int64_t most = 2048ll / threads * sms * (E == 8 ? 1 : 1);
-  const unsigned grid = (unsigned)(p.M < most ? p.M : most);
-  if (E == 8)
-    norm_kernel<false, 8, V><<<grid, threads, 0, st>>>(p);
-  else if (E == 16)
-    norm_kernel<false, 16, V><<<grid, threads, 0, st>>>(p);
+cudaError_t launch_short(const NormParams& p, int sms, cudaStream_t st) {
+  const int64_t need = (p.M + 7) / 8, most = 8ll * sms;
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  if (p.N <= 128)
+    norm_short_kernel<4, V><<<grid, 256, 0, st>>>(p);
+  else if (p.N <= 256)
+    norm_short_kernel<8, V><<<grid, 256, 0, st>>>(p);
   else
-    norm_kernel<false, 32, V><<<grid, threads, 0, st>>>(p);
+    norm_short_kernel<16, V><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();
+}
+
+template <int E, int V>
+cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) {
+  const int threads = ((p.N + E - 1) / E + 31) / 32 * 32;
+  const int ys = p.y_dt == QMM_DT_F32 ? 4 : 2, rs = p.res_dt == QMM_DT_F32 ? 4 : 2;
+  const int stage = (p.y ? (p.N * ys + 31) & ~15 : 0) + ((p.N * rs + 31) & ~15) + (p.gate && p.ld_gate ? (p.N * 4 + 31) & ~15 : 0);
+  // CTAs that an SM's registers allow (64 a thread), and two to four stages of shared memory each
+  constexpr int SMEM = 220 * 1024;
+  int ctas = 1024 / threads;
+  while (ctas > 1 && SMEM / ctas < 2 * stage + 1024) --ctas;
+  int stages = (SMEM / ctas - 1024) / stage;
+  stages = stages > 4 ? 4 : (stages < 2 ? 0 : stages);
+  const int64_t most = (int64_t)ctas * sms;
+  if (p.M <= most) stages = 0;  // a row alone has no next one to wait for
+  const unsigned grid = (unsigned)(p.M < most ? p.M : most);
+  if (stages) {
+    static std::atomic<bool> set[MAX_DEVICES];  // once for a device
+    if (dev >= MAX_DEVICES || !set[dev].load(std::memory_order_relaxed)) {
+      const cudaError_t e = cudaFuncSetAttribute(norm_kernel<E, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+      if (e != cudaSuccess) return e;
+      if (dev < MAX_DEVICES) set[dev].store(true, std::memory_order_relaxed);
+    }
+  }
+  norm_kernel<E, V><<<grid, threads, stages * stage, st>>>(p, stages, stage);
+  return cudaGetLastError();
+}
+
+template <int V>
+cudaError_t launch(const NormParams& p, int dev, int sms, cudaStream_t st) {
+  if (p.N <= SHORT) return launch_short<V>(p, sms, st);
+  if (p.N <= 2048) return launch_long<8, V>(p, dev, sms, st);
+  return p.N <= 16384 ? launch_long<16, V>(p, dev, sms, st) : launch_long<32, V>(p, dev, sms, st);
 }
 
 }  // namespace
@@ -237,6 +340,6 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
   // vectors of four where every one of them lies on its boundary
   const bool wide = !((p.N | p.ld_res | p.ld_y | p.ld_res_out | p.ld_out | p.ld_gate) & 3) && !(res & (4 * rs - 1)) &&
                     !(y & (4 * ys - 1)) && !(out & (4 * os - 1)) && !(f32 & 15);
-  const cudaError_t e = wide ? launch<4>(p, sms, (cudaStream_t)stream) : launch<1>(p, sms, (cudaStream_t)stream);
+  const cudaError_t e = wide ? launch<4>(p, dev, sms, (cudaStream_t)stream) : launch<1>(p, dev, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? QMM_OK : host_cuda_fail(e);
 }

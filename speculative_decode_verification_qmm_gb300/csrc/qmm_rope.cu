@@ -9,10 +9,10 @@
 // position 131,071 would be off by 0.008).  Its upper 32 bits, rounded, go to
 // sincospi; what they lose is below 2^-25 turns.
 //
-// Work.  A CTA takes the heads of one row, or a share of them where there are few
-// rows: its threads work out the row's sines and cosines once, for all heads,
-// and then each turns vectors of V dimensions.  Loads are issued before the angles
-// are worked out.
+// Work.  A unit is V dimensions of a head and the V that they are paired with.  A CTA takes
+// up to 256 units of up to 16 rows: its threads work out the rows' sines and cosines once,
+// for all heads, and each thread keeps its unit and walks the rows, a few of them in
+// flight, the first ones requested before the angles are worked out.
 // What bounds it: memory.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -27,36 +27,39 @@ namespace qmm {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_PAIRS = QMM_ROPE_MAX_DIM / 2;
-constexpr int AHEAD = 4;  // units of a thread whose loads are in flight
-
-template <int DT>
-struct Elem {
-  using type = uint16_t;
-};
-template <>
-struct Elem<QMM_DT_F32> {
-  using type = float;
-};
+constexpr int MAX_ROWS = 16;      // of a CTA
+constexpr int MAX_ANGLES = 1024;  // of a CTA
+static_assert(MAX_ANGLES >= QMM_ROPE_MAX_DIM / 2, "a row's angles");
 
 template <int DT, int V>
 __device__ __forceinline__ void load_vec(const void* base, int64_t at, float (&x)[V]) {
   if constexpr (DT == QMM_DT_F32) {
     const float* p = static_cast<const float*>(base) + at;
-    if constexpr (V == 4) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
+    if constexpr (V == 1) {
       x[0] = __ldcs(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(p + i));
+        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+      }
     }
   } else {
+    constexpr bool BF = DT == QMM_DT_BF16;
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if constexpr (V == 4) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
-      x[0] = unpack16<DT == QMM_DT_BF16>((uint16_t)v.x), x[1] = unpack16<DT == QMM_DT_BF16>((uint16_t)(v.x >> 16));
-      x[2] = unpack16<DT == QMM_DT_BF16>((uint16_t)v.y), x[3] = unpack16<DT == QMM_DT_BF16>((uint16_t)(v.y >> 16));
+    if constexpr (V == 1) {
+      x[0] = unpack16<BF>(__ldcs(p));
     } else {
-      x[0] = unpack16<DT == QMM_DT_BF16>(*p);
+      uint32_t w[V / 2];
+      if constexpr (V == 8) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+        w[0] = v.x, w[1] = v.y;
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) x[2 * i] = unpack16<BF>((uint16_t)w[i]), x[2 * i + 1] = unpack16<BF>((uint16_t)(w[i] >> 16));
     }
   }
 }
@@ -65,24 +68,33 @@ template <int DT, int V>
 __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&x)[V]) {
   if constexpr (DT == QMM_DT_F32) {
     float* p = static_cast<float*>(base) + at;
-    if constexpr (V == 4)
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    else
+    if constexpr (V == 1) {
       *p = x[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    }
   } else {
+    constexpr bool BF = DT == QMM_DT_BF16;
     uint16_t* p = static_cast<uint16_t*>(base) + at;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(p) =
-          make_uint2(pack16<DT == QMM_DT_BF16>(x[0], x[1]), pack16<DT == QMM_DT_BF16>(x[2], x[3]));
+    if constexpr (V == 1)
+      *p = (uint16_t)pack16<BF>(x[0], 0.f);
+    else if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]));
     else
-      *p = (uint16_t)pack16<DT == QMM_DT_BF16>(x[0], 0.f);
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]), pack16<BF>(x[4], x[5]), pack16<BF>(x[6], x[7]));
   }
 }
 
-// A unit of a head: V dimensions and, where they are turned, the V that they are
-// paired with.  Units of a head, in order: the m / V turned ones (with V = 1 single
-// pairs in either layout), then the rest, V dimensions each.  Interleaved with V = 4:
-// two pairs in one vector, which has no second one.
+// Units of a head, in order: the m / V turned ones (with V = 1 single pairs in either
+// layout), then the rest, V dimensions each.  Interleaved with V > 1: V / 2 pairs in one
+// vector, which has no second one.
+template <int V>
+__host__ __device__ __forceinline__ int units_of(const RopeParams& p) {
+  return V > 1 && !p.half ? p.D / V : p.m / V + (p.D - 2 * p.m) / V;
+}
+
 template <int V>
 __device__ __forceinline__ void unit_place(const RopeParams& p, int unit, int& first, int& second, int& pair, bool& turn) {
   if (V > 1 && !p.half) {
@@ -100,135 +112,146 @@ __device__ __forceinline__ void unit_place(const RopeParams& p, int unit, int& f
   }
 }
 
+// grid: groups of `rows` rows, times groups of THREADS units.
 template <int SRC, int DST, int V, bool PACKED>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 s_cs[MAX_PAIRS];
+__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeParams p, int rows) {
+  constexpr int U = V == 8 ? 2 : 4;  // rows in flight
+  __shared__ float2 s_cs[MAX_ANGLES];
+  __shared__ int64_t s_pool[MAX_ROWS];  // PACKED: the row's place in a pool, -1: none
+  __shared__ int s_pos[MAX_ROWS];
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  int b = 0, i = 0;          // sequence, row in it
-  int64_t pool_at = 0;       // of the row, in a pool
-  int pos;
-  if constexpr (PACKED) {
-    // the sequence that the row is of; a row behind the last one is left alone
-    int lo = 0, hi = p.B;
-    while (lo < hi) {  // the number of sequences that end at or before the row
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.starts + mid + 1) <= row) lo = mid + 1;
-      else hi = mid;
-    }
-    if (lo >= p.B || row < __ldg(p.starts + lo)) return;
-    b = lo;
-    i = (int)(row - __ldg(p.starts + b));
-    const int L = __ldg(p.lens + b);
-    const int64_t at = (int64_t)L + i;
-    if (L < 0 || at >= ((int64_t)p.table_width << p.page_shift)) {
-      if (tid == 0) atomicOr(p.status, DEV_ERR_INDEX);
-      return;
-    }
-    const int page = __ldg(p.table + b * p.ld_table + (at >> p.page_shift));
-    if (page < 0 || page >= p.n_pages) {
-      if (tid == 0) atomicOr(p.status, DEV_ERR_INDEX);
-      return;
-    }
-    pool_at = page * p.page_stride + (at & ((1 << p.page_shift) - 1)) * p.D;
-    pos = p.positions ? __ldg(p.positions + row) : (int)at;
-  } else {
-    b = (int)(row / p.T);
-    i = (int)(row - (int64_t)b * p.T);
-    pos = __ldg(p.positions + row);
+  const int64_t row0 = (int64_t)blockIdx.x * rows;
+  const int n = p.rows - row0 < rows ? (int)(p.rows - row0) : rows;
+  const int units = units_of<V>(p), total = p.heads * units;
+  const int u = blockIdx.y * THREADS + tid;
+  const bool mine = u < total;
+  int h = u / units, first = 0, second = -1, pair = 0, part = 0;
+  bool turn = false;
+  if (mine) {
+    unit_place<V>(p, u - h * units, first, second, pair, turn);
+    while (h >= p.part[part].heads) h -= p.part[part].heads, ++part;
   }
-  const int units = V > 1 && !p.half ? p.D / V : p.m / V + (p.D - 2 * p.m) / V;
-  // a unit of a head that is not turned is the same places, copied
-  const int total = p.heads * units, step = gridDim.y * THREADS;
-  bool ready = p.m == 0;
-  for (int u0 = blockIdx.y * THREADS + tid; __syncthreads_or(u0 < total); u0 += step * AHEAD) {
-    float x[AHEAD][V], y[AHEAD][V];
+  const RopeHeads& t = p.part[part];
+  turn = turn && t.turned;
+  const char* src = static_cast<const char*>(t.src) + (h * t.s_head + first) * (SRC == QMM_DT_F32 ? 4 : 2);
+  char* dst = static_cast<char*>(t.dst) + (h * t.d_head + first) * (DST == QMM_DT_F32 ? 4 : 2);
+  const int64_t s_seq = PACKED ? 0 : t.s_seq, s_row = t.s_row, d_seq = PACKED ? 0 : t.d_seq, d_row = t.d_row;
+  const bool pool = PACKED && t.pool;
+  second = second < 0 ? -1 : second - first;
+  // sequence and row in it, of the rows that are loaded and of those that are stored
+  int lb = 0, li = 0;
+  if (!PACKED) lb = (int)(row0 / p.T), li = (int)(row0 - (int64_t)lb * p.T);
+  int sb = lb, si = li;
+  float x[U][V], y[U][V];
+  auto load = [&](int r0) {
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int u = u0 + k * step;
-      if (u >= total) continue;
-      int h = u / units, first, second, pair;
-      bool turn;
-      unit_place<V>(p, u - h * units, first, second, pair, turn);
-      int part = 0;
-      while (h >= p.part[part].heads) h -= p.part[part].heads, ++part;
-      const RopeHeads& t = p.part[part];
-      const int64_t at = (PACKED ? row * t.s_row : b * t.s_seq + i * t.s_row) + h * t.s_head;
-      load_vec<SRC, V>(t.src, at + first, x[k]);
-      if (second >= 0) load_vec<SRC, V>(t.src, at + second, y[k]);
+    for (int k = 0; k < U; ++k) {
+      if (!mine || r0 + k >= n) continue;
+      const int64_t at = PACKED ? (row0 + r0 + k) * s_row : lb * s_seq + li * s_row;
+      load_vec<SRC, V>(src, at, x[k]);
+      if (second >= 0) load_vec<SRC, V>(src, at + second, y[k]);
+      if (!PACKED && ++li == p.T) li = 0, ++lb;
     }
-    if (!ready) {
-      for (int j = tid; j < p.m; j += THREADS) {
-        const uint64_t w = (uint64_t)(int64_t)pos * __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + j);
-        const int frac = (int)((w + 0x80000000ull) >> 32);
-        float s, c;
-        sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2 / 2^32: half turns
-        s_cs[j] = make_float2(c * p.amplitude, s * p.amplitude);
+  };
+  load(0);
+  if (tid < n) {
+    const int64_t row = row0 + tid;
+    if constexpr (PACKED) {
+      // the sequence that the row is of; a row behind the last one is left alone
+      int lo = 0, hi = p.B;
+      while (lo < hi) {  // the number of sequences that end at or before the row
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.starts + mid + 1) <= row) lo = mid + 1;
+        else hi = mid;
       }
-      __syncthreads();
-      ready = true;
+      int64_t place = -1, at = 0;
+      if (lo < p.B && row >= __ldg(p.starts + lo)) {
+        const int L = __ldg(p.lens + lo);
+        at = (int64_t)L + (row - __ldg(p.starts + lo));
+        int page = -1;
+        if (L >= 0 && at < ((int64_t)p.table_width << p.page_shift)) page = __ldg(p.table + lo * p.ld_table + (at >> p.page_shift));
+        if (page >= 0 && page < p.n_pages)
+          place = page * p.page_stride + (at & ((1 << p.page_shift) - 1)) * p.D;
+        else if (blockIdx.y == 0)
+          atomicOr(p.status, DEV_ERR_INDEX);
+      }
+      s_pool[tid] = place;
+      s_pos[tid] = p.positions ? __ldg(p.positions + row) : (int)at;
+    } else {
+      s_pos[tid] = __ldg(p.positions + row);
     }
+  }
+  __syncthreads();
+  for (int j = tid; j < n * p.m; j += THREADS) {
+    const int r = j / p.m;
+    const uint64_t w = (uint64_t)(int64_t)s_pos[r] * __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + (j - r * p.m));
+    const int frac = (int)((w + 0x80000000ull) >> 32);
+    float s, c;
+    sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2 / 2^32: half turns
+    s_cs[j] = make_float2(c * p.amplitude, s * p.amplitude);
+  }
+  __syncthreads();
+  for (int r0 = 0; r0 < n; r0 += U) {
+    if (r0 > 0) load(r0);
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int u = u0 + k * step;
-      if (u >= total) continue;
-      int h = u / units, first, second, pair;
-      bool turn;
-      unit_place<V>(p, u - h * units, first, second, pair, turn);
-      int part = 0;
-      while (h >= p.part[part].heads) h -= p.part[part].heads, ++part;
-      const RopeHeads& t = p.part[part];
-      if (turn && t.turned) {
+    for (int k = 0; k < U; ++k) {
+      if (!mine || r0 + k >= n) continue;
+      if (turn) {
+        const float2* cs = s_cs + (r0 + k) * p.m + pair;
         if (second >= 0) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float2 cs = s_cs[pair + e];
             const float a = x[k][e], c = y[k][e];
-            x[k][e] = a * cs.x - c * cs.y;
-            y[k][e] = a * cs.y + c * cs.x;
+            x[k][e] = a * cs[e].x - c * cs[e].y;
+            y[k][e] = a * cs[e].y + c * cs[e].x;
           }
         } else {
 #pragma unroll
           for (int e = 0; e + 1 < V; e += 2) {
-            const float2 cs = s_cs[pair + e / 2];
             const float a = x[k][e], c = x[k][e + 1];
-            x[k][e] = a * cs.x - c * cs.y;
-            x[k][e + 1] = a * cs.y + c * cs.x;
+            x[k][e] = a * cs[e / 2].x - c * cs[e / 2].y;
+            x[k][e + 1] = a * cs[e / 2].y + c * cs[e / 2].x;
           }
         }
       }
-      const int64_t at = (PACKED ? (t.pool ? pool_at : row * t.d_row) : b * t.d_seq + i * t.d_row) + h * t.d_head;
-      store_vec<DST, V>(t.dst, at + first, x[k]);
-      if (second >= 0) store_vec<DST, V>(t.dst, at + second, y[k]);
+      int64_t at = PACKED ? (row0 + r0 + k) * d_row : sb * d_seq + si * d_row;
+      if (!PACKED && ++si == p.T) si = 0, ++sb;
+      if constexpr (PACKED) {
+        const int64_t place = s_pool[r0 + k];
+        if (place < 0) continue;
+        if (pool) at = place;
+      }
+      store_vec<DST, V>(dst, at, x[k]);
+      if (second >= 0) store_vec<DST, V>(dst, at + second, y[k]);
     }
   }
 }
 
 template <int SRC, int DST, int V, bool PACKED>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t st) {
-  const int units = V > 1 && !p.half ? p.D / V : p.m / V + (p.D - 2 * p.m) / V;
-  const int64_t total = (int64_t)p.heads * units;
-  // shares of a row: one unit a thread where the rows alone do not fill the GPU
-  int64_t most = (total + THREADS - 1) / THREADS, y = (4ll * sms + p.rows - 1) / p.rows;
-  if (y > most) y = most;
-  if (y > 65535) y = 65535;
-  if (y < 1) y = 1;
-  rope_kernel<SRC, DST, V, PACKED><<<dim3((unsigned)p.rows, (unsigned)y), THREADS, 0, st>>>(p);
+  const int64_t total = (int64_t)p.heads * units_of<V>(p), groups = (total + THREADS - 1) / THREADS;
+  // rows of a CTA: as many as leave eight CTAs to an SM
+  int64_t rows = p.rows * groups / (8ll * sms);
+  const int most = p.m > 0 && MAX_ANGLES / p.m < MAX_ROWS ? MAX_ANGLES / p.m : MAX_ROWS;
+  rows = rows < 1 ? 1 : (rows > most ? most : rows);
+  rope_kernel<SRC, DST, V, PACKED><<<dim3((unsigned)((p.rows + rows - 1) / rows), (unsigned)groups), THREADS, 0, st>>>(p, (int)rows);
   return cudaGetLastError();
 }
 
 template <int SRC, int DST, bool PACKED>
 cudaError_t launch_v(const RopeParams& p, int sms, cudaStream_t st) {
-  // Vectors of four where every one of them lies on its boundary.
+  // Vectors of eight or four where every one of them lies on its boundary, of 16 bytes at most.
   const int s = SRC == QMM_DT_F32 ? 4 : 2, d = DST == QMM_DT_F32 ? 4 : 2;
   int64_t bits = p.D | (p.half ? p.m : 2 * p.m);
-  bool wide = true;
+  uintptr_t src = 0, dst = 0;
   for (int i = 0; i < p.parts; ++i) {
     const RopeHeads& t = p.part[i];
     bits |= t.s_seq | t.s_row | t.s_head | t.d_seq | t.d_row | t.d_head;
-    wide = wide && !((uintptr_t)t.src & (4 * s - 1)) && !((uintptr_t)t.dst & (4 * d - 1));
+    src |= (uintptr_t)t.src, dst |= (uintptr_t)t.dst;
   }
-  return wide && !(bits & 3) ? launch<SRC, DST, 4, PACKED>(p, sms, st) : launch<SRC, DST, 1, PACKED>(p, sms, st);
+  if (!(bits & 7) && !((src | dst) & 15)) return launch<SRC, DST, 8, PACKED>(p, sms, st);
+  if (!(bits & 3) && !(src & (4 * s - 1)) && !(dst & (4 * d - 1))) return launch<SRC, DST, 4, PACKED>(p, sms, st);
+  return launch<SRC, DST, 1, PACKED>(p, sms, st);
 }
 
 template <int SRC>

@@ -6,14 +6,17 @@
 // included: x -> x / r (x > 0) or x r where v was seen; x - f c - p [c > 0] + bias; -inf
 // where the grammar bit is 0.
 //
-// A CTA takes a range of the vocabulary of one sequence and walks its nodes: the
-// counts, prompt bits and biases of the range are read once, for all nodes.  Which
-// nodes lie on a node's path is one bit each of a 64-bit word; a node's tokens that
-// fall into the range, mostly none, are added to the counts.
+// A CTA takes a range of the vocabulary of one sequence and walks its nodes, the scores of
+// AHEAD of them in flight: the counts, prompt bits and biases of the range are read once, for
+// all nodes, as two factors and a term for each entry.  Which nodes lie on a node's path
+// is one bit each of a 64-bit word; where a node's tokens fall into the range, which few
+// do, their entries are worked out anew.
 // What bounds it: memory.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "qmm.h"
 #include "qmm_attn.cuh"
@@ -26,6 +29,7 @@ constexpr int MAX_T = QMM_TREE_MAX_T;
 constexpr int THREADS = 256;
 constexpr int E = 8;  // entries of a thread
 constexpr int RANGE = THREADS * E;
+constexpr int AHEAD = 2;
 
 struct AdjustParams {
   const void* scores;
@@ -47,38 +51,60 @@ struct AdjustParams {
   int per;  // nodes of a CTA
 };
 
-// Entry e of thread t lies at RANGE's place place(e, t): 8 side by side, or every 256th.
+// Entry e of thread t lies at the range's place(e, t): 8 side by side, or every 32nd of a
+// warp's 256, for which no alignment is needed.
 template <bool WIDE>
 __device__ __forceinline__ int place(int e, int t) {
-  return WIDE ? t * E + e : e * THREADS + t;
+  return WIDE ? t * E + e : (t >> 5) * 32 * E + e * 32 + (t & 31);
 }
 
+// A thread's eight scores as they are in memory (fp32: 8 words, else 4), and their values.
+template <int DT>
+struct Raw {
+  static constexpr int WORDS = DT == QMM_DT_F32 ? 8 : 4;
+  uint32_t w[WORDS];
+};
+
 template <int DT, bool WIDE>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t left, float (&x)[E]) {
+__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t left, Raw<DT>& r) {
   const int t = threadIdx.x;
-  if constexpr (WIDE && DT == QMM_DT_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + t * E);
-    const bool a = t * E < left, b = t * E + 4 < left;
-    const float4 u = a ? __ldcs(p) : make_float4(0.f, 0.f, 0.f, 0.f), v = b ? __ldcs(p + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-  } else if constexpr (WIDE) {
-    const uint4 v = t * E < left ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + t * E))
-                                 : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (WIDE) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + (at + t * E) * (DT == QMM_DT_F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = unpack16<DT == QMM_DT_BF16>((uint16_t)w[i]);
-      x[2 * i + 1] = unpack16<DT == QMM_DT_BF16>((uint16_t)(w[i] >> 16));
+    for (int i = 0; i < Raw<DT>::WORDS / 4; ++i) {
+      const uint4 v = t * E + i * 4 < left ? __ldcs(p + i) : make_uint4(0u, 0u, 0u, 0u);
+      r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
     }
   } else {
+    const int k = place<false>(0, t);
+    const char* p = static_cast<const char*>(base) + (at + k) * (DT == QMM_DT_F32 ? 4 : 2);
+    auto get = [&](auto whole) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int k = place<false>(e, t);
-      if constexpr (DT == QMM_DT_F32)
-        x[e] = k < left ? __ldcs(static_cast<const float*>(base) + at + k) : 0.f;
-      else
-        x[e] = k < left ? unpack16<DT == QMM_DT_BF16>(static_cast<const uint16_t*>(base)[at + k]) : 0.f;
-    }
+      for (int e = 0; e < E; ++e) {
+        const bool in = decltype(whole)::value || k + 32 * e < left;
+        if constexpr (DT == QMM_DT_F32) {
+          r.w[e] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p) + 32 * e) : 0u;
+        } else {
+          const uint32_t x = in ? __ldcs(reinterpret_cast<const uint16_t*>(p) + 32 * e) : 0;
+          r.w[e / 2] = e & 1 ? r.w[e / 2] | x << 16 : x;
+        }
+      }
+    };
+    if (left >= RANGE)
+      get(std::true_type());
+    else
+      get(std::false_type());
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void values(const Raw<DT>& r, float (&x)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if constexpr (DT == QMM_DT_F32)
+      x[e] = __uint_as_float(r.w[e]);
+    else
+      x[e] = unpack16<DT == QMM_DT_BF16>((uint16_t)(e & 1 ? r.w[e / 2] >> 16 : r.w[e / 2]));
   }
 }
 
@@ -95,37 +121,49 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int64_t left, con
       __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at + t * E),
              make_uint4(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]), pack16<BF>(x[4], x[5]), pack16<BF>(x[6], x[7])));
   } else {
+    const int k = place<false>(0, t);
+    char* p = static_cast<char*>(base) + (at + k) * (DT == QMM_DT_F32 ? 4 : 2);
+    auto put = [&](auto whole) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int k = place<false>(e, t);
-      if (k >= left) continue;
-      if constexpr (DT == QMM_DT_F32)
-        static_cast<float*>(base)[at + k] = x[e];
-      else
-        static_cast<uint16_t*>(base)[at + k] = (uint16_t)pack16<DT == QMM_DT_BF16>(x[e], 0.f);
-    }
+      for (int e = 0; e < E; ++e) {
+        if (!decltype(whole)::value && k + 32 * e >= left) continue;
+        if constexpr (DT == QMM_DT_F32)
+          __stcs(reinterpret_cast<float*>(p) + 32 * e, x[e]);
+        else
+          __stcs(reinterpret_cast<uint16_t*>(p) + 32 * e, (uint16_t)pack16<DT == QMM_DT_BF16>(x[e], 0.f));
+      }
+    };
+    if (left >= RANGE)
+      put(std::true_type());
+    else
+      put(std::false_type());
   }
 }
 
-// The bits of a thread's eight entries in words that begin with bit 0 of the range
-// (a range is whole words).
+// The bits of a thread's eight entries in words that begin with bit 0 of the range (a
+// range is whole words): WIDE, a byte of a word; else lane e has the word of the warp's
+// entries e (bits_of tells them apart).
 template <bool WIDE>
-__device__ __forceinline__ uint32_t bits8(const uint32_t* words, int64_t left) {
+__device__ __forceinline__ uint32_t load_bits(const uint32_t* words, int64_t left) {
   const int t = threadIdx.x;
   if constexpr (WIDE) return t * E < left ? __ldg(words + t / 4) >> (8 * (t & 3)) & 255u : 0u;
+  const int word = (t >> 5) * E + (t & 31);
+  return (t & 31) < E && word * 32 < left ? __ldg(words + word) : 0u;
+}
+template <bool WIDE>
+__device__ __forceinline__ uint32_t bits_of(uint32_t loaded) {
+  if constexpr (WIDE) return loaded;
   uint32_t r = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int k = place<false>(e, t);
-    if (k < left) r |= (__ldg(words + k / 32) >> (k & 31) & 1u) << e;
-  }
+  for (int e = 0; e < E; ++e) r |= (__shfl_sync(0xFFFFFFFFu, loaded, e) >> (threadIdx.x & 31) & 1u) << e;
   return r;
 }
 
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(THREADS) adjust_kernel(const __grid_constant__ AdjustParams p) {
-  __shared__ int s_token[MAX_T];               // place in the range, or -1
-  __shared__ unsigned long long s_path[MAX_T];  // the nodes on a node's path that lie in the range
+__global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constant__ AdjustParams p) {
+  __shared__ int s_token[MAX_T];                // place in the range
+  __shared__ unsigned long long s_path[MAX_T];  // the nodes of a node's path whose tokens lie in the range
+  __shared__ int s_up[MAX_T];
   const int t = threadIdx.x, b = blockIdx.y;
   const int64_t v0 = (int64_t)blockIdx.x * RANGE, left = p.V - v0;
   int n = p.T;
@@ -140,7 +178,21 @@ __global__ void __launch_bounds__(THREADS) adjust_kernel(const __grid_constant__
   uint32_t asked = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) c[e] = 0.f, bias[e] = 0.f;
+  const uint32_t* mask = p.mask ? p.mask + b * p.m_sb + v0 / 32 : nullptr;
+  // the first nodes' scores and bits are on their way while the rest is looked up
+  Raw<DT> raw[AHEAD];
+  uint32_t may[AHEAD];
+  auto request = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (i0 + k >= end) continue;
+      load8<DT, WIDE>(p.scores, b * p.s_sb + (i0 + k) * p.s_st + v0, left, raw[k]);
+      if (mask) may[k] = load_bits<WIDE>(mask + (i0 + k) * p.m_st, left);
+    }
+  };
+  request(first);
   float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
+  bool paths = false;
   if (penal) {
     if (p.repetition) rep = __ldg(p.repetition + b), inv = 1.f / rep;
     if (p.frequency) freq = __ldg(p.frequency + b);
@@ -157,25 +209,32 @@ __global__ void __launch_bounds__(THREADS) adjust_kernel(const __grid_constant__
         for (int e = 0; e < E; ++e) c[e] = place<false>(e, t) < left ? (float)__ldg(row + place<false>(e, t)) : 0.f;
       }
     }
-    if (p.prompt) asked = bits8<WIDE>(p.prompt + b * p.ld_prompt + v0 / 32, left);
-    if (t < MAX_T) {
-      int64_t x = -1;
-      if (p.tokens && t < n) x = __ldg(p.tokens + (int64_t)b * p.T + t) - v0;
-      s_token[t] = x >= 0 && x < RANGE && x < left ? (int)x : -1;
-    }
-    __syncthreads();
-    if (t < MAX_T && t < n) {
-      unsigned long long path = 0;
-      int node = t;
-      while (node > 0) {
-        if (s_token[node] >= 0) path |= 1ull << node;
-        const int up = p.parents ? __ldg(p.parents + (int64_t)b * p.T + node) : node - 1;
-        if (up >= node) break;
-        node = up;
+    if (p.prompt) asked = load_bits<WIDE>(p.prompt + b * p.ld_prompt + v0 / 32, left);
+    int64_t x = -1;
+    if (t < n && p.tokens) x = __ldg(p.tokens + (int64_t)b * p.T + t) - v0;
+    const bool here = t > 0 && t < n && x >= 0 && x < RANGE && x < left;
+    // (mostly no node's token falls into the range)
+    paths = __syncthreads_or(here);
+    if (paths) {
+      // A path is the nodes' own bits and the parent's path: each round doubles how far it
+      // reaches.  What does not come before its node ends it.
+      if (t < MAX_T) {
+        int up = 0;
+        if (t > 0 && t < n) up = p.parents ? __ldg(p.parents + (int64_t)b * p.T + t) : t - 1;
+        s_up[t] = up > 0 && up < t ? up : 0;
+        s_path[t] = here ? 1ull << t : 0;
+        s_token[t] = here ? (int)x : -1;
       }
-      s_path[t] = path;
+      for (int reach = 1; reach < n; reach *= 2) {
+        __syncthreads();
+        unsigned long long path = 0;
+        int up = 0;
+        if (t < MAX_T) path = s_path[t] | s_path[s_up[t]], up = s_up[s_up[t]];
+        __syncthreads();
+        if (t < MAX_T) s_path[t] = path, s_up[t] = up;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   if (p.bias) {
     const float* row = p.bias + b * p.ld_bias + v0;
@@ -189,32 +248,53 @@ __global__ void __launch_bounds__(THREADS) adjust_kernel(const __grid_constant__
       for (int e = 0; e < E; ++e) bias[e] = place<false>(e, t) < left ? __ldg(row + place<false>(e, t)) : 0.f;
     }
   }
-  const uint32_t* mask = p.mask ? p.mask + b * p.m_sb + v0 / 32 : nullptr;
-#pragma unroll 2
-  for (int i = first; i < end; ++i) {
-    float x[E];
-    load8<DT, WIDE>(p.scores, b * p.s_sb + i * p.s_st + v0, left, x);
-    const uint32_t may = mask ? bits8<WIDE>(mask + i * p.m_st, left) : 255u;
-    if (penal) {
-      float k[E];
+  // An entry becomes x (1, or where it was seen inv or rep) - term.
+  uint32_t seen = bits_of<WIDE>(asked);
+  float term[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) k[e] = c[e];
-      for (unsigned long long path = s_path[i]; path; path &= path - 1) {
-        const int at = s_token[__ffsll((long long)path) - 1];
+  for (int e = 0; e < E; ++e) {
+    if (c[e] > 0.f) seen |= 1u << e;
+    term[e] = freq * c[e] + (c[e] > 0.f ? pres : 0.f) - bias[e];
+  }
+  for (int i0 = first; i0 < end; i0 += AHEAD) {
+    if (i0 > first) request(i0);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (place<WIDE>(e, t) == at) k[e] += 1.f;
-      }
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = i0 + k;
+      if (i >= end) continue;
+      float x[E], y[E];
+      values<DT>(raw[k], x);
+      const uint32_t bits = mask ? bits_of<WIDE>(may[k]) : 255u;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const bool some = k[e] > 0.f;
-        if (some || (asked >> e & 1)) x[e] *= x[e] > 0.f ? inv : rep;
-        x[e] = x[e] - freq * k[e] - (some ? pres : 0.f);
+        const float f = x[e] > 0.f ? inv : rep;
+        y[e] = fmaf(x[e], seen >> e & 1 ? f : 1.f, -term[e]);
       }
-    }
+      const unsigned long long path = paths ? s_path[i] : 0;
+      if (path) {
+        uint64_t more = 0;  // how often each entry is on the path, in bytes
+        for (unsigned long long rest = path; rest; rest &= rest - 1) {
+          const int at = s_token[__ffsll((long long)rest) - 1];
+          const int owner = WIDE ? at / E : (at / (32 * E)) * 32 + at % 32, e = WIDE ? at % E : at / 32 % E;
+          if (owner == t) more += 1ull << (8 * e);
+        }
+        if (more) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = may >> e & 1 ? x[e] + bias[e] : -INFINITY;
-    store8<DT, WIDE>(p.out, b * p.o_sb + i * p.o_st + v0, left, x);
+          for (int e = 0; e < E; ++e) {
+            const int again = (int)(more >> (8 * e)) & 255;
+            if (!again) continue;
+            // (what it was emitted before is not kept in registers for this)
+            const int64_t v = v0 + place<WIDE>(e, t);
+            const float k = (float)(again + (p.counts ? __ldg(p.counts + b * p.ld_counts + v) : 0));
+            const float add = p.bias ? __ldg(p.bias + b * p.ld_bias + v) : 0.f;
+            y[e] = fmaf(x[e], x[e] > 0.f ? inv : rep, add - (freq * k + pres));
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = bits >> e & 1 ? y[e] : -INFINITY;
+      store8<DT, WIDE>(p.out, b * p.o_sb + i * p.o_st + v0, left, y);
+    }
   }
 }
 
