@@ -59,6 +59,7 @@ __device__ __forceinline__ int place(int e, int t) {
 }
 
 // A thread's eight scores as they are in memory (fp32: 8 words, else 4), and their values.
+// `mine` is where its first entry lies, `left` how many entries there are from it on.
 template <int DT>
 struct Raw {
   static constexpr int WORDS = DT == QMM_DT_F32 ? 8 : 4;
@@ -66,31 +67,28 @@ struct Raw {
 };
 
 template <int DT, bool WIDE>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int64_t left, Raw<DT>& r) {
-  const int t = threadIdx.x;
+__device__ __forceinline__ void load8(const char* mine, int left, Raw<DT>& r) {
   if constexpr (WIDE) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + (at + t * E) * (DT == QMM_DT_F32 ? 4 : 2));
+    const uint4* p = reinterpret_cast<const uint4*>(mine);
 #pragma unroll
     for (int i = 0; i < Raw<DT>::WORDS / 4; ++i) {
-      const uint4 v = t * E + i * 4 < left ? __ldcs(p + i) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 v = i * 4 < left ? __ldcs(p + i) : make_uint4(0u, 0u, 0u, 0u);
       r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
     }
   } else {
-    const int k = place<false>(0, t);
-    const char* p = static_cast<const char*>(base) + (at + k) * (DT == QMM_DT_F32 ? 4 : 2);
     auto get = [&](auto whole) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const bool in = decltype(whole)::value || k + 32 * e < left;
+        const bool in = decltype(whole)::value || 32 * e < left;
         if constexpr (DT == QMM_DT_F32) {
-          r.w[e] = in ? __ldcs(reinterpret_cast<const uint32_t*>(p) + 32 * e) : 0u;
+          r.w[e] = in ? __ldcs(reinterpret_cast<const uint32_t*>(mine) + 32 * e) : 0u;
         } else {
-          const uint32_t x = in ? __ldcs(reinterpret_cast<const uint16_t*>(p) + 32 * e) : 0;
+          const uint32_t x = in ? __ldcs(reinterpret_cast<const uint16_t*>(mine) + 32 * e) : 0;
           r.w[e / 2] = e & 1 ? r.w[e / 2] | x << 16 : x;
         }
       }
     };
-    if (left >= RANGE)
+    if (left > 32 * (E - 1))
       get(std::true_type());
     else
       get(std::false_type());
@@ -109,50 +107,39 @@ __device__ __forceinline__ void values(const Raw<DT>& r, float (&x)[E]) {
 }
 
 template <int DT, bool WIDE>
-__device__ __forceinline__ void store8(void* base, int64_t at, int64_t left, const float (&x)[E]) {
-  const int t = threadIdx.x;
+__device__ __forceinline__ void store8(char* mine, int left, const float (&x)[E]) {
   if constexpr (WIDE && DT == QMM_DT_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at + t * E);
-    if (t * E < left) __stcs(p, make_float4(x[0], x[1], x[2], x[3]));
-    if (t * E + 4 < left) __stcs(p + 1, make_float4(x[4], x[5], x[6], x[7]));
+    float4* p = reinterpret_cast<float4*>(mine);
+    if (left > 0) __stcs(p, make_float4(x[0], x[1], x[2], x[3]));
+    if (left > 4) __stcs(p + 1, make_float4(x[4], x[5], x[6], x[7]));
   } else if constexpr (WIDE) {
     constexpr bool BF = DT == QMM_DT_BF16;
-    if (t * E < left)
-      __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at + t * E),
+    if (left > 0)
+      __stcs(reinterpret_cast<uint4*>(mine),
              make_uint4(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]), pack16<BF>(x[4], x[5]), pack16<BF>(x[6], x[7])));
   } else {
-    const int k = place<false>(0, t);
-    char* p = static_cast<char*>(base) + (at + k) * (DT == QMM_DT_F32 ? 4 : 2);
     auto put = [&](auto whole) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (!decltype(whole)::value && k + 32 * e >= left) continue;
+        if (!decltype(whole)::value && 32 * e >= left) continue;
         if constexpr (DT == QMM_DT_F32)
-          __stcs(reinterpret_cast<float*>(p) + 32 * e, x[e]);
+          __stcs(reinterpret_cast<float*>(mine) + 32 * e, x[e]);
         else
-          __stcs(reinterpret_cast<uint16_t*>(p) + 32 * e, (uint16_t)pack16<DT == QMM_DT_BF16>(x[e], 0.f));
+          __stcs(reinterpret_cast<uint16_t*>(mine) + 32 * e, (uint16_t)pack16<DT == QMM_DT_BF16>(x[e], 0.f));
       }
     };
-    if (left >= RANGE)
+    if (left > 32 * (E - 1))
       put(std::true_type());
     else
       put(std::false_type());
   }
 }
 
-// The bits of a thread's eight entries in words that begin with bit 0 of the range (a
-// range is whole words): WIDE, a byte of a word; else lane e has the word of the warp's
-// entries e (bits_of tells them apart).
-template <bool WIDE>
-__device__ __forceinline__ uint32_t load_bits(const uint32_t* words, int64_t left) {
-  const int t = threadIdx.x;
-  if constexpr (WIDE) return t * E < left ? __ldg(words + t / 4) >> (8 * (t & 3)) & 255u : 0u;
-  const int word = (t >> 5) * E + (t & 31);
-  return (t & 31) < E && word * 32 < left ? __ldg(words + word) : 0u;
-}
+// The bits of a thread's eight entries, from the word that it loaded (a range is whole
+// words): WIDE, a byte of it; else lane e has the word of the warp's entries e.
 template <bool WIDE>
 __device__ __forceinline__ uint32_t bits_of(uint32_t loaded) {
-  if constexpr (WIDE) return loaded;
+  if constexpr (WIDE) return loaded >> (8 * (threadIdx.x & 3)) & 255u;
   uint32_t r = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) r |= (__shfl_sync(0xFFFFFFFFu, loaded, e) >> (threadIdx.x & 31) & 1u) << e;
@@ -178,7 +165,16 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
   uint32_t asked = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) c[e] = 0.f, bias[e] = 0.f;
-  const uint32_t* mask = p.mask ? p.mask + b * p.m_sb + v0 / 32 : nullptr;
+  // what this thread has of each row, and of its bits
+  constexpr int ELEM = DT == QMM_DT_F32 ? 4 : 2;
+  const int own = place<WIDE>(0, t);
+  const int have = left - own > RANGE ? RANGE : (left - own < 0 ? 0 : (int)(left - own));
+  const char* src = static_cast<const char*>(p.scores) + (b * p.s_sb + first * p.s_st + v0 + own) * ELEM;
+  char* dst = static_cast<char*>(p.out) + (b * p.o_sb + first * p.o_st + v0 + own) * ELEM;
+  const int64_t src_step = p.s_st * ELEM, dst_step = p.o_st * ELEM;
+  const int word = WIDE ? t / 4 : (t >> 5) * E + (t & 31);
+  const bool has_word = (WIDE || (t & 31) < E) && word * 32 < left;
+  const uint32_t* mask = p.mask ? p.mask + b * p.m_sb + first * p.m_st + v0 / 32 + word : nullptr;
   // the first nodes' scores and bits are on their way while the rest is looked up
   Raw<DT> raw[AHEAD];
   uint32_t may[AHEAD];
@@ -186,8 +182,12 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       if (i0 + k >= end) continue;
-      load8<DT, WIDE>(p.scores, b * p.s_sb + (i0 + k) * p.s_st + v0, left, raw[k]);
-      if (mask) may[k] = load_bits<WIDE>(mask + (i0 + k) * p.m_st, left);
+      load8<DT, WIDE>(src, have, raw[k]);
+      src += src_step;
+      if (mask) {
+        may[k] = has_word ? __ldg(mask) : 0u;
+        mask += p.m_st;
+      }
     }
   };
   request(first);
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
         for (int e = 0; e < E; ++e) c[e] = place<false>(e, t) < left ? (float)__ldg(row + place<false>(e, t)) : 0.f;
       }
     }
-    if (p.prompt) asked = load_bits<WIDE>(p.prompt + b * p.ld_prompt + v0 / 32, left);
+    if (p.prompt && has_word) asked = __ldg(p.prompt + b * p.ld_prompt + v0 / 32 + word);
     int64_t x = -1;
     if (t < n && p.tokens) x = __ldg(p.tokens + (int64_t)b * p.T + t) - v0;
     const bool here = t > 0 && t < n && x >= 0 && x < RANGE && x < left;
@@ -248,12 +248,14 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
       for (int e = 0; e < E; ++e) bias[e] = place<false>(e, t) < left ? __ldg(row + place<false>(e, t)) : 0.f;
     }
   }
-  // An entry becomes x (1, or where it was seen inv or rep) - term.
-  uint32_t seen = bits_of<WIDE>(asked);
-  float term[E];
+  // An entry becomes x (up for x > 0, else down) - term.
+  const uint32_t in_prompt = bits_of<WIDE>(asked);
+  float up[E], down[E], term[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    if (c[e] > 0.f) seen |= 1u << e;
+    const bool seen = c[e] > 0.f || (in_prompt >> e & 1);
+    up[e] = seen ? inv : 1.f;
+    down[e] = seen ? rep : 1.f;
     term[e] = freq * c[e] + (c[e] > 0.f ? pres : 0.f) - bias[e];
   }
   for (int i0 = first; i0 < end; i0 += AHEAD) {
@@ -266,10 +268,7 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
       values<DT>(raw[k], x);
       const uint32_t bits = mask ? bits_of<WIDE>(may[k]) : 255u;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float f = x[e] > 0.f ? inv : rep;
-        y[e] = fmaf(x[e], seen >> e & 1 ? f : 1.f, -term[e]);
-      }
+      for (int e = 0; e < E; ++e) y[e] = fmaf(x[e], x[e] > 0.f ? up[e] : down[e], -term[e]);
       const unsigned long long path = paths ? s_path[i] : 0;
       if (path) {
         uint64_t more = 0;  // how often each entry is on the path, in bytes
@@ -291,9 +290,12 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
           }
         }
       }
+      if (mask) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = bits >> e & 1 ? y[e] : -INFINITY;
-      store8<DT, WIDE>(p.out, b * p.o_sb + i * p.o_st + v0, left, y);
+        for (int e = 0; e < E; ++e) y[e] = bits >> e & 1 ? y[e] : -INFINITY;
+      }
+      store8<DT, WIDE>(dst, have, y);
+      dst += dst_step;
     }
   }
 }
