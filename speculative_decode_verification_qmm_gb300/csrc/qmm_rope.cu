@@ -10,10 +10,12 @@
 // sincospi; what they lose is below 2^-25 turns.
 //
 // Work.  A unit is V dimensions of a head and the V that they are paired with.  A CTA takes
-// up to 256 units of up to 16 rows: its threads work out the rows' sines and cosines once,
+// up to 256 units of up to 32 rows: its threads work out the rows' sines and cosines once,
 // for all heads, and each thread keeps its unit and walks the rows, a few of them in
 // flight, the first ones requested before the angles are worked out.
-// What bounds it: memory.
+// What bounds it: memory for many rows (8,192 rows of 40 + 20 + 20 heads of 128 from fp32 into
+// a cache: 82 us, 6.1 TB/s, 91 % of a copy; 4,101 rows of 36 heads of 96, a quarter turned, 16
+// bits: 15 us, 3.8 TB/s, of which a CTA's start takes a third), a launch for few.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -27,47 +29,50 @@ namespace qmm {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_ROWS = 16;      // of a CTA
-constexpr int MAX_ANGLES = 1024;  // of a CTA
+constexpr int MAX_ROWS = 32;      // of a CTA
+constexpr int MAX_ANGLES = 2048;  // of a CTA
 static_assert(MAX_ANGLES >= QMM_ROPE_MAX_DIM / 2, "a row's angles");
 
+// V dimensions as they are in memory, and their values.
 template <int DT, int V>
-__device__ __forceinline__ void load_vec(const void* base, int64_t at, float (&x)[V]) {
-  if constexpr (DT == QMM_DT_F32) {
-    const float* p = static_cast<const float*>(base) + at;
-    if constexpr (V == 1) {
-      x[0] = __ldcs(p);
-    } else {
+struct Raw {
+  static constexpr int WORDS = DT == QMM_DT_F32 ? V : (V + 1) / 2;
+  uint32_t w[WORDS];
+};
+
+template <int DT, int V>
+__device__ __forceinline__ void load_vec(const char* at, Raw<DT, V>& r) {
+  if constexpr (Raw<DT, V>::WORDS >= 4) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(p + i));
-        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-      }
+    for (int i = 0; i < Raw<DT, V>::WORDS; i += 4) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(at) + i / 4);
+      r.w[i] = v.x, r.w[i + 1] = v.y, r.w[i + 2] = v.z, r.w[i + 3] = v.w;
     }
+  } else if constexpr (Raw<DT, V>::WORDS == 2) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(at));
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else if constexpr (DT == QMM_DT_F32) {
+    r.w[0] = __ldcs(reinterpret_cast<const uint32_t*>(at));
   } else {
-    constexpr bool BF = DT == QMM_DT_BF16;
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if constexpr (V == 1) {
-      x[0] = unpack16<BF>(__ldcs(p));
-    } else {
-      uint32_t w[V / 2];
-      if constexpr (V == 8) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-      } else {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
-        w[0] = v.x, w[1] = v.y;
-      }
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) x[2 * i] = unpack16<BF>((uint16_t)w[i]), x[2 * i + 1] = unpack16<BF>((uint16_t)(w[i] >> 16));
-    }
+    r.w[0] = __ldcs(reinterpret_cast<const uint16_t*>(at));
   }
 }
 
 template <int DT, int V>
-__device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&x)[V]) {
+__device__ __forceinline__ void values(const Raw<DT, V>& r, float (&x)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if constexpr (DT == QMM_DT_F32)
+      x[e] = __uint_as_float(r.w[e]);
+    else
+      x[e] = unpack16<DT == QMM_DT_BF16>((uint16_t)(e & 1 ? r.w[e / 2] >> 16 : r.w[e / 2]));
+  }
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_vec(char* at, const float (&x)[V]) {
   if constexpr (DT == QMM_DT_F32) {
-    float* p = static_cast<float*>(base) + at;
+    float* p = reinterpret_cast<float*>(at);
     if constexpr (V == 1) {
       *p = x[0];
     } else {
@@ -76,13 +81,12 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&
     }
   } else {
     constexpr bool BF = DT == QMM_DT_BF16;
-    uint16_t* p = static_cast<uint16_t*>(base) + at;
     if constexpr (V == 1)
-      *p = (uint16_t)pack16<BF>(x[0], 0.f);
+      *reinterpret_cast<uint16_t*>(at) = (uint16_t)pack16<BF>(x[0], 0.f);
     else if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(p) = make_uint2(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]));
+      *reinterpret_cast<uint2*>(at) = make_uint2(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]));
     else
-      *reinterpret_cast<uint4*>(p) =
+      *reinterpret_cast<uint4*>(at) =
           make_uint4(pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3]), pack16<BF>(x[4], x[5]), pack16<BF>(x[6], x[7]));
   }
 }
@@ -112,20 +116,33 @@ __device__ __forceinline__ void unit_place(const RopeParams& p, int unit, int& f
   }
 }
 
-// grid: groups of `rows` rows, times groups of THREADS units.
+// A place that walks rows: `step` bytes from one to the next, `wrap` more behind the last row
+// of a sequence.
+struct Walk {
+  int64_t step, wrap;
+  int i, T;
+  template <typename P>
+  __device__ __forceinline__ void on(P*& at) {
+    at += step;
+    if (++i == T) i = 0, at += wrap;
+  }
+};
+
+// grid: groups of `rows` rows, times groups of blockDim units.
 template <int SRC, int DST, int V, bool PACKED>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeParams p, int rows) {
-  constexpr int U = V == 8 ? 2 : 4;  // rows in flight
+__global__ void __launch_bounds__(THREADS, 3) rope_kernel(const __grid_constant__ RopeParams p, int rows) {
+  constexpr int AHEAD = 4;  // rows in flight
+  constexpr int SS = SRC == QMM_DT_F32 ? 4 : 2, DS = DST == QMM_DT_F32 ? 4 : 2;
   __shared__ float2 s_cs[MAX_ANGLES];
   __shared__ int64_t s_pool[MAX_ROWS];  // PACKED: the row's place in a pool, -1: none
   __shared__ int s_pos[MAX_ROWS];
-  const int tid = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * rows;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const uint32_t row0 = blockIdx.x * (uint32_t)rows;
   const int n = p.rows - row0 < rows ? (int)(p.rows - row0) : rows;
-  const int units = units_of<V>(p), total = p.heads * units;
-  const int u = blockIdx.y * THREADS + tid;
+  const uint32_t units = units_of<V>(p), total = p.heads * units;
+  const uint32_t u = blockIdx.y * threads + tid;
   const bool mine = u < total;
-  int h = u / units, first = 0, second = -1, pair = 0, part = 0;
+  int h = mine ? u / units : 0, first = 0, second = -1, pair = 0, part = 0;
   bool turn = false;
   if (mine) {
     unit_place<V>(p, u - h * units, first, second, pair, turn);
@@ -133,27 +150,24 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
   }
   const RopeHeads& t = p.part[part];
   turn = turn && t.turned;
-  const char* src = static_cast<const char*>(t.src) + (h * t.s_head + first) * (SRC == QMM_DT_F32 ? 4 : 2);
-  char* dst = static_cast<char*>(t.dst) + (h * t.d_head + first) * (DST == QMM_DT_F32 ? 4 : 2);
-  const int64_t s_seq = PACKED ? 0 : t.s_seq, s_row = t.s_row, d_seq = PACKED ? 0 : t.d_seq, d_row = t.d_row;
-  const bool pool = PACKED && t.pool;
-  second = second < 0 ? -1 : second - first;
-  // sequence and row in it, of the rows that are loaded and of those that are stored
-  int lb = 0, li = 0;
-  if (!PACKED) lb = (int)(row0 / p.T), li = (int)(row0 - (int64_t)lb * p.T);
-  int sb = lb, si = li;
-  float x[U][V], y[U][V];
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (!mine || r0 + k >= n) continue;
-      const int64_t at = PACKED ? (row0 + r0 + k) * s_row : lb * s_seq + li * s_row;
-      load_vec<SRC, V>(src, at, x[k]);
-      if (second >= 0) load_vec<SRC, V>(src, at + second, y[k]);
-      if (!PACKED && ++li == p.T) li = 0, ++lb;
-    }
+  const bool two = second >= 0, pool = PACKED && t.pool;
+  const int64_t other = two ? second - first : 0;
+  const uint32_t b0 = PACKED ? 0 : row0 / (uint32_t)p.T, i0 = PACKED ? row0 : row0 - b0 * p.T;
+  const char* src = static_cast<const char*>(t.src) + (b0 * t.s_seq + i0 * t.s_row + h * t.s_head + first) * SS;
+  char* const dst0 = static_cast<char*>(t.dst) + (h * t.d_head + first) * DS;
+  char* dst = dst0 + (b0 * t.d_seq + i0 * t.d_row) * DS;
+  const int T = PACKED ? -1 : p.T;
+  Walk from{t.s_row * SS, (t.s_seq - p.T * t.s_row) * SS, (int)i0, T};
+  Walk to{t.d_row * DS, (t.d_seq - p.T * t.d_row) * DS, (int)i0, T};
+  Raw<SRC, V> a[AHEAD], c[AHEAD];
+  auto load = [&](int k) {
+    load_vec<SRC, V>(src, a[k]);
+    if (two) load_vec<SRC, V>(src + other * SS, c[k]);
+    from.on(src);
   };
-  load(0);
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (mine && k < n) load(k);
   if (tid < n) {
     const int64_t row = row0 + tid;
     if constexpr (PACKED) {
@@ -182,8 +196,8 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
     }
   }
   __syncthreads();
-  for (int j = tid; j < n * p.m; j += THREADS) {
-    const int r = j / p.m;
+  for (uint32_t j = tid; j < (uint32_t)(n * p.m); j += threads) {
+    const uint32_t r = j / (uint32_t)p.m;
     const uint64_t w = (uint64_t)(int64_t)s_pos[r] * __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + (j - r * p.m));
     const int frac = (int)((w + 0x80000000ull) >> 32);
     float s, c;
@@ -191,38 +205,46 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
     s_cs[j] = make_float2(c * p.amplitude, s * p.amplitude);
   }
   __syncthreads();
-  for (int r0 = 0; r0 < n; r0 += U) {
-    if (r0 > 0) load(r0);
+  if (!mine) return;
+  const float2* cs = s_cs + pair;
+  for (int r0 = 0; r0 < n; r0 += AHEAD) {
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (!mine || r0 + k >= n) continue;
+    for (int k = 0; k < AHEAD; ++k) {
+      const int r = r0 + k;
+      if (r >= n) break;
+      float x[V], y[V];
+      values<SRC, V>(a[k], x);
+      if (two) values<SRC, V>(c[k], y);
+      if (r + AHEAD < n) load(k);
       if (turn) {
-        const float2* cs = s_cs + (r0 + k) * p.m + pair;
-        if (second >= 0) {
+        if (two) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float a = x[k][e], c = y[k][e];
-            x[k][e] = a * cs[e].x - c * cs[e].y;
-            y[k][e] = a * cs[e].y + c * cs[e].x;
+            const float2 f = cs[e];
+            const float v = x[e], w = y[e];
+            x[e] = v * f.x - w * f.y;
+            y[e] = v * f.y + w * f.x;
           }
         } else {
 #pragma unroll
           for (int e = 0; e + 1 < V; e += 2) {
-            const float a = x[k][e], c = x[k][e + 1];
-            x[k][e] = a * cs[e / 2].x - c * cs[e / 2].y;
-            x[k][e + 1] = a * cs[e / 2].y + c * cs[e / 2].x;
+            const float2 f = cs[e / 2];
+            const float v = x[e], w = x[e + 1];
+            x[e] = v * f.x - w * f.y;
+            x[e + 1] = v * f.y + w * f.x;
           }
         }
       }
-      int64_t at = PACKED ? (row0 + r0 + k) * d_row : sb * d_seq + si * d_row;
-      if (!PACKED && ++si == p.T) si = 0, ++sb;
+      cs += p.m;
+      char* at = dst;
+      to.on(dst);
       if constexpr (PACKED) {
-        const int64_t place = s_pool[r0 + k];
+        const int64_t place = s_pool[r];
         if (place < 0) continue;
-        if (pool) at = place;
+        if (pool) at = dst0 + place * DS;
       }
-      store_vec<DST, V>(dst, at, x[k]);
-      if (second >= 0) store_vec<DST, V>(dst, at + second, y[k]);
+      store_vec<DST, V>(at, x);
+      if (two) store_vec<DST, V>(at + other * DS, y);
     }
   }
 }
@@ -230,17 +252,22 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
 template <int SRC, int DST, int V, bool PACKED>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t st) {
   const int64_t total = (int64_t)p.heads * units_of<V>(p), groups = (total + THREADS - 1) / THREADS;
-  // rows of a CTA: as many as leave eight CTAs to an SM
-  int64_t rows = p.rows * groups / (8ll * sms);
-  const int most = p.m > 0 && MAX_ANGLES / p.m < MAX_ROWS ? MAX_ANGLES / p.m : MAX_ROWS;
-  rows = rows < 1 ? 1 : (rows > most ? most : rows);
-  rope_kernel<SRC, DST, V, PACKED><<<dim3((unsigned)((p.rows + rows - 1) / rows), (unsigned)groups), THREADS, 0, st>>>(p, (int)rows);
+  const int threads = (int)((total + groups - 1) / groups + 31) / 32 * 32;
+  // rows of a CTA: many, since each CTA has its units to work out, in whole waves
+  const int64_t most = p.m > 0 && MAX_ANGLES / p.m < MAX_ROWS ? MAX_ANGLES / p.m : MAX_ROWS;
+  const int64_t slots = (int64_t)sms * (3 * THREADS / threads), all = p.rows * groups;
+  const int64_t waves = (all + slots * most - 1) / (slots * most);
+  int64_t rows = (all + slots * waves - 1) / (slots * waves);
+  rows = rows > most ? most : rows;
+  rope_kernel<SRC, DST, V, PACKED><<<dim3((unsigned)((p.rows + rows - 1) / rows), (unsigned)groups), threads, 0, st>>>(p, (int)rows);
   return cudaGetLastError();
 }
 
 template <int SRC, int DST, bool PACKED>
 cudaError_t launch_v(const RopeParams& p, int sms, cudaStream_t st) {
-  // Vectors of eight or four where every one of them lies on its boundary, of 16 bytes at most.
+  // Vectors of 16 bytes of the source, or four dimensions of 16 bits, where every one of them
+  // lies on its boundary.  (fp32 with eight: 91 us for 8,192 rows of 40 + 20 + 20 heads, with
+  // four 82.)
   const int s = SRC == QMM_DT_F32 ? 4 : 2, d = DST == QMM_DT_F32 ? 4 : 2;
   int64_t bits = p.D | (p.half ? p.m : 2 * p.m);
   uintptr_t src = 0, dst = 0;
@@ -249,7 +276,8 @@ cudaError_t launch_v(const RopeParams& p, int sms, cudaStream_t st) {
     bits |= t.s_seq | t.s_row | t.s_head | t.d_seq | t.d_row | t.d_head;
     src |= (uintptr_t)t.src, dst |= (uintptr_t)t.dst;
   }
-  if (!(bits & 7) && !((src | dst) & 15)) return launch<SRC, DST, 8, PACKED>(p, sms, st);
+  if constexpr (SRC != QMM_DT_F32)
+    if (!(bits & 7) && !((src | dst) & 15)) return launch<SRC, DST, 8, PACKED>(p, sms, st);
   if (!(bits & 3) && !(src & (4 * s - 1)) && !(dst & (4 * d - 1))) return launch<SRC, DST, 4, PACKED>(p, sms, st);
   return launch<SRC, DST, 1, PACKED>(p, sms, st);
 }
