@@ -45,81 +45,90 @@ struct NormParams {
 constexpr int SHORT = 512;
 constexpr int MAX_DEVICES = 64;
 
-// Entries of a thread: vectors of V, a group's threads side by side.  FRESH: read once.
-template <int E, int V, bool FRESH>
-__device__ __forceinline__ void load_row(int dt, const void* row, int t, int threads, int n, float (&x)[E]) {
+// Entries of a thread: vectors of V, a group's threads side by side.  FULL: the group's
+// threads have no places past the row.  FRESH: read once.
+template <int E, int V, bool FULL, bool FRESH>
+__device__ __forceinline__ void load_row(int dt, const char* row, int t, int threads, int n, float (&x)[E]) {
   if (dt == QMM_DT_F32) {
-    const float* p = static_cast<const float*>(row);
+    const char* at = row + t * V * 4;
+    const int step = threads * V * 4;
 #pragma unroll
-    for (int i = 0; i < E / V; ++i) {
-      const int k = (i * threads + t) * V;
+    for (int i = 0; i < E / V; ++i, at += step) {
+      const bool in = FULL || (i * threads + t) * V < n;
       if constexpr (V == 4) {
-        const float4* q = reinterpret_cast<const float4*>(p + k);
-        const float4 v = k < n ? (FRESH ? __ldcs(q) : *q) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* q = reinterpret_cast<const float4*>(at);
+        const float4 v = in ? (FRESH ? __ldcs(q) : *q) : make_float4(0.f, 0.f, 0.f, 0.f);
         x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
       } else {
-        x[i] = k < n ? (FRESH ? __ldcs(p + k) : p[k]) : 0.f;
+        const float* q = reinterpret_cast<const float*>(at);
+        x[i] = in ? (FRESH ? __ldcs(q) : *q) : 0.f;
       }
     }
     return;
   }
-  const uint16_t* p = static_cast<const uint16_t*>(row);
   uint32_t w[(E + 1) / 2];
+  const char* at = row + t * V * 2;
+  const int step = threads * V * 2;
 #pragma unroll
-  for (int i = 0; i < E / V; ++i) {
-    const int k = (i * threads + t) * V;
+  for (int i = 0; i < E / V; ++i, at += step) {
+    const bool in = FULL || (i * threads + t) * V < n;
     if constexpr (V == 4) {
-      const uint2* q = reinterpret_cast<const uint2*>(p + k);
-      const uint2 v = k < n ? (FRESH ? __ldcs(q) : *q) : make_uint2(0u, 0u);
+      const uint2* q = reinterpret_cast<const uint2*>(at);
+      const uint2 v = in ? (FRESH ? __ldcs(q) : *q) : make_uint2(0u, 0u);
       w[2 * i] = v.x, w[2 * i + 1] = v.y;
     } else {
-      const uint32_t v = k < n ? (FRESH ? __ldcs(p + k) : p[k]) : 0;
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(at);
+      const uint32_t v = in ? (FRESH ? __ldcs(q) : *q) : 0;
       w[i / 2] = i & 1 ? w[i / 2] | v << 16 : v;
     }
   }
   if (dt == QMM_DT_BF16) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = unpack16<true>((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]));
+    for (int i = 0; i < E; ++i) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = unpack16<false>((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]));
   }
 }
 
-template <int E, int V>
-__device__ __forceinline__ void store_row(int dt, void* row, int t, int threads, int n, const float (&x)[E]) {
+template <int E, int V, bool FULL>
+__device__ __forceinline__ void store_row(int dt, char* row, int t, int threads, int n, const float (&x)[E]) {
   if (dt == QMM_DT_F32) {
-    float* p = static_cast<float*>(row);
+    char* at = row + t * V * 4;
+    const int step = threads * V * 4;
 #pragma unroll
-    for (int i = 0; i < E / V; ++i) {
-      const int k = (i * threads + t) * V;
-      if (k >= n) continue;
+    for (int i = 0; i < E / V; ++i, at += step) {
+      if (!FULL && (i * threads + t) * V >= n) continue;
       if constexpr (V == 4)
-        *reinterpret_cast<float4*>(p + k) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        *reinterpret_cast<float4*>(at) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
       else
-        p[k] = x[i];
+        *reinterpret_cast<float*>(at) = x[i];
     }
     return;
   }
-  uint16_t* p = static_cast<uint16_t*>(row);
   uint32_t w[(E + 1) / 2];
+  if (dt == QMM_DT_BF16) {
 #pragma unroll
-  for (int i = 0; i < E; i += 2)
-    w[i / 2] = dt == QMM_DT_BF16 ? pack16<true>(x[i], i + 1 < E ? x[i + 1] : 0.f) : pack16<false>(x[i], i + 1 < E ? x[i + 1] : 0.f);
+    for (int i = 0; i < E; i += 2) w[i / 2] = pack16<true>(x[i], i + 1 < E ? x[i + 1] : 0.f);
+  } else {
 #pragma unroll
-  for (int i = 0; i < E / V; ++i) {
-    const int k = (i * threads + t) * V;
-    if (k >= n) continue;
+    for (int i = 0; i < E; i += 2) w[i / 2] = pack16<false>(x[i], i + 1 < E ? x[i + 1] : 0.f);
+  }
+  char* at = row + t * V * 2;
+  const int step = threads * V * 2;
+#pragma unroll
+  for (int i = 0; i < E / V; ++i, at += step) {
+    if (!FULL && (i * threads + t) * V >= n) continue;
     if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(p + k) = make_uint2(w[2 * i], w[2 * i + 1]);
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[2 * i], w[2 * i + 1]);
     else
-      p[k] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+      *reinterpret_cast<uint16_t*>(at) = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
   }
 }
 
 __device__ __forceinline__ int size_of(int dt) { return dt == QMM_DT_F32 ? 4 : 2; }
-__device__ __forceinline__ const char* row_of(const void* base, int64_t m, int64_t ld, int dt) {
-  return static_cast<const char*>(base) + m * ld * size_of(dt);
+__device__ __forceinline__ char* row_of(const void* base, int64_t m, int64_t ld, int dt) {
+  return const_cast<char*>(static_cast<const char*>(base)) + m * ld * size_of(dt);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -129,7 +138,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // x <- norm(x) w + b; entries past the row stay zero.
-template <int E, int V, typename S>
+template <int E, int V, bool FULL, typename S>
 __device__ __forceinline__ void normed(const NormParams& p, float (&x)[E], const float* w, const float* b, int t, int threads,
                                        S sum_all) {
   if (p.centered) {
@@ -139,46 +148,46 @@ __device__ __forceinline__ void normed(const NormParams& p, float (&x)[E], const
     const float mean = sum_all(s) * p.inv_n;
 #pragma unroll
     for (int i = 0; i < E; ++i)
-      if (((i / V) * threads + t) * V + i % V < p.N) x[i] -= mean;
+      if (FULL || ((i / V) * threads + t) * V + i % V < p.N) x[i] -= mean;
   }
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) s = fmaf(x[i], x[i], s);
   float wv[E];
-  load_row<E, V, false>(QMM_DT_F32, w, t, threads, p.N, wv);
+  load_row<E, V, FULL, false>(QMM_DT_F32, reinterpret_cast<const char*>(w), t, threads, p.N, wv);
   const float f = rsqrtf(fmaf(sum_all(s), p.inv_n, p.eps));
 #pragma unroll
   for (int i = 0; i < E; ++i) x[i] = x[i] * f * wv[i];
   if (b) {
-    load_row<E, V, false>(QMM_DT_F32, b, t, threads, p.N, wv);
+    load_row<E, V, FULL, false>(QMM_DT_F32, reinterpret_cast<const char*>(b), t, threads, p.N, wv);
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] += wv[i];
   }
 }
 
 // One row, from where y, the residual and the gate lie.
-template <int E, int V, bool FRESH, typename S>
-__device__ __forceinline__ void one_row(const NormParams& p, int64_t m, const void* y, const void* res, const void* gate, int t,
+template <int E, int V, bool FULL, bool FRESH, typename S>
+__device__ __forceinline__ void one_row(const NormParams& p, int64_t m, const char* y, const char* res, const char* gate, int t,
                                         int threads, S sum_all) {
   float r[E];
-  load_row<E, V, FRESH>(p.res_dt, res, t, threads, p.N, r);
+  load_row<E, V, FULL, FRESH>(p.res_dt, res, t, threads, p.N, r);
   if (p.y) {
     float z[E];
-    load_row<E, V, FRESH>(p.y_dt, y, t, threads, p.N, z);
-    if (p.post_weight) normed<E, V>(p, z, p.post_weight, p.post_bias, t, threads, sum_all);
+    load_row<E, V, FULL, FRESH>(p.y_dt, y, t, threads, p.N, z);
+    if (p.post_weight) normed<E, V, FULL>(p, z, p.post_weight, p.post_bias, t, threads, sum_all);
     if (p.gate) {
       float g[E];
-      load_row<E, V, false>(QMM_DT_F32, gate, t, threads, p.N, g);
+      load_row<E, V, FULL, false>(QMM_DT_F32, gate, t, threads, p.N, g);
 #pragma unroll
       for (int i = 0; i < E; ++i) z[i] *= g[i];
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) r[i] = fmaf(p.scale, z[i], r[i]);
-    store_row<E, V>(p.res_dt, const_cast<char*>(row_of(p.res_out, m, p.ld_res_out, p.res_dt)), t, threads, p.N, r);
+    store_row<E, V, FULL>(p.res_dt, row_of(p.res_out, m, p.ld_res_out, p.res_dt), t, threads, p.N, r);
   }
   if (p.out) {
-    normed<E, V>(p, r, p.weight, p.bias, t, threads, sum_all);
-    store_row<E, V>(p.out_dt, const_cast<char*>(row_of(p.out, m, p.ld_out, p.out_dt)), t, threads, p.N, r);
+    normed<E, V, FULL>(p, r, p.weight, p.bias, t, threads, sum_all);
+    store_row<E, V, FULL>(p.out_dt, row_of(p.out, m, p.ld_out, p.out_dt), t, threads, p.N, r);
   }
 }
 
@@ -187,12 +196,12 @@ template <int E, int V>
 __global__ void __launch_bounds__(256) norm_short_kernel(const __grid_constant__ NormParams p) {
   const int lane = threadIdx.x & 31;
   for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < p.M; m += (int64_t)gridDim.x * 8)
-    one_row<E, V, true>(p, m, row_of(p.y, m, p.ld_y, p.y_dt), row_of(p.res, m, p.ld_res, p.res_dt),
+    one_row<E, V, false, true>(p, m, row_of(p.y, m, p.ld_y, p.y_dt), row_of(p.res, m, p.ld_res, p.res_dt),
                         row_of(p.gate, m, p.ld_gate, QMM_DT_F32), lane, 32, warp_sum);
 }
 
-// Longer rows: a CTA each, `stages` of them in shared memory; 0: straight from memory.
-template <int E, int V>
+// Longer rows: a CTA each; STAGED: `stages` of them in shared memory, else straight from memory.
+template <int E, int V, bool FULL, bool STAGED>
 __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams p, int stages, int stage_bytes) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float s_sum[2][32];
@@ -207,46 +216,54 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     turn ^= 1;
     return v;
   };
-  const int y_room = p.y ? (p.N * size_of(p.y_dt) + 31) & ~15 : 0, r_room = (p.N * size_of(p.res_dt) + 31) & ~15;
+  if constexpr (!STAGED) {
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x)
+      one_row<E, V, FULL, true>(p, m, row_of(p.y, m, p.ld_y, p.y_dt), row_of(p.res, m, p.ld_res, p.res_dt),
+                                row_of(p.gate, m, p.ld_gate, QMM_DT_F32), t, threads, sum_all);
+    return;
+  }
+  const int y_bytes = p.N * size_of(p.y_dt), r_bytes = p.N * size_of(p.res_dt);
+  const int y_room = p.y ? (y_bytes + 31) & ~15 : 0, r_room = (r_bytes + 31) & ~15;
+  const bool gates = p.gate && p.ld_gate;
   // where a row begins behind the boundary that its copy starts from
   auto skew = [](const char* row) { return (int)((uintptr_t)row & 15); };
   auto request = [&](int64_t m, int stage) {
     if (m < p.M) {
-      const uint32_t to = smem_u32(smem) + stage * stage_bytes;
-      auto copy = [&](uint32_t dst, const char* row, int bytes) {
-        const int groups = (skew(row) + bytes + 15) >> 4;
-        for (int c = t; c < groups; c += threads) cp_async16(dst + c * 16, row - skew(row) + c * 16, 16);
+      auto copy = [&](int to, const char* row, int bytes) {
+        const int s = skew(row), end = s + bytes;
+        const uint32_t dst = smem_u32(smem) + to;
+        row -= s;
+        for (int c = t * 16; c < end; c += threads * 16) cp_async16(dst + c, row + c, 16);
       };
-      if (p.y) copy(to, row_of(p.y, m, p.ld_y, p.y_dt), p.N * size_of(p.y_dt));
-      copy(to + y_room, row_of(p.res, m, p.ld_res, p.res_dt), p.N * size_of(p.res_dt));
-      if (p.gate && p.ld_gate) copy(to + y_room + r_room, row_of(p.gate, m, p.ld_gate, QMM_DT_F32), p.N * 4);
+      const int to = stage * stage_bytes;
+      if (p.y) copy(to, row_of(p.y, m, p.ld_y, p.y_dt), y_bytes);
+      copy(to + y_room, row_of(p.res, m, p.ld_res, p.res_dt), r_bytes);
+      if (gates) copy(to + y_room + r_room, row_of(p.gate, m, p.ld_gate, QMM_DT_F32), p.N * 4);
     }
     cp_async_commit();
   };
   int64_t ahead = blockIdx.x;
   for (int s = 0; s + 1 < stages; ++s, ahead += gridDim.x) request(ahead, s);
   int stage = 0;
-  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-    const char *y = row_of(p.y, m, p.ld_y, p.y_dt), *res = row_of(p.res, m, p.ld_res, p.res_dt),
-               *gate = row_of(p.gate, m, p.ld_gate, QMM_DT_F32);
-    if (stages) {
-      // the row has come, and the last one's place is free
-      if (stages == 3)
-        cp_async_wait<1>();
-      else if (stages == 2)
-        cp_async_wait<0>();
-      else
-        cp_async_wait<2>();
-      __syncthreads();
-      request(ahead, stage == 0 ? stages - 1 : stage - 1);
-      ahead += gridDim.x;
-      const char* from = smem + stage * stage_bytes;
-      y = from + skew(y);
-      res = from + y_room + skew(res);
-      if (p.ld_gate) gate = from + y_room + r_room + skew(gate);
-      if (++stage == stages) stage = 0;
-    }
-    one_row<E, V, false>(p, m, y, res, gate, t, threads, sum_all);
+  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, ahead += gridDim.x) {
+    // the row has come, and the last one's place is free
+    if (stages == 2)
+      cp_async_wait<0>();
+    else if (stages == 3)
+      cp_async_wait<1>();
+    else
+      cp_async_wait<2>();
+    __syncthreads();
+    request(ahead, stage == 0 ? stages - 1 : stage - 1);
+    const char* from = smem + stage * stage_bytes;
+    if (++stage == stages) stage = 0;
+    const char* y = from + skew(row_of(p.y, m, p.ld_y, p.y_dt));
+    const char* res = from + y_room + skew(row_of(p.res, m, p.ld_res, p.res_dt));
+    if (gates)
+      one_row<E, V, FULL, false>(p, m, y, res, from + y_room + r_room + skew(row_of(p.gate, m, p.ld_gate, QMM_DT_F32)), t, threads,
+                                 sum_all);
+    else
+      one_row<E, V, FULL, false>(p, m, y, res, reinterpret_cast<const char*>(p.gate), t, threads, sum_all);
   }
 }
 
@@ -263,13 +280,28 @@ cudaError_t launch_short(const NormParams& p, int sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+constexpr int SMEM = 220 * 1024;  // of an SM, for stages
+
+template <int E, int V, bool FULL, bool STAGED>
+cudaError_t launch_kernel(const NormParams& p, int dev, unsigned grid, int threads, int stages, int stage, cudaStream_t st) {
+  if (STAGED) {
+    static std::atomic<bool> set[MAX_DEVICES];  // once for a device
+    if (dev >= MAX_DEVICES || !set[dev].load(std::memory_order_relaxed)) {
+      const cudaError_t e = cudaFuncSetAttribute(norm_kernel<E, V, FULL, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+      if (e != cudaSuccess) return e;
+      if (dev < MAX_DEVICES) set[dev].store(true, std::memory_order_relaxed);
+    }
+  }
+  norm_kernel<E, V, FULL, STAGED><<<grid, threads, stages * stage, st>>>(p, stages, stage);
+  return cudaGetLastError();
+}
+
 template <int E, int V>
 cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) {
   const int threads = ((p.N + E - 1) / E + 31) / 32 * 32;
   const int ys = p.y_dt == QMM_DT_F32 ? 4 : 2, rs = p.res_dt == QMM_DT_F32 ? 4 : 2;
   const int stage = (p.y ? (p.N * ys + 31) & ~15 : 0) + ((p.N * rs + 31) & ~15) + (p.gate && p.ld_gate ? (p.N * 4 + 31) & ~15 : 0);
   // CTAs that an SM's registers allow (64 a thread), and two to four stages of shared memory each
-  constexpr int SMEM = 220 * 1024;
   int ctas = 1024 / threads;
   while (ctas > 1 && SMEM / ctas < 2 * stage + 1024) --ctas;
   int stages = (SMEM / ctas - 1024) / stage;
@@ -277,16 +309,12 @@ cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) 
   const int64_t most = (int64_t)ctas * sms;
   if (p.M <= most) stages = 0;  // a row alone has no next one to wait for
   const unsigned grid = (unsigned)(p.M < most ? p.M : most);
-  if (stages) {
-    static std::atomic<bool> set[MAX_DEVICES];  // once for a device
-    if (dev >= MAX_DEVICES || !set[dev].load(std::memory_order_relaxed)) {
-      const cudaError_t e = cudaFuncSetAttribute(norm_kernel<E, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-      if (e != cudaSuccess) return e;
-      if (dev < MAX_DEVICES) set[dev].store(true, std::memory_order_relaxed);
-    }
-  }
-  norm_kernel<E, V><<<grid, threads, stages * stage, st>>>(p, stages, stage);
-  return cudaGetLastError();
+  const bool full = V == 4 && p.N == threads * E;
+  if (stages)
+    return full ? launch_kernel<E, V, V == 4, true>(p, dev, grid, threads, stages, stage, st)
+                : launch_kernel<E, V, false, true>(p, dev, grid, threads, stages, stage, st);
+  return full ? launch_kernel<E, V, V == 4, false>(p, dev, grid, threads, 0, 0, st)
+              : launch_kernel<E, V, false, false>(p, dev, grid, threads, 0, 0, st);
 }
 
 template <int V>
