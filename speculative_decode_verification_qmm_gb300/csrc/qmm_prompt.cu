@@ -64,8 +64,8 @@ struct Smem {
   static constexpr int NBAR = 2 * KS + 3 * VS + 17;
   static constexpr int BAD = BAR + NBAR * 8;        // rows with non-finite V, by segment
   static constexpr int FLAG = BAD + BAD_BUFS * BAD_WORDS * 4;  // [0] abort, [1] tensor memory
-  static constexpr int START = FLAG + 16;           // the CTA's share, and the cursor at its start
-  static constexpr int BYTES = START + 48;
+  static constexpr int START = FLAG + 16;           // the CTA's share, and the places of its first and last unit
+  static constexpr int BYTES = START + 80;
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
@@ -188,8 +188,9 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// The start of CTA c's share of the work, and the share's weight, for every lane of a warp.
-__device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, int64_t& left) {
+// The place of the first (or last) unit of CTA c's share of the work, and the share's weight,
+// for every lane of a warp.
+__device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, bool last, int64_t& share) {
   Cursor cur{};
   int64_t W = 0, head = 0;  // of a key/value head of the lane's sequence
   auto look = [&](int b0) {
@@ -200,7 +201,7 @@ __device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, 
     return ok;
   };
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
-    if (!look(b0) && c == 0) atomicOr(p.a.status, DEV_ERR_INDEX);
+    if (!look(b0) && c == 0 && !last) atomicOr(p.a.status, DEV_ERR_INDEX);
     int64_t w = head * p.a.Hkv;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
@@ -208,10 +209,10 @@ __device__ __forceinline__ Cursor begin(const PromptParams& p, int lane, int c, 
   }
   // no CTA without a share between two that have one: the joining kernel counts on it
   const int G = W < p.a.grid ? (int)W : p.a.grid;
-  left = 0;
+  share = 0;
   if (c >= G) return cur;
-  const int64_t u0 = quotient(W * c, G);
-  left = quotient(W * (c + 1), G) - u0;
+  const int64_t first = quotient(W * c, G), end = quotient(W * (c + 1), G), u0 = last ? end - 1 : first;
+  share = end - first;
   int64_t before = 0;
   for (int b0 = 0; b0 < p.a.B; b0 += 32) {
     if (p.a.B > 32) look(b0);
@@ -387,12 +388,12 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   // then may the joining kernel take its place.
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) {
+  if (warp < 2) {
     int64_t share;
-    const Cursor cur = begin(pp, lane, blockIdx.x, share);
+    const Cursor c = begin(pp, lane, blockIdx.x, warp == 1, share);
     if (lane == 0) {
-      *reinterpret_cast<int64_t*>(smem + S::START) = share;
-      *reinterpret_cast<Cursor*>(smem + S::START + 8) = cur;
+      *reinterpret_cast<Cursor*>(smem + S::START + 8 + 32 * warp) = c;
+      if (warp == 0) *reinterpret_cast<int64_t*>(smem + S::START) = share;
     }
   }
   tc_fence_before();
@@ -402,10 +403,31 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   if (tid == 0) p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
   const uint64_t lim = p.wait_limit_ns;
   auto fail = [&](int code) { s_flag[0] = code; };  // by all lanes of a warp
-  // Each role reads the CTA's share anew, for registers of its own.
-  auto start = [&](Cursor& c) {
-    c = *reinterpret_cast<const Cursor*>(smem + S::START + 8);
-    return *reinterpret_cast<const int64_t*>(smem + S::START);
+  // The share's parts, each a place and a weight; every role reads them anew, for registers
+  // of its own.  What the CTA has of its last item, if others go on with it, comes first:
+  // then the CTAs that a long cache's items are spread over read about the same rows at a time, and
+  // these once from memory.  (512 rows behind 65,536, 64/8 heads of 128: 4.3 GB in order.)
+  auto start = [&](int part, Cursor& c) -> int64_t {
+    const int64_t share = *reinterpret_cast<const int64_t*>(smem + S::START);
+    const Cursor* at = reinterpret_cast<const Cursor*>(smem + S::START + 8);
+    c = at[0];
+    if (share == 0) return 0;
+    const int64_t in_last = at[1].w + 1;  // of the share, if the last item begins in it
+    const bool split = in_last < share && in_last < at[1].tiles + ITEM_WEIGHT;
+    if (part == 0 && split) {
+      c = at[1];
+      c.w = 0;
+      return in_last;
+    }
+    return split ? share - in_last : (part == 0 ? share : 0);
+  };
+  // On to the next item of the share.
+  auto go_on = [&](Cursor& c, int64_t& share, int& part) {
+    if (share > 0)
+      next(pp, c);
+    else
+      share = part == 0 ? start(++part, c) : 0;
+    return share > 0;
   };
   // Tokens of the cursor's row tile.
   auto tokens = [&](const Cursor& c) {
@@ -416,7 +438,8 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------------ load
     Cursor cur;
-    int64_t share = start(cur);
+    int part = 0;
+    int64_t share = start(part, cur);
     const bool is_v = warp > LOAD_WARP;
     const uint32_t full = base + (is_v ? O_VFULL : O_KFULL), empty = base + (is_v ? O_VEMPTY : O_KEMPTY);
     const uint32_t ring = base + (is_v ? S::V : S::K);
@@ -432,7 +455,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
     };
     int slot = 0, round = 0, seg = 0;
     unsigned landing = 0, landed = 0;  // bits by slot: a copy counts on vland; vland's parity
-    while (share > 0 && ok) {
+    for (bool on = share > 0; on && ok; on = go_on(cur, share, part)) {
       int tile;
       const int count = take(cur, share, tile);
       if (count > 0) ++seg;
@@ -492,7 +515,6 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         }
         if (++slot == slots) slot = 0, ++round;
       }
-      if (share > 0) next(pp, cur);
     }
     // Tensor copies in flight land before the CTA leaves: the last tile of every
     // slot.  Always: another role can give up after this one's last look at the flag.
@@ -511,7 +533,8 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
     uint32_t leader;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
     Cursor cur_next;
-    int64_t share = start(cur_next);
+    int part = 0;
+    int64_t share = start(part, cur_next);
     // What the products' operands come from is made uniform: they then live in uniform
     // registers.
     auto uniform = [](uint32_t x) { return __reduce_max_sync(0xFFFFFFFFu, x); };
@@ -556,11 +579,13 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
     auto s_column = [&](int q, int n) { return tmem + (NQ == 2 ? q * COL_Q : (n & 1) * TK); };
     // The segments one after the other; the next one is looked up ahead, for its Q.
     int count = 0, count_next = 0;
+    bool on = share > 0, fresh = true;
     auto look_ahead = [&] {
       count_next = 0;
-      while (share > 0 && count_next == 0) {  // (a share can end before an item's first tile)
-        if (cur_next.w == cur_next.tiles + ITEM_WEIGHT) next(pp, cur_next);
+      while (on && count_next == 0) {  // (a part can end before an item's first tile)
         int from;
+        if (!fresh && !(on = go_on(cur_next, share, part))) break;
+        fresh = false;
         count_next = take(cur_next, share, from);
       }
       count_next = (int)uniform((uint32_t)count_next);
@@ -667,7 +692,8 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   } else {
     // ------------------------------------------------------------ softmax
     Cursor cur;
-    int64_t share = start(cur);
+    int part = 0;
+    int64_t share = start(part, cur);
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
     const int q = warp >> 2;
     const int row = q * 128 + (warp & 3) * 32 + lane;
@@ -684,13 +710,10 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       return ok;
     };
     int done = 0, seg = 0;  // done: parities only
-    while (share > 0) {
+    for (bool on = share > 0; on; on = go_on(cur, share, part)) {
       int tile;
       const int count = take(cur, share, tile);
-      if (count == 0) {
-        if (share > 0) next(pp, cur);
-        continue;
-      }
+      if (count == 0) continue;
       const int toks = tokens(cur);
       const bool in = t_in < toks, idle = !__any_sync(0xFFFFFFFFu, in);
       const int t_row = cur.rt * pp.per + t_in;
@@ -802,7 +825,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       if (tid == 0 && !last_tile)
         p.cuts[blockIdx.x] = make_int4(cur.first + cur.rt * pp.per, cur.h, toks * p.g, attn_cut(true, tile == 0));
       constexpr int PART = ROWS * (D + 2);
-      float* part = p.ws + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * PART;
+      float* partial = p.ws + ((int64_t)blockIdx.x * 2 + (tile == 0 ? 1 : 0)) * PART;
       const unsigned* bad = s_bad + (seg & (BAD_BUFS - 1)) * BAD_WORDS;
       unsigned any_bad = 0;
 #pragma unroll
@@ -859,7 +882,6 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         if (ok && in && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
         done += count;
         ++seg;
-        if (share > 0) next(pp, cur);
         continue;
       }
 #pragma unroll 1
@@ -914,7 +936,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
                 const float x = __shfl_xor_sync(0xFFFFFFFFu, lane & h ? lo : hi, h);
                 (lane & h ? lo : hi) = x;
               }
-        float* to = part + (row & ~7) * D + c + (lane & 7) * 4;
+        float* to = partial + (row & ~7) * D + c + (lane & 7) * 4;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<float4*>(to + k * D) = make_float4(a[k * 4], a[k * 4 + 1], a[k * 4 + 2], a[k * 4 + 3]);
@@ -925,12 +947,11 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       if (whole) {
         if (ok && in && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
       } else if (ok) {
-        part[ROWS * D + row] = m;
-        part[ROWS * D + ROWS + row] = l;
+        partial[ROWS * D + row] = m;
+        partial[ROWS * D + ROWS + row] = l;
       }
       done += count;
       ++seg;
-      if (share > 0) next(pp, cur);
     }
   }
 
