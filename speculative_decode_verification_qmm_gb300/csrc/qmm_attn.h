@@ -40,7 +40,8 @@ cudaError_t launch_attn_tc(const AttnParams& p, bool bf16, int D, const void* km
 // Sums of the partials that a launch with those tiles left (qmm_attn_join.cu).
 cudaError_t launch_attn_join(const AttnParams& p, bool bf16, int D, int tk, int rows, int sms, cudaStream_t st);
 
-// The same for the prompt attention: rows a row tile.
+// The same for the prompt attention, by at most ATTN_PROMPT_GRID_MAX CTAs: rows a row tile.
+constexpr int ATTN_PROMPT_GRID_MAX = 160;
 cudaError_t launch_prompt_join(const AttnParams& p, bool bf16, int D, int rows, int sms, cudaStream_t st);
 
 // Whether a description of rotary positions fits heads of D (qmm_rope.cu).

@@ -16,7 +16,10 @@
 // each reads what its worker left (AttnParams::cuts) and joins the item that goes
 // on behind the worker's range, if one began in it.
 // Items of the prompt attention (qmm_prompt.cu) are joined by cuts always; there a cut
-// holds the item's first row among the packed ones, its head and its number of rows.
+// holds the item's first row among the packed ones, its head and its number of rows.  A
+// few long items can be all that there is: the CTAs share out the cuts that begin an item, as many
+// to each (64 rows of 32 heads of 64 behind 20,000: 38 us with CTAs for every worker, so 24;
+// 1,024 rows, 12 heads of 128: 23 and 21).
 // Everything that does not depend on the partials is done before the wait for
 // the kernel that writes them (programmatic dependent launch).  As a tail of the
 // attention kernels' last CTA of an item the same sums took up to 30 us (64
@@ -34,6 +37,7 @@ constexpr int WARPS = 4;
 constexpr int RU = 4;  // rows of a lane
 constexpr int U = 2;   // parts in flight
 constexpr int CTAS_PER_SM = 8;
+constexpr int GRID_MAX = ATTN_PROMPT_GRID_MAX;
 enum { ITEMS, CUTS_OF_TREES, CUTS_OF_PROMPTS };
 
 template <bool BF16, int D, int MODE>
@@ -46,7 +50,7 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
   __shared__ float s_m[WARPS][RPC], s_l[WARPS][RPC];
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
+  int unit = blockIdx.x / chunks, chunk = blockIdx.x - unit * chunks;
   AttnCursor cur{};
   int c0 = unit, c1 = unit;
   if constexpr (!CUTS) {
@@ -65,7 +69,49 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
     c1 = attn_owner(u + nt - 1, W, G);
   }
   pdl_wait();  // every CTA: the call has not ended before the attention kernel has
-  if constexpr (CUTS) {
+  if constexpr (PROMPT) {
+    // The CTAs share out the cuts that begin an item, as one warp finds them.  (By all four, 1.5 us more.)
+    __shared__ int s_item[6];
+    if (warp == 0) {
+      int4 cut[GRID_MAX / 32];
+      unsigned begins[GRID_MAX / 32];
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < GRID_MAX / 32; ++k)
+        cut[k] = k * 32 + lane + 1 < p.grid ? __ldcg(p.cuts + k * 32 + lane) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < GRID_MAX / 32; ++k) {
+        begins[k] = __ballot_sync(0xFFFFFFFFu, cut[k].w == 1);
+        n += __popc(begins[k]);
+      }
+      chunk = n ? blockIdx.x / n : 0;
+      unit = n ? blockIdx.x - chunk * n : 0;
+      c0 = c1 = -1;
+#pragma unroll
+      for (int k = 0; k < GRID_MAX / 32; ++k) {
+        const bool here = cut[k].w == 1 && __popc(begins[k] & ((1u << lane) - 1)) == unit;
+        if (here) s_item[3] = cut[k].x, s_item[4] = cut[k].y, s_item[5] = cut[k].z;
+        const unsigned at = __ballot_sync(0xFFFFFFFFu, here);
+        if (at) c0 = k * 32 + __ffs(at) - 1;
+        unit -= __popc(begins[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < GRID_MAX / 32; ++k) {
+        // the first worker from the next one on whose last unit is not of this item
+        const unsigned end = __ballot_sync(0xFFFFFFFFu, k * 32 + lane > c0 && cut[k].w != 2);
+        if (end && c1 < 0) c1 = k * 32 + __ffs(end) - 1;
+      }
+      if (lane == 0) s_item[0] = n, s_item[1] = c0, s_item[2] = c1;
+    }
+    __syncthreads();
+    const int n = s_item[0];
+    if (n == 0) return;
+    chunks = gridDim.x / n;  // (n < grid <= gridDim.x)
+    chunk = blockIdx.x / n;
+    if (chunk >= chunks) return;
+    c0 = s_item[1], c1 = s_item[2];
+    cur.b = s_item[3], cur.h = s_item[4], cur.rt = s_item[5];
+  } else if constexpr (CUTS) {
     const int4 cut = __ldcg(p.cuts + c0);
     if (cut.w == 1) {
       // the first worker from the next one on whose last unit is not of this item,
@@ -95,7 +141,8 @@ __global__ void __launch_bounds__(WARPS * 32, D == 128 ? 7 : 5) attn_join_kernel
   }
   const int sub = lane % LPR, row = lane / LPR;
 
-  const bool alone = c1 - c0 < 4 && (CUTS || left >= 128);  // a warp joins its rows alone
+  // a warp joins its rows alone
+  const bool alone = c1 - c0 < 4 && (PROMPT ? chunks * RPC < left : CUTS || left >= 128);
   const int from = alone ? c0 : c0 + warp, step = alone ? 1 : WARPS;
   const int first = alone ? (chunk * WARPS + warp) * RPC : chunk * RPC;
   const int hop = chunks * (alone ? WARPS * RPC : RPC);
@@ -181,7 +228,7 @@ cudaError_t launch(const AttnParams& p, int tk, int rows, int ctas, cudaStream_t
   const int64_t most = (ctas + units - 1) / units;
   if (chunks > most) chunks = (int)most;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * chunks));
+  cfg.gridDim = dim3((unsigned)(MODE == CUTS_OF_PROMPTS ? ctas : units * chunks));
   cfg.blockDim = dim3(WARPS * 32);
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -206,7 +253,7 @@ cudaError_t launch_one(const AttnParams& p, int tk, int rows, int sms, cudaStrea
 
 template <bool BF16, int D>
 cudaError_t launch_prompts(const AttnParams& p, int rows, int sms, cudaStream_t st) {
-  return p.grid > 1 ? launch<BF16, D, CUTS_OF_PROMPTS>(p, 0, rows, CTAS_PER_SM * sms, st) : cudaSuccess;
+  return p.grid > 1 ? launch<BF16, D, CUTS_OF_PROMPTS>(p, 0, rows, (D == 128 ? 7 : CTAS_PER_SM) * sms, st) : cudaSuccess;
 }
 
 }  // namespace

@@ -228,6 +228,25 @@ bool attn_solo(const AttnParams& p, int64_t cap, int ctas, int D) {
   return tiles <= 2 && cap <= SOLO_MAX / tiles && (int64_t)p.B * p.Hkv * D >= (int64_t)3 * 128 * ctas;
 }
 
+// Rows of a row tile.  256 rows read K and V half as often, but an item of theirs takes longer to
+// begin and end, and there are fewer items to share out.  What the lengths on the device are, the
+// host takes from the rows on average and from what the table holds; where it holds far
+// more than is used, 256 costs as much as the following figures say.  128 : 256 rows, us, all with
+// one sequence from nothing unless said:
+// heads of 128: 64/8 heads, 1,024 rows 41 : 44, 2,048 85 : 94, 4,096 253 : 243, 16 times 200 rows behind
+// 500 100 : 119, 512 behind 20,000 278 : 241; 40/20 heads, 8,192 rows 579 : 512; 12/12 heads, 4,096
+// rows 64 : 71, 512 behind 20,000 72 : 69.  It is the cache tiles of an item that count.
+// heads of 64: 12/12 heads, 1,024 rows 17 : 21, 8 times 300 20 : 23, 16 times 200 behind 500 35 : 34,
+// 512 behind 20,000 52 : 49; 32/4 heads, 512 rows 16 : 19, 1,024 25 : 25, 4,096 103 : 95, 8 times 300
+// 30 : 28, 16 times 200 behind 500 48 : 46.  There (the row tiles run apart) it is the work for each CTA.
+int prompt_rows(int D, int g, int64_t N, int B, int64_t capacity, int Hkv, int grid) {
+  if (N * g <= (int64_t)128 * B) return 128;  // no more rows than that, on average
+  const int64_t n = (N + B - 1) / B, seen = capacity - n / 2, tiles = seen > 128 ? seen / 128 : 1;
+  if (D == 128) return tiles >= 20 ? 256 : 128;
+  const int64_t items = (n * g + 255) / 256 * B * Hkv;
+  return items * (tiles + 3) >= (int64_t)8 * grid ? 256 : 128;
+}
+
 }  // namespace
 
 extern "C" {
@@ -492,12 +511,11 @@ int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* a, void* stream) 
   p.cuts = h->cuts;
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
-  p.grid = h->sm_count;
+  p.grid = h->sm_count < ATTN_PROMPT_GRID_MAX ? h->sm_count : ATTN_PROMPT_GRID_MAX;
   p.row0 = (int64_t)a->layer * d.n_pages * d.n_kv_heads * d.page_size;
   pp.starts = a->starts;
   pp.N = (int)a->N;
-  // a row tile of 128 where a sequence's rows of a head are no more on average
-  pp.rows = a->N * p.g <= (int64_t)128 * a->B ? 128 : 256;
+  pp.rows = prompt_rows(d.head_dim, p.g, a->N, a->B, (int64_t)a->table_width << h->page_shift, p.Hkv, p.grid);
   pp.per = pp.rows / p.g;
   p.R = pp.rows;
   const bool bf16 = d.dtype == QMM_DT_BF16;
