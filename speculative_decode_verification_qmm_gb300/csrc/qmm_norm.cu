@@ -10,7 +10,9 @@
 // unrounded; the inputs of its next rows are on their way into shared memory meanwhile.
 // They are copied in whole 16-byte groups, which at a row's ends may hold other values,
 // so that rows need no alignment.
-// What bounds it: memory for many rows, the chain load -> sum -> sum for few.
+// What bounds it: memory for many rows (8,192 rows of 5,120, bf16 + fp32 with a norm of both to bf16: 68.8
+// us, 6.1 TB/s, 91 % of a copy; with a gate a row too, 80 us and 5.2 TB/s), the chain load -> sum -> sum
+// for few (8 rows: 2.5 us).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -42,7 +44,7 @@ struct NormParams {
   float eps, scale, inv_n;
 };
 
-constexpr int SHORT = 512;
+constexpr int SHORT = 64;
 constexpr int MAX_DEVICES = 64;
 
 // Entries of a thread: vectors of V, a group's threads side by side.  FULL: the group's
@@ -191,7 +193,8 @@ __device__ __forceinline__ void one_row(const NormParams& p, int64_t m, const ch
   }
 }
 
-// Short rows: a warp each.
+// Short rows: a warp each.  (20,000 rows of 64: 8.3 us, by CTAs of a warp 8.6, of 7 6.6 : 10.3; of 128 9.8 :
+// 8.5, of 384 with 16 entries a lane 21.5 : 18.8.)
 template <int E, int V>
 __global__ void __launch_bounds__(256) norm_short_kernel(const __grid_constant__ NormParams p) {
   const int lane = threadIdx.x & 31;
@@ -271,12 +274,7 @@ template <int V>
 cudaError_t launch_short(const NormParams& p, int sms, cudaStream_t st) {
   const int64_t need = (p.M + 7) / 8, most = 8ll * sms;
   const unsigned grid = (unsigned)(need < most ? need : most);
-  if (p.N <= 128)
-    norm_short_kernel<4, V><<<grid, 256, 0, st>>>(p);
-  else if (p.N <= 256)
-    norm_short_kernel<8, V><<<grid, 256, 0, st>>>(p);
-  else
-    norm_short_kernel<16, V><<<grid, 256, 0, st>>>(p);
+  norm_short_kernel<4, V><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -301,7 +299,9 @@ cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) 
   const int threads = ((p.N + E - 1) / E + 31) / 32 * 32;
   const int ys = p.y_dt == QMM_DT_F32 ? 4 : 2, rs = p.res_dt == QMM_DT_F32 ? 4 : 2;
   const int stage = (p.y ? (p.N * ys + 31) & ~15 : 0) + ((p.N * rs + 31) & ~15) + (p.gate && p.ld_gate ? (p.N * 4 + 31) & ~15 : 0);
-  // CTAs that an SM's registers allow (64 a thread), and two to four stages of shared memory each
+  // CTAs that an SM's registers allow (64 a thread), and two to four stages of shared memory each.
+  // (Straight from memory 8,192 rows of 5,120 take 77.7 us instead of 68.8, 8,000 of 2,048 35.4
+  // instead of 31.1, 2,000 of 16,000 76.6 instead of 70.6.)
   int ctas = 1024 / threads;
   while (ctas > 1 && SMEM / ctas < 2 * stage + 1024) --ctas;
   int stages = (SMEM / ctas - 1024) / stage;
@@ -320,7 +320,12 @@ cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) 
 template <int V>
 cudaError_t launch(const NormParams& p, int dev, int sms, cudaStream_t st) {
   if (p.N <= SHORT) return launch_short<V>(p, sms, st);
-  if (p.N <= 2048) return launch_long<8, V>(p, dev, sms, st);
+  // Few rows wait for one another's sums least with few entries a thread, many rows want few
+  // threads for those sums.  us, of bf16 + fp32 to bf16, 8 : 16 entries: 8 rows of 777 2.7 : 3.7, of 2,048
+  // 2.4 : 2.5, of 5,000 3.3 : 3.2; 20,000 rows of 1,024 37.3 : 34.6, of 2,048 69.8 : 65.5; 4 : 8 entries, 20,000
+  // rows of 128 8.5 : 9.6.  (16 : 32 entries, 2,000 rows of 16,000: 70.6 : 128, for registers.)
+  if (p.N <= 128) return launch_long<4, V>(p, dev, sms, st);
+  if (p.N <= (p.M <= 2 * sms ? 2048 : 512)) return launch_long<8, V>(p, dev, sms, st);
   return p.N <= 16384 ? launch_long<16, V>(p, dev, sms, st) : launch_long<32, V>(p, dev, sms, st);
 }
 

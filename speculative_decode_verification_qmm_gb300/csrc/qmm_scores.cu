@@ -29,7 +29,7 @@ constexpr int MAX_T = QMM_TREE_MAX_T;
 constexpr int THREADS = 256;
 constexpr int E = 8;  // entries of a thread
 constexpr int RANGE = THREADS * E;
-constexpr int AHEAD = 2;
+constexpr int CTAS_PER_SM = 4;
 
 struct AdjustParams {
   const void* scores;
@@ -146,8 +146,8 @@ __device__ __forceinline__ uint32_t bits_of(uint32_t loaded) {
   return r;
 }
 
-template <int DT, bool WIDE>
-__global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constant__ AdjustParams p) {
+template <int DT, bool WIDE, int AHEAD>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) adjust_kernel(const __grid_constant__ AdjustParams p) {
   __shared__ int s_token[MAX_T];                // place in the range
   __shared__ unsigned long long s_path[MAX_T];  // the nodes of a node's path whose tokens lie in the range
   __shared__ int s_up[MAX_T];
@@ -303,16 +303,26 @@ __global__ void __launch_bounds__(THREADS, 4) adjust_kernel(const __grid_constan
 template <int DT>
 cudaError_t launch_adjust(const AdjustParams& p, int B, bool wide, int sms, cudaStream_t st) {
   AdjustParams q = p;
-  const int64_t ranges = (p.V + RANGE - 1) / RANGE, ctas = ranges * B;
-  // all nodes of a sequence in one CTA, unless that leaves SMs idle
-  int64_t parts = (4ll * sms + ctas - 1) / ctas;
-  if (parts > p.T) parts = p.T;
-  q.per = (int)((p.T + parts - 1) / parts);
+  const int64_t ranges = (p.V + RANGE - 1) / RANGE, ctas = ranges * B, slots = (int64_t)CTAS_PER_SM * sms;
+  // How many CTAs share a sequence's nodes: what takes the fewest nodes one after another,
+  // where a CTA begins as long as two nodes take.  (32 x 16 nodes of 50,256, bf16: 31.3 us by one CTA, in two
+  // waves the second of which is a third full, 27.4 by two, in three waves; 8 x 16 of 50,257, fp32: 16.3
+  // by four, 15.6 by six; 64 nodes of 50,256: 9.9 by 22 in one wave, 11.2 by 32 in two.)
+  int64_t best = INT64_MAX;
+  for (int per = 1; per <= p.T; ++per) {
+    const int64_t cost = (ctas * ((p.T + per - 1) / per) + slots - 1) / slots * (per + 2);
+    if (cost <= best) best = cost, q.per = per;
+  }
   const dim3 grid((unsigned)ranges, (unsigned)B, (unsigned)((p.T + q.per - 1) / q.per));
-  if (wide)
-    adjust_kernel<DT, true><<<grid, THREADS, 0, st>>>(q);
+  // Two nodes in flight, but for a CTA's only node, and where entries are loaded one by one, which
+  // keeps enough in flight.  (One : two, us: 32 x 16 nodes of 151,936, bf16, 74 : 66; 8 nodes of
+  // 151,936, one a CTA, 4.5 : 5.0; 32 x 16 of 50,257, bf16, 36 : 38.)
+  if (wide && q.per > 1)
+    adjust_kernel<DT, true, 2><<<grid, THREADS, 0, st>>>(q);
+  else if (wide)
+    adjust_kernel<DT, true, 1><<<grid, THREADS, 0, st>>>(q);
   else
-    adjust_kernel<DT, false><<<grid, THREADS, 0, st>>>(q);
+    adjust_kernel<DT, false, 1><<<grid, THREADS, 0, st>>>(q);
   return cudaGetLastError();
 }
 

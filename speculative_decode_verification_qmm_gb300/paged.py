@@ -149,16 +149,18 @@ def qmm_cache_append(h, layer, q, k, v, q_out, page_table, lens, starts, rope=No
     """q CUDA [N, Hq, D] (or None), k, v [N, Hkv, D] in fp32, bf16 or f16, q_out
     [N, Hq, D] in the cache's type; page_table int32 [B, pages]; lens int32 [B];
     starts int32 [B + 1]; positions int32 [N]; rope: a Rope; asynchronous."""
-    qs = os = (0, 0, 0)
-    if q is not None:
-        qs, os = q.stride(), q_out.stride()
-    ks, vs = k.stride(), v.stride()
+    none = (0, 0)
+    _cache_append(h, layer, q, k, v, q_out, page_table, lens, starts, rope, positions, stream, none if q is None else q.stride(),
+                  k.stride(), v.stride(), none if q is None else q_out.stride(), page_table.stride(0))
+
+
+def _cache_append(h, layer, q, k, v, q_out, table, lens, starts, rope, positions, stream, qs, ks, vs, os, ld_table):
     rc = load().qmm_cache_append(h, _APPEND.pack(
         _APPEND.size, _dtype(k.dtype), layer, lens.shape[0], k.shape[0], 0 if q is None else q.data_ptr(), k.data_ptr(),
         v.data_ptr(), 0 if q is None else q_out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os[0], os[1],
-        page_table.data_ptr(), page_table.stride(0), page_table.shape[1], lens.data_ptr(), starts.data_ptr(),
+        table.data_ptr(), ld_table, table.shape[1], lens.data_ptr(), starts.data_ptr(),
         0 if positions is None else positions.data_ptr(), 0 if rope is None else rope.address),
-        _stream_ptr(stream, k.device.index))
+        _stream_ptr(stream, k.get_device()))
     if rc:
         _check("qmm_cache_append", rc)
 
@@ -166,11 +168,16 @@ def qmm_cache_append(h, layer, q, k, v, q_out, page_table, lens, starts, rope=No
 def qmm_prompt_attention(h, layer, q, page_table, lens, starts, out, lse=None, scale=None, stream=None) -> None:
     """q, out CUDA [N, Hq, D]; page_table int32 [B, pages]; lens int32 [B]; starts
     int32 [B + 1]; lse fp32 [N, Hq] or None; asynchronous."""
-    qs, os = q.stride(), out.stride()
+    _prompt_attention(h, layer, q, page_table, lens, starts, out, lse, scale, stream, q.stride(), out.stride(),
+                      page_table.stride(0))
+
+
+def _prompt_attention(h, layer, q, table, lens, starts, out, lse, scale, stream, qs, os, ld_table):
+    N, _, D = q.shape
     rc = load().qmm_prompt_attention(h, _PROMPT.pack(
-        _PROMPT.size, layer, lens.shape[0], page_table.shape[1], q.shape[0], q.data_ptr(), out.data_ptr(), qs[0], qs[1],
-        os[0], os[1], 0 if lse is None else lse.data_ptr(), page_table.data_ptr(), page_table.stride(0), lens.data_ptr(),
-        starts.data_ptr(), q.shape[2] ** -0.5 if scale is None else scale), _stream_ptr(stream, q.device.index))
+        _PROMPT.size, layer, lens.shape[0], table.shape[1], N, q.data_ptr(), out.data_ptr(), qs[0], qs[1],
+        os[0], os[1], 0 if lse is None else lse.data_ptr(), table.data_ptr(), ld_table, lens.data_ptr(),
+        starts.data_ptr(), D ** -0.5 if scale is None else scale), _stream_ptr(stream, q.get_device()))
     if rc:
         _check("qmm_prompt_attention", rc)
 
@@ -370,15 +377,18 @@ class PagedCache:
             raise ValueError("k must be [N, n_kv_heads, head_dim]")
         dt, at, i32 = k.dtype, self._device, torch.int32
         N, D = k.shape[0], self.head_dim
-        new, wide = (N, self.n_kv_heads, D), (N, self.n_q_heads, D)
-        _dtype(dt)
-        _strided("k", k, dt, new, at)
-        _strided("v", v, dt, new, at)
+        new, wide, ks, vs = (N, self.n_kv_heads, D), (N, self.n_q_heads, D), k.stride(), v.stride()
+        # the usual call's checks in one expression; what fails is named after it
+        if (k.shape != new or k.get_device() != at or ks[2] != 1 or v.shape != new or v.dtype is not dt
+                or v.get_device() != at or vs[2] != 1):
+            _strided("k", k, dt, new, at)
+            _strided("v", v, dt, new, at)
         self._packed(page_table, lens, starts)
         if positions is not None:
             _flat("positions", positions, i32, (N,), at)
         if rope is not None and rope.device_index != at:
             raise ValueError(f"rope must be on cuda:{at}, not cuda:{rope.device_index}")
+        qs = os = (0, 0)
         if q is None:
             if out is not None:
                 raise ValueError("out without q")
@@ -388,7 +398,9 @@ class PagedCache:
                 out = torch.empty(wide, dtype=self.dtype, device=k.device)
             else:
                 _strided("out", out, self.dtype, wide, at)
-        qmm_cache_append(self.handle, layer, q, k, v, out, page_table, lens, starts, rope, positions)
+            qs, os = q.stride(), out.stride()
+        _cache_append(self.handle, layer, q, k, v, out, page_table, lens, starts, rope, positions, None, qs, ks, vs, os,
+                      page_table.stride(0))
         return out
 
     def attend_prompt(self, layer: int, q, page_table, lens, starts, scale=None, out=None, lse=None, stream=None):
@@ -413,16 +425,22 @@ class PagedCache:
             lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device)
         else:
             _flat("lse", lse, torch.float32, (N, Hq), at)
-        qmm_prompt_attention(self.handle, layer, q, page_table, lens, starts, out, lse, scale)
+        _prompt_attention(self.handle, layer, q, page_table, lens, starts, out, lse, scale, None, q.stride(), out.stride(),
+                          page_table.stride(0))
         return out, lse
 
     def _packed(self, page_table, lens, starts):
         import torch
-        if lens.dim() != 1:
-            raise ValueError("lens must be [B]")
-        B = lens.shape[0]
-        self._table(page_table, lens, B)
-        _flat("starts", starts, torch.int32, (B + 1,), self._device)
+        seqs, table, at, i32 = lens.shape, page_table.shape, self._device, torch.int32
+        # the usual call's checks in one expression; what fails is named after it
+        if (len(seqs) != 1 or lens.dtype is not i32 or lens.get_device() != at or not lens.is_contiguous()
+                or len(table) != 2 or table[0] != seqs[0] or page_table.dtype is not i32 or page_table.get_device() != at
+                or page_table.stride(1) != 1 or starts.shape != (seqs[0] + 1,) or starts.dtype is not i32
+                or starts.get_device() != at or not starts.is_contiguous()):
+            if len(seqs) != 1:
+                raise ValueError("lens must be [B]")
+            self._table(page_table, lens, seqs[0])
+            _flat("starts", starts, i32, (seqs[0] + 1,), at)
 
     def commit(self, page_table, lens, path, accept, lens_out=None, stream=None):
         """The new lengths: the accepted branches' rows move behind the cached ones

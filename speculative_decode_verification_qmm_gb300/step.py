@@ -117,18 +117,17 @@ class Rope:
         dtype = (x.dtype if dtype is None else dtype) if out is None else out.dtype if dtype is None else dtype
         if at != self.device_index:
             raise ValueError(f"x must be on cuda:{self.device_index}, not cuda:{at}")
+        shape = x.shape
         _rows("x", x)
-        H, D = x.shape[-2:]
-        heads = H if heads is None else heads
-        _flat("positions", positions, torch.int32, tuple(x.shape[:-2]), at)
+        _flat("positions", positions, torch.int32, shape[:-2], at)
         if out is None:
-            out = torch.empty(x.shape, dtype=dtype, device=x.device)
+            out = torch.empty(shape, dtype=dtype, device=x.device)
         else:
-            _strided("out", out, dtype, x.shape, at)
+            _strided("out", out, dtype, shape, at)
         if x.numel() == 0:
             return out
         _current("rotate", at)
-        qmm_rotate(x, out, positions, self, heads)
+        qmm_rotate(x, out, positions, self, shape[-2] if heads is None else heads)
         return out
 
 
@@ -136,24 +135,30 @@ def qmm_rotate(x, out, positions, rope, heads, stream=None) -> None:
     """x, out CUDA [B, T, H, D] or [T, H, D]; positions int32; rope: a Rope;
     asynchronous."""
     xs, os = x.stride(), out.stride()
-    B, xs, os = (1, (0, *xs), (0, *os)) if x.dim() == 3 else (x.shape[0], xs, os)
-    T, H, D = x.shape[-3:]
+    if len(xs) == 3:
+        B, (T, H, D), xs, os = 1, x.shape, (0, *xs), (0, *os)
+    else:
+        B, T, H, D = x.shape
     rc = load().qmm_rotate(_ROTATE.pack(
-        _ROTATE.size, _dtype(x.dtype), _dtype(out.dtype), B, T, H, heads, D, x.data_ptr(), out.data_ptr(), *xs[:3], *os[:3],
-        positions.data_ptr(), *rope._fields), _stream_ptr(stream, x.device.index))
+        _ROTATE.size, _dtype(x.dtype), _dtype(out.dtype), B, T, H, heads, D, x.data_ptr(), out.data_ptr(), xs[0], xs[1], xs[2],
+        os[0], os[1], os[2], positions.data_ptr(), *rope._fields), _stream_ptr(stream, x.get_device()))
     if rc:
         _check("qmm_rotate", rc)
 
 
 # ------------------------------------------------------------------ residual sums and norms
-def _matrix(name, t, shape, at):
-    """t [..., N] as [M, N] without a copy."""
+def _row_stride(name, t, shape, at):
+    """The distance of the rows of t [..., N]."""
+    if t.shape == shape and t.get_device() == at and t.is_contiguous():
+        return shape[-1]
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor, not on {t.device}")
     if t.get_device() != at:
         raise ValueError(f"{name} must be on cuda:{at}, not {t.device}")
+    if t.numel() == 0:
+        return shape[-1]
     if t.dim() != 2:
         try:
             t = t.view(-1, shape[-1])
@@ -161,7 +166,7 @@ def _matrix(name, t, shape, at):
             raise ValueError(f"{name}: its rows must lie a fixed distance apart") from None
     if t.stride(1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t
+    return t.stride(0)
 
 
 def residual_norm(residual, y=None, weight=None, bias=None, post_weight=None, post_bias=None, gate=None,
@@ -187,40 +192,48 @@ def residual_norm(residual, y=None, weight=None, bias=None, post_weight=None, po
         raise ValueError("post_bias without post_weight")
     if weight is None and not (bias is out is dtype is None):
         raise ValueError("bias, dtype and out are for weight")
-    shape, at = residual.shape, residual.get_device()
-    N = shape[-1]
-    f32 = torch.float32
-    r = _matrix("residual", residual, shape, at)
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight), ("post_bias", post_bias)):
-        if t is not None:
-            _flat(name, t, f32, (N,), at)
-    ld_gate = 0
+    shape, at, f32 = residual.shape, residual.get_device(), torch.float32
+    N, vector = shape[-1], shape[-1:]
+    ld = _row_stride("residual", residual, shape, at)
+    if weight is not None:
+        _flat("weight", weight, f32, vector, at)
+        if bias is not None:
+            _flat("bias", bias, f32, vector, at)
+    if post_weight is not None:
+        _flat("post_weight", post_weight, f32, vector, at)
+        if post_bias is not None:
+            _flat("post_bias", post_bias, f32, vector, at)
+    ld_y = ld_gate = ld_sums = ld_out = 0
     if gate is not None:
         if gate.dtype is not f32:
             raise TypeError(f"gate must be float32, not {gate.dtype}")
-        if gate.shape == (N,):
-            _flat("gate", gate, f32, (N,), at)
+        if gate.shape == vector:
+            _flat("gate", gate, f32, vector, at)
         else:
-            ld_gate = _matrix("gate", gate, shape, at).stride(0)
+            ld_gate = _row_stride("gate", gate, shape, at)
+    sums = residual
     if y is not None:
-        y = _matrix("y", y, shape, at)
+        ld_y = _row_stride("y", y, shape, at)
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=residual.device)
-        elif residual_out.dtype is not residual.dtype:
-            raise TypeError(f"residual_out must be {residual.dtype}, not {residual_out.dtype}")
+            sums, ld_sums = torch.empty(shape, dtype=residual.dtype, device=residual.device), N
+        else:
+            if residual_out.dtype is not residual.dtype:
+                raise TypeError(f"residual_out must be {residual.dtype}, not {residual_out.dtype}")
+            sums, ld_sums = residual_out, _row_stride("residual_out", residual_out, shape, at)
     if weight is not None:
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=residual.device)
-        elif dtype is not None and out.dtype is not dtype:
-            raise TypeError(f"out must be {dtype}, not {out.dtype}")
-    sums = None if y is None else _matrix("residual_out", residual_out, shape, at)
-    rows = None if out is None else _matrix("out", out, shape, at)
-    r_out = residual if y is None else residual_out
-    if residual.numel() == 0:
-        return r_out, out
+            out, ld_out = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=residual.device), N
+        else:
+            if dtype is not None and out.dtype is not dtype:
+                raise TypeError(f"out must be {dtype}, not {out.dtype}")
+            ld_out = _row_stride("out", out, shape, at)
+    numel = residual.numel()
+    if numel == 0:
+        return sums, out
     _current("residual_norm", at)
-    qmm_residual_norm(r, y, sums, rows, weight, bias, post_weight, post_bias, gate, ld_gate, scale, eps, centered)
-    return r_out, out
+    _residual_norm(numel // N, N, residual, ld, y, ld_y, None if y is None else sums, ld_sums, out, ld_out, weight, bias,
+                   post_weight, post_bias, gate, ld_gate, scale, eps, centered, _stream_ptr(None, at))
+    return sums, out
 
 
 def qmm_residual_norm(residual, y, residual_out, out, weight=None, bias=None, post_weight=None, post_bias=None, gate=None,
@@ -232,12 +245,20 @@ def qmm_residual_norm(residual, y, residual_out, out, weight=None, bias=None, po
     def ld(t):
         return 0 if t is None else t.stride(0)
 
+    _residual_norm(M, N, residual, ld(residual), y, ld(y), residual_out, ld(residual_out), out, ld(out), weight, bias,
+                   post_weight, post_bias, gate, ld_gate, scale, eps, centered, _stream_ptr(stream, residual.get_device()))
+
+
+def _residual_norm(M, N, residual, ld, y, ld_y, sums, ld_sums, out, ld_out, weight, bias, post_weight, post_bias, gate, ld_gate,
+                   scale, eps, centered, stream):
     dt = _dtype(residual.dtype)
     rc = load().qmm_residual_norm(_NORM.pack(
         _NORM.size, QMM_NORM_CENTERED if centered else 0, M, N, dt, dt if y is None else _dtype(y.dtype),
-        dt if out is None else _dtype(out.dtype), eps, residual.data_ptr(), ld(residual), _at(y), ld(y), _at(residual_out),
-        ld(residual_out), _at(out), ld(out), _at(weight), _at(bias), _at(post_weight), _at(post_bias), _at(gate), ld_gate,
-        scale), _stream_ptr(stream, residual.device.index))
+        dt if out is None else _dtype(out.dtype), eps, residual.data_ptr(), ld, 0 if y is None else y.data_ptr(), ld_y,
+        0 if sums is None else sums.data_ptr(), ld_sums, 0 if out is None else out.data_ptr(), ld_out,
+        0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+        0 if post_weight is None else post_weight.data_ptr(), 0 if post_bias is None else post_bias.data_ptr(),
+        0 if gate is None else gate.data_ptr(), ld_gate, scale), stream)
     if rc:
         _check("qmm_residual_norm", rc)
 
@@ -268,15 +289,24 @@ def adjust_scores(scores, tokens=None, parents=None, counts=None, prompt=None, r
     B, T, V = scores.shape
     words, at, i32, f32 = (V + 31) // 32, scores.get_device(), torch.int32, torch.float32
     _rows("scores", scores)
-    for name, t, dt, shape in (("tokens", tokens, i32, (B, T)), ("parents", parents, i32, (B, T)),
-                               ("n_tokens", n_tokens, i32, (B,)), ("repetition", repetition, f32, (B,)),
-                               ("frequency", frequency, f32, (B,)), ("presence", presence, f32, (B,))):
-        if t is not None:
-            _flat(name, t, dt, shape, at)
-    for name, t, dt, shape in (("counts", counts, i32, (B, V)), ("prompt", prompt, i32, (B, words)),
-                               ("mask", mask, i32, (B, T, words))):
-        if t is not None:
-            _strided(name, t, dt, shape, at)
+    if tokens is not None:
+        _flat("tokens", tokens, i32, (B, T), at)
+    if parents is not None:
+        _flat("parents", parents, i32, (B, T), at)
+    if n_tokens is not None:
+        _flat("n_tokens", n_tokens, i32, (B,), at)
+    if repetition is not None:
+        _flat("repetition", repetition, f32, (B,), at)
+    if frequency is not None:
+        _flat("frequency", frequency, f32, (B,), at)
+    if presence is not None:
+        _flat("presence", presence, f32, (B,), at)
+    if counts is not None:
+        _strided("counts", counts, i32, (B, V), at)
+    if prompt is not None:
+        _strided("prompt", prompt, i32, (B, words), at)
+    if mask is not None:
+        _strided("mask", mask, i32, (B, T, words), at)
     if bias is not None:
         _strided("bias", bias, f32, (V,) if bias.dim() == 1 else (B, V), at)
     if out is None:
@@ -302,7 +332,7 @@ def qmm_adjust_scores(scores, out, tokens=None, parents=None, counts=None, promp
         _at(tokens), _at(parents), _at(n_tokens), _at(counts), 0 if counts is None else counts.stride(0), _at(prompt),
         0 if prompt is None else prompt.stride(0), _at(repetition), _at(frequency), _at(presence), _at(bias),
         0 if bias is None or bias.dim() == 1 else bias.stride(0), _at(mask), ms[0], ms[1]),
-        _stream_ptr(stream, scores.device.index))
+        _stream_ptr(stream, scores.get_device()))
     if rc:
         _check("qmm_adjust_scores", rc)
 
