@@ -504,7 +504,8 @@ typedef struct {
   const void* q;             /* [N][n_q_heads][head_dim]; NULL: keys and values alone */
   const void* k;             /* [N][n_kv_heads][head_dim]                       */
   const void* v;
-  void* q_out;               /* [N][n_q_heads][head_dim] in the cache's type    */
+  void* q_out;               /* [N][n_q_heads][head_dim] in the cache's type; q
+                                itself where type and strides agree            */
   int64_t q_stride[2];       /* in elements: row, head; any                     */
   int64_t k_stride[2];
   int64_t v_stride[2];
@@ -525,7 +526,7 @@ typedef struct {
  * is out of range is skipped and reported (qmm_cache_sync_status).  The caller
  * sees to it that no two rows of a call have the same place.  Asynchronous.
  * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), q or q_out NULL alone,
- * bad struct_size, dtype or rope), SHAPE (layer, B, N, table_width, rope->dims), ALIGN (a pointer
+ * q_out == q with other strides or element size, bad struct_size, dtype or rope), SHAPE (layer, B, N, table_width, rope->dims), ALIGN (a pointer
  * not aligned to its element, ld_table < table_width with B > 1), DEVICE, CUDA. */
 int qmm_cache_append(qmm_cache_t h, const qmm_append_args* args, void* stream);
 
@@ -536,7 +537,7 @@ typedef struct {
   int32_t table_width;
   int64_t N;                 /* rows of q, out and lse, 0 .. QMM_CACHE_MAX_ROWS */
   const void* q;             /* [N][n_q_heads][head_dim], 16-byte aligned       */
-  void* out;                 /* [N][n_q_heads][head_dim], 16-byte aligned       */
+  void* out;                 /* [N][n_q_heads][head_dim], 16-byte aligned; not q */
   int64_t q_stride[2];       /* in elements: row, head; multiples of 8          */
   int64_t out_stride[2];
   float* lse;                /* [N][n_q_heads], contiguous, or NULL             */
@@ -556,7 +557,7 @@ typedef struct {
  * hold, NaN and infinities included.  Rows of q past starts[B], and their outputs,
  * are not touched.  Numerics as in qmm_tree_attention; equal calls give equal
  * bits.  Asynchronous.
- * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), bad struct_size or scale), SHAPE
+ * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), out == q, bad struct_size or scale), SHAPE
  * (layer, B, N or table_width out of range), ALIGN (pointers, strides, ld_table <
  * table_width; not strides of dimensions of one entry), DEVICE, CUDA.  Lengths,
  * starts and page ids are checked on the device (qmm_cache_sync_status): a sequence
@@ -582,7 +583,7 @@ typedef struct {
   int64_t ld_residual;
   const void* y;            /* the block's output, or NULL                      */
   int64_t ld_y;
-  void* residual_out;       /* may be residual itself; with y only              */
+  void* residual_out;       /* with y only                                      */
   int64_t ld_residual_out;
   void* out;                /* or NULL: the residual sum alone                  */
   int64_t ld_out;
@@ -601,9 +602,11 @@ typedef struct {
  *     out = norm(r') weight + bias
  * with norm(x) = x / sqrt(mean(x^2) + eps), or, QMM_NORM_CENTERED, the same of
  * x - mean(x).  Without y, r' is the residual and residual_out is not written.
- * Arithmetic and sums in fp32, the sums in an order fixed by N; out is of the
- * unrounded r'.  Asynchronous.  Errors: INVALID_ARG (NULL, bad struct_size, flags,
- * dtype, eps or scale; neither y nor out), SHAPE, ALIGN (a pointer not aligned to
+ * Arithmetic and sums in fp32, the sums in an order fixed by N and by whether all rows
+ * begin on four entries; out is of the unrounded r'.  residual_out and out, which differ, may each be the residual or y
+ * where element size and row stride agree.  Asynchronous.  Errors: INVALID_ARG (NULL, bad
+ * struct_size, flags, dtype, eps or scale; neither y nor out; an output onto another
+ * one or onto an input that it does not lie like), SHAPE, ALIGN (a pointer not aligned to
  * its element, a row stride below N), DEVICE, CUDA. */
 int qmm_residual_norm(const qmm_norm_args* args, void* stream);
 

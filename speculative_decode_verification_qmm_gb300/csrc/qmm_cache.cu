@@ -429,6 +429,10 @@ int qmm_cache_append(qmm_cache_t h, const qmm_append_args* a, void* stream) {
       (((uintptr_t)a->page_table | (uintptr_t)a->lens | (uintptr_t)a->starts | (uintptr_t)a->positions) & 3) ||
       (a->B > 1 && a->ld_table < a->table_width))
     return QMM_ERR_ALIGN;
+  // in place: every element is read by the thread that writes it, if it stays where it is
+  if (a->N > 0 && a->q && a->q == a->q_out &&
+      (elem != 2 || (a->N > 1 && a->q_stride[0] != a->q_out_stride[0]) || (d.n_q_heads > 1 && a->q_stride[1] != a->q_out_stride[1])))
+    return QMM_ERR_INVALID_ARG;
   rc = check_current(h);
   if (rc != QMM_OK) return rc;
   if (a->N == 0) return QMM_OK;
@@ -472,6 +476,7 @@ int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* a, void* stream) 
   if (!a || a->struct_size != sizeof(qmm_prompt_args)) return QMM_ERR_INVALID_ARG;
   if ((a->N != 0 && (!a->q || !a->out)) || !a->page_table || !a->lens || !a->starts) return QMM_ERR_INVALID_ARG;
   if (!(a->scale > 0.f) || !isfinite(a->scale)) return QMM_ERR_INVALID_ARG;
+  if (a->N > 0 && a->q == a->out) return QMM_ERR_INVALID_ARG;  // q is read again where V is not finite
   const qmm_cache_desc& d = h->d;
   if (a->layer < 0 || a->layer >= d.n_layers || a->B < 1 || a->B > d.max_batch || a->N < 0 || a->N > QMM_CACHE_MAX_ROWS ||
       a->table_width < 1 || ((int64_t)a->table_width << h->page_shift) > INT32_MAX - 4096)

@@ -320,12 +320,13 @@ cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) 
 template <int V>
 cudaError_t launch(const NormParams& p, int dev, int sms, cudaStream_t st) {
   if (p.N <= SHORT) return launch_short<V>(p, sms, st);
-  // Few rows wait for one another's sums least with few entries a thread, many rows want few
-  // threads for those sums.  us, of bf16 + fp32 to bf16, 8 : 16 entries: 8 rows of 777 2.7 : 3.7, of 2,048
-  // 2.4 : 2.5, of 5,000 3.3 : 3.2; 20,000 rows of 1,024 37.3 : 34.6, of 2,048 69.8 : 65.5; 4 : 8 entries, 20,000
-  // rows of 128 8.5 : 9.6.  (16 : 32 entries, 2,000 rows of 16,000: 70.6 : 128, for registers.)
+  // By N alone, so that a row's sums do not depend on how many others there are.  Few rows are
+  // done sooner with few entries a thread, many rows want few threads for a sum.  us, of bf16 + fp32
+  // to bf16, 8 : 16 entries: 8 rows of 777 2.7 : 3.7, of 1,024 2.3 : 2.5, of 2,048 2.4 : 2.5; 20,000 rows of
+  // 777 46.5 : 40.2, of 1,024 37.3 : 34.6, of 2,048 69.8 : 65.5; 4 : 8 entries, 20,000 rows of 128
+  // 8.5 : 9.6.  (16 : 32 entries, 2,000 rows of 16,000: 70.6 : 128, for registers.)
   if (p.N <= 128) return launch_long<4, V>(p, dev, sms, st);
-  if (p.N <= (p.M <= 2 * sms ? 2048 : 512)) return launch_long<8, V>(p, dev, sms, st);
+  if (p.N <= 1024) return launch_long<8, V>(p, dev, sms, st);
   return p.N <= 16384 ? launch_long<16, V>(p, dev, sms, st) : launch_long<32, V>(p, dev, sms, st);
 }
 
@@ -351,6 +352,14 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
   if (a->M > 1 && (a->ld_residual < a->N || (a->y && (a->ld_y < a->N || a->ld_residual_out < a->N)) ||
                    (a->out && a->ld_out < a->N) || (a->gate && a->ld_gate && a->ld_gate < a->N)))
     return QMM_ERR_ALIGN;
+  // onto an input: every element is read by the thread that writes it, if it stays where it is
+  auto moves = [&](const void* to, int64_t ld, int size, const void* from, int64_t ld_from, int size_from) {
+    return to && to == from && (size != size_from || (a->M > 1 && ld != ld_from));
+  };
+  if ((a->y && a->residual_out == a->out) || (a->y && moves(a->residual_out, a->ld_residual_out, rs, a->residual, a->ld_residual, rs)) ||
+      (a->y && moves(a->residual_out, a->ld_residual_out, rs, a->y, a->ld_y, ys)) || moves(a->out, a->ld_out, os, a->y, a->ld_y, ys) ||
+      moves(a->out, a->ld_out, os, a->residual, a->ld_residual, rs))
+    return QMM_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   const int rc = host_check_device(&dev, &sms);
   if (rc != QMM_OK) return rc;

@@ -368,7 +368,7 @@ class PagedCache:
     def append(self, layer: int, q, k, v, page_table, lens, starts, rope=None, positions=None, out=None, stream=None):
         """Writes the packed rows' keys, turned by their positions, and values behind
         the cached rows, and returns their turned queries in the cache's type (None
-        where q is None).  See qmm_cache_append."""
+        where q is None); out may be q.  See qmm_cache_append."""
         import torch
         if stream is not None:  # the result is allocated on the stream that writes it
             with torch.cuda.stream(stream):

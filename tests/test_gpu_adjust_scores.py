@@ -68,6 +68,13 @@ def test_sizes(B, T, V, dtype):
     Case(B, T, V, dtype, seed=V).check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,V", [(24, 9, 10001), (24, 9, 10000), (61, 7, 15008), (61, 7, 15009), (300, 2, 2048), (700, 1, 99)])
+def test_several_nodes_of_a_range(B, T, V, dtype):
+    """Some, all or one of a sequence's nodes walked by the same threads."""
+    Case(B, T, V, dtype, seed=V).check()
+
+
 @pytest.mark.parametrize("V", [999, 2304])
 @pytest.mark.parametrize("have", [(), ("mask",), ("bias",), ("bias", "mask"), ("repetition", "prompt"), ("frequency", "counts"),
                                   ("presence", "tokens"), ("presence", "frequency", "tokens", "parents"), ("counts", "prompt", "tokens"),

@@ -53,6 +53,29 @@ def test_shapes(dtype, D, Hq, Hkv, page, lens, counts):
     run(Prompt(dtype, D, Hq, Hkv, page, lens, counts, seed=D + Hq))
 
 
+# Row tiles are of 256 rows where sequences have more than 128 on average and the table has room for
+# many cache tiles: here always.
+WIDE = 160_000
+
+
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,page,lens,counts", [s for s in SHAPES if sum(s[6]) * s[2] // s[3] > 128 * len(s[6])] + [
+    ("f16", 128, 8, 1, 16, [130, 0, 3], [77, 1, 33]), ("bf16", 64, 12, 4, 128, [1, 500], [90, 257]), ("bf16", 128, 7, 7, 64, [0], [1000])])
+def test_row_tiles_of_256(dtype, D, Hq, Hkv, page, lens, counts):
+    run(Prompt(dtype, D, Hq, Hkv, page, lens, counts, extra_columns=WIDE // page, seed=D + Hq + 1))
+
+
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,page,lens,counts", [
+    ("bf16", 128, 8, 1, 16, [20000], [9]),                     # one item over all SMs
+    ("bf16", 128, 16, 2, 64, [20000], [64]),                   # few items of 256 rows
+    ("f16", 64, 16, 2, 128, [9000, 300], [40, 3]),
+    ("f16", 64, 8, 1, 16, [30000], [70]),
+    ("bf16", 64, 4, 2, 32, [6000, 0, 100, 9000], [1, 700, 0, 130]),
+    ("f16", 128, 4, 4, 16, [(37 * i) % 300 for i in range(97)], [(11 * i) % 23 for i in range(97)]),  # sequences, 32 at a time
+])
+def test_long_chains_of_parts(dtype, D, Hq, Hkv, page, lens, counts):
+    run(Prompt(dtype, D, Hq, Hkv, page, lens, counts, seed=D + len(lens)))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("sigma", [0.01, 6.0])
 def test_flat_and_sharp_rows(dtype, sigma):
@@ -60,10 +83,11 @@ def test_flat_and_sharp_rows(dtype, sigma):
     run(Prompt(dtype, 128, 4, 2, 16, [300, 0], [200, 500], sigma=sigma, seed=3))
 
 
+@pytest.mark.parametrize("columns", [0, WIDE // 16])
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f16", 64)])
-def test_growing_scores(dtype, D):
+def test_growing_scores(dtype, D, columns):
     """Every later key fits better: the running maximum moves in every tile."""
-    p = Prompt(dtype, D, 2, 1, 16, [900], [300], seed=4)
+    p = Prompt(dtype, D, 2, 1, 16, [900], [300], extra_columns=columns, seed=4)
     n = 1200
     ids = p.table[0].long()
     grow = torch.linspace(0.1, 4.0, n, device="cuda")
@@ -83,9 +107,10 @@ def test_rows_that_no_sequence_has(fill, counts):
 
 @pytest.mark.parametrize("dtype,D,Hq,Hkv,L,n", [("bf16", 128, 2, 2, 100, 260), ("f16", 64, 8, 1, 3, 150), ("bf16", 64, 2, 1, 0, 40),
                                                ("f16", 128, 1, 1, 128, 400)])
-def test_later_rows_that_are_not_finite(dtype, D, Hq, Hkv, L, n):
+@pytest.mark.parametrize("columns", [0, WIDE // 16])
+def test_later_rows_that_are_not_finite(dtype, D, Hq, Hkv, L, n, columns):
     """A value or key of a new row that is infinite or NaN counts for the rows from it on."""
-    p = Prompt(dtype, D, Hq, Hkv, 16, [L], [n], seed=7)
+    p = Prompt(dtype, D, Hq, Hkv, 16, [L], [n], extra_columns=columns, seed=7)
     ids = p.table[0].long()
     for j, what, where, pool in ((L + 1, math.inf, 3, p.v_pool), (L + n // 2, -math.inf, D - 1, p.v_pool), (L + n // 2 + 1, math.nan, 5, p.v_pool),
                                  (L + n - 1, math.nan, 0, p.v_pool), (L + n - 2, math.nan, 1, p.k_pool)):
@@ -134,8 +159,9 @@ def test_offsets_past_32_bits():
     run(p)
 
 
-def test_equal_calls_give_equal_bits():
-    p = Prompt("bf16", 128, 8, 2, 16, [1000, 0, 50], [200, 300, 7], seed=12)
+@pytest.mark.parametrize("D,columns", [(128, 0), (128, WIDE // 16), (64, 0), (64, WIDE // 16)])
+def test_equal_calls_give_equal_bits(D, columns):
+    p = Prompt("bf16", D, 8, 2, 16, [1000, 0, 50], [200, 300, 7], extra_columns=columns, seed=12)
     cache = p.make_cache(q)
     a, la = p.call(cache)
     for _ in range(5):
@@ -198,8 +224,9 @@ def test_bad_sizes_and_pages_are_reported():
 
 
 @pytest.mark.parametrize("counts", [[5], [400]])
-def test_expired_waits(counts):
-    p = Prompt("bf16", 128, 4, 2, 16, [300], counts, seed=15)
+@pytest.mark.parametrize("D,columns", [(128, 0), (128, WIDE // 16), (64, 0), (64, WIDE // 16)])
+def test_expired_waits(counts, D, columns):
+    p = Prompt("bf16", D, 4, 2, 16, [300], counts, extra_columns=columns, seed=15)
     cache = p.make_cache(q)
     q.qmm_debug_set_cache_wait_limit(cache.handle, 0)
     p.call(cache)
@@ -246,6 +273,7 @@ def test_refusals():
     refuse(ValueError, lse=torch.empty(40, 5, device="cuda"))
     for scale in (0.0, -1.0, math.inf, math.nan):
         refuse(q.QmmError, scale=scale)
+    refuse(q.QmmError, out=p.q)
     refuse(q.QmmError, layer=1)
     refuse(q.QmmError, layer=-1)
     refuse(q.QmmError, q=torch.empty(40, 4, 72, dtype=torch.bfloat16, device="cuda")[:, :, 4:68])  # not on 16 bytes

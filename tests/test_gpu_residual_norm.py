@@ -126,6 +126,51 @@ def test_strides_in_place_and_leading_dimensions(N):
     assert all((w[..., N:] == 3).all() for w in wide.values())
 
 
+# more rows than are at work at a time: the next ones are fetched ahead
+@pytest.mark.parametrize("M,N", [(11000, 7), (6000, 65), (5000, 128), (5000, 100), (5000, 300), (2600, 1001), (700, 3001), (700, 5120),
+                                 (200, 16384), (200, 17000), (310, 20001)])
+@pytest.mark.parametrize("res,y,out", [("bf16", "f32", "bf16"), ("f32", "bf16", "f16"), ("f16", "f16", "f32")])
+def test_many_rows(M, N, res, y, out):
+    check(make(M, N, res, y, post=True, gate="full", seed=N), dtype=U.TYPES[out])
+    check(make(M, N, res, y, gate="row", bias=True, seed=M), dtype=U.TYPES[out], centered=True)
+
+
+@pytest.mark.parametrize("M,N", [(5, 777), (700, 3001), (2000, 520)])
+@pytest.mark.parametrize("ahead", [1, 2, 5])
+def test_many_rows_with_strides(M, N, ahead):
+    """Rows that begin anywhere, and results onto the inputs."""
+    a = make(M, N, "bf16", "f32", post=True, gate="full", seed=ahead)
+    wide = {k: torch.full((M, N + 2 * ahead + 1), 3.0, dtype=a[k].dtype, device="cuda") for k in ("residual", "y", "gate")}
+    for k, w in wide.items():
+        w[:, ahead:ahead + N] = a[k]
+    b = a | {k: w[:, ahead:ahead + N] for k, w in wide.items()}
+    r, h = check(b, dtype=torch.float32)
+    want, h = r.clone(), h.clone()
+    r2, h2 = q.residual_norm(**b, residual_out=b["residual"], out=b["y"], dtype=torch.float32)
+    assert r2 is b["residual"] and h2 is b["y"] and torch.equal(r2, want) and torch.equal(h2, h)
+    for w in wide.values():
+        assert (w[:, :ahead] == 3).all() and (w[:, ahead + N:] == 3).all()
+
+
+def test_results_onto_inputs():
+    for M, N in ((6, 900), (3000, 900)):
+        a = make(M, N, "bf16", "bf16", seed=8)
+        r, h = q.residual_norm(**a)
+        for onto in (dict(residual_out="y"), dict(out="y"), dict(out="residual"), dict(residual_out="residual", out="y"), dict(residual_out="y", out="residual")):
+            b = a | dict(residual=a["residual"].clone(), y=a["y"].clone())
+            r2, h2 = q.residual_norm(**b, **{k: b[v] for k, v in onto.items()})
+            assert torch.equal(r2, r) and torch.equal(h2, h), onto
+        b = a | dict(residual=a["residual"].clone())
+        x = torch.empty_like(r)
+        flat = b["residual"].view(-1)
+        for bad in (dict(out=x, residual_out=x), dict(out=b["y"].view(-1).view(torch.float32)[:M // 2 * N].view(-1, N)),
+                    dict(out=flat.as_strided((M // 2, N), (2 * N, 1)))):
+            c = b if bad["out"].shape[0] == M else b | {k: b[k][:M // 2] for k in ("residual", "y")}
+            with pytest.raises(q.QmmError) as e:
+                q.residual_norm(**c, **bad)
+            assert e.value.code == q.QMM_ERR_INVALID_ARG
+
+
 def test_rows_do_not_depend_on_their_company():
     for N in (128, 5120, 1001):
         a = make(700, N, seed=8, post=True)

@@ -267,6 +267,25 @@ def test_append_strides_and_keys_alone():
     cache.close()
 
 
+@pytest.mark.parametrize("src", ["f16", "bf16"])
+def test_append_turns_queries_in_place(src):
+    """With the queries' own strides, whatever 16-bit type they come in."""
+    a = Append("f16", src, 128, 4, 2, 16, [10, 20], [30, 40], 128, True, seed=6)
+    cache = a.make_cache(q)
+    want = a.check(cache)
+    x = a.x.clone()
+    out = x.view(torch.float16)
+    assert cache.append(0, x, a.k, a.v, a.table, a.d_lens, a.d_starts, rope=a.rope, out=out) is out
+    assert torch.equal(out, want)
+    other = a.x.clone()
+    for bad in (other.view(torch.float16).view(-1).as_strided(other.shape, (other.stride(0) // 2, other.stride(1), 1)),
+                other.view(torch.float16).view(-1).as_strided(other.shape, (other.stride(0), other.stride(1) - 8, 1))):
+        with pytest.raises(q.QmmError) as e:
+            cache.append(0, other, a.k, a.v, a.table, a.d_lens, a.d_starts, rope=a.rope, out=bad)
+        assert e.value.code == q.QMM_ERR_INVALID_ARG
+    cache.close()
+
+
 def test_append_bad_places_are_skipped():
     a = Append("bf16", "f32", 64, 2, 1, 16, [20, 30, 40], [30, 20, 10], 64, True, seed=3)
     cache = a.make_cache(q)

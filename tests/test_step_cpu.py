@@ -130,13 +130,16 @@ def test_norm(L, memory):
     m = (memory & ~15) + 16
 
     def call(**kw):
-        a = _args(_lib.qmm_norm_args, **(dict(M=2, N=8, res_dtype=0, y_dtype=2, out_dtype=0, eps=1e-6, residual=m, ld_residual=8, y=m, ld_y=8,
-                                              residual_out=m, ld_residual_out=8, out=m, ld_out=8, weight=m, scale=1.0) | kw))
+        a = _args(_lib.qmm_norm_args, **(dict(M=2, N=8, res_dtype=0, y_dtype=2, out_dtype=0, eps=1e-6, residual=m, ld_residual=8, y=m + 512, ld_y=8,
+                                              residual_out=m, ld_residual_out=8, out=m + 1024, ld_out=8, weight=m, scale=1.0) | kw))
         return L.qmm_residual_norm(ctypes.byref(a), None)
 
     assert L.qmm_residual_norm(None, None) == q.QMM_ERR_INVALID_ARG
     for kw in (dict(struct_size=8), dict(flags=2), dict(res_dtype=3), dict(y_dtype=3), dict(out_dtype=3), dict(residual=None),
-               dict(y=None, out=None), dict(residual_out=None), dict(weight=None), dict(eps=-1.0), dict(eps=math.nan), dict(scale=math.inf)):
+               dict(y=None, out=None), dict(residual_out=None), dict(weight=None), dict(eps=-1.0), dict(eps=math.nan), dict(scale=math.inf),
+               # onto one another, and onto inputs that lie otherwise
+               dict(out=m), dict(residual_out=m + 1024), dict(ld_residual_out=9), dict(residual_out=m + 512), dict(out=m + 512),
+               dict(out=m, y=None, ld_out=9), dict(out=m + 512, y_dtype=1, ld_out=9)):
         assert call(**kw) == q.QMM_ERR_INVALID_ARG, kw
     for kw in (dict(M=0), dict(M=1 << 31), dict(N=0), dict(N=32769)):
         assert call(**kw) == q.QMM_ERR_SHAPE, kw
@@ -144,7 +147,8 @@ def test_norm(L, memory):
                dict(ld_residual=7), dict(ld_residual_out=0), dict(gate=m, ld_gate=4)):
         assert call(**kw) == q.QMM_ERR_ALIGN, kw
     if not torch.cuda.is_available():
-        assert call() == q.QMM_ERR_DEVICE
+        for kw in (dict(), dict(out=m, y=None), dict(out=m + 512, y_dtype=1), dict(out=m + 512, y_dtype=1, ld_out=9, M=1)):
+            assert call(**kw) == q.QMM_ERR_DEVICE
 
 
 def test_adjust(L, memory):
