@@ -4,11 +4,15 @@ A small decoder (Q4_0 matrices) runs one batched forward over the trees of two
 sequences a step, with the library's operators for everything that touches
 weights, cache or vocabulary:
 
+    prompt     PagedCache.append turns its rows by their positions into the cache,
+               PagedCache.attend_prompt is their attention, in one piece
     draft      a tree a sequence from a bigram table (siblings drawn without
                replacement)
-    forward    Matrix.verify for the projections, PagedCache.attend for the
-               attention: every node sees the cached rows and its ancestors
-    verify     verify_sample walks each tree by rejection sampling
+    forward    Matrix.verify for the projections, Rope.rotate for the positions,
+               PagedCache.attend for the attention (every node sees the cached rows and
+               its ancestors), residual_norm between the blocks
+    verify     adjust_scores penalises repeated tokens, verify_sample walks each
+               tree by rejection sampling, count_tokens counts what it emitted
     commit     PagedCache.commit moves the accepted branch behind the cached rows
 
 At the end one sequence is forked and both go on from the same prefix.
@@ -46,34 +50,49 @@ class Model:
                        for _ in range(LAYERS)]
         self.head = matrix(VOCAB, HIDDEN, sharp * HIDDEN ** -0.5)
         # the drafter: the target's own scores without its layers, and some noise
-        bigram = self.norm(self.embed) @ (self.head.dequantize().t())
-        self.bigram = bigram + torch.randn(VOCAB, VOCAB, generator=g, device="cuda")
-        self.freq = 10000.0 ** (-torch.arange(0, HEAD_DIM, 2, device="cuda") / HEAD_DIM)
+        self.ones = torch.ones(HIDDEN, device="cuda")
+        _, start = q.residual_norm(self.embed, weight=self.ones, dtype=torch.float32)
+        self.bigram = start @ self.head.dequantize().t() + torch.randn(VOCAB, VOCAB, generator=g, device="cuda")
+        self.rope = q.Rope(*q.rope_frequencies(HEAD_DIM), layout="interleaved")
 
     @staticmethod
-    def norm(x):
-        return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
+    def product(w, x):
+        """Of any number of rows, 16 at a time."""
+        return torch.cat([w.verify(part) for part in x.split(16)])
 
-    def rotate(self, x, positions):
-        a = positions[..., None, None] * self.freq
-        c, s = a.cos(), a.sin()
-        x, y = x[..., ::2], x[..., 1::2]
-        return torch.stack([x * c - y * s, x * s + y * c], -1).flatten(-2)
+    def blocks(self, tokens, attention):
+        """The normed state [rows, HIDDEN] after all layers; attention(layer, qkv) of the rows'
+        heads [rows, heads, HEAD_DIM]."""
+        x = self.embed[tokens.long()].view(-1, HIDDEN)
+        _, h = q.residual_norm(x, weight=self.ones)
+        for i, w in enumerate(self.layers):
+            att = attention(i, self.product(w["qkv"], h).view(len(x), -1, HEAD_DIM))
+            x, h = q.residual_norm(x, self.product(w["out"], att.reshape(len(x), -1)), self.ones)
+            up = self.product(w["up"], h)
+            y = self.product(w["down"], (torch.nn.functional.silu(up[:, :MLP]) * up[:, MLP:]).bfloat16())
+            x, h = q.residual_norm(x, y, self.ones)
+        return h
 
     def forward(self, cache, tokens, depths, table, lens, mask):
         """Scores [B, T, V] after every node of tokens [B, T]."""
         B, T = tokens.shape
-        x = self.embed[tokens.long()].view(B * T, HIDDEN)
-        positions = (lens[:, None] + depths).float()
-        for i, w in enumerate(self.layers):
-            qkv = w["qkv"].verify(self.norm(x).bfloat16()).view(B, T, -1, HEAD_DIM)
-            qk = self.rotate(qkv[:, :, :HEADS + KV_HEADS], positions)
-            x_q, x_k = qk[:, :, :HEADS].bfloat16(), qk[:, :, HEADS:].bfloat16()
-            att, _ = cache.attend(i, x_q, x_k, qkv[:, :, HEADS + KV_HEADS:].bfloat16(), table, lens, mask=mask)
-            x = x + w["out"].verify(att.view(B * T, -1))
-            up = w["up"].verify(self.norm(x).bfloat16())
-            x = x + w["down"].verify((torch.nn.functional.silu(up[:, :MLP]) * up[:, MLP:]).bfloat16())
-        return self.head.verify(self.norm(x).bfloat16()).view(B, T, VOCAB)
+        positions = (lens[:, None] + depths).int()
+
+        def attention(i, qkv):
+            x = self.rope.rotate(qkv.view(B, T, -1, HEAD_DIM), positions, heads=HEADS + KV_HEADS, dtype=torch.bfloat16)
+            return cache.attend(i, x[:, :, :HEADS], x[:, :, HEADS:HEADS + KV_HEADS], x[:, :, HEADS + KV_HEADS:], table, lens,
+                                mask=mask)[0]
+
+        return self.product(self.head, self.blocks(tokens, attention)).view(B, T, VOCAB)
+
+    def prompt(self, cache, tokens, table, lens, starts):
+        """Packed rows of prompts into the cache."""
+        def attention(i, qkv):
+            x, k, v = qkv.split([HEADS, KV_HEADS, KV_HEADS], 1)
+            x = cache.append(i, x, k, v, table, lens, starts, rope=self.rope)
+            return cache.attend_prompt(i, x, table, lens, starts)[0]
+
+        self.blocks(tokens, attention)
 
 
 class Decoder:
@@ -82,8 +101,9 @@ class Decoder:
     # node 0 is the last committed token; two branches from it, the first goes on
     PARENTS = [-1, 0, 0, 1, 1, 2, 3, 6]
 
-    def __init__(self, model, nodes=8, pages=64, temperature=1.0, seed=1):
+    def __init__(self, model, nodes=8, pages=64, temperature=1.0, seed=1, repetition=1.0, presence=0.0):
         self.model, self.temperature = model, temperature
+        self.repetition, self.presence = repetition, presence
         self.cache = q.PagedCache(LAYERS, pages, 16, HEADS, KV_HEADS, HEAD_DIM, max_batch=2)
         self.g = torch.Generator(device="cuda")
         self.g.manual_seed(seed)
@@ -94,13 +114,16 @@ class Decoder:
         """A sequence with all of the prompt but its last token in the cache."""
         seq = self.cache.new_sequence()
         seq.tokens = list(prompt)
-        body = seq.tokens[:-1]
-        for at in range(0, len(body), 16):  # chains of up to 16 rows, what one verify call takes
-            part = torch.tensor([body[at:at + 16]], dtype=torch.int32, device="cuda")
-            self.cache.reserve([seq], part.shape[1])
-            table, lens = self.cache.tables([seq])
-            self.model.forward(self.cache, part, torch.arange(part.shape[1], device="cuda")[None], table, lens, None)
-            self.cache.advance([seq], [part.shape[1]])
+        seq.counts = torch.zeros(VOCAB, dtype=torch.int32, device="cuda")  # what was emitted
+        words = [0] * (-(-VOCAB // 32))
+        for t in seq.tokens:
+            words[t // 32] |= 1 << t % 32
+        seq.prompt = torch.tensor([w - (w >> 31 << 32) for w in words], dtype=torch.int32, device="cuda")
+        body = torch.tensor(seq.tokens[:-1], dtype=torch.int32, device="cuda")
+        if len(body):
+            self.cache.reserve([seq], len(body))
+            self.model.prompt(self.cache, body, *self.cache.tables([seq]), self.cache.starts([len(body)]))
+            self.cache.advance([seq], [len(body)])
         return seq
 
     def draft(self, seqs):
@@ -131,23 +154,29 @@ class Decoder:
         tokens, drafted = self.draft(seqs)
         scores = self.model.forward(cache, tokens, torch.tensor([depths] * B, device="cuda"), table, lens,
                                     q.tree_mask(parents).cuda())
+        parents, counts = parents.cuda(), torch.stack([s.counts for s in seqs])
+        scores = q.adjust_scores(scores, tokens, parents, counts=counts, prompt=torch.stack([s.prompt for s in seqs]),
+                                 repetition=torch.full((B,), self.repetition, device="cuda"),
+                                 presence=torch.full((B,), self.presence, device="cuda"), out=scores)
         accept, path = q.verify_sample(
             scores, drafted, tokens, torch.rand(B, T, generator=self.g, device="cuda"),
-            torch.empty(B, VOCAB, device="cuda").exponential_(generator=self.g), parents=parents.cuda(),
+            torch.empty(B, VOCAB, device="cuda").exponential_(generator=self.g), parents=parents,
             temperature=torch.full((B,), self.temperature, device="cuda"))
+        q.count_tokens(counts, tokens, path, accept)
         cache.commit(table, lens, path, accept)
         # the host learns what was kept
         kept, walk, tokens = accept.tolist(), path.tolist(), tokens.tolist()
         for b, s in enumerate(seqs):
             k, last = kept[b]
             s.tokens += [tokens[b][n] for n in walk[b][:k]] + [last]
+            s.counts = counts[b]
             self.accepted += k
             self.steps += 1
         cache.advance(seqs, [k + 1 for k, _ in kept])
 
     def fork(self, seq):
         other = self.cache.fork(seq)
-        other.tokens = list(seq.tokens)
+        other.tokens, other.counts, other.prompt = list(seq.tokens), seq.counts, seq.prompt
         return other
 
     def check(self):
@@ -159,7 +188,7 @@ class Decoder:
 
 def main():
     model = Model()
-    d = Decoder(model)
+    d = Decoder(model, repetition=1.1, presence=0.2)
     seqs = [d.start(range(5, 45)), d.start([7, 1, 3])]
     for _ in range(20):
         d.step(seqs)
