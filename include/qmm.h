@@ -47,7 +47,11 @@
  *
  * Around the product, for steps that draft a tree: a paged key/value cache, the
  * nodes' attention over it, acceptance for sampled decoding, and the compaction
- * of the accepted branch (qmm_cache_create and what follows it below).
+ * of the accepted branch (qmm_cache_create and what follows it below).  Prompts of any
+ * length reach that cache and attend over it (qmm_cache_append, qmm_prompt_attention);
+ * between the products stand rotary positions, residual sums and norms (qmm_rotate,
+ * qmm_residual_norm), and before sampling penalties, biases and grammar masks
+ * (qmm_adjust_scores, qmm_count_tokens).
  *
  * Conventions for every entry point:
  *   - Return value: QMM_OK (0) or one of the QMM_ERR_* codes below.  No call

@@ -25,6 +25,14 @@
 // are replaced; of V, where 0 times NaN would, the loading warp takes the values that
 // are not finite out of the tiles that some row of the item does not see wholly, and
 // the rows that see them add them at the end.
+// What bounds it.  Heads of 128: the tensor cores with shared memory, which delivers both operands
+// of S at its full rate while TMA writes; 8,192 rows of 40/20 heads 513 us, 1,340 TFLOP/s, 71 % of a large
+// product's rate; 512 rows behind 65,536, 64/8 heads, 735 us, 1,490 TFLOP/s.  Heads of 64: the softmax,
+// whose exponentials take as long as the products and cannot all run beside them; 512 rows behind
+// 16,384, 64/8 heads, 152 us, 921 TFLOP/s.  Short prompts: an item's start and end, and the joining launch.
+// Tried and slower: waits by test instead of try (2 to 3 %), the wait for P's place after the first 32
+// exponentials instead of before them (heads of 64: 4 %), a register split between roles (spills stay).
+//
 // Every wait is bounded; on a timeout the CTA records it, its roles run out of
 // their loops without waiting, copies and MMAs in flight are drained and tensor
 // memory is freed.
@@ -45,6 +53,9 @@ namespace {
 constexpr int TK = 128;      // cache rows of a tile
 constexpr int BAD_BUFS = 16; // more than twice the segments that the rings hold
 constexpr int BAD_WORDS = 8; // an item's tokens after its first: at most 255
+// What an item costs besides its tiles, in tiles.  (1, 3, 6 and 12, us: 9 ragged prompts of up to
+// 1,501 rows, 28/4 heads of 64: 114, 112, 116, 126; 2,048 rows, 32/4 heads of 128: 72, 59, 60, 66; 16 of up
+// to 300, 64/8: 68, 66, 68, 66.)
 constexpr int ITEM_WEIGHT = 3;
 
 // Four softmax warps a row tile, two MMA warps, two loading warps.
