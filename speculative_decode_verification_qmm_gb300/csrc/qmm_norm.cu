@@ -193,8 +193,8 @@ __device__ __forceinline__ void one_row(const NormParams& p, int64_t m, const ch
   }
 }
 
-// Short rows: a warp each.  (20,000 rows of 64: 8.3 us, by CTAs of a warp 8.6, of 7 6.6 : 10.3; of 128 9.8 :
-// 8.5, of 384 with 16 entries a lane 21.5 : 18.8.)
+// Short rows: a warp each.  (Against CTAs of a warp, us: 20,000 rows of 7 6.6 : 10.3, of 64 8.3 : 8.6, of 128
+// 9.8 : 8.3; with 16 entries a lane, of 384 21.5 : 17.3.)
 template <int E, int V>
 __global__ void __launch_bounds__(256) norm_short_kernel(const __grid_constant__ NormParams p) {
   const int lane = threadIdx.x & 31;
@@ -203,9 +203,10 @@ __global__ void __launch_bounds__(256) norm_short_kernel(const __grid_constant__
                         row_of(p.gate, m, p.ld_gate, QMM_DT_F32), lane, 32, warp_sum);
 }
 
-// Longer rows: a CTA each; STAGED: `stages` of them in shared memory, else straight from memory.
+// Longer rows: a CTA each; STAGED: the next one's inputs on their way into shared memory, else
+// straight from memory.
 template <int E, int V, bool FULL, bool STAGED>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams p, int stages, int stage_bytes) {
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormParams p, int stage_bytes) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float s_sum[2][32];
   const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5;
@@ -246,20 +247,16 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
     cp_async_commit();
   };
   int64_t ahead = blockIdx.x;
-  for (int s = 0; s + 1 < stages; ++s, ahead += gridDim.x) request(ahead, s);
+  request(ahead, 0);
+  ahead += gridDim.x;
   int stage = 0;
   for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, ahead += gridDim.x) {
     // the row has come, and the last one's place is free
-    if (stages == 2)
-      cp_async_wait<0>();
-    else if (stages == 3)
-      cp_async_wait<1>();
-    else
-      cp_async_wait<2>();
+    cp_async_wait<0>();
     __syncthreads();
-    request(ahead, stage == 0 ? stages - 1 : stage - 1);
     const char* from = smem + stage * stage_bytes;
-    if (++stage == stages) stage = 0;
+    stage ^= 1;
+    request(ahead, stage);
     const char* y = from + skew(row_of(p.y, m, p.ld_y, p.y_dt));
     const char* res = from + y_room + skew(row_of(p.res, m, p.ld_res, p.res_dt));
     if (gates)
@@ -281,7 +278,7 @@ cudaError_t launch_short(const NormParams& p, int sms, cudaStream_t st) {
 constexpr int SMEM = 220 * 1024;  // of an SM, for stages
 
 template <int E, int V, bool FULL, bool STAGED>
-cudaError_t launch_kernel(const NormParams& p, int dev, unsigned grid, int threads, int stages, int stage, cudaStream_t st) {
+cudaError_t launch_kernel(const NormParams& p, int dev, unsigned grid, int threads, int stage, cudaStream_t st) {
   if (STAGED) {
     static std::atomic<bool> set[MAX_DEVICES];  // once for a device
     if (dev >= MAX_DEVICES || !set[dev].load(std::memory_order_relaxed)) {
@@ -290,7 +287,7 @@ cudaError_t launch_kernel(const NormParams& p, int dev, unsigned grid, int threa
       if (dev < MAX_DEVICES) set[dev].store(true, std::memory_order_relaxed);
     }
   }
-  norm_kernel<E, V, FULL, STAGED><<<grid, threads, stages * stage, st>>>(p, stages, stage);
+  norm_kernel<E, V, FULL, STAGED><<<grid, threads, STAGED ? 2 * stage : 0, st>>>(p, stage);
   return cudaGetLastError();
 }
 
@@ -299,22 +296,22 @@ cudaError_t launch_long(const NormParams& p, int dev, int sms, cudaStream_t st) 
   const int threads = ((p.N + E - 1) / E + 31) / 32 * 32;
   const int ys = p.y_dt == QMM_DT_F32 ? 4 : 2, rs = p.res_dt == QMM_DT_F32 ? 4 : 2;
   const int stage = (p.y ? (p.N * ys + 31) & ~15 : 0) + ((p.N * rs + 31) & ~15) + (p.gate && p.ld_gate ? (p.N * 4 + 31) & ~15 : 0);
-  // CTAs that an SM's registers allow (64 a thread), and two to four stages of shared memory each.
+  // CTAs that an SM's registers allow (64 a thread), with two stages of shared memory each; more
+  // stages leave less for the weights in L1 (8,192 rows of 1,024: 17.6 us with four, 15.9 with two).
   // (Straight from memory 8,192 rows of 5,120 take 77.7 us instead of 68.8, 8,000 of 2,048 35.4
   // instead of 31.1, 2,000 of 16,000 76.6 instead of 70.6.)
   int ctas = 1024 / threads;
   while (ctas > 1 && SMEM / ctas < 2 * stage + 1024) --ctas;
-  int stages = (SMEM / ctas - 1024) / stage;
-  stages = stages > 4 ? 4 : (stages < 2 ? 0 : stages);
   const int64_t most = (int64_t)ctas * sms;
-  if (p.M <= most) stages = 0;  // a row alone has no next one to wait for
+  // a row alone has no next one to wait for
+  const bool staged = SMEM / ctas >= 2 * stage + 1024 && p.M > most;
   const unsigned grid = (unsigned)(p.M < most ? p.M : most);
   const bool full = V == 4 && p.N == threads * E;
-  if (stages)
-    return full ? launch_kernel<E, V, V == 4, true>(p, dev, grid, threads, stages, stage, st)
-                : launch_kernel<E, V, false, true>(p, dev, grid, threads, stages, stage, st);
-  return full ? launch_kernel<E, V, V == 4, false>(p, dev, grid, threads, 0, 0, st)
-              : launch_kernel<E, V, false, false>(p, dev, grid, threads, 0, 0, st);
+  if (staged)
+    return full ? launch_kernel<E, V, V == 4, true>(p, dev, grid, threads, stage, st)
+                : launch_kernel<E, V, false, true>(p, dev, grid, threads, stage, st);
+  return full ? launch_kernel<E, V, V == 4, false>(p, dev, grid, threads, 0, st)
+              : launch_kernel<E, V, false, false>(p, dev, grid, threads, 0, st);
 }
 
 template <int V>
@@ -322,9 +319,9 @@ cudaError_t launch(const NormParams& p, int dev, int sms, cudaStream_t st) {
   if (p.N <= SHORT) return launch_short<V>(p, sms, st);
   // By N alone, so that a row's sums do not depend on how many others there are.  Few rows are
   // done sooner with few entries a thread, many rows want few threads for a sum.  us, of bf16 + fp32
-  // to bf16, 8 : 16 entries: 8 rows of 777 2.7 : 3.7, of 1,024 2.3 : 2.5, of 2,048 2.4 : 2.5; 20,000 rows of
-  // 777 46.5 : 40.2, of 1,024 37.3 : 34.6, of 2,048 69.8 : 65.5; 4 : 8 entries, 20,000 rows of 128
-  // 8.5 : 9.6.  (16 : 32 entries, 2,000 rows of 16,000: 70.6 : 128, for registers.)
+  // to bf16, 4 : 8 entries: 20,000 rows of 128 8.3 : 9.6, of 256 14.6 : 10.8, of 512 26.1 : 18.9; 8 : 16 entries:
+  // 8 rows of 777 2.7 : 3.6, 20,000 of 777 47 : 39, of 1,024 34.0 : 34.4, of 1,500 51.7 : 52.3, of 2,048
+  // 66.3 : 65.0; 16 : 32 entries, 2,000 rows of 16,000: 69 : 128, for registers.
   if (p.N <= 128) return launch_long<4, V>(p, dev, sms, st);
   if (p.N <= 1024) return launch_long<8, V>(p, dev, sms, st);
   return p.N <= 16384 ? launch_long<16, V>(p, dev, sms, st) : launch_long<32, V>(p, dev, sms, st);
