@@ -209,8 +209,9 @@ def measured_peak_gbs():
 def kernel_source_hash() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_decode_verification_qmm_gb300", "csrc")
-    # (the paged cache's, the attention's and the sampling's have no part in these workloads)
-    others = ("qmm_attn", "qmm_cache", "qmm_sample")
+    # (those of the paged cache, the attention, the sampling and what stands between the products
+    # have no part in these workloads)
+    others = ("qmm_attn", "qmm_cache", "qmm_sample", "qmm_prompt", "qmm_rope", "qmm_norm", "qmm_scores")
     for name in sorted(os.listdir(csrc)):
         if name.endswith((".cu", ".cuh", ".h")) and not name.startswith(others):
             with open(os.path.join(csrc, name), "rb") as f:
