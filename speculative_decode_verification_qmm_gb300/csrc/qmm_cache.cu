@@ -233,18 +233,19 @@ bool attn_solo(const AttnParams& p, int64_t cap, int ctas, int D) {
 // host takes from the rows on average and from what the table holds; where it holds far
 // more than is used, 256 costs as much as the following figures say.  128 : 256 rows, us, all with
 // one sequence from nothing unless said:
-// heads of 128: 64/8 heads, 1,024 rows 41 : 44, 2,048 85 : 94, 4,096 253 : 243, 16 times 200 rows behind
-// 500 100 : 119, 512 behind 20,000 278 : 241; 40/20 heads, 8,192 rows 579 : 512; 12/12 heads, 4,096
-// rows 64 : 71, 512 behind 20,000 72 : 69.  It is the cache tiles of an item that count.
-// heads of 64: 12/12 heads, 1,024 rows 17 : 21, 8 times 300 20 : 23, 16 times 200 behind 500 35 : 34,
-// 512 behind 20,000 52 : 49; 32/4 heads, 512 rows 16 : 19, 1,024 25 : 25, 4,096 103 : 95, 8 times 300
-// 30 : 28, 16 times 200 behind 500 48 : 46.  There (the row tiles run apart) it is the work for each CTA.
+// heads of 128: 64/8 heads, 1,024 rows 38 : 44, 2,048 85 : 94, 4,096 258 : 243, 16 times 200 rows behind
+// 500 98 : 119, 512 behind 20,000 281 : 237; 40/20 heads, 8,192 rows 581 : 512; 12/12 heads, 4,096
+// rows 62 : 71, 512 behind 20,000 71 : 67.  It is the cache tiles of an item that count.
+// heads of 64: 12/12 heads, 1,024 rows 17 : 21, 8 times 300 18 : 23, 16 times 200 behind 500 30 : 32, 4,096
+// 49 : 49, 512 behind 20,000 52 : 48; 32/4 heads, 512 rows 15 : 19, 2,048 40 : 41, 4,096 106 : 95, 8 times
+// 300 25 : 26, 16 times 200 behind 500 45 : 44.  There (the row tiles run apart) it is the work
+// for each CTA.
 int prompt_rows(int D, int g, int64_t N, int B, int64_t capacity, int Hkv, int grid) {
   if (N * g <= (int64_t)128 * B) return 128;  // no more rows than that, on average
   const int64_t n = (N + B - 1) / B, seen = capacity - n / 2, tiles = seen > 128 ? seen / 128 : 1;
   if (D == 128) return tiles >= 20 ? 256 : 128;
   const int64_t items = (n * g + 255) / 256 * B * Hkv;
-  return items * (tiles + 3) >= (int64_t)8 * grid ? 256 : 128;
+  return items * (tiles + 3) >= (int64_t)20 * grid ? 256 : 128;
 }
 
 }  // namespace

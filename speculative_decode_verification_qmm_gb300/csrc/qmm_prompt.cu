@@ -15,7 +15,8 @@
 // its place, the units before it are a sum of ceil((L + k i) / 128), which has a
 // closed form by Euclid's algorithm (floor_sum).  What is cut leaves (O, m, l)
 // partials to qmm_attn_join.cu.
-//   warps 0 .. 4 NQ - 1   softmax, rescaling, output; a thread owns a row
+//   warps 0 .. 7          softmax, rescaling, output; a thread owns a row, or, NQ = 1, half of
+//                         its columns: then its two threads tell each other their maxima
 //   two warps (NQ = 2: one) issue the MMAs
 //   two warps             load K and V, tensor copies of 16 rows, a ring each; Q by both
 // With NQ = 2 the row tiles take turns: O += P V of one, then its next S, while the
@@ -58,8 +59,15 @@ constexpr int BAD_WORDS = 8; // an item's tokens after its first: at most 255
 // to 300, 64/8: 68, 66, 68, 66.)
 constexpr int ITEM_WEIGHT = 3;
 
-// Four softmax warps a row tile, two MMA warps, two loading warps.
-constexpr int threads_of(int NQ) { return NQ * 128 + 128; }
+// Threads of a row: a single row tile's softmax has nothing else to run beside it.  (One : two, us: 75
+// rows, 40/20 heads of 128, 10.0 : 9.6; 8 times 300, 64/8, 57 : 49; 16 times 200 behind 500, 12/12, 42.1 : 39.8;
+// 1,024, 32/4 heads of 64, 24.3 : 23.4; most others within 2 %.  Two row tiles with two, heads of 64: 9
+// ragged prompts 113 : 119, 512 behind 20,000 98 : 102.)
+template <int NQ>
+constexpr int SPLIT = NQ == 1 ? 2 : 1;
+// Four softmax warps a row tile and thread of a row, two MMA warps, two loading warps.
+template <int NQ>
+constexpr int THREADS = NQ * 128 * SPLIT<NQ> + 128;
 template <int D, int NQ>
 struct Smem {
   static constexpr int TILE = TK * D * 2;           // one of K, V; also 128 rows of Q
@@ -71,12 +79,13 @@ struct Smem {
   static constexpr int V = K + KS * TILE;
   static constexpr int BAR = V + VS * TILE;
   // kfull[KS], kempty[KS], vfull[VS], vempty[VS], vland[VS], sfull[2], sfree[2],
-  // pfull[4], odone[2], olast[2], oempty[2], qfull, qempty, drain
-  static constexpr int NBAR = 2 * KS + 3 * VS + 17;
+  // pfull[4], odone[2], olast[2], oempty[2], qfull, qempty, drain, met[8]
+  static constexpr int NBAR = 2 * KS + 3 * VS + 25;
   static constexpr int BAD = BAR + NBAR * 8;        // rows with non-finite V, by segment
   static constexpr int FLAG = BAD + BAD_BUFS * BAD_WORDS * 4;  // [0] abort, [1] tensor memory
   static constexpr int START = FLAG + 16;           // the CTA's share, and the places of its first and last unit
-  static constexpr int BYTES = START + 80;
+  static constexpr int MEET = START + 80;           // what a row's threads tell each other: [turn][thread][row]
+  static constexpr int BYTES = MEET + (SPLIT<NQ> > 1 ? 2 * 2 * NQ * 128 * 4 : 0);
   static_assert(BYTES <= 232448, "shared memory of one CTA");
 };
 
@@ -333,13 +342,16 @@ __device__ __forceinline__ void clean(uint32_t tile, int r0, int left, int lane,
 }
 
 template <bool BF16, int D, int NQ>
-__global__ void __launch_bounds__(threads_of(NQ), 1)
+__global__ void __launch_bounds__(THREADS<NQ>, 1)
     prompt_kernel(const __grid_constant__ PromptParams pp, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
   using S = Smem<D, NQ>;
   const AttnParams& p = pp.a;
   constexpr int ROWS = NQ * 128;
-  constexpr int SUB = NQ, SW = TK / SUB;  // steps that P is handed over in, columns of one
+  constexpr int H = SPLIT<NQ>, W = TK / H;  // columns of S of a thread
+  // Steps that P is handed over in, columns of one.  Two threads of a row: one, since either may
+  // still rescale its part of O.
+  constexpr int SUB = H == 2 ? 1 : 2, SW = TK / SUB;
   constexpr int NB = 2 / NQ;              // buffers of S of a row tile
   constexpr uint32_t IDESC_S = tc_idesc_n(BF16 ? 1u : 0u, TK);
   constexpr uint32_t IDESC_O = tc_idesc_n(BF16 ? 1u : 0u, D) | (1u << 16);  // B along N
@@ -355,7 +367,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   // products), and the other loads Q.
   constexpr bool ONE = NQ == 2 && !APART;
   constexpr int ISSUERS = APART ? 2 : 1;  // that use a tile of K, or of V
-  constexpr int MMA_WARP = NQ * 4, MMA_WARPS = 2, LOAD_WARP = MMA_WARP + MMA_WARPS;
+  constexpr int MMA_WARP = NQ * 4 * H, MMA_WARPS = 2, LOAD_WARP = MMA_WARP + MMA_WARPS;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = smem_u32(smem);
@@ -363,8 +375,9 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
   constexpr uint32_t O_KFULL = S::BAR, O_KEMPTY = O_KFULL + S::KS * 8, O_VFULL = O_KEMPTY + S::KS * 8,
                      O_VEMPTY = O_VFULL + S::VS * 8, O_VLAND = O_VEMPTY + S::VS * 8, O_SFULL = O_VLAND + S::VS * 8,
                      O_SFREE = O_SFULL + 16, O_PFULL = O_SFREE + 16, O_ODONE = O_PFULL + 32, O_OLAST = O_ODONE + 16,
-                     O_OEMPTY = O_OLAST + 16, O_QFULL = O_OEMPTY + 16, O_QEMPTY = O_QFULL + 8, O_DRAIN = O_QEMPTY + 8;
-  // sfull, sfree: [row tile], NQ = 1: [buffer]; pfull: [row tile][step], NQ = 1: [buffer]
+                     O_OEMPTY = O_OLAST + 16, O_QFULL = O_OEMPTY + 16, O_QEMPTY = O_QFULL + 8, O_DRAIN = O_QEMPTY + 8, O_MET = O_DRAIN + 8;
+  // sfull, sfree: [row tile], NQ = 1: [buffer]; pfull: [row tile][step], NQ = 1: [buffer][step];
+  // met: [row tile][warp's rows]
   volatile int* s_flag = reinterpret_cast<volatile int*>(smem + S::FLAG);
   unsigned* s_bad = reinterpret_cast<unsigned*>(smem + S::BAD);
 
@@ -380,15 +393,16 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(base + O_SFULL + 8 * i, 1);
-      mbar_init(base + O_SFREE + 8 * i, APART ? 4 : 1);
+      mbar_init(base + O_SFREE + 8 * i, APART ? 4 * H : 1);
       mbar_init(base + O_ODONE + 8 * i, 1);
       mbar_init(base + O_OLAST + 8 * i, 1);
-      mbar_init(base + O_OEMPTY + 8 * i, 4);
+      mbar_init(base + O_OEMPTY + 8 * i, 4 * H);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(base + O_PFULL + 8 * i, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(base + O_PFULL + 8 * i, 4 * H);
     mbar_init(base + O_QFULL, 1);
     mbar_init(base + O_QEMPTY, 1);
     mbar_init(base + O_DRAIN, MMA_WARPS);
+    for (int i = 0; i < 8; ++i) mbar_init(base + O_MET + 8 * i, 2);
     for (int i = 0; i < BAD_BUFS * BAD_WORDS; ++i) s_bad[i] = 0;
     // a limit of 0 makes every wait give up
     s_flag[0] = base & 1023u ? DEV_ERR_SMEM_ALIGN : (p.wait_limit_ns == 0 ? DEV_ERR_TIMEOUT_EMPTY : 0);
@@ -637,7 +651,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       if (j == 0 && seg > 0 && !need(base + O_OEMPTY + 8 * q, seg - 1)) return false;
 #pragma unroll
       for (int sub = 0; sub < SUB; ++sub) {
-        if (!need(base + O_PFULL + 8 * (NQ == 2 ? 2 * q + sub : n & 1), s_phase(n))) return false;
+        if (!need(base + O_PFULL + 8 * (2 * s_index(q, n) + sub), s_phase(n))) return false;
         const uint32_t a = (APART ? tmem + COL_P + q * 64 : s_column(q, n)) + sub * (SW / 2), d = tmem + q * COL_Q + COL_O;
         const uint32_t b = desc_lo_mn(base + S::V + vslot * S::TILE + sub * SW * 128, S::HALF);
         tc_fence_after();
@@ -706,7 +720,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
     int part = 0;
     int64_t share = start(part, cur);
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, (uint32_t)s_flag[1], 0);
-    const int q = warp >> 2;
+    const int q = warp / (4 * H), half = H == 2 ? warp >> 2 & 1 : 0;  // the row's thread
     const int row = q * 128 + (warp & 3) * 32 + lane;
     const int t_in = row / p.g, i_row = row - t_in * p.g;  // token in the row tile, query head
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + q * COL_Q;
@@ -719,6 +733,20 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         ok = false;
       }
       return ok;
+    };
+    // The row's threads give each other a value: f(one's own, the other's).
+    float* const s_meet = reinterpret_cast<float*>(smem + S::MEET);
+    const uint32_t met = base + O_MET + 8 * (q * 4 + (warp & 3));
+    int meetings = 0;
+    auto meet = [&](float mine, float& other) {
+      const int at = (meetings & 1) * 2 * ROWS + row;
+      s_meet[at + half * ROWS] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(met);
+      if (!need(met, meetings)) return false;
+      other = s_meet[at + (half ^ 1) * ROWS];
+      ++meetings;
+      return true;
     };
     int done = 0, seg = 0;  // done: parities only
     for (bool on = share > 0; on; on = go_on(cur, share, part)) {
@@ -734,7 +762,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       for (int j = 0; j < count; ++j) {
         const int n = done + j;
         const uint32_t t_s = tl + (NB == 2 ? (n & 1) * TK : 0);
-        const uint32_t pfull = base + O_PFULL + 8 * (NQ == 2 ? 2 * q : n & 1);
+        const uint32_t pfull = base + O_PFULL + 16 * (NQ == 2 ? q : n & 1);  // of the first step
         need(base + O_SFULL + 8 * (NQ == 2 ? q : n & 1), NQ == 2 ? n : n >> 1);
         if (!ok) continue;
         if (idle) {  // no row of the warp is the item's: whatever P is, nobody looks
@@ -748,9 +776,9 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         }
         tc_fence_after();
         const int j0 = (tile + j) * TK;
-        uint32_t v[TK / 32][32];  // the row's scores
+        uint32_t v[W / 32][32];  // the thread's scores of the row
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c) tmem_ld32(t_s + c * 32, v[c]);
+        for (int c = 0; c < W / 32; ++c) tmem_ld32(t_s + half * W + c * 32, v[c]);
         tmem_wait_ld();
         if constexpr (APART) {
           tc_fence_before();
@@ -758,9 +786,9 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
           if (lane == 0) mbar_arrive(base + O_SFREE + 8 * q);
         }
         if (j0 + TK - 1 > all_see) {
-          const int last = sees - j0;
+          const int last = sees - j0 - half * W;
 #pragma unroll
-          for (int c = 0; c < TK / 32; ++c)
+          for (int c = 0; c < W / 32; ++c)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (c * 32 + i > last) v[c][i] = 0xFF800000u;  // -inf
@@ -781,11 +809,19 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         {
           float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < TK / 32; ++c)
+          for (int c = 0; c < W / 32; ++c)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
               x[(i >> 1) & 3] = fmaxf(x[(i >> 1) & 3], fmaxf(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1])));
           mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        }
+        if constexpr (H == 2) {
+          // (P can lie where the other thread's S did: it has read that)
+          tc_fence_before();
+          float other;
+          if (!meet(mx, other)) continue;
+          tc_fence_after();
+          mx = fmaxf(mx, other);
         }
         mx = mx * p.scale_log2 - ATTN_BASE_BELOW<BF16>;
         // P's place, and O, are free when the last product with V has ended: with P in the
@@ -802,7 +838,7 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
           l *= a;
           if (j > 0) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = half * (D / 16 / H); c < (half + 1) * (D / 16 / H); ++c) {
               uint32_t x[16];
               tmem_ld16(t_o + c * 16, x);
               tmem_wait_ld();
@@ -813,23 +849,28 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
           }
         }
         m2.x = m2.y = m == -INFINITY ? 0.f : -m;
-        const uint32_t t_p = APART ? tmem + ((uint32_t)((warp & 3) * 32) << 16) + COL_P + q * 64 : t_s;
+        const uint32_t t_p = (APART ? tmem + ((uint32_t)((warp & 3) * 32) << 16) + COL_P + q * 64 : t_s) + half * (W / 2);
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c) {
+        for (int c = 0; c < W / 32; ++c) {
           uint32_t w[16];
           powers(c, w);
           tmem_st16(t_p + c * 16, w);
-          if ((c + 1) % (SW / 32) == 0) {
+          if ((c + 1) % (W / 32 / SUB) == 0) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(pfull + 8 * (c / (SW / 32)));
+            if (lane == 0) mbar_arrive(pfull + 8 * (c / (W / 32 / SUB)));
           }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
 
       // ------------------------------------------------ end of the segment
+      if constexpr (H == 2) {
+        float other = 0.f;
+        if (ok && !idle) meet(l, other);
+        l += other;
+      }
       need(base + O_OLAST + 8 * q, seg);
       tc_fence_after();
       const bool last_tile = tile + count == cur.tiles, whole = tile == 0 && last_tile;
@@ -849,15 +890,16 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       if (whole && !any_bad && !idle) {
         // The rows' outputs are taken out of tensor memory, which is then free for the
         // next item, before they are stored.
-        uint32_t w[D / 2];
+        constexpr int DH = D / H, STEP = DH < 64 ? DH : 64;  // columns of a thread
+        uint32_t w[DH / 2];
 #pragma unroll
-        for (int c = 0; c < D; c += 64) {
-          uint32_t v[2][32];
-          tmem_ld32(t_o + c, v[0]);
-          tmem_ld32(t_o + c + 32, v[1]);
+        for (int c = 0; c < DH; c += STEP) {
+          uint32_t v[STEP / 32][32];
+#pragma unroll
+          for (int i = 0; i < STEP / 32; ++i) tmem_ld32(t_o + half * DH + c + 32 * i, v[i]);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 64; i += 2)
+          for (int i = 0; i < STEP; i += 2)
             w[(c + i) / 2] = pack16<BF16>(__uint_as_float(v[i >> 5][i & 31]) * inv, __uint_as_float(v[i >> 5][(i & 31) + 1]) * inv);
         }
         tc_fence_before();
@@ -868,11 +910,11 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
         bool have[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          rows[k] = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)to16, (lane & 28) + k)) + (lane & 3) * 8;
+          rows[k] = reinterpret_cast<uint16_t*>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)to16, (lane & 28) + k)) + half * DH + (lane & 3) * 8;
           have[k] = __shfl_sync(0xFFFFFFFFu, in && ok, (lane & 28) + k);
         }
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < DH; c += 32) {
           uint32_t* x = w + c / 2;
 #pragma unroll
           for (int h = 2; h > 0; h >>= 1)
@@ -890,13 +932,13 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
             if (have[k])
               *reinterpret_cast<uint4*>(rows[k] + c) = make_uint4(x[k * 4], x[k * 4 + 1], x[k * 4 + 2], x[k * 4 + 3]);
         }
-        if (ok && in && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
+        if (ok && in && half == 0 && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
         done += count;
         ++seg;
         continue;
       }
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = half * (D / H); c < (half + 1) * (D / H); c += 32) {
         uint32_t v[32];
         tmem_ld32(t_o + c, v);
         tmem_wait_ld();
@@ -956,8 +998,8 @@ __global__ void __launch_bounds__(threads_of(NQ), 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(base + O_OEMPTY + 8 * q);
       if (whole) {
-        if (ok && in && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
-      } else if (ok) {
+        if (ok && in && half == 0 && p.lse) p.lse[at * p.Hq + cur.h * p.g + i_row] = (m + log2f(l)) * 0.69314718055994531f;
+      } else if (ok && half == 0) {
         partial[ROWS * D + row] = m;
         partial[ROWS * D + ROWS + row] = l;
       }
@@ -983,7 +1025,7 @@ template <bool BF16, int D, int NQ>
 cudaError_t launch(const PromptParams& p, const void* kmap, const void* vmap, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.a.grid);
-  cfg.blockDim = dim3(threads_of(NQ));
+  cfg.blockDim = dim3(THREADS<NQ>);
   cfg.dynamicSmemBytes = Smem<D, NQ>::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute at;

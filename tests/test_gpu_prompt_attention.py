@@ -55,7 +55,7 @@ def test_shapes(dtype, D, Hq, Hkv, page, lens, counts):
 
 # Row tiles are of 256 rows where sequences have more than 128 on average and the table has room for
 # many cache tiles: here always.
-WIDE = 160_000
+WIDE = 400_000
 
 
 @pytest.mark.parametrize("dtype,D,Hq,Hkv,page,lens,counts", [s for s in SHAPES if sum(s[6]) * s[2] // s[3] > 128 * len(s[6])] + [
