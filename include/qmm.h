@@ -560,7 +560,9 @@ typedef struct {
  * Later rows do not influence it, whatever they or the rest of the last page
  * hold, NaN and infinities included.  Rows of q past starts[B], and their outputs,
  * are not touched.  Numerics as in qmm_tree_attention; equal calls give equal
- * bits.  Asynchronous.
+ * bits.  What a call costs depends on table_width too: a table about as wide as the
+ * sequences need lets the rows of a tile be chosen by how many cached rows they see.
+ * Asynchronous.
  * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), out == q, bad struct_size or scale), SHAPE
  * (layer, B, N or table_width out of range), ALIGN (pointers, strides, ld_table <
  * table_width; not strides of dimensions of one entry), DEVICE, CUDA.  Lengths,
