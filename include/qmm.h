@@ -609,11 +609,12 @@ typedef struct {
  * with norm(x) = x / sqrt(mean(x^2) + eps), or, QMM_NORM_CENTERED, the same of
  * x - mean(x).  Without y, r' is the residual and residual_out is not written.
  * Arithmetic and sums in fp32, the sums in an order fixed by N and by whether all rows
- * begin on four entries; out is of the unrounded r'.  residual_out and out, which differ, may each be the residual or y
- * where element size and row stride agree.  Asynchronous.  Errors: INVALID_ARG (NULL, bad
- * struct_size, flags, dtype, eps or scale; neither y nor out; an output onto another
- * one or onto an input that it does not lie like), SHAPE, ALIGN (a pointer not aligned to
- * its element, a row stride below N), DEVICE, CUDA. */
+ * begin on four entries; out is of the unrounded r'.  residual_out and out, which
+ * differ, may each be the residual, y or the gate where element size and row stride
+ * agree.  Asynchronous.  Errors: INVALID_ARG (NULL, bad struct_size, flags, dtype, eps or
+ * scale; neither y nor out; an output at the address of another one, or of a residual, y
+ * or gate that it does not lie like), SHAPE, ALIGN (a pointer not aligned to its element,
+ * a row stride below N), DEVICE, CUDA. */
 int qmm_residual_norm(const qmm_norm_args* args, void* stream);
 
 /* ---- adjustment of scores before sampling -------------------------------------------- */

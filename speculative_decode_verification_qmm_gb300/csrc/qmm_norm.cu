@@ -353,9 +353,11 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
   auto moves = [&](const void* to, int64_t ld, int size, const void* from, int64_t ld_from, int size_from) {
     return to && to == from && (size != size_from || (a->M > 1 && ld != ld_from));
   };
-  if ((a->y && a->residual_out == a->out) || (a->y && moves(a->residual_out, a->ld_residual_out, rs, a->residual, a->ld_residual, rs)) ||
-      (a->y && moves(a->residual_out, a->ld_residual_out, rs, a->y, a->ld_y, ys)) || moves(a->out, a->ld_out, os, a->y, a->ld_y, ys) ||
-      moves(a->out, a->ld_out, os, a->residual, a->ld_residual, rs))
+  auto onto = [&](const void* to, int64_t ld, int size) {
+    return moves(to, ld, size, a->residual, a->ld_residual, rs) || moves(to, ld, size, a->y, a->ld_y, ys) ||
+           moves(to, ld, size, a->gate, a->ld_gate, 4);
+  };
+  if ((a->y && a->residual_out == a->out) || (a->y && onto(a->residual_out, a->ld_residual_out, rs)) || onto(a->out, a->ld_out, os))
     return QMM_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   const int rc = host_check_device(&dev, &sms);

@@ -175,8 +175,8 @@ def residual_norm(residual, y=None, weight=None, bias=None, post_weight=None, po
     """(r', h): r' = residual + scale gate z with z = y or its norm with post_weight
     and post_bias, and h = norm(r') weight + bias in `dtype` (None: bf16).  Without y
     r' is the residual, without weight h is None.  Tensors are [..., N], weights and
-    biases fp32 [N], gate fp32 [N] or [..., N]; residual_out may be residual, and either
-    result y, where types agree.  See qmm_residual_norm."""
+    biases fp32 [N], gate fp32 [N] or [..., N]; residual_out and out may each be residual,
+    y or a gate [..., N] where types and strides agree.  See qmm_residual_norm."""
     import torch
     if stream is not None:  # the results are allocated on the stream that writes them
         with torch.cuda.stream(stream):

@@ -244,3 +244,20 @@ def test_refusals():
         q.residual_norm(a["residual"][:1].expand(4, 64).clone(), y=a["y"], weight=a["weight"], out=torch.zeros(1, 64, device="cuda").expand(4, 64))
     r, h = q.residual_norm(a["residual"][:0], a["y"][:0], a["weight"])
     assert r.shape == h.shape == (0, 64)
+
+
+def test_results_onto_the_gate():
+    """Each row onto its own gate's row; a row of gates for all is refused."""
+    for M, N in ((6, 900), (3000, 900), (700, 1001), (1, 515)):
+        a = make(M, N, "f32", "bf16", post=True, gate="full", seed=10)
+        r, h = q.residual_norm(**a, dtype=torch.float32)
+        for name, want in (("residual_out", r), ("out", h)):
+            b = a | dict(gate=a["gate"].clone())
+            got = q.residual_norm(**b, dtype=torch.float32, **{name: b["gate"]})
+            assert torch.equal(got[0], r) and torch.equal(got[1], h) and torch.equal(b["gate"], want)
+    gates = torch.zeros(6, 900, device="cuda")
+    a = make(6, 900, "f32", "bf16", seed=10) | dict(gate=gates[0])
+    for kw in (dict(out=gates, dtype=torch.float32), dict(residual_out=gates)):
+        with pytest.raises(q.QmmError) as e:
+            q.residual_norm(**a, **kw)
+        assert e.value.code == q.QMM_ERR_INVALID_ARG

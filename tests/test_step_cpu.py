@@ -263,3 +263,30 @@ def test_starts():
     assert c.starts([3, 0, 2]).tolist() == [0, 3, 3, 5] and c.starts([]).tolist() == [0]
     with pytest.raises(ValueError):
         c.starts([1, -1])
+
+
+# ------------------------------------------------------------------ outputs onto inputs
+def _norm_call(L, m, **kw):
+    a = _args(_lib.qmm_norm_args, **(dict(M=2, N=8, res_dtype=2, y_dtype=0, out_dtype=0, eps=1e-6, residual=m, ld_residual=8, y=m + 256, ld_y=8,
+                                          residual_out=m + 512, ld_residual_out=8, out=m + 768, ld_out=8, weight=m + 1024, scale=1.0,
+                                          gate=m + 1280, ld_gate=8) | kw))
+    return L.qmm_residual_norm(ctypes.byref(a), None)
+
+
+@pytest.mark.parametrize("kw", [dict(out="gate"), dict(out="gate", out_dtype=2, ld_out=9), dict(out="gate", out_dtype=2, ld_gate=0),
+                                dict(residual_out="gate", ld_residual_out=12), dict(residual_out="gate", ld_gate=0),
+                                dict(residual_out="gate", res_dtype=1), dict(out="gate", M=1)])
+def test_norm_outputs_onto_a_gate_that_lies_otherwise(L, memory, kw):
+    """A row of the output is not the gate's row that its thread reads."""
+    m = (memory & ~15) + 16
+    kw = {k: m + 1280 if v == "gate" else v for k, v in kw.items()}
+    assert _norm_call(L, m, **kw) == q.QMM_ERR_INVALID_ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("kw", [dict(out="gate", out_dtype=2), dict(residual_out="gate"), dict(out="gate", out_dtype=2, ld_out=9, M=1),
+                                dict(residual_out="gate", ld_gate=0, M=1)])
+def test_norm_outputs_onto_a_gate_that_lies_alike(L, memory, kw):
+    m = (memory & ~15) + 16
+    kw = {k: m + 1280 if v == "gate" else v for k, v in kw.items()}
+    assert _norm_call(L, m, **kw) == q.QMM_ERR_DEVICE
