@@ -613,8 +613,8 @@ typedef struct {
  * differ, may each be the residual, y or the gate where element size and row stride
  * agree.  Asynchronous.  Errors: INVALID_ARG (NULL, bad struct_size, flags, dtype, eps or
  * scale; neither y nor out; an output at the address of another one, or of a residual, y
- * or gate that it does not lie like), SHAPE, ALIGN (a pointer not aligned to its element,
- * a row stride below N), DEVICE, CUDA. */
+ * or gate that it does not lie like; a row of an output over a weight or bias), SHAPE, ALIGN
+ * (a pointer not aligned to its element, a row stride below N), DEVICE, CUDA. */
 int qmm_residual_norm(const qmm_norm_args* args, void* stream);
 
 /* ---- adjustment of scores before sampling -------------------------------------------- */

@@ -362,6 +362,18 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
   int dev = 0, sms = 0;
   const int rc = host_check_device(&dev, &sms);
   if (rc != QMM_OK) return rc;
+  // weights and biases are read for every row: no row of an output may touch them
+  auto touches = [&](const void* to, int64_t ld, int size, const float* vec) {
+    if (!to || !vec) return false;
+    const int64_t row = a->N * size, step = a->M > 1 ? ld * size : row, len = a->N * 4;
+    const int64_t d = (int64_t)((uintptr_t)vec - (uintptr_t)to);  // of the vector behind the first row's start
+    if (d < 0) return d + len > 0;
+    const int64_t m = d / step;  // the last row that begins at or before the vector
+    return (m < a->M && d - m * step < row) || (m + 1 < a->M && d + len > (m + 1) * step);
+  };
+  for (const float* vec : {a->weight, a->bias, a->post_weight, a->post_bias})
+    if ((a->y && touches(a->residual_out, a->ld_residual_out, rs, vec)) || touches(a->out, a->ld_out, os, vec))
+      return QMM_ERR_INVALID_ARG;
   NormParams p;
   p.res = a->residual, p.y = a->y, p.res_out = a->residual_out, p.out = a->out;
   const bool many = a->M > 1;  // the stride of a single row is not followed

@@ -261,3 +261,26 @@ def test_results_onto_the_gate():
         with pytest.raises(q.QmmError) as e:
             q.residual_norm(**a, **kw)
         assert e.value.code == q.QMM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["weight", "bias", "post_weight", "post_bias"])
+@pytest.mark.parametrize("onto", ["out", "residual_out"])
+@pytest.mark.parametrize("M,N,ld,at,bad", [
+    (4, 64, 64, 0, True), (4, 64, 64, 3 * 64, True), (4, 64, 64, 4 * 64, False),  # a row's place; behind the last row
+    (1, 64, 64, 0, True), (1, 64, 64, 32, True), (1, 64, 64, 64, False),
+    (4, 64, 200, 64, False), (4, 64, 200, 136, False), (4, 64, 200, 63, True), (4, 64, 200, 137, True),  # between rows, and beyond
+    (4, 64, 200, 600 + 64, False), (4, 64, 200, 600 + 63, True), (4, 64, 200, -64, False), (4, 64, 200, -63, True)])
+def test_outputs_over_weights(name, onto, M, N, ld, at, bad):
+    """A weight or bias that a row of an output lies over is refused, one between rows is not."""
+    a = make(M, N, post=True, post_bias=True, bias=True, seed=11)
+    buffer = torch.zeros(N + M * ld + N, device="cuda")
+    vector = buffer[N + at:2 * N + at]
+    vector.copy_(a[name])
+    b, kw = a | {name: vector}, {onto: buffer.as_strided((M, N), (ld, 1), N), "dtype": torch.float32}
+    if bad:
+        with pytest.raises(q.QmmError) as e:
+            q.residual_norm(**b, **kw)
+        assert e.value.code == q.QMM_ERR_INVALID_ARG
+    else:
+        check(b, **kw)
+    assert torch.equal(vector, a[name])
