@@ -8,8 +8,8 @@
 // Rows of up to SHORT entries: a warp each, straight from memory.  Longer ones: a CTA each,
 // which holds a whole row in registers, E entries a thread, so that r' is normalised
 // unrounded; the inputs of its next rows are on their way into shared memory meanwhile.
-// They are copied in whole 16-byte groups, which at a row's ends may hold other values,
-// so that rows need no alignment.
+// They are copied in groups of 16 bytes, so that rows need no alignment; the first of a row's may
+// begin in the row before it, and nothing outside the tensor is read (qmm_row_copy.h).
 // What bounds it: memory for many rows (8,192 rows of 5,120, bf16 + fp32 with a norm of both to bf16: 68.8
 // us, 6.1 TB/s, 91 % of a copy; with a gate a row too, 80 us and 5.2 TB/s), the chain load -> sum -> sum
 // for few (8 rows: 2.5 us).
@@ -22,6 +22,7 @@
 #include "qmm.h"
 #include "qmm_attn.cuh"
 #include "qmm_attn.h"
+#include "qmm_row_copy.h"
 
 namespace qmm {
 namespace {
@@ -234,10 +235,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ Norm
   auto request = [&](int64_t m, int stage) {
     if (m < p.M) {
       auto copy = [&](int to, const char* row, int bytes) {
-        const int s = skew(row), end = s + bytes;
-        const uint32_t dst = smem_u32(smem) + to;
+        const int s = skew(row);
         row -= s;
-        for (int c = t * 16; c < end; c += threads * 16) cp_async16(dst + c, row + c, 16);
+        copy_row(
+            t, threads, m, s, bytes, [&](int at, int n) { cp_async16(smem_u32(smem) + to + at, row + at, n); },
+            [&](int at) { *reinterpret_cast<uint16_t*>(smem + to + at) = *reinterpret_cast<const uint16_t*>(row + at); });
       };
       const int to = stage * stage_bytes;
       if (p.y) copy(to, row_of(p.y, m, p.ld_y, p.y_dt), y_bytes);
