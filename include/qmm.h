@@ -638,7 +638,7 @@ typedef struct {
   const uint32_t* prompt;   /* [B][ceil(V / 32)], row stride ld_prompt: bit v % 32 of
                                word v / 32: token v is in the prompt; NULL: none */
   int64_t ld_prompt;
-  const float* repetition;  /* [B], > 0; NULL: 1                                */
+  const float* repetition;  /* [B], 2^-126 .. 2^126; NULL: 1                    */
   const float* frequency;   /* [B]; NULL: 0                                     */
   const float* presence;    /* [B]; NULL: 0                                     */
   const float* bias;        /* [B][V], row stride ld_bias (0: one row for all); NULL: 0 */
@@ -656,7 +656,8 @@ typedef struct {
  *     c > 0 or v in the prompt:  x = x / repetition for x > 0, else x repetition
  *     x = x - frequency c - presence [c > 0] + bias[v]
  *     x = -inf where the node's mask bit is 0
- * in fp32, rounded once.  Rows t >= n_tokens[b] of out are not touched.  Nodes whose
+ * in fp32 (x / repetition as x times the rounded inverse, the terms after it as one sum),
+ * rounded once to the type of out.  Rows t >= n_tokens[b] of out are not touched.  Nodes whose
  * token is outside [0, V) count for nothing; a parent that does not come before its
  * node ends the path.  Asynchronous.
  * Errors: INVALID_ARG (NULL scores or out, bad struct_size or dtype, out == scores

@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) adjust_kernel(const __gr
       for (int e = 0; e < E; ++e) bias[e] = place<false>(e, t) < left ? __ldg(row + place<false>(e, t)) : 0.f;
     }
   }
-  // An entry becomes x (up for x > 0, else down) - term.
+  // An entry becomes x (up for x > 0, else down) - term.  (The inverse costs one rounding of fp32 more
+  // than a division, which took 77 to 112 us instead of 65 for 32 x 16 x 151,936, bf16, as more
+  // entries were seen.)
   const uint32_t in_prompt = bits_of<WIDE>(asked);
   float up[E], down[E], term[E];
 #pragma unroll
