@@ -399,3 +399,55 @@ def test_prompts_in_pieces_and_drafted_steps(dtype, Hq, Hkv, D, half):
     check_prompt(p, out, lse)
     check_prompt(p, got, got_lse)
     whole.close(), a.close()
+
+
+# ------------------------------------------------------------------ places out of range
+@pytest.mark.parametrize("change", [dict(lens=-1), dict(lens=-2 ** 31), dict(lens=59), dict(lens=64), dict(lens=2 ** 31 - 1),
+                                    dict(column=2, page=-1), dict(column=3, page=-2 ** 31), dict(column=2, page="all"),
+                                    dict(column=3, page=2 ** 31 - 1)])
+@pytest.mark.parametrize("dtype,src,D,dims,half,aligned", [("bf16", "f32", 64, 64, True, True), ("f16", "f16", 128, 96, False, True),
+                                                           ("bf16", "bf16", 64, 10, False, False)])
+def test_append_writes_only_what_has_a_place(change, dtype, src, D, dims, half, aligned):
+    """Both whole pools and the queries, bit for bit: rows without a place leave everything as it
+    was, all others are written as in a call without bad places."""
+    counts = [30, 20, 10]  # each sequence fills 50 rows of its four pages of 16
+    a = Append(dtype, src, D, 4, 2, 16, [20, 30, 40], counts, dims, half, seed=21, layers=3, layer=1, extra_rows=4)
+    assert a.table.shape == (3, 4)
+    if not aligned:
+        wide = torch.randn(a.N, 10, D + 1, device="cuda").to(TYPES[src])
+        a.x, a.k, a.v = wide[:, :4, 1:], wide[:, 4:6, 1:], wide[:, 7:9, 1:]
+    cache = a.make_cache(q)
+    positions = torch.arange(100, 100 + a.N, dtype=torch.int32, device="cuda")  # so that keys do not depend on lens
+    old = a.k_pool.clone(), a.v_pool.clone()
+    good = torch.full((a.N, 4, D), 3.0, dtype=a.dtype, device="cuda")
+
+    def call(out, lens, table):
+        a.k_pool.copy_(old[0]), a.v_pool.copy_(old[1])
+        cache.append(a.layer, a.x, a.k, a.v, table, lens, a.d_starts, rope=a.rope, positions=positions, out=out)
+        return cache.sync_status()
+
+    assert call(good, a.d_lens, a.table) == q.QMM_OK
+    keys = [[pool[a.layer, a.table[b, j // 16], :, j % 16].clone() for b in range(3) for j in range(a.lens[b], 50)] for pool in (a.k_pool, a.v_pool)]
+    lens, table = a.d_lens.clone(), a.table.clone()
+    if "lens" in change:
+        lens[1] = change["lens"]
+    else:
+        table[1, change["column"]] = a.k_pool.shape[1] if change["page"] == "all" else change["page"]
+    out = torch.full_like(good, 3.0)
+    assert call(out, lens, table) == q.QMM_ERR_INDEX
+    assert cache.sync_status() == q.QMM_OK
+    want, want_out, written = [p.clone() for p in old], torch.full_like(good, 3.0), 0
+    r = 0
+    for b in range(3):
+        for i in range(counts[b]):
+            j = int(lens[b]) + i
+            if lens[b] >= 0 and j < 64 and 0 <= int(table[b, j // 16]) < a.k_pool.shape[1]:
+                for pool, rows in zip(want, keys):
+                    pool[a.layer, table[b, j // 16], :, j % 16] = rows[r]
+                want_out[r] = good[r]
+                written += 1
+            r += 1
+    assert written < r == 60
+    for got, w in ((a.k_pool, want[0]), (a.v_pool, want[1]), (out, want_out)):
+        assert torch.equal(got.view(torch.int16), w.view(torch.int16))
+    cache.close()
