@@ -803,6 +803,10 @@ int qmm_debug_set_wait_limit(qmm_t h, int64_t ns);
 /* The same for the attention kernels of a cache handle. */
 int qmm_debug_set_cache_wait_limit(qmm_cache_t h, int64_t ns);
 
+/* Test hook: the rows of a row tile, 128 or 256, that qmm_prompt_attention takes for a
+ * call of these sizes.  Errors: STATE, INVALID_ARG (NULL rows), SHAPE (as there). */
+int qmm_debug_prompt_rows(qmm_cache_t h, int B, int64_t N, int table_width, int* rows);
+
 /* Test hook: make the n-th device allocation made by qmm_create from now on
  * fail as if cudaMalloc had failed (n = 0 disables; the hook fires once). */
 int qmm_debug_fail_allocs(int n);

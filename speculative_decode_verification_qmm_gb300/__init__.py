@@ -24,7 +24,7 @@ from ._lib import (QMM_DT_BF16, QMM_DT_F16, QMM_DT_F32, QMM_ERR_INDEX, QMM_TREE_
                    QMM_FLAG_HADAMARD32, QMM_FLAG_HADAMARD64, QMM_FLAG_HADAMARD128, QMM_FLAG_TCGEN05, QMM_FLAG_SIMT, QMM_FMT_FP8_E4M3_B128, QMM_FMT_Q4_0, QMM_FMT_Q8_0,
                    QMM_OK, QmmError, load, qmm_desc, qmm_info)
 from .paged import (PagedCache, Sequence, qmm_cache_append, qmm_cache_commit, qmm_cache_copy, qmm_cache_create,
-                    qmm_cache_destroy, qmm_cache_sync_status, qmm_debug_set_cache_wait_limit, qmm_prompt_attention,
+                    qmm_cache_destroy, qmm_cache_sync_status, qmm_debug_prompt_rows, qmm_debug_set_cache_wait_limit, qmm_prompt_attention,
                     qmm_tree_attention, qmm_verify_sample, qmm_verify_sample_workspace, tree_mask, verify_sample)
 from .step import (Rope, adjust_scores, count_tokens, qmm_adjust_scores, qmm_count_tokens, qmm_residual_norm, qmm_rotate,
                    residual_norm, rope_frequencies)
@@ -42,7 +42,7 @@ __all__ = [
     "QMM_FLAG_TCGEN05", "QMM_FLAG_HADAMARD64", "QMM_FLAG_HADAMARD128", "qmm_hadamard",
     "rotation_flag", "hadamard",
     "PagedCache", "Sequence", "verify_sample", "tree_mask", "qmm_cache_create", "qmm_cache_destroy",
-    "qmm_cache_sync_status", "qmm_debug_set_cache_wait_limit", "qmm_tree_attention", "qmm_cache_commit", "qmm_cache_copy",
+    "qmm_cache_sync_status", "qmm_debug_prompt_rows", "qmm_debug_set_cache_wait_limit", "qmm_tree_attention", "qmm_cache_commit", "qmm_cache_copy",
     "qmm_verify_sample", "qmm_verify_sample_workspace", "QMM_ERR_INDEX", "QMM_DT_BF16", "QMM_DT_F16",
     "QMM_DT_F32", "QMM_TREE_MAX_T",
     "Rope", "rope_frequencies", "residual_norm", "adjust_scores", "count_tokens", "qmm_rotate", "qmm_cache_append",

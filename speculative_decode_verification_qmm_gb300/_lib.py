@@ -311,6 +311,7 @@ SIGNATURES = {
     "qmm_quantize_fp8": (_INT, [_P, _I64, _I64, _U32, _P, _P, _P]),
     "qmm_debug_set_wait_limit": (_INT, [_P, _I64]),
     "qmm_debug_set_cache_wait_limit": (_INT, [_P, _I64]),
+    "qmm_debug_prompt_rows": (_INT, [_P, _INT, _I64, _INT, ctypes.POINTER(_INT)]),
     "qmm_debug_fail_allocs": (_INT, [_INT]),
     "qmm_debug_set_trace": (_INT, [_P, _P, _I64]),
 }

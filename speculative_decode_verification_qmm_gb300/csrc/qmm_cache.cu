@@ -248,6 +248,18 @@ int prompt_rows(int D, int g, int64_t N, int B, int64_t capacity, int Hkv, int g
   return items * (tiles + 3) >= (int64_t)20 * grid ? 256 : 128;
 }
 
+int prompt_grid(int sms) { return sms < ATTN_PROMPT_GRID_MAX ? sms : ATTN_PROMPT_GRID_MAX; }
+
+// Of a prompt call: whether its sizes are in range, and its rows of a row tile.
+bool prompt_sizes_ok(const qmm_cache* h, int B, int64_t N, int table_width) {
+  return B >= 1 && B <= h->d.max_batch && N >= 0 && N <= QMM_CACHE_MAX_ROWS && table_width >= 1 &&
+         ((int64_t)table_width << h->page_shift) <= INT32_MAX - 4096;
+}
+int prompt_rows_of(const qmm_cache* h, int B, int64_t N, int table_width) {
+  return prompt_rows(h->d.head_dim, h->d.n_q_heads / h->d.n_kv_heads, N, B, (int64_t)table_width << h->page_shift,
+                     h->d.n_kv_heads, prompt_grid(h->sm_count));
+}
+
 }  // namespace
 
 extern "C" {
@@ -420,9 +432,7 @@ int qmm_cache_append(qmm_cache_t h, const qmm_append_args* a, void* stream) {
   if (a->dtype > QMM_DT_F32 || (a->N != 0 && (!a->k || !a->v || !a->q != !a->q_out)) || !a->page_table || !a->lens || !a->starts)
     return QMM_ERR_INVALID_ARG;
   const qmm_cache_desc& d = h->d;
-  if (a->layer < 0 || a->layer >= d.n_layers || a->B < 1 || a->B > d.max_batch || a->N < 0 || a->N > QMM_CACHE_MAX_ROWS ||
-      a->table_width < 1 || ((int64_t)a->table_width << h->page_shift) > INT32_MAX - 4096)
-    return QMM_ERR_SHAPE;
+  if (a->layer < 0 || a->layer >= d.n_layers || !prompt_sizes_ok(h, a->B, a->N, a->table_width)) return QMM_ERR_SHAPE;
   int rc = a->rope ? rope_check(a->rope, d.head_dim) : QMM_OK;
   if (rc != QMM_OK) return rc;
   const int elem = a->dtype == QMM_DT_F32 ? 4 : 2;
@@ -479,9 +489,7 @@ int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* a, void* stream) 
   if (!(a->scale > 0.f) || !isfinite(a->scale)) return QMM_ERR_INVALID_ARG;
   if (a->N > 0 && a->q == a->out) return QMM_ERR_INVALID_ARG;  // q is read again where V is not finite
   const qmm_cache_desc& d = h->d;
-  if (a->layer < 0 || a->layer >= d.n_layers || a->B < 1 || a->B > d.max_batch || a->N < 0 || a->N > QMM_CACHE_MAX_ROWS ||
-      a->table_width < 1 || ((int64_t)a->table_width << h->page_shift) > INT32_MAX - 4096)
-    return QMM_ERR_SHAPE;
+  if (a->layer < 0 || a->layer >= d.n_layers || !prompt_sizes_ok(h, a->B, a->N, a->table_width)) return QMM_ERR_SHAPE;
   if ((((uintptr_t)a->q | (uintptr_t)a->out) & 15) ||
       (((uintptr_t)a->lse | (uintptr_t)a->page_table | (uintptr_t)a->lens | (uintptr_t)a->starts) & 3))
     return QMM_ERR_ALIGN;
@@ -517,11 +525,11 @@ int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* a, void* stream) 
   p.cuts = h->cuts;
   p.status = h->status;
   p.wait_limit_ns = h->wait_limit_ns;
-  p.grid = h->sm_count < ATTN_PROMPT_GRID_MAX ? h->sm_count : ATTN_PROMPT_GRID_MAX;
+  p.grid = prompt_grid(h->sm_count);
   p.row0 = (int64_t)a->layer * d.n_pages * d.n_kv_heads * d.page_size;
   pp.starts = a->starts;
   pp.N = (int)a->N;
-  pp.rows = prompt_rows(d.head_dim, p.g, a->N, a->B, (int64_t)a->table_width << h->page_shift, p.Hkv, p.grid);
+  pp.rows = prompt_rows_of(h, a->B, a->N, a->table_width);
   pp.per = pp.rows / p.g;
   p.R = pp.rows;
   const bool bf16 = d.dtype == QMM_DT_BF16;
@@ -607,6 +615,14 @@ int qmm_debug_set_cache_wait_limit(qmm_cache_t h, int64_t ns) {
   if (!is_live(h)) return QMM_ERR_STATE;
   if (ns < 0) return QMM_ERR_INVALID_ARG;
   h->wait_limit_ns = (uint64_t)ns;
+  return QMM_OK;
+}
+
+int qmm_debug_prompt_rows(qmm_cache_t h, int B, int64_t N, int table_width, int* rows) {
+  if (!is_live(h)) return QMM_ERR_STATE;
+  if (!rows) return QMM_ERR_INVALID_ARG;
+  if (!prompt_sizes_ok(h, B, N, table_width)) return QMM_ERR_SHAPE;
+  *rows = prompt_rows_of(h, B, N, table_width);
   return QMM_OK;
 }
 

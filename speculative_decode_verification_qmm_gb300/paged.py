@@ -203,6 +203,12 @@ def qmm_debug_set_cache_wait_limit(h, ns: int) -> None:
     _check("qmm_debug_set_cache_wait_limit", load().qmm_debug_set_cache_wait_limit(h, ns))
 
 
+def qmm_debug_prompt_rows(h, B: int, N: int, table_width: int) -> int:
+    rows = ctypes.c_int()
+    _check("qmm_debug_prompt_rows", load().qmm_debug_prompt_rows(h, B, N, table_width, ctypes.byref(rows)))
+    return rows.value
+
+
 @functools.lru_cache(maxsize=256)
 def qmm_verify_sample_workspace(B: int, T: int, V: int) -> int:
     """Bytes of device workspace qmm_verify_sample needs for those sizes (and them alone)."""

@@ -291,3 +291,71 @@ def test_a_destroyed_cache():
     with pytest.raises(q.QmmError) as e:
         q.qmm_prompt_attention(handle, 0, p.q, p.table, p.d_lens, p.d_starts, torch.empty_like(p.q))
     assert e.value.code == q.QMM_ERR_STATE
+
+
+# ------------------------------------------------------------------ both kernels, each by name
+def tall(p, cache):
+    return q.qmm_debug_prompt_rows(cache.handle, p.B, p.N, p.table.shape[1])
+
+
+# a table that 1,000,000 rows fit in: 256 rows a tile wherever a sequence has more than 128 on average
+FAR = 1_000_000
+
+
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,page,lens,counts", [s for s in SHAPES if sum(s[6]) * s[2] // s[3] > 128 * len(s[6])])
+def test_tables_choose_the_kernel(dtype, D, Hq, Hkv, page, lens, counts):
+    for columns, rows in ((0, 128), (FAR // page, 256)):
+        p = Prompt(dtype, D, Hq, Hkv, page, lens, counts, extra_columns=columns, seed=D)
+        cache = p.make_cache(q)
+        assert tall(p, cache) == rows
+        out, lse = p.call(cache)
+        assert cache.sync_status() == q.QMM_OK
+        check_prompt(p, out, lse)
+        cache.close()
+
+
+@pytest.mark.parametrize("columns,rows", [(0, 128), (FAR // 16, 256)])
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,L,n", [("bf16", 64, 2, 1, 0, 90), ("bf16", 64, 4, 1, 5, 40), ("f16", 128, 4, 1, 60, 33), ("bf16", 128, 1, 1, 3, 131)])
+def test_few_rows_that_are_not_finite(dtype, D, Hq, Hkv, L, n, columns, rows):
+    """Values and keys of new rows, of little more than a row tile of 128, by both kernels."""
+    p = Prompt(dtype, D, Hq, Hkv, 16, [L], [n], extra_columns=columns, seed=19)
+    ids = p.table[0].long()
+    for j, what, where, pool in ((L + 1, math.inf, 3, p.v_pool), (L + n // 2, -math.inf, D - 1, p.v_pool), (L + n // 2 + 1, math.nan, 5, p.v_pool),
+                                 (L + n - 1, math.nan, 0, p.v_pool), (L + n - 2, math.nan, 1, p.k_pool)):
+        pool[0, ids[j // 16], :, j % 16, where] = what
+    cache = p.make_cache(q)
+    assert tall(p, cache) == rows
+    cache.close()
+    run(p)
+
+
+@pytest.mark.parametrize("columns,rows", [(0, 128), (FAR // 16, 256)])
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("counts", [[70], [40, 120]])
+def test_expired_waits_of_both_kernels(counts, D, columns, rows):
+    p = Prompt("bf16", D, 4, 2, 16, [300] * len(counts), counts, extra_columns=columns, seed=20)
+    cache = p.make_cache(q)
+    assert tall(p, cache) == rows
+    q.qmm_debug_set_cache_wait_limit(cache.handle, 0)
+    p.call(cache)
+    assert cache.sync_status() == q.QMM_ERR_TIMEOUT
+    q.qmm_debug_set_cache_wait_limit(cache.handle, 2_000_000_000)
+    out, lse = p.call(cache)
+    assert cache.sync_status() == q.QMM_OK
+    check_prompt(p, out, lse)
+    cache.close()
+
+
+def test_prompt_rows_refusals():
+    p = Prompt("bf16", 64, 4, 2, 16, [20], [30], seed=21)
+    cache = p.make_cache(q)
+    assert tall(p, cache) == 128
+    for sizes in ((0, 30, 4), (2, 30, 4), (1, -1, 4), (1, (1 << 24) + 1, 4), (1, 30, 0), (1, 30, 1 << 27)):
+        with pytest.raises(q.QmmError) as e:
+            q.qmm_debug_prompt_rows(cache.handle, *sizes)
+        assert e.value.code == q.QMM_ERR_SHAPE
+    handle = cache.handle
+    cache.close()
+    with pytest.raises(q.QmmError) as e:
+        q.qmm_debug_prompt_rows(handle, 1, 30, 4)
+    assert e.value.code == q.QMM_ERR_STATE
