@@ -9,7 +9,7 @@
 // which holds a whole row in registers, E entries a thread, so that r' is normalised
 // unrounded; the inputs of its next rows are on their way into shared memory meanwhile.
 // They are copied in groups of 16 bytes, so that rows need no alignment; the first of a row's may
-// begin in the row before it, and nothing outside the tensor is read (qmm_row_copy.h).
+// begin in the row before it, and nothing outside the tensor is read (qmm_norm_copy.h).
 // What bounds it: memory for many rows (8,192 rows of 5,120, bf16 + fp32 with a norm of both to bf16: 68.8
 // us, 6.1 TB/s, 91 % of a copy; with a gate a row too, 80 us and 5.2 TB/s), the chain load -> sum -> sum
 // for few (8 rows: 2.5 us).
@@ -22,7 +22,7 @@
 #include "qmm.h"
 #include "qmm_attn.cuh"
 #include "qmm_attn.h"
-#include "qmm_row_copy.h"
+#include "qmm_norm_copy.h"
 
 namespace qmm {
 namespace {

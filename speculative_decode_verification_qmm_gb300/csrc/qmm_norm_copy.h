@@ -1,4 +1,4 @@
-// qmm_row_copy.h -- how the threads of a CTA share the copy of a row whose ends lie
+// qmm_norm_copy.h -- how the threads of a CTA share the copy of a row whose ends lie
 // anywhere (internal; qmm_norm.cu).  Host and device, so that its bounds are tested
 // without a GPU.
 #pragma once

@@ -9,7 +9,7 @@ PROGRAM = r"""
 #include <stdio.h>
 #include <string.h>
 #include <vector>
-#include "qmm_row_copy.h"
+#include "qmm_norm_copy.h"
 
 // A tensor of M rows of N elements, `ld` apart, that begins `base` bytes behind a boundary of 16.
 static int check(int size, int N, int64_t M, int64_t ld, int base, int threads) {
