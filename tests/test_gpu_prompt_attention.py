@@ -359,3 +359,25 @@ def test_prompt_rows_refusals():
     with pytest.raises(q.QmmError) as e:
         q.qmm_debug_prompt_rows(handle, 1, 30, 4)
     assert e.value.code == q.QMM_ERR_STATE
+
+
+def test_two_caches_at_once():
+    """Calls of two handles on two streams run side by side and give what they give alone."""
+    shapes = [("bf16", 128, 8, 2, 16, [1000, 0], [100, 700]), ("f16", 64, 8, 2, 32, [0, 900], [500, 60])]
+    ps = [Prompt(*s, extra_columns=c, seed=22 + i) for i, (s, c) in enumerate(zip(shapes, (0, FAR // 32)))]
+    caches = [p.make_cache(q) for p in ps]
+    alone = [p.call(c) for p, c in zip(ps, caches)]
+    for p, (out, lse) in zip(ps, alone):
+        check_prompt(p, out, lse)
+    streams = [torch.cuda.Stream() for _ in ps]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    results = [[p.call(c, stream=s) for p, c, s in zip(ps, caches, streams)] for _ in range(20)]
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for both in results:
+        for (out, lse), (want, want_lse) in zip(both, alone):
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, want_lse)
+    for c in caches:
+        assert c.sync_status() == q.QMM_OK
+        c.close()
