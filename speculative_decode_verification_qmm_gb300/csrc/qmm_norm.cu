@@ -357,7 +357,7 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
   };
   auto onto = [&](const void* to, int64_t ld, int size) {
     return moves(to, ld, size, a->residual, a->ld_residual, rs) || moves(to, ld, size, a->y, a->ld_y, ys) ||
-           moves(to, ld, size, a->gate, a->ld_gate, 4);
+           (a->y && moves(to, ld, size, a->gate, a->ld_gate, 4));
   };
   if ((a->y && a->residual_out == a->out) || (a->y && onto(a->residual_out, a->ld_residual_out, rs)) || onto(a->out, a->ld_out, os))
     return QMM_ERR_INVALID_ARG;
@@ -373,9 +373,11 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
     const int64_t m = d / step;  // the last row that begins at or before the vector
     return (m < a->M && d - m * step < row) || (m + 1 < a->M && d + len > (m + 1) * step);
   };
-  for (const float* vec : {a->weight, a->bias, a->post_weight, a->post_bias})
-    if ((a->y && touches(a->residual_out, a->ld_residual_out, rs, vec)) || touches(a->out, a->ld_out, os, vec))
-      return QMM_ERR_INVALID_ARG;
+  auto over = [&](const float* vec) {
+    return (a->y && touches(a->residual_out, a->ld_residual_out, rs, vec)) || touches(a->out, a->ld_out, os, vec);
+  };
+  if ((a->out && (over(a->weight) || over(a->bias))) || (a->y && (over(a->post_weight) || over(a->post_bias))))
+    return QMM_ERR_INVALID_ARG;
   NormParams p;
   p.res = a->residual, p.y = a->y, p.res_out = a->residual_out, p.out = a->out;
   const bool many = a->M > 1;  // the stride of a single row is not followed
@@ -385,7 +387,8 @@ extern "C" int qmm_residual_norm(const qmm_norm_args* a, void* stream) {
   p.ld_out = many && a->out ? a->ld_out : 0;
   p.ld_gate = many && a->gate ? a->ld_gate : 0;
   p.weight = a->weight, p.bias = a->bias;
-  p.post_weight = a->post_weight, p.post_bias = a->post_bias, p.gate = a->gate;
+  p.post_weight = a->post_weight, p.post_bias = a->post_bias;
+  p.gate = a->y ? a->gate : nullptr;  // (rows ahead are copied with their gates)
   p.M = a->M;
   p.N = (int)a->N;
   p.res_dt = a->res_dtype, p.y_dt = a->y_dtype, p.out_dt = a->out_dtype;

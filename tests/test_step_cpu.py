@@ -290,3 +290,9 @@ def test_norm_outputs_onto_a_gate_that_lies_alike(L, memory, kw):
     m = (memory & ~15) + 16
     kw = {k: m + 1280 if v == "gate" else v for k, v in kw.items()}
     assert _norm_call(L, m, **kw) == q.QMM_ERR_DEVICE
+
+
+@no_gpu
+def test_norm_without_y_has_no_gate(L, memory):
+    m = (memory & ~15) + 16
+    assert _norm_call(L, m, y=None, residual_out=None, out=m + 1280) == q.QMM_ERR_DEVICE
