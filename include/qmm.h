@@ -403,7 +403,8 @@ typedef struct {
  * L + n - 1 is read.
  * Scores, softmax statistics and sums are fp32; the exponentials are rounded
  * to the 16-bit type for the product with V, as the outputs are at the end (in
- * f16 one below 2^-32 of the row's largest counts in the sum of exponentials alone).
+ * f16 one below 2^-32 of the row's largest counts in the sum of exponentials alone,
+ * and an infinite value of its gives NaN).
  * All pointers to 16-bit data are 16-byte aligned.  What a call costs depends on
  * table_width too: a table no wider than the sequences need lets short batches
  * take shorter paths (at most 1,024 rows a sequence; no joining launch where one
@@ -529,9 +530,10 @@ typedef struct {
  * belong to no sequence: nothing is written for them.  A row whose place or page
  * is out of range is skipped and reported (qmm_cache_sync_status).  The caller
  * sees to it that no two rows of a call have the same place.  Asynchronous.
- * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), q or q_out NULL alone,
- * q_out == q with other strides or element size, bad struct_size, dtype or rope), SHAPE (layer, B, N, table_width, rope->dims), ALIGN (a pointer
- * not aligned to its element, ld_table < table_width with B > 1), DEVICE, CUDA. */
+ * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), q or q_out NULL
+ * alone, q_out == q with other strides or element size, bad struct_size, dtype or
+ * rope), SHAPE (layer, B, N, table_width, rope->dims), ALIGN (a pointer not aligned to
+ * its element, ld_table < table_width with B > 1), DEVICE, CUDA. */
 int qmm_cache_append(qmm_cache_t h, const qmm_append_args* args, void* stream);
 
 typedef struct {
@@ -563,12 +565,12 @@ typedef struct {
  * bits.  What a call costs depends on table_width too: a table about as wide as the
  * sequences need lets the rows of a tile be chosen by how many cached rows they see.
  * Asynchronous.
- * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), out == q, bad struct_size or scale), SHAPE
- * (layer, B, N or table_width out of range), ALIGN (pointers, strides, ld_table <
- * table_width; not strides of dimensions of one entry), DEVICE, CUDA.  Lengths,
- * starts and page ids are checked on the device (qmm_cache_sync_status): a sequence
- * that the table or N cannot hold is left alone, and a page that does not exist is
- * read as page 0. */
+ * Errors: STATE, INVALID_ARG (NULL pointers (of rows: with N > 0), out == q, bad
+ * struct_size or scale), SHAPE (layer, B, N or table_width out of range), ALIGN
+ * (pointers, strides, ld_table < table_width; not strides of dimensions of one entry),
+ * DEVICE, CUDA.  Lengths, starts and page ids are checked on the device
+ * (qmm_cache_sync_status): a sequence that the table or N cannot hold is left alone,
+ * and a page that does not exist is read as page 0. */
 int qmm_prompt_attention(qmm_cache_t h, const qmm_prompt_args* args, void* stream);
 
 /* ---- residual sums and norms -------------------------------------------------------- */
@@ -667,8 +669,8 @@ int qmm_adjust_scores(const qmm_adjust_args* args, void* stream);
 
 /* After a step: counts[b][v] += 1 for every token that sequence b emitted, the
  * accepted nodes' tokens[b][path[b][j]], j < accept[2 b], and the next token
- * accept[2 b + 1] (the layouts of qmm_verify_sample).  Tokens outside [0, V) and path entries outside
- * [0, T) are skipped.  tokens, path: device, int32 [B][T], contiguous.
+ * accept[2 b + 1] (the layouts of qmm_verify_sample).  Tokens outside [0, V) and path
+ * entries outside [0, T) are skipped.  tokens, path: device, int32 [B][T], contiguous.
  * Asynchronous.  Errors: INVALID_ARG (NULL), SHAPE (B, T, V as above), ALIGN
  * (pointers, ld_counts < V with B > 1), DEVICE, CUDA. */
 int qmm_count_tokens(int32_t* counts, int64_t ld_counts, int B, int T, int64_t V, const int32_t* tokens,

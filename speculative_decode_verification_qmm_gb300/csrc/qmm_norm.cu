@@ -10,9 +10,9 @@
 // unrounded; the inputs of its next rows are on their way into shared memory meanwhile.
 // They are copied in groups of 16 bytes, so that rows need no alignment; the first of a row's may
 // begin in the row before it, and nothing outside the tensor is read (qmm_norm_copy.h).
-// What bounds it: memory for many rows (8,192 rows of 5,120, bf16 + fp32 with a norm of both to bf16: 68.8
-// us, 6.1 TB/s, 91 % of a copy; with a gate a row too, 80 us and 5.2 TB/s), the chain load -> sum -> sum
-// for few (8 rows: 2.5 us).
+// What bounds it: memory for many rows (8,192 rows of 5,120, bf16 + fp32 to bf16, us: one norm 65.1, 6.4 TB/s,
+// 96 % of a copy; a norm of y too 68.6, 6.1 TB/s; and one row of gates 80, 5.2; a row of gates each
+// 104, 5.7), the chain load -> sum -> sum for few (8 rows: 2.6 us), registers past 16,384 entries.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -323,7 +323,8 @@ cudaError_t launch(const NormParams& p, int dev, int sms, cudaStream_t st) {
   // done sooner with few entries a thread, many rows want few threads for a sum.  us, of bf16 + fp32
   // to bf16, 4 : 8 entries: 20,000 rows of 128 8.3 : 9.6, of 256 14.6 : 10.8, of 512 26.1 : 18.9; 8 : 16 entries:
   // 8 rows of 777 2.7 : 3.6, 20,000 of 777 47 : 39, of 1,024 34.0 : 34.4, of 1,500 51.7 : 52.3, of 2,048
-  // 66.3 : 65.0; 16 : 32 entries, 2,000 rows of 16,000: 69 : 128, for registers.
+  // 66.3 : 65.0; 16 : 32 entries, 2,000 rows of 16,000: 69 : 128, for registers.  (Many rows of 513 to
+  // 1,023 entries off four would be done sooner with 16, few rows and those on four would not.)
   if (p.N <= 128) return launch_long<4, V>(p, dev, sms, st);
   if (p.N <= 1024) return launch_long<8, V>(p, dev, sms, st);
   return p.N <= 16384 ? launch_long<16, V>(p, dev, sms, st) : launch_long<32, V>(p, dev, sms, st);

@@ -11,10 +11,10 @@
 // all nodes, as two factors and a term for each entry.  Which nodes lie on a node's path
 // is one bit each of a 64-bit word; where a node's tokens fall into the range, which few
 // do, their entries are worked out anew.
-// What bounds it: memory for large batches (32 chains of 16 x 151,936, bf16, with biases and masks 73.5 us,
-// 4.7 TB/s, 70 % of a copy; without them 65.7 and 5.0), a launch and two dependent loads for one tree (8 x
-// 151,936, fp32: 4.5 us); rows that do not begin on 16 bytes are bound by the number of loads and
-// stores, one an entry (32 x 16 x 50,257, bf16: 36 us, of 50,256 27.4).
+// What bounds it: memory for large batches (32 chains of 16 x 151,936, bf16, with biases and masks 73.6 us,
+// 4.6 TB/s, 69 % of a copy; without them 68.4 and 4.8, trees 65.0 and 5.1), a launch and two dependent
+// loads for one tree (8 x 151,936, fp32: 4.7 us); rows that do not begin on 16 bytes are bound by the number
+// of loads and stores, one an entry (32 x 16 x 50,257, bf16: 38 us, of 50,256 29.5).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
